@@ -25,6 +25,9 @@ __all__ = [
     "add_rmsnorm_fp8_fwd", "rmsnorm_fp8_fwd", "add_rmsnorm_fp4_fwd", "rmsnorm_fp4_fwd",
     "fused_qk_rmsnorm_group_quant_fwd", "qk_resolve_config", "QkPlan",
     "lse_merge_fwd", "invariant_unary_fwd", "UNARY_OPS",
+    "dropout_fwd", "dropout_add_fwd", "dropout_add_rmsnorm_fwd", "dropout_add_rmsnorm_bwd", "add_rmsnorm_bwd",
+    "rmsnorm_bwd", "rope_fwd", "rope_bwd", "qk_rmsnorm_rope_fwd", "qk_rmsnorm_rope_bwd", "rope_frequencies",
+    "ROPE_SCALINGS",
     "LaunchConfig", "DraddError", "resolve_config",
     "device_status", "last_device_status", "bf16_convert_range", "status_string", "abi_version", "lib",
     "library_path", "VARIANT_AUTO", "VARIANT_ROWS", "VARIANT_STAGED", "VARIANT_SPLIT", "VARIANT_WARP",
@@ -42,6 +45,7 @@ OP_ADD_RMSNORM_FP4, OP_RMSNORM_FP4 = 6, 7
 STATUS_NAMES = {
     0: "OK", 1: "NULL_PTR", 2: "BAD_SHAPE", 3: "UNSUPPORTED_HIDDEN", 4: "MISALIGNED",
     5: "BAD_EPS", 6: "ALIAS", 7: "CUDA", 8: "TIMEOUT", 9: "BAD_CONFIG", 10: "UNDRAINED",
+    11: "BAD_ARG", 12: "WORKSPACE",
 }
 
 
@@ -161,6 +165,8 @@ def lib() -> ctypes.CDLL:
         f = getattr(L, name)
         f.argtypes = args
         f.restype = ctypes.c_int
+    from . import train
+    train._bind(L)
     L.dradd_status_string.argtypes = [ctypes.c_int]
     L.dradd_status_string.restype = ctypes.c_char_p
     L.dradd_abi_version.argtypes = []
@@ -624,3 +630,8 @@ def bf16_convert_range(out, first: int, count: int, method: int = 0, stream=None
                                           _stream_handle(stream, out.device)),
            "dradd_bf16_convert_range")
     return out
+
+
+from .train import (  # noqa: E402  (train uses the helpers above)
+    ROPE_SCALINGS, add_rmsnorm_bwd, dropout_add_fwd, dropout_add_rmsnorm_bwd, dropout_add_rmsnorm_fwd, dropout_fwd,
+    qk_rmsnorm_rope_bwd, qk_rmsnorm_rope_fwd, rmsnorm_bwd, rope_bwd, rope_frequencies, rope_fwd)

@@ -4,82 +4,25 @@
 // Nothing here changes a result bit: the configuration only decides how rows
 // and blocks are spread over threads, CTAs and SMs, and the kernels combine
 // the partial sums in the same canonical pairwise order for every choice.
-#include <atomic>
 #include <cmath>
-#include <initializer_list>
 #include <cstdint>
 #include <cstring>
 
 #include "dradd.h"
+#include "dradd_host.h"
 #include "dradd_internal.h"
 
 namespace {
 
 using dradd::Params;
 
-constexpr int kMaxDevices = 64;
-constexpr uint64_t kDefaultWaitLimitNs = 1000000000ull;  // 1 s
-
-// Shared-memory and thread limits used to size grids and stages.  Defaults
-// are GB300's; with a live device they come from the device.
-struct DeviceLimits {
-    int sm_count = 152;
-    int smem_per_block_optin = 232448;  // 227 KiB
-    int smem_per_sm = 233472;           // 228 KiB
-    int max_threads_per_sm = 2048;
-    int max_blocks_per_sm = 32;
-};
-
-std::atomic<int> g_limits_ready[kMaxDevices];
-DeviceLimits g_limits[kMaxDevices];
-
-dradd_status query_limits(DeviceLimits* out)
-{
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess)
-        return DRADD_ERR_CUDA;
-    if (dev >= 0 && dev < kMaxDevices && g_limits_ready[dev].load(std::memory_order_acquire)) {
-        *out = g_limits[dev];
-        return DRADD_OK;
-    }
-    DeviceLimits L;
-    if (cudaDeviceGetAttribute(&L.sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&L.smem_per_block_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) !=
-            cudaSuccess ||
-        cudaDeviceGetAttribute(&L.smem_per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) !=
-            cudaSuccess ||
-        cudaDeviceGetAttribute(&L.max_threads_per_sm, cudaDevAttrMaxThreadsPerMultiProcessor, dev) !=
-            cudaSuccess ||
-        cudaDeviceGetAttribute(&L.max_blocks_per_sm, cudaDevAttrMaxBlocksPerMultiprocessor, dev) !=
-            cudaSuccess)
-        return DRADD_ERR_CUDA;
-    if (dev >= 0 && dev < kMaxDevices) {
-        g_limits[dev] = L;  // identical values if two threads race here
-        g_limits_ready[dev].store(1, std::memory_order_release);
-    }
-    *out = L;
-    return DRADD_OK;
-}
-
-// True when every non-NULL pointer is device memory.  Other memory the GPU
-// can address (pinned or registered host memory, memory the GPU reaches
-// through the host link, managed memory) is served by the register-load
-// variant only: the staged variant's bulk copies are used on device memory.
-bool all_device_memory(std::initializer_list<const void*> ptrs)
-{
-    for (const void* p : ptrs) {
-        if (!p)
-            continue;
-        cudaPointerAttributes a;
-        if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-            cudaGetLastError();  // not a sticky error; the pointer is simply not device memory
-            return false;
-        }
-        if (a.type != cudaMemoryTypeDevice)
-            return false;
-    }
-    return true;
-}
+using dradd::aligned;
+using dradd::all_device_memory;
+using dradd::DeviceLimits;
+using dradd::kDefaultWaitLimitNs;
+using dradd::query_limits;
+using dradd::Range;
+using dradd::range_of;
 
 bool is_pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
 
@@ -90,23 +33,6 @@ int64_t next_pow2(int64_t v)
         p *= 2;
     return p;
 }
-
-// Byte ranges of the buffers of one call, for the overlap rules.
-struct Range {
-    uintptr_t lo = 0, hi = 0;  // [lo, hi)
-    bool overlaps(const Range& o) const { return lo < o.hi && o.lo < hi; }
-    bool same(const Range& o) const { return lo == o.lo && hi == o.hi; }
-};
-
-Range range_of(const void* p, int64_t bytes)
-{
-    Range r;
-    r.lo = reinterpret_cast<uintptr_t>(p);
-    r.hi = r.lo + static_cast<uintptr_t>(bytes);
-    return r;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Outputs must not overlap one another.  A bf16 output may coincide exactly
 // with x or residual (inputs 0 and 2: each element is read by the thread that
@@ -1771,6 +1697,9 @@ const char* dradd_status_string(dradd_status status)
     case DRADD_ERR_BAD_CONFIG: return "DRADD_ERR_BAD_CONFIG: invalid launch configuration";
     case DRADD_ERR_UNDRAINED:
         return "DRADD_ERR_UNDRAINED: a bounded wait expired and an issued copy had not landed";
+    case DRADD_ERR_BAD_ARG:
+        return "DRADD_ERR_BAD_ARG: a probability, scale, type or layout argument is out of its range";
+    case DRADD_ERR_WORKSPACE: return "DRADD_ERR_WORKSPACE: the workspace is NULL or too small";
     default: return "DRADD_ERR_UNKNOWN";
     }
 }

@@ -1,0 +1,112 @@
+// dradd_dropnorm.cu -- how the rows of dropout + residual add + RMSNorm and
+// of its gradients are spread (dradd_dropnorm.cuh), and the sums of dweight's
+// parts.
+#include "dradd_elem.cuh"
+#include "dradd_internal.h"
+#include "dradd_train_internal.h"
+
+namespace dradd {
+
+namespace {
+
+constexpr int kSms = 152;  // a constant, not the device's count: the parts of dweight follow the grid
+constexpr int kSmemPerSm = 227 * 1024;
+constexpr int kMaxStages = 4;
+
+}  // namespace
+
+DropNormPlan drop_norm_plan(int64_t n_rows, int hidden, int elem, bool backward, bool device_memory)
+{
+    DropNormPlan p = {};
+    int P = 64;
+    while (P < hidden)
+        P *= 2;
+    int per_sm;
+    int64_t units;
+    if (P <= 1024) {
+        p.warp = true;
+        p.lanes = P / 8 < 32 ? P / 8 : 32;
+        p.K = P / 8 / p.lanes;
+        p.threads = 256;
+        const int rows = p.threads / p.lanes;
+        units = (n_rows + rows - 1) / rows;
+        per_sm = 4;
+    } else {
+        p.K = P <= 2048 ? 1 : P <= 8192 ? 2 : P / 4096;
+        p.threads = P / 8 / p.K;
+        units = n_rows;
+        // As many CTAs per SM as leave each of them enough slots (the
+        // backward pass refills a slot one row later, so it wants one more).
+        const int64_t slot = static_cast<int64_t>(hidden) * (elem == kElemF32 ? 4 : 2) * (backward ? 3 : 2);
+        int stages = 0;
+        for (per_sm = p.K <= 2 ? 1024 / p.threads : 1;; per_sm /= 2) {
+            const int64_t room = kSmemPerSm / per_sm - 4096;  // less the system's share and the kernel's own
+            stages = static_cast<int>(room / slot);
+            if (stages >= (backward ? 3 : 2) || per_sm == 1)
+                break;
+        }
+        if (stages > kMaxStages)
+            stages = kMaxStages;
+        if (device_memory && stages >= 2) {
+            p.staged = true;
+            p.stages = stages;
+            p.smem = static_cast<size_t>(stages * slot) + 8 * stages;
+        }
+    }
+    const int64_t most = static_cast<int64_t>(kSms) * per_sm;
+    p.grid = static_cast<int>(units < most ? units : most);
+    return p;
+}
+
+cudaError_t launch_drop_norm_fwd(const DropNormArgs& a, const DropNormPlan& p, int elem, cudaStream_t stream)
+{
+    return elem == kElemBf16  ? launch_drop_norm_bf16(a, p, false, stream)
+           : elem == kElemF16 ? launch_drop_norm_f16(a, p, false, stream)
+                              : launch_drop_norm_f32(a, p, false, stream);
+}
+
+cudaError_t launch_drop_norm_bwd(const DropNormArgs& a, const DropNormPlan& p, int elem, cudaStream_t stream)
+{
+    return elem == kElemBf16  ? launch_drop_norm_bf16(a, p, true, stream)
+           : elem == kElemF16 ? launch_drop_norm_f16(a, p, true, stream)
+                              : launch_drop_norm_f32(a, p, true, stream);
+}
+
+// Warp w of a CTA adds parts w, w + 32, ... of its 32 columns in order; the
+// 32 warps' sums are then added in warp order.
+__global__ void __launch_bounds__(1024) column_sums_kernel(const float* partials, int parts, int cols, float* out0,
+                                                           int first, float* out1)
+{
+    __shared__ float sums[32][33];
+    wait_prior_grids();
+    allow_next_grid();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (col < cols) {
+        const float* p = partials + col;
+#pragma unroll 4
+        for (int i = warp; i < parts; i += 32)
+            s = __fadd_rn(s, __ldcs(p + static_cast<int64_t>(i) * cols));
+    }
+    sums[warp][lane] = s;
+    __syncthreads();
+    // warp w now holds column w of the CTA, one warp's sum a lane
+    s = butterfly_sum(sums[lane][warp], 32);
+    const int c = blockIdx.x * 32 + warp;
+    if (lane == 0 && c < cols) {
+        if (c < first && out0)
+            out0[c] = s;
+        if (c >= first && out1)
+            out1[c - first] = s;
+    }
+}
+
+cudaError_t launch_column_sums(const float* partials, int parts, int cols, float* out0, int first, float* out1,
+                               cudaStream_t stream)
+{
+    return launch(column_sums_kernel, (cols + 31) / 32, 1024, 0, false, stream, partials, parts, cols, out0, first,
+                  out1);
+}
+
+}  // namespace dradd

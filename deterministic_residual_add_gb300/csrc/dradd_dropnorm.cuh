@@ -1,0 +1,607 @@
+// dradd_dropnorm.cuh -- dropout + residual add + RMSNorm, and its gradients.
+//
+// Forward, per row (the row function of add_rmsnorm_fwd with the dropout in
+// front of it, so p = 0 gives its bits):
+//   acc = residual + (kept ? RN(x scale) : 0); residual_out = E(acc)
+//   out = E((acc * inv) * w), inv = 1 / sqrt(S / hidden + eps),
+// S the canonical pairwise sum of acc^2 (see dradd_kernels.cuh).
+//
+// Backward from h = residual_out (the rounded sum is what a training step
+// keeps), with g = dout * w:
+//   S1 = sum h^2, S2 = sum g h, both in the canonical tree
+//   inv from S1; c = (inv * (inv * (S2 / hidden)))
+//   d = dresidual_out + inv * (g - h * c)
+//   dresidual = E(d); dx = E(kept ? d scale : 0)
+//   dweight[i] = sum over rows of dout * (h * inv), in fp32: every CTA (part)
+//   adds its rows in order and a second kernel adds the parts in a fixed
+//   order, so the bits depend on the shape and the element type alone.
+//
+// Bound by the memory: 4 elements of traffic an element forward, 5 backward.
+// Rows of P >= 2048 (P: hidden rounded up to a power of two) go through
+// shared memory, one CTA a row, staged `stages` rows ahead by bulk copies;
+// the backward pass needs h and dout twice, before and after the row's sums,
+// and takes them from the stage both times.  Narrower rows are loaded
+// straight into registers, a warp (or 8 or 16 lanes) a row.
+#pragma once
+
+#include "dradd_elem.cuh"
+#include "dradd_internal.h"
+#include "dradd_kernels.cuh"
+#include "dradd_train_internal.h"
+
+namespace dradd {
+
+// ------------------------------------------------------------- block helpers
+// acc of one block; the residual sum is stored.
+template <int E>
+__device__ __forceinline__ void fwd_block(const DropNormArgs& a, const DropKey& key,
+                                          const typename Elem<E>::Block& xv, const typename Elem<E>::Block& rv,
+                                          int64_t row, int b, float (&acc)[8])
+{
+    using T = typename Elem<E>::T;
+    float r[8];
+    Elem<E>::unpack(xv, acc);
+    Elem<E>::unpack(rv, r);
+    if (key.threshold)
+        drop8(acc, key, static_cast<uint32_t>(b), static_cast<uint32_t>(row));
+#pragma unroll
+    for (int e = 0; e < 8; e += 2)
+        add2_rn(acc[e], acc[e + 1], r[e], r[e + 1], acc[e], acc[e + 1]);
+    st_block_stream(static_cast<T*>(a.residual_out) + row * a.hidden, b, Elem<E>::pack(acc));
+}
+
+// out of one block.
+template <int E>
+__device__ __forceinline__ void fwd_finish(const DropNormArgs& a, float (&acc)[8], float inv,
+                                           const typename Elem<E>::Block& wv, int64_t row, int b)
+{
+    using T = typename Elem<E>::T;
+    float w[8];
+    Elem<E>::unpack(wv, w);
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        mul2_rn(acc[e], acc[e + 1], inv, inv, acc[e], acc[e + 1]);
+        mul2_rn(acc[e], acc[e + 1], w[e], w[e + 1], acc[e], acc[e + 1]);
+    }
+    st_block_stream(static_cast<T*>(a.out) + row * a.hidden, b, Elem<E>::pack(acc));
+}
+
+// The block's parts of sum g h (as fold8_squares adds the squares).
+__device__ __forceinline__ float fold8_products(const float (&p)[8])
+{
+    return __fadd_rn(__fadd_rn(__fadd_rn(p[0], p[1]), __fadd_rn(p[2], p[3])),
+                     __fadd_rn(__fadd_rn(p[4], p[5]), __fadd_rn(p[6], p[7])));
+}
+
+template <int E>
+__device__ __forceinline__ void bwd_sums(const typename Elem<E>::Block& hv, const typename Elem<E>::Block& gv,
+                                         const typename Elem<E>::Block& wv, float& s1, float& s2)
+{
+    float h[8], g[8], w[8];
+    Elem<E>::unpack(hv, h);
+    Elem<E>::unpack(gv, g);
+    Elem<E>::unpack(wv, w);
+    s1 = fold8_squares(h);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        g[e] = __fmul_rn(__fmul_rn(g[e], w[e]), h[e]);
+    s2 = fold8_products(g);
+}
+
+// The gradients of one block, and its rows' share of dweight.
+template <int E>
+__device__ __forceinline__ void bwd_finish(const DropNormArgs& a, const DropKey& key,
+                                           const typename Elem<E>::Block& hv, const typename Elem<E>::Block& gv,
+                                           const typename Elem<E>::Block& wv, const typename Elem<E>::Block& dv,
+                                           float inv, float c, int64_t row, int b, float (&dw)[8])
+{
+    using T = typename Elem<E>::T;
+    float h[8], g[8], w[8], d[8];
+    Elem<E>::unpack(hv, h);
+    Elem<E>::unpack(gv, g);
+    Elem<E>::unpack(wv, w);
+    Elem<E>::unpack(dv, d);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        dw[e] = __fmaf_rn(g[e], __fmul_rn(h[e], inv), dw[e]);
+        const float t = __fmaf_rn(-h[e], c, __fmul_rn(g[e], w[e]));
+        d[e] = __fmaf_rn(inv, t, d[e]);
+    }
+    st_block_stream(static_cast<T*>(a.dresidual) + row * a.hidden, b, Elem<E>::pack(d));
+    if (a.dx) {
+        if (key.threshold)
+            drop8(d, key, static_cast<uint32_t>(b), static_cast<uint32_t>(row));
+        st_block_stream(static_cast<T*>(a.dx) + row * a.hidden, b, Elem<E>::pack(d));
+    }
+}
+
+// c of the row: inv^2 S2 / hidden.
+__device__ __forceinline__ float bwd_coefficient(const DropNormArgs& a, float s2, float inv)
+{
+    const float mean = a.inv_hidden != 0.0f ? __fmul_rn(s2, a.inv_hidden)
+                                            : __fdiv_rn(s2, static_cast<float>(a.hidden));
+    return __fmul_rn(inv, __fmul_rn(inv, mean));
+}
+
+// ------------------------------------------------------------- narrow rows
+// L lanes a row (8, 16 or 32), K blocks of 8 a lane: P = 8 L K <= 1024.  A
+// CTA takes (warps x 32 / L) rows at a time.
+constexpr int kNarrowThreads = 256;
+
+template <int E, int L, int K>
+__global__ void __launch_bounds__(kNarrowThreads) drop_norm_fwd_narrow(const DropNormArgs a)
+{
+    using T = typename Elem<E>::T;
+    using V = typename Elem<E>::Block;
+    const int t = threadIdx.x & (L - 1);
+    const int nblocks = a.hidden >> 3;
+    wait_prior_grids();
+    allow_next_grid();
+    const DropKey key = make_drop_key(a.drop);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kNarrowThreads / L);
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (kNarrowThreads / L) + threadIdx.x / L;
+    // rows of one warp start together, so every lane of it makes the same
+    // number of steps and takes part in the shuffles
+    const int64_t lead = first - (threadIdx.x & 31) / L;
+    for (int64_t base = 0; lead + base < a.n_rows; base += step) {
+        const int64_t row = first + base;
+        const bool active = row < a.n_rows;
+        V xv[K], rv[K], wv[K];
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const int b = t + j * L;
+            if (active && b < nblocks) {
+                ld_block_stream(static_cast<const T*>(a.x) + row * a.hidden, b, xv[j]);
+                ld_block_stream(static_cast<const T*>(a.residual) + row * a.hidden, b, rv[j]);
+                ld_block(static_cast<const T*>(a.weight), b, wv[j]);
+            }
+        }
+        float acc[K][8], part[K];
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const int b = t + j * L;
+            part[j] = 0.0f;
+            if (active && b < nblocks) {
+                fwd_block<E>(a, key, xv[j], rv[j], row, b, acc[j]);
+                part[j] = fold8_squares(acc[j]);
+            }
+            part[j] = butterfly_sum(part[j], L);
+        }
+        const float inv = inv_rms(fold_k<K>(part), a.hidden, a.inv_hidden, a.eps);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const int b = t + j * L;
+            if (active && b < nblocks)
+                fwd_finish<E>(a, acc[j], inv, wv[j], row, b);
+        }
+    }
+}
+
+template <int E, int L, int K>
+__global__ void __launch_bounds__(kNarrowThreads) drop_norm_bwd_narrow(const DropNormArgs a)
+{
+    using T = typename Elem<E>::T;
+    using V = typename Elem<E>::Block;
+    constexpr int kGroups = kNarrowThreads / L;
+    __shared__ float sums[L * K * 8];
+    const int t = threadIdx.x & (L - 1);
+    const int group = threadIdx.x / L;
+    const int nblocks = a.hidden >> 3;
+    wait_prior_grids();
+    allow_next_grid();
+    const DropKey key = make_drop_key(a.drop);
+    float dw[K][8] = {};
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kGroups + group;
+    const int64_t lead = first - (threadIdx.x & 31) / L;  // as in the forward
+    for (int64_t base = 0; lead + base < a.n_rows; base += step) {
+        const int64_t row = first + base;
+        const bool active = row < a.n_rows;
+        V hv[K], gv[K], wv[K], dv[K];
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const int b = t + j * L;
+            dv[j] = V{};
+            if (active && b < nblocks) {
+                ld_block_stream(static_cast<const T*>(a.h) + row * a.hidden, b, hv[j]);
+                ld_block_stream(static_cast<const T*>(a.dout) + row * a.hidden, b, gv[j]);
+                if (a.dresidual_out)
+                    ld_block_stream(static_cast<const T*>(a.dresidual_out) + row * a.hidden, b, dv[j]);
+                ld_block(static_cast<const T*>(a.weight), b, wv[j]);
+            }
+        }
+        float p1[K], p2[K];
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            p1[j] = p2[j] = 0.0f;
+            if (active && t + j * L < nblocks)
+                bwd_sums<E>(hv[j], gv[j], wv[j], p1[j], p2[j]);
+            p1[j] = butterfly_sum(p1[j], L);
+            p2[j] = butterfly_sum(p2[j], L);
+        }
+        const float inv = inv_rms(fold_k<K>(p1), a.hidden, a.inv_hidden, a.eps);
+        const float c = bwd_coefficient(a, fold_k<K>(p2), inv);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const int b = t + j * L;
+            if (active && b < nblocks)
+                bwd_finish<E>(a, key, hv[j], gv[j], wv[j], dv[j], inv, c, row, b, dw[j]);
+        }
+    }
+    if (!a.partials)
+        return;
+    // the CTA's part: its groups' sums, added in group order
+    for (int g = 0; g < kGroups; ++g) {
+        if (group == g) {
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float& s = sums[(t + j * L) * 8 + e];
+                    s = g == 0 ? dw[j][e] : __fadd_rn(s, dw[j][e]);
+                }
+            }
+        }
+        __syncthreads();
+    }
+    for (int i = threadIdx.x; i < a.hidden; i += kNarrowThreads)
+        a.partials[static_cast<int64_t>(blockIdx.x) * a.hidden + i] = sums[i];
+}
+
+// --------------------------------------------------------------- wide rows
+// One CTA a row, T threads of K blocks: P = 8 T K.  Rows reach the threads
+// through stages of shared memory (STAGED) or straight from global memory
+// (buffers that are not device memory, rows of which two do not fit).
+
+// Resident CTAs per SM the kernels are compiled for: 1024 threads of 64
+// registers up to two blocks a thread, else one CTA of 512 threads.
+constexpr int wide_min_blocks(int T, int K) { return K <= 2 ? 1024 / T : 1; }
+
+// N arrays of rows staged in turn: a ring of `stages` slots, each one row of
+// every array, filled by thread 0.
+template <int N>
+struct RowRing {
+    unsigned char* mem;
+    uint64_t* bars;
+    const unsigned char* src[N];
+    uint32_t row_bytes;
+    int stages;
+    uint64_t policy;
+
+    __device__ __forceinline__ const unsigned char* slot(int s) const
+    {
+        return mem + static_cast<size_t>(s) * N * row_bytes;
+    }
+    __device__ __forceinline__ void issue(int s, int64_t row) const
+    {
+        unsigned char* dst = mem + static_cast<size_t>(s) * N * row_bytes;
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            bytes += src[i] ? row_bytes : 0u;
+        mbar_arrive_expect_tx(&bars[s], bytes);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (src[i])
+                bulk_copy_g2s(dst + i * row_bytes, src[i] + row * static_cast<int64_t>(row_bytes), row_bytes,
+                              &bars[s], policy);
+        }
+    }
+};
+
+// After an expired wait: thread 0 records it and waits, with a limit, for
+// the copies of slots that were filled and not yet taken (`pending` of them
+// from slot s), so that none lands after the CTA has gone.
+__device__ __forceinline__ void give_up(const DropNormArgs& a, uint64_t* bars, int s, uint32_t parity, int64_t pending)
+{
+    atomicOr(a.status, kDeviceStatusTimeout);
+    for (int64_t i = 0; i < pending; ++i) {
+        bool landed = false;
+        for (int r = 0; r < kDrainRounds && !landed; ++r)
+            landed = mbar_wait_bounded(&bars[s], parity, a.wait_limit_ns);
+        if (!landed)
+            atomicOr(a.status, kDeviceStatusUndrained);
+        if (++s == a.stages) {
+            s = 0;
+            parity ^= 1u;
+        }
+    }
+}
+
+template <int E, int T, int K, bool STAGED>
+__global__ void __launch_bounds__(T, wide_min_blocks(T, K)) drop_norm_fwd_wide(const DropNormArgs a)
+{
+    using X = typename Elem<E>::T;
+    using V = typename Elem<E>::Block;
+    constexpr int W = T / 32;
+    extern __shared__ __align__(128) unsigned char stage_mem[];
+    __shared__ float red[2][K * W];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nblocks = a.hidden >> 3;
+    const int64_t stride = gridDim.x;
+    RowRing<2> ring;
+    if constexpr (STAGED) {
+        ring.mem = stage_mem;
+        ring.row_bytes = static_cast<uint32_t>(a.hidden * sizeof(X));
+        ring.stages = a.stages;
+        ring.bars = reinterpret_cast<uint64_t*>(stage_mem + static_cast<size_t>(a.stages) * 2 * ring.row_bytes);
+        ring.src[0] = static_cast<const unsigned char*>(a.x);
+        ring.src[1] = static_cast<const unsigned char*>(a.residual);
+        ring.policy = l2_policy_evict_first();
+        if (tid == 0) {
+            for (int s = 0; s < a.stages; ++s)
+                mbar_init(&ring.bars[s], 1);
+            fence_mbar_init();
+        }
+        __syncthreads();
+    }
+    wait_prior_grids();
+    allow_next_grid();
+    if constexpr (STAGED) {
+        if (tid == 0) {
+            for (int s = 0; s < a.stages && blockIdx.x + s * stride < a.n_rows; ++s)
+                ring.issue(s, blockIdx.x + s * stride);
+        }
+    }
+    const DropKey key = make_drop_key(a.drop);
+    V wv[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        const int b = tid + j * T;
+        if (block_in_row<K>(j, b, nblocks))
+            ld_block(static_cast<const X*>(a.weight), b, wv[j]);
+    }
+    int s = 0, buf = 0;
+    uint32_t parity = 0;
+    for (int64_t row = blockIdx.x; row < a.n_rows; row += stride) {
+        bool ok = true;
+        const X *xs, *rs;
+        if constexpr (STAGED) {
+            ok = mbar_wait_bounded(&ring.bars[s], parity, a.wait_limit_ns);
+            xs = reinterpret_cast<const X*>(ring.slot(s));
+            rs = xs + a.hidden;
+        } else {
+            xs = static_cast<const X*>(a.x) + row * a.hidden;
+            rs = static_cast<const X*>(a.residual) + row * a.hidden;
+        }
+        float acc[K][8], part[K];
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const int b = tid + j * T;
+            part[j] = 0.0f;
+            if (block_in_row<K>(j, b, nblocks)) {
+                V xv, rv;
+                ld_block(xs, b, xv);
+                ld_block(rs, b, rv);
+                fwd_block<E>(a, key, xv, rv, row, b, acc[j]);
+                part[j] = fold8_squares(acc[j]);
+            }
+        }
+        int jsub;
+        const float v = warp_halving_sum<K>(part, lane, jsub);
+        if (lane < K)
+            red[buf][jsub * W + warp] = v;
+        if constexpr (STAGED) {
+            // every thread has read the slot; an expired wait ends the CTA
+            if (__syncthreads_or(!ok)) {
+                if (tid == 0) {
+                    const int64_t left = (a.n_rows - row + stride - 1) / stride;
+                    give_up(a, ring.bars, s, parity, left < a.stages ? left : a.stages);
+                }
+                return;
+            }
+            if (tid == 0 && row + a.stages * stride < a.n_rows) {
+                fence_proxy_async_smem();
+                ring.issue(s, row + a.stages * stride);
+            }
+        } else {
+            __syncthreads();
+        }
+        const float inv = inv_rms(cross_warp_sum<K, W>(red[buf], lane), a.hidden, a.inv_hidden, a.eps);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const int b = tid + j * T;
+            if (block_in_row<K>(j, b, nblocks))
+                fwd_finish<E>(a, acc[j], inv, wv[j], row, b);
+        }
+        buf ^= 1;
+        if constexpr (STAGED) {
+            if (++s == a.stages) {
+                s = 0;
+                parity ^= 1u;
+            }
+        }
+    }
+}
+
+template <int E, int T, int K, bool STAGED>
+__global__ void __launch_bounds__(T, wide_min_blocks(T, K)) drop_norm_bwd_wide(const DropNormArgs a)
+{
+    using X = typename Elem<E>::T;
+    using V = typename Elem<E>::Block;
+    constexpr int W = T / 32;
+    extern __shared__ __align__(128) unsigned char stage_mem[];
+    __shared__ float red1[2][K * W], red2[2][K * W];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nblocks = a.hidden >> 3;
+    const int64_t stride = gridDim.x;
+    RowRing<3> ring;
+    if constexpr (STAGED) {
+        ring.mem = stage_mem;
+        ring.row_bytes = static_cast<uint32_t>(a.hidden * sizeof(X));
+        ring.stages = a.stages;
+        ring.bars = reinterpret_cast<uint64_t*>(stage_mem + static_cast<size_t>(a.stages) * 3 * ring.row_bytes);
+        ring.src[0] = static_cast<const unsigned char*>(a.h);
+        ring.src[1] = static_cast<const unsigned char*>(a.dout);
+        ring.src[2] = static_cast<const unsigned char*>(a.dresidual_out);
+        ring.policy = l2_policy_evict_first();
+        if (tid == 0) {
+            for (int s = 0; s < a.stages; ++s)
+                mbar_init(&ring.bars[s], 1);
+            fence_mbar_init();
+        }
+        __syncthreads();
+    }
+    wait_prior_grids();
+    allow_next_grid();
+    if constexpr (STAGED) {
+        if (tid == 0) {
+            for (int s = 0; s < a.stages && blockIdx.x + s * stride < a.n_rows; ++s)
+                ring.issue(s, blockIdx.x + s * stride);
+        }
+    }
+    const DropKey key = make_drop_key(a.drop);
+    const X* wrow = static_cast<const X*>(a.weight);
+    float dw[K][8] = {};
+    int s = 0, buf = 0;
+    uint32_t parity = 0;
+    for (int64_t row = blockIdx.x; row < a.n_rows; row += stride) {
+        bool ok = true;
+        const X *hs, *gs, *ds;
+        if constexpr (STAGED) {
+            ok = mbar_wait_bounded(&ring.bars[s], parity, a.wait_limit_ns);
+            hs = reinterpret_cast<const X*>(ring.slot(s));
+            gs = hs + a.hidden;
+            ds = gs + a.hidden;
+        } else {
+            hs = static_cast<const X*>(a.h) + row * a.hidden;
+            gs = static_cast<const X*>(a.dout) + row * a.hidden;
+            ds = static_cast<const X*>(a.dresidual_out) + row * a.hidden;
+        }
+        float p1[K], p2[K];
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const int b = tid + j * T;
+            p1[j] = p2[j] = 0.0f;
+            if (block_in_row<K>(j, b, nblocks)) {
+                V hv, gv, wv;
+                ld_block(hs, b, hv);
+                ld_block(gs, b, gv);
+                ld_block(wrow, b, wv);
+                bwd_sums<E>(hv, gv, wv, p1[j], p2[j]);
+            }
+        }
+        int jsub;
+        const float v1 = warp_halving_sum<K>(p1, lane, jsub);
+        const float v2 = warp_halving_sum<K>(p2, lane, jsub);
+        if (lane < K) {
+            red1[buf][jsub * W + warp] = v1;
+            red2[buf][jsub * W + warp] = v2;
+        }
+        if constexpr (STAGED) {
+            if (__syncthreads_or(!ok)) {
+                if (tid == 0) {
+                    // filled and not taken: this row's slot and those after
+                    // it, short of the slot of the row before (not refilled)
+                    const int64_t left = (a.n_rows - row + stride - 1) / stride;
+                    const int64_t filled = row == blockIdx.x ? a.stages : a.stages - 1;
+                    give_up(a, ring.bars, s, parity, left < filled ? left : filled);
+                }
+                return;
+            }
+            // Past this barrier every thread is done with the row before
+            // this one, so its slot takes the next row: no second barrier a
+            // row, at the price of one slot's depth.
+            if (tid == 0 && row != blockIdx.x && row + (a.stages - 1) * stride < a.n_rows) {
+                fence_proxy_async_smem();
+                ring.issue(s == 0 ? a.stages - 1 : s - 1, row + (a.stages - 1) * stride);
+            }
+        } else {
+            __syncthreads();
+        }
+        const float inv = inv_rms(cross_warp_sum<K, W>(red1[buf], lane), a.hidden, a.inv_hidden, a.eps);
+        const float c = bwd_coefficient(a, cross_warp_sum<K, W>(red2[buf], lane), inv);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const int b = tid + j * T;
+            if (block_in_row<K>(j, b, nblocks)) {
+                V hv, gv, wv, dv = V{};
+                ld_block(hs, b, hv);
+                ld_block(gs, b, gv);
+                ld_block(wrow, b, wv);
+                if (a.dresidual_out)
+                    ld_block(ds, b, dv);
+                bwd_finish<E>(a, key, hv, gv, wv, dv, inv, c, row, b, dw[j]);
+            }
+        }
+        buf ^= 1;
+        if constexpr (STAGED) {
+            if (++s == a.stages) {
+                s = 0;
+                parity ^= 1u;
+            }
+        }
+    }
+    if (!a.partials)
+        return;
+    float* part = a.partials + static_cast<int64_t>(blockIdx.x) * a.hidden;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        const int b = tid + j * T;
+        if (block_in_row<K>(j, b, nblocks)) {
+            float4* p = reinterpret_cast<float4*>(part) + 2 * b;
+            p[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
+            p[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------- launch
+template <typename F>
+cudaError_t launch_sized(F fn, const DropNormArgs& a, const DropNormPlan& p, cudaStream_t stream)
+{
+    if (p.smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(p.smem));
+        if (e != cudaSuccess)
+            return e;
+    }
+    return launch(fn, p.grid, p.threads, p.smem, false, stream, a);
+}
+
+template <int E, int T, int K>
+cudaError_t launch_wide(const DropNormArgs& a, const DropNormPlan& p, bool backward, cudaStream_t stream)
+{
+    if (p.staged)
+        return backward ? launch_sized(drop_norm_bwd_wide<E, T, K, true>, a, p, stream)
+                        : launch_sized(drop_norm_fwd_wide<E, T, K, true>, a, p, stream);
+    return backward ? launch_sized(drop_norm_bwd_wide<E, T, K, false>, a, p, stream)
+                    : launch_sized(drop_norm_fwd_wide<E, T, K, false>, a, p, stream);
+}
+
+template <int E, int L, int K>
+cudaError_t launch_narrow(const DropNormArgs& a, const DropNormPlan& p, bool backward, cudaStream_t stream)
+{
+    return backward ? launch_sized(drop_norm_bwd_narrow<E, L, K>, a, p, stream)
+                    : launch_sized(drop_norm_fwd_narrow<E, L, K>, a, p, stream);
+}
+
+template <int E>
+cudaError_t launch_drop_norm_of(const DropNormArgs& a, const DropNormPlan& p, bool backward, cudaStream_t stream)
+{
+    if (p.warp) {
+        if (p.K == 1)
+            return p.lanes == 8    ? launch_narrow<E, 8, 1>(a, p, backward, stream)
+                   : p.lanes == 16 ? launch_narrow<E, 16, 1>(a, p, backward, stream)
+                                   : launch_narrow<E, 32, 1>(a, p, backward, stream);
+        return p.K == 2 ? launch_narrow<E, 32, 2>(a, p, backward, stream)
+                        : launch_narrow<E, 32, 4>(a, p, backward, stream);
+    }
+    switch (p.threads * 8 * p.K) {
+    case 2048:
+        return launch_wide<E, 256, 1>(a, p, backward, stream);
+    case 4096:
+        return launch_wide<E, 256, 2>(a, p, backward, stream);
+    case 8192:
+        return launch_wide<E, 512, 2>(a, p, backward, stream);
+    case 16384:
+        return launch_wide<E, 512, 4>(a, p, backward, stream);
+    case 32768:
+        return launch_wide<E, 512, 8>(a, p, backward, stream);
+    default:
+        return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace dradd

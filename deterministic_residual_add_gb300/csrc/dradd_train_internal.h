@@ -1,0 +1,128 @@
+// dradd_train_internal.h -- argument blocks and launchers of the dropout, RMSNorm
+// gradient and rotary kernels, shared by the C-ABI layer and the kernels.
+// Not part of the public interface.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "dradd_philox.cuh"
+
+namespace dradd {
+
+// ------------------------------------------------------------------ dropout
+// Row strides in elements.  residual NULL: plain dropout.
+struct DropoutArgs {
+    void* out;
+    const void* x;
+    const void* residual;
+    int64_t out_stride, x_stride, residual_stride;
+    int64_t n_rows, hidden;
+    DropParams drop;
+};
+
+constexpr int kDropoutThreads = 256;
+// CTAs launched per SM at most: eight waves of the eight that fit at once.
+constexpr int kDropoutCtasPerSm = 64;
+
+// blocks: hidden, strides and addresses let every row move as aligned blocks
+// of 8 elements.
+cudaError_t launch_dropout(const DropoutArgs& a, int elem, bool blocks, int sm_count, cudaStream_t stream);
+
+// ------------------------------------- dropout + residual add + RMSNorm
+struct DropNormArgs {
+    void* out;           // forward: the normalised rows
+    void* residual_out;  // forward: acc rounded
+    const void* x;
+    const void* residual;
+    const void* weight;
+    // backward
+    void* dx;               // or NULL
+    void* dresidual;
+    float* partials;        // parts x hidden sums of dweight, or NULL
+    const void* dout;
+    const void* dresidual_out;  // or NULL (zero)
+    const void* h;              // the forward's residual_out
+    int64_t n_rows;
+    int hidden;
+    float inv_hidden;  // 1 / hidden if a power of two, else 0
+    float eps;
+    DropParams drop;  // threshold 0: no generator call
+    int stages;       // staged kernels: rows in flight per CTA
+    unsigned* status;
+    uint64_t wait_limit_ns;
+};
+
+// How a call's rows are spread: a function of (n_rows, hidden, element type,
+// direction, memory) alone.
+struct DropNormPlan {
+    bool warp;     // several rows a warp, or a warp a row (P <= 1024)
+    bool staged;   // rows staged through shared memory by bulk copies
+    int lanes;     // warp: lanes per row
+    int threads;   // threads per CTA
+    int K;         // blocks of 8 per thread
+    int stages;
+    int grid;      // CTAs; backward: also the number of dweight partial sums
+    size_t smem;
+};
+
+DropNormPlan drop_norm_plan(int64_t n_rows, int hidden, int elem, bool backward, bool device_memory);
+cudaError_t launch_drop_norm_fwd(const DropNormArgs& a, const DropNormPlan& p, int elem, cudaStream_t stream);
+cudaError_t launch_drop_norm_bwd(const DropNormArgs& a, const DropNormPlan& p, int elem, cudaStream_t stream);
+// One pair per element type, each in its own translation unit.
+cudaError_t launch_drop_norm_bf16(const DropNormArgs& a, const DropNormPlan& p, bool backward, cudaStream_t stream);
+cudaError_t launch_drop_norm_f16(const DropNormArgs& a, const DropNormPlan& p, bool backward, cudaStream_t stream);
+cudaError_t launch_drop_norm_f32(const DropNormArgs& a, const DropNormPlan& p, bool backward, cudaStream_t stream);
+
+// Column sums of parts x cols partial sums in a fixed order: columns
+// [0, first) to out0, the others to out1 (either may be NULL: not wanted).
+cudaError_t launch_column_sums(const float* partials, int parts, int cols, float* out0, int first, float* out1,
+                               cudaStream_t stream);
+
+// ------------------------------------------------------------------- rotary
+// One of q and k.  Strides in elements (batch, sequence, head).
+struct RopeSide {
+    void* out;
+    const void* in;        // forward: x; gradient of the fused call: x
+    const void* grad;      // gradient of the fused call: dy
+    const void* weight;    // fused call
+    int64_t out_b, out_s, out_h;
+    int64_t in_b, in_s, in_h;
+    int64_t grad_b, grad_s, grad_h;
+    int heads;
+    float eps;
+    int skip_rest;  // in place without a norm: the columns past rot_dim stay
+};
+
+struct RopeArgs {
+    RopeSide q, k;
+    const double* inv_freq;
+    const int64_t* positions;  // [batch, seq], or NULL: position0 + s
+    int64_t position0;
+    int64_t tokens;  // batch * seq
+    int64_t seq;
+    int dim, rot;
+    int rot_units, units, group;  // 16-element units that rotate, in all; lanes per head (a power of two)
+    float inv_dim;                // 1 / dim if a power of two, else 0
+    float scale;
+    float sign;                   // +1, or -1 for the inverse rotation
+    int tokens_per_step;
+    float* partials;              // gradient: grid x 2 dim sums
+};
+
+enum RopeMode : int { kRopePlain = 0, kRopeNorm = 1, kRopeNormBwd = 2 };
+constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxDim = 512;
+
+// Tokens a CTA takes at once, and CTAs; backward: the grid is also the
+// number of partial sums.  A function of the shape alone.
+void rope_plan(RopeArgs* a, bool backward, int* grid);
+
+cudaError_t launch_rope(const RopeArgs& a, int mode, int elem, bool interleaved, bool blocks, int grid,
+                        cudaStream_t stream);
+cudaError_t launch_rope_bf16(const RopeArgs& a, int mode, bool interleaved, bool blocks, int grid, cudaStream_t stream);
+cudaError_t launch_rope_f16(const RopeArgs& a, int mode, bool interleaved, bool blocks, int grid, cudaStream_t stream);
+cudaError_t launch_rope_f32(const RopeArgs& a, int mode, bool interleaved, bool blocks, int grid, cudaStream_t stream);
+
+}  // namespace dradd

@@ -84,8 +84,11 @@ enum {
     DRADD_ERR_CUDA = 7,               /* a CUDA runtime call failed                    */
     DRADD_ERR_TIMEOUT = 8,            /* a kernel's bounded wait expired (device)      */
     DRADD_ERR_BAD_CONFIG = 9,         /* an explicit launch configuration is invalid   */
-    DRADD_ERR_UNDRAINED = 10          /* after a timeout, an issued bulk copy had not
+    DRADD_ERR_UNDRAINED = 10,         /* after a timeout, an issued bulk copy had not
                                          landed when the kernel stopped waiting (device) */
+    DRADD_ERR_BAD_ARG = 11,           /* dradd_train.h: a probability, scale, type or layout
+                                         argument is out of its range              */
+    DRADD_ERR_WORKSPACE = 12          /* dradd_train.h: the workspace is NULL or too small */
 };
 
 /*
