@@ -261,11 +261,11 @@ dradd_status rope_shape(const dradd_rope* r, int dtype, RopeArgs* a, bool backwa
 // Pointers, strides and overlaps of one call's views: out[i] may be exactly
 // in[i] or grad[i].  *blocks: every head moves as aligned blocks of 8.
 struct RopeSideArgs {
-    const dradd_heads *out, *in, *grad;  // grad NULL without one
-    const void* weight;                  // NULL without one
+    const dradd_heads *out, *in, *grad;  // grad: the norm's backward only
+    const void* weight;                  // the norm only
 };
 
-dradd_status rope_check(const dradd_rope& r, const RopeSideArgs (&sides)[2], bool norm, int64_t eb,
+dradd_status rope_check(const dradd_rope& r, const RopeSideArgs (&sides)[2], bool norm, bool has_grad, int64_t eb,
                         const void* extra_out0, int64_t extra_bytes0, const void* extra_out1, int64_t extra_bytes1,
                         const void* extra_out2, int64_t extra_bytes2, bool* blocks)
 {
@@ -282,9 +282,9 @@ dradd_status rope_check(const dradd_rope& r, const RopeSideArgs (&sides)[2], boo
     for (int s = 0; s < n_sides; ++s) {
         const dradd_heads* t[3] = {sides[s].out, sides[s].in, sides[s].grad};
         for (int i = 0; i < 3; ++i) {
-            if (!t[i])
+            if (i == 2 && !has_grad)
                 continue;
-            if (!t[i]->data)
+            if (!t[i] || !t[i]->data)
                 return DRADD_ERR_NULL_PTR;
             if (!aligned(t[i]->data, eb))
                 return DRADD_ERR_MISALIGNED;
@@ -354,7 +354,7 @@ void fill_side(RopeSide* s, const RopeSideArgs& t, float eps)
     s->eps = eps;
 }
 
-dradd_status run_rope(const dradd_heads& q_out, const dradd_heads& k_out, const dradd_heads& q, const dradd_heads& k,
+dradd_status run_rope(const dradd_heads* q_out, const dradd_heads* k_out, const dradd_heads* q, const dradd_heads* k,
                       const void* q_weight, const void* k_weight, float q_eps, float k_eps, bool norm, float sign,
                       const dradd_rope* r, int dtype, cudaStream_t stream)
 {
@@ -367,14 +367,15 @@ dradd_status run_rope(const dradd_heads& q_out, const dradd_heads& k_out, const 
         return DRADD_ERR_BAD_EPS;
     if (a.tokens == 0)
         return DRADD_OK;
-    const RopeSideArgs sides[2] = {{&q_out, &q, nullptr, q_weight}, {&k_out, &k, nullptr, k_weight}};
+    const RopeSideArgs sides[2] = {{q_out, q, nullptr, q_weight}, {k_out, k, nullptr, k_weight}};
     bool blocks = false;
-    st = rope_check(*r, sides, norm, elem_bytes(dtype), nullptr, 0, nullptr, 0, nullptr, 0, &blocks);
+    st = rope_check(*r, sides, norm, false, elem_bytes(dtype), nullptr, 0, nullptr, 0, nullptr, 0, &blocks);
     if (st != DRADD_OK)
         return st;
     a.sign = sign;
     fill_side(&a.q, sides[0], q_eps);
-    fill_side(&a.k, sides[1], k_eps);
+    if (r->k_heads > 0)
+        fill_side(&a.k, sides[1], k_eps);
     if (!norm) {
         a.q.skip_rest = a.q.out == a.q.in;
         a.k.skip_rest = a.k.out == a.k.in;
@@ -476,28 +477,28 @@ size_t rmsnorm_bwd_workspace_bytes(int64_t n_rows, int64_t hidden, int dtype)
     return static_cast<size_t>(p.grid) * static_cast<size_t>(hidden) * sizeof(float);
 }
 
-dradd_status rope_fwd(dradd_heads q_out, dradd_heads k_out, dradd_heads q, dradd_heads k, const dradd_rope* rope,
-                      int dtype, cudaStream_t stream)
+dradd_status rope_fwd(const dradd_heads* q_out, const dradd_heads* k_out, const dradd_heads* q,
+                      const dradd_heads* k, const dradd_rope* rope, int dtype, cudaStream_t stream)
 {
     return run_rope(q_out, k_out, q, k, nullptr, nullptr, 0.0f, 0.0f, false, 1.0f, rope, dtype, stream);
 }
 
-dradd_status rope_bwd(dradd_heads dq, dradd_heads dk, dradd_heads dq_out, dradd_heads dk_out, const dradd_rope* rope,
-                      int dtype, cudaStream_t stream)
+dradd_status rope_bwd(const dradd_heads* dq, const dradd_heads* dk, const dradd_heads* dq_out,
+                      const dradd_heads* dk_out, const dradd_rope* rope, int dtype, cudaStream_t stream)
 {
     return run_rope(dq, dk, dq_out, dk_out, nullptr, nullptr, 0.0f, 0.0f, false, -1.0f, rope, dtype, stream);
 }
 
-dradd_status qk_rmsnorm_rope_fwd(dradd_heads q_out, dradd_heads k_out, dradd_heads q, dradd_heads k,
-                                 const void* q_weight, const void* k_weight, float q_eps, float k_eps,
-                                 const dradd_rope* rope, int dtype, cudaStream_t stream)
+dradd_status qk_rmsnorm_rope_fwd(const dradd_heads* q_out, const dradd_heads* k_out, const dradd_heads* q,
+                                 const dradd_heads* k, const void* q_weight, const void* k_weight, float q_eps,
+                                 float k_eps, const dradd_rope* rope, int dtype, cudaStream_t stream)
 {
     return run_rope(q_out, k_out, q, k, q_weight, k_weight, q_eps, k_eps, true, 1.0f, rope, dtype, stream);
 }
 
-dradd_status qk_rmsnorm_rope_bwd(dradd_heads dq, dradd_heads dk, float* dq_weight, float* dk_weight,
-                                 dradd_heads dq_out, dradd_heads dk_out, dradd_heads q, dradd_heads k,
-                                 const void* q_weight, const void* k_weight, float q_eps, float k_eps,
+dradd_status qk_rmsnorm_rope_bwd(const dradd_heads* dq, const dradd_heads* dk, float* dq_weight, float* dk_weight,
+                                 const dradd_heads* dq_out, const dradd_heads* dk_out, const dradd_heads* q,
+                                 const dradd_heads* k, const void* q_weight, const void* k_weight, float q_eps, float k_eps,
                                  const dradd_rope* rope, int dtype, void* workspace, size_t workspace_bytes,
                                  cudaStream_t stream)
 {
@@ -525,15 +526,16 @@ dradd_status qk_rmsnorm_rope_bwd(dradd_heads dq, dradd_heads dk, float* dq_weigh
         return DRADD_ERR_MISALIGNED;
     if (sums && (!workspace || workspace_bytes < need))
         return DRADD_ERR_WORKSPACE;
-    const RopeSideArgs sides[2] = {{&dq, &q, &dq_out, q_weight}, {&dk, &k, &dk_out, k_weight}};
+    const RopeSideArgs sides[2] = {{dq, q, dq_out, q_weight}, {dk, k, dk_out, k_weight}};
     bool blocks = false;
-    st = rope_check(*rope, sides, true, elem_bytes(dtype), dq_weight, a.dim * 4, dk_weight, a.dim * 4,
+    st = rope_check(*rope, sides, true, true, elem_bytes(dtype), dq_weight, a.dim * 4, dk_weight, a.dim * 4,
                     sums ? workspace : nullptr, static_cast<int64_t>(need), &blocks);
     if (st != DRADD_OK)
         return st;
     a.sign = -1.0f;
     fill_side(&a.q, sides[0], q_eps);
-    fill_side(&a.k, sides[1], k_eps);
+    if (has_k)
+        fill_side(&a.k, sides[1], k_eps);
     a.partials = sums ? static_cast<float*>(workspace) : nullptr;
     if (launch_rope(a, kRopeNormBwd, dtype, rope->interleaved != 0, blocks, grid, stream) != cudaSuccess)
         return DRADD_ERR_CUDA;

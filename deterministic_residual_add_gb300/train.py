@@ -12,10 +12,17 @@ those of the tensor seen as [rows, last dimension]; forward and backward
 take the same seed and offset.  `step` is an optional device int64 that the
 kernel adds to the offset, so that a captured graph draws a new mask at
 every replay when the program advances it in between.
+
+A decode step's kernels take a few microseconds, less than a call's host
+side, so that side is kept short: one chain of tests per tensor, the C
+structures packed as bytes, and stream and device switched (_switched) only
+where they are not current already.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import struct
 
 import torch
 
@@ -24,21 +31,16 @@ ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
 _vp, _i64, _f32, _f64, _int, _size = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_double, ctypes.c_int,
                                       ctypes.c_size_t)
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_U64 = 0xFFFFFFFFFFFFFFFF
 
+# dradd_dropout, dradd_heads and dradd_rope of the header, natively aligned
+_pack_dropout = struct.Struct("fQQP").pack
+_pack_heads = struct.Struct("Pqqq").pack
+_pack_rope = struct.Struct("6qiPPqf0q").pack
 
-class _Dropout(ctypes.Structure):
-    _fields_ = [("p", _f32), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("step", _vp)]
-
-
-class _Heads(ctypes.Structure):
-    _fields_ = [("data", _vp), ("batch_stride", _i64), ("seq_stride", _i64), ("head_stride", _i64)]
-
-
-class _Rope(ctypes.Structure):
-    _fields_ = [("batch", _i64), ("seq", _i64), ("q_heads", _i64), ("k_heads", _i64), ("head_dim", _i64),
-                ("rot_dim", _i64), ("interleaved", _int), ("inv_freq", _vp), ("positions", _vp), ("position0", _i64),
-                ("scale", _f32)]
-
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = torch.cuda.current_device
 
 _L = None
 
@@ -46,23 +48,21 @@ _L = None
 def _bind(L):
     """Argument types of the entry points, set once when the library loads."""
     global _L
-    drop, rope, heads4 = ctypes.POINTER(_Dropout), ctypes.POINTER(_Rope), [_Heads] * 4
     for name, args in [
-            ("dropout_fwd", [_vp, _i64, _vp, _i64, _i64, _i64, drop, _int, _vp]),
-            ("dropout_add_fwd", [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, drop, _int, _vp]),
-            ("dropout_add_rmsnorm_fwd", [_vp] * 5 + [_f32, _i64, _i64, drop, _int, _vp]),
-            ("dropout_add_rmsnorm_bwd", [_vp] * 7 + [_f32, _i64, _i64, drop, _int, _vp, _size, _vp]),
+            ("dropout_fwd", [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _int, _vp]),
+            ("dropout_add_fwd", [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _int, _vp]),
+            ("dropout_add_rmsnorm_fwd", [_vp] * 5 + [_f32, _i64, _i64, _vp, _int, _vp]),
+            ("dropout_add_rmsnorm_bwd", [_vp] * 7 + [_f32, _i64, _i64, _vp, _int, _vp, _size, _vp]),
             ("add_rmsnorm_bwd", [_vp] * 6 + [_f32, _i64, _i64, _int, _vp, _size, _vp]),
-            ("rope_fwd", heads4 + [rope, _int, _vp]),
-            ("rope_bwd", heads4 + [rope, _int, _vp]),
-            ("qk_rmsnorm_rope_fwd", heads4 + [_vp, _vp, _f32, _f32, rope, _int, _vp]),
-            ("qk_rmsnorm_rope_bwd", [_Heads, _Heads, _vp, _vp] + heads4 + [_vp, _vp, _f32, _f32, rope, _int, _vp,
-                                                                           _size, _vp]),
+            ("rope_fwd", [_vp] * 5 + [_int, _vp]),
+            ("rope_bwd", [_vp] * 5 + [_int, _vp]),
+            ("qk_rmsnorm_rope_fwd", [_vp] * 6 + [_f32, _f32, _vp, _int, _vp]),
+            ("qk_rmsnorm_rope_bwd", [_vp] * 10 + [_f32, _f32, _vp, _int, _vp, _size, _vp]),
             ("rope_frequencies", [_vp, _i64, _f64, _int, _f64, _f64, _f64, _f64])]:
         f = getattr(L, name)
         f.argtypes, f.restype = args, _int
     L.rmsnorm_bwd_workspace_bytes.argtypes, L.rmsnorm_bwd_workspace_bytes.restype = [_i64, _i64, _int], _size
-    L.qk_rmsnorm_rope_bwd_workspace_bytes.argtypes = [rope, _int]
+    L.qk_rmsnorm_rope_bwd_workspace_bytes.argtypes = [_vp, _int]
     L.qk_rmsnorm_rope_bwd_workspace_bytes.restype = _size
     _L = L
 
@@ -74,42 +74,28 @@ def _lib():
     return _L
 
 
-class _On:
-    """Makes `device` and the launch stream current for a call; .handle is
-    the stream's.  Where both already are, nothing is switched."""
+def _failed(status: int, where: str):
+    from . import DraddError
+    raise DraddError(status, where)
 
-    __slots__ = ("handle", "contexts")
 
-    def __init__(self, device, stream):
-        self.contexts = ()
-        if device.index != torch.cuda.current_device():
-            self.contexts = (torch.cuda.device(device),)
+@contextlib.contextmanager
+def _switched(x, stream):
+    """x's device and the launch stream current; inside, a call without a
+    stream takes the current one."""
+    with torch.cuda.device(x.device):
         if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-        else:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device)
-            if stream.device != device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-            self.handle = stream.cuda_stream
-            self.contexts += (torch.cuda.stream(stream),)
-
-    def __enter__(self):
-        for c in self.contexts:
-            c.__enter__()
-        return self.handle
-
-    def __exit__(self, *a):
-        for c in reversed(self.contexts):
-            c.__exit__(*a)
+            yield
+            return
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, x.device)
+        if stream.device != x.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {x.device}")
+        with torch.cuda.stream(stream):
+            yield
 
 
-def _done(status: int, where: str):
-    if status != 0:
-        from . import DraddError
-        raise DraddError(status, where)
-
-
+# ------------------------------------------------------------------- checks
 def _dtype(x, name: str) -> int:
     code = _DTYPES.get(x.dtype)
     if code is None:
@@ -119,60 +105,67 @@ def _dtype(x, name: str) -> int:
     return code
 
 
-def _like(t, x, name: str, shape=None, dtype=None):
-    """Checks that t is of x's type (or dtype) and device, and of `shape`."""
-    if t.dtype != (x.dtype if dtype is None else dtype):
-        raise TypeError(f"{name} must hold {x.dtype if dtype is None else dtype} (got {t.dtype})")
-    if t.device != x.device:
-        raise ValueError(f"{name} is on {t.device}, expected {x.device}")
+def _refuse(t, name, dtype, device, shape, contiguous):
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must hold {dtype} (got {t.dtype})")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-
-
-def _flat(t, x, name: str, shape=None, dtype=None) -> int:
-    """data_ptr of a contiguous tensor checked by _like."""
-    _like(t, x, name, shape, dtype)
-    if not t.is_contiguous():
+    if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must have unit stride in its last dimension")
+
+
+def _flat(t, name, dtype, device, shape) -> int:
+    """data_ptr of a contiguous tensor of this type, device and shape."""
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape or not t.is_contiguous():
+        _refuse(t, name, dtype, device, shape, True)
     return t.data_ptr()
 
 
-def _drop(p, seed, offset, step, x):
-    if step is not None:
-        if step.numel() != 1:
-            raise ValueError("step must hold one int64")
-        step = _flat(step, x, "step", dtype=torch.int64)
-    return _Dropout(p, seed & 0xFFFFFFFFFFFFFFFF, offset & 0xFFFFFFFFFFFFFFFF, step)
+def _drop(p, seed, offset, step, device) -> bytes:
+    if step is None:
+        return _pack_dropout(p, seed & _U64, offset & _U64, 0)
+    if step.numel() != 1:
+        raise ValueError("step must hold one int64")
+    return _pack_dropout(p, seed & _U64, offset & _U64, _flat(step, "step", torch.int64, device, step.shape))
 
 
 # ------------------------------------------------------------------ dropout
-def _rows(t, name: str):
-    """(rows, columns, row stride): any contiguous tensor as [rows, last
-    dimension], or a 2-D tensor with unit column stride."""
+def _rows(t, name, dtype, device, shape):
+    """(data_ptr, rows, columns, row stride): a contiguous tensor as [rows,
+    last dimension], or a 2-D tensor with unit column stride."""
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape:
+        _refuse(t, name, dtype, device, shape, False)
     if t.is_contiguous():
-        cols = t.shape[-1] if t.dim() else 1
-        return (t.numel() // cols if cols else 0), cols, cols
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        cols = shape[-1] if shape else 1
+        return t.data_ptr(), (t.numel() // cols if cols else 0), cols, cols
+    if len(shape) != 2 or (shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be contiguous, or 2-D with unit column stride")
-    return t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.data_ptr(), shape[0], shape[1], t.stride(0) if shape[0] > 1 else shape[1]
 
 
 def dropout_fwd(x, p: float, *, seed: int, offset: int = 0, step=None, out=None, stream=None):
     """out = x where kept, times 1 / (1 - p) (p applied in steps of 2^-16),
     and 0 where dropped.  The gradient is the same call on the gradient.
     x: contiguous, or 2-D with any row stride; out may be x."""
-    code = _dtype(x, "x")
-    with _On(x.device, stream) as handle:
-        if out is None:
-            out = torch.empty_like(x, memory_format=torch.contiguous_format)
-        _like(out, x, "out", x.shape)
-        n, h, xs = _rows(x, "x")
-        _, _, os = _rows(out, "out")
-        if n == 0:
-            return out
-        d = _drop(p, seed, offset, step, x)
-        _done(_lib().dropout_fwd(out.data_ptr(), os, x.data_ptr(), xs, n, h, ctypes.byref(d), code, handle),
-              "dropout_fwd")
+    code, device = _dtype(x, "x"), x.get_device()
+    if stream is not None or device != _current_device():
+        with _switched(x, stream):
+            return dropout_fwd(x, p, seed=seed, offset=offset, step=step, out=out)
+    dtype, shape = x.dtype, x.shape
+    xp, n, hidden, xs = _rows(x, "x", dtype, device, shape)
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        op, os = out.data_ptr(), hidden
+    else:
+        op, _, _, os = _rows(out, "out", dtype, device, shape)
+    if hidden:
+        st = _lib().dropout_fwd(op, os, xp, xs, n, hidden, _drop(p, seed, offset, step, device), code,
+                                _raw_stream(device))
+        if st:
+            _failed(st, "dropout_fwd")
     return out
 
 
@@ -180,29 +173,32 @@ def dropout_add_fwd(x, residual, p: float, *, seed: int, offset: int = 0, step=N
     """residual_out = residual + dropout(x), rounded once.  Gradients:
     dresidual = dy, dx = dropout_fwd(dy) with the same p, seed and offset.
     residual_out may be x or residual."""
-    code = _dtype(x, "x")
-    with _On(x.device, stream) as handle:
-        if residual_out is None:
-            residual_out = torch.empty_like(x, memory_format=torch.contiguous_format)
-        _like(residual, x, "residual", x.shape)
-        _like(residual_out, x, "residual_out", x.shape)
-        n, h, xs = _rows(x, "x")
-        _, _, rs = _rows(residual, "residual")
-        _, _, os = _rows(residual_out, "residual_out")
-        if n == 0:
-            return residual_out
-        d = _drop(p, seed, offset, step, x)
-        _done(_lib().dropout_add_fwd(residual_out.data_ptr(), os, x.data_ptr(), xs, residual.data_ptr(), rs, n, h,
-                                     ctypes.byref(d), code, handle), "dropout_add_fwd")
+    code, device = _dtype(x, "x"), x.get_device()
+    if stream is not None or device != _current_device():
+        with _switched(x, stream):
+            return dropout_add_fwd(x, residual, p, seed=seed, offset=offset, step=step, residual_out=residual_out)
+    dtype, shape = x.dtype, x.shape
+    xp, n, hidden, xs = _rows(x, "x", dtype, device, shape)
+    rp, _, _, rs = _rows(residual, "residual", dtype, device, shape)
+    if residual_out is None:
+        residual_out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        op, os = residual_out.data_ptr(), hidden
+    else:
+        op, _, _, os = _rows(residual_out, "residual_out", dtype, device, shape)
+    if hidden:
+        st = _lib().dropout_add_fwd(op, os, xp, xs, rp, rs, n, hidden, _drop(p, seed, offset, step, device), code,
+                                    _raw_stream(device))
+        if st:
+            _failed(st, "dropout_add_fwd")
     return residual_out
 
 
 # ------------------------------------- dropout + residual add + RMSNorm
 def _norm_shape(x):
-    if x.dim() == 0 or x.shape[-1] == 0:
+    shape = x.shape
+    if not shape or shape[-1] == 0:
         raise ValueError("the last dimension must not be empty")
-    hidden = x.shape[-1]
-    return x.numel() // hidden, hidden
+    return shape, x.numel() // shape[-1], shape[-1]
 
 
 def dropout_add_rmsnorm_fwd(x, residual, weight, p: float, eps: float = 1e-6, *, seed: int, offset: int = 0, step=None,
@@ -212,29 +208,67 @@ def dropout_add_rmsnorm_fwd(x, residual, weight, p: float, eps: float = 1e-6, *,
     weight).  With p = 0 the bits are add_rmsnorm_fwd's.  Contiguous
     [..., hidden] tensors, hidden a multiple of 8; out and residual_out may
     each be x or residual."""
-    code = _dtype(x, "x")
-    n, hidden = _norm_shape(x)
-    shape = x.shape
-    with _On(x.device, stream) as handle:
-        if out is None:
-            out = torch.empty_like(x)
-        if residual_out is None:
-            residual_out = torch.empty_like(x)
-        d = _drop(p, seed, offset, step, x)
-        _done(_lib().dropout_add_rmsnorm_fwd(
-            _flat(out, x, "out", shape), _flat(residual_out, x, "residual_out", shape), _flat(x, x, "x"),
-            _flat(residual, x, "residual", shape), _flat(weight, x, "weight", shape[-1:]), eps, n, hidden,
-            ctypes.byref(d), code, handle), "dropout_add_rmsnorm_fwd")
+    code, device = _dtype(x, "x"), x.get_device()
+    if stream is not None or device != _current_device():
+        with _switched(x, stream):
+            return dropout_add_rmsnorm_fwd(x, residual, weight, p, eps, seed=seed, offset=offset, step=step, out=out,
+                                           residual_out=residual_out)
+    dtype = x.dtype
+    shape, n, hidden = _norm_shape(x)
+    xp = _flat(x, "x", dtype, device, shape)
+    rp = _flat(residual, "residual", dtype, device, shape)
+    wp = _flat(weight, "weight", dtype, device, shape[-1:])
+    if out is None:
+        out = torch.empty_like(x)
+    if residual_out is None:
+        residual_out = torch.empty_like(x)
+    st = _lib().dropout_add_rmsnorm_fwd(
+        _flat(out, "out", dtype, device, shape), _flat(residual_out, "residual_out", dtype, device, shape), xp, rp, wp,
+        eps, n, hidden, _drop(p, seed, offset, step, device), code, _raw_stream(device))
+    if st:
+        _failed(st, "dropout_add_rmsnorm_fwd")
     return out, residual_out
 
 
-def _workspace(given, need: int, x):
-    """A workspace of `need` bytes on the current stream, or the one given."""
+def _workspace(given, need, device):
+    """(tensor to keep alive, data_ptr, bytes)."""
     if given is None:
-        return torch.empty(need, dtype=torch.uint8, device=x.device)
-    if given.device != x.device or not given.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {x.device}")
-    return given
+        given = torch.empty(need, dtype=torch.uint8, device=device)
+        return given, given.data_ptr(), need
+    if given.get_device() != device.index or not given.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return given, given.data_ptr(), given.numel() * given.element_size()
+
+
+def _norm_bwd(where, drop, dx, want_dx, dresidual, dresidual_name, dweight, weight_grad, dout, dresidual_out, x, weight,
+              eps, workspace, code, device):
+    dtype = x.dtype
+    shape, n, hidden = _norm_shape(x)
+    hp = _flat(x, "residual_out", dtype, device, shape)
+    gp = _flat(dout, "dout", dtype, device, shape)
+    dp = None if dresidual_out is None else _flat(dresidual_out, "dresidual_out", dtype, device, shape)
+    wp = _flat(weight, "weight", dtype, device, shape[-1:])
+    if dresidual is None:
+        dresidual = torch.empty_like(x)
+    outs = [_flat(dresidual, dresidual_name, dtype, device, shape)]
+    if want_dx:
+        if dx is None:
+            dx = torch.empty_like(x)
+        outs.insert(0, _flat(dx, "dx", dtype, device, shape))
+    L = _lib()
+    dwp = wsp = None
+    nbytes = 0
+    if weight_grad:
+        if dweight is None:
+            dweight = torch.empty(hidden, dtype=torch.float32, device=x.device)
+        dwp = _flat(dweight, "dweight", torch.float32, device, shape[-1:])
+        workspace, wsp, nbytes = _workspace(workspace, L.rmsnorm_bwd_workspace_bytes(n, hidden, code), x.device)
+    elif dweight is not None:
+        raise ValueError("dweight is given but weight_grad is False")
+    st = getattr(L, where)(*outs, dwp, gp, dp, hp, wp, eps, n, hidden, *drop, code, wsp, nbytes, _raw_stream(device))
+    if st:
+        _failed(st, where)
+    return dx, dresidual, dweight
 
 
 def dropout_add_rmsnorm_bwd(dout, dresidual_out, residual_out, weight, p: float, eps: float = 1e-6, *, seed: int,
@@ -244,61 +278,34 @@ def dropout_add_rmsnorm_bwd(dout, dresidual_out, residual_out, weight, p: float,
     those of its two outputs (dresidual_out None: zero) and its residual_out.
     dweight is fp32, None with weight_grad=False.  dx and dresidual may each
     be dout, dresidual_out or residual_out.  workspace: a tensor of at least
-    rmsnorm_bwd_workspace_bytes; by default one is allocated."""
-    x = residual_out
-    code = _dtype(x, "residual_out")
-    n, hidden = _norm_shape(x)
-    shape = x.shape
-    with _On(x.device, stream) as handle:
-        if dx is None:
-            dx = torch.empty_like(x)
-        if dresidual is None:
-            dresidual = torch.empty_like(x)
-        dweight, work, nbytes = _weight_sums(dweight, weight_grad, workspace, n, hidden, code, x)
-        d = _drop(p, seed, offset, step, x)
-        _done(_lib().dropout_add_rmsnorm_bwd(
-            _flat(dx, x, "dx", shape), _flat(dresidual, x, "dresidual", shape),
-            None if dweight is None else dweight.data_ptr(), _flat(dout, x, "dout", shape),
-            None if dresidual_out is None else _flat(dresidual_out, x, "dresidual_out", shape),
-            _flat(x, x, "residual_out"), _flat(weight, x, "weight", shape[-1:]), eps, n, hidden, ctypes.byref(d), code,
-            None if work is None else work.data_ptr(), nbytes, handle), "dropout_add_rmsnorm_bwd")
-    return dx, dresidual, dweight
-
-
-def _weight_sums(dweight, wanted, workspace, n, hidden, code, x):
-    if not wanted:
-        if dweight is not None:
-            raise ValueError("dweight is given but weight_grad is False")
-        return None, None, 0
-    if dweight is None:
-        dweight = torch.empty(hidden, dtype=torch.float32, device=x.device)
-    _flat(dweight, x, "dweight", torch.Size((hidden,)), torch.float32)
-    work = _workspace(workspace, _lib().rmsnorm_bwd_workspace_bytes(n, hidden, code), x)
-    return dweight, work, work.numel() * work.element_size()
+    rmsnorm_bwd_workspace_bytes (C ABI); by default one is allocated."""
+    code, device = _dtype(residual_out, "residual_out"), residual_out.get_device()
+    if stream is not None or device != _current_device():
+        with _switched(residual_out, stream):
+            return dropout_add_rmsnorm_bwd(dout, dresidual_out, residual_out, weight, p, eps, seed=seed, offset=offset,
+                                           step=step, dx=dx, dresidual=dresidual, dweight=dweight,
+                                           weight_grad=weight_grad, workspace=workspace)
+    return _norm_bwd("dropout_add_rmsnorm_bwd", (_drop(p, seed, offset, step, device),), dx, True, dresidual,
+                     "dresidual", dweight, weight_grad, dout, dresidual_out, residual_out, weight, eps, workspace, code,
+                     device)
 
 
 def add_rmsnorm_bwd(dout, dresidual_out, residual_out, weight, eps: float = 1e-6, *, dh=None, dweight=None,
                     weight_grad: bool = True, workspace=None, stream=None):
     """(dh, dweight): gradients of add_rmsnorm_fwd; dh is that of x and of
     residual.  Arguments as in dropout_add_rmsnorm_bwd."""
-    x = residual_out
-    code = _dtype(x, "residual_out")
-    n, hidden = _norm_shape(x)
-    shape = x.shape
-    with _On(x.device, stream) as handle:
-        if dh is None:
-            dh = torch.empty_like(x)
-        dweight, work, nbytes = _weight_sums(dweight, weight_grad, workspace, n, hidden, code, x)
-        _done(_lib().add_rmsnorm_bwd(
-            _flat(dh, x, "dh", shape), None if dweight is None else dweight.data_ptr(), _flat(dout, x, "dout", shape),
-            None if dresidual_out is None else _flat(dresidual_out, x, "dresidual_out", shape),
-            _flat(x, x, "residual_out"), _flat(weight, x, "weight", shape[-1:]), eps, n, hidden, code,
-            None if work is None else work.data_ptr(), nbytes, handle), "add_rmsnorm_bwd")
-    return dh, dweight
+    code, device = _dtype(residual_out, "residual_out"), residual_out.get_device()
+    if stream is not None or device != _current_device():
+        with _switched(residual_out, stream):
+            return add_rmsnorm_bwd(dout, dresidual_out, residual_out, weight, eps, dh=dh, dweight=dweight,
+                                   weight_grad=weight_grad, workspace=workspace)
+    return _norm_bwd("add_rmsnorm_bwd", (), None, False, dh, "dh", dweight, weight_grad, dout, dresidual_out,
+                     residual_out, weight, eps, workspace, code, device)[1:]
 
 
 def rmsnorm_bwd(dout, x, weight, eps: float = 1e-6, **kw):
-    """(dx, dweight): gradients of rmsnorm_fwd."""
+    """(dx, dweight): gradients of rmsnorm_fwd.  Keywords as in
+    add_rmsnorm_bwd."""
     return add_rmsnorm_bwd(dout, None, x, weight, eps, **kw)
 
 
@@ -313,55 +320,67 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "non
     factor, those between are blended)."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
-    f = torch.empty(max(int(rot_dim), 0) // 2, dtype=torch.float64)
-    _done(_lib().rope_frequencies(f.data_ptr() if f.numel() else ctypes.addressof(_f64()), int(rot_dim), float(base),
-                                  ROPE_SCALINGS[scaling], float(factor), float(original_length), float(low),
-                                  float(high)), "rope_frequencies")
+    f = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.float64)
+    st = _lib().rope_frequencies(f.data_ptr(), int(rot_dim), float(base), ROPE_SCALINGS[scaling], float(factor),
+                                 float(original_length), float(low), float(high))
+    if st:
+        _failed(st, "rope_frequencies")
     return f if device is None else f.to(device)
 
 
-_NO_HEADS = _Heads(None, 0, 0, 0)
+def _heads(t, name, dtype, device, shape) -> bytes:
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape:
+        _refuse(t, name, dtype, device, shape, False)
+    b, s, h, d = t.stride()
+    if d != 1 and shape[3] > 1:
+        _refuse(t, name, dtype, device, shape, False)
+    return _pack_heads(t.data_ptr(), b, s, h)
 
 
-def _heads(t, x, name: str, shape=None):
-    _like(t, x, name, shape)
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name} must have unit stride in its last dimension")
-    return _Heads(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+def _new(x):
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
-def _rope(q, k, inv_freq, positions, position0, interleaved, scale):
-    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3])):
-        raise ValueError("q and k must be [batch, seq, heads, head_dim], alike but for their heads")
-    b, s, hq, d = q.shape
-    freq = _flat(inv_freq, q, "inv_freq", dtype=torch.float64)
-    if inv_freq.dim() != 1:
+def _rope(q, k, inv_freq, positions, position0, interleaved, scale, device) -> bytes:
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q and k must be [batch, seq, heads, head_dim]")
+    b, s, hq, d = shape
+    hk = 0
+    if k is not None:
+        ks = k.shape
+        if len(ks) != 4 or ks[0] != b or ks[1] != s or ks[3] != d:
+            raise ValueError("q and k must be [batch, seq, heads, head_dim], alike but for their heads")
+        hk = ks[2]
+    if len(inv_freq.shape) != 1:
         raise ValueError("inv_freq must be 1-D: one frequency per pair")
+    freq = _flat(inv_freq, "inv_freq", torch.float64, device, inv_freq.shape)
+    pos = 0
     if positions is not None:
         if position0:
             raise ValueError("give positions or position0, not both")
-        if positions.numel() != b * s or (positions.dim() == 2 and positions.shape != q.shape[:2]):
-            raise ValueError(f"positions must be [{b}, {s}]")
-        positions = _flat(positions, q, "positions", dtype=torch.int64)
-    return _Rope(b, s, hq, 0 if k is None else k.shape[2], d, 2 * inv_freq.shape[0], int(bool(interleaved)), freq,
-                 positions, position0, scale)
-
-
-def _out(t, like):
-    return torch.empty(like.shape, dtype=like.dtype, device=like.device) if t is None else t
+        pos = _flat(positions, "positions", torch.int64, device, shape[:2])
+    return _pack_rope(b, s, hq, hk, d, 2 * inv_freq.shape[0], 1 if interleaved else 0, freq, pos, position0, scale)
 
 
 def _turn(where, q, k, inv_freq, positions, position0, interleaved, scale, q_out, k_out, stream):
-    code = _dtype(q, "q")
-    r = _rope(q, k, inv_freq, positions, position0, interleaved, scale)
-    with _On(q.device, stream) as handle:
-        q_out = _out(q_out, q)
-        ko, ki = _NO_HEADS, _NO_HEADS
-        if k is not None:
-            k_out = _out(k_out, k)
-            ko, ki = _heads(k_out, q, "k_out", k.shape), _heads(k, q, "k")
-        _done(getattr(_lib(), where)(_heads(q_out, q, "q_out", q.shape), ko, _heads(q, q, "q"), ki, ctypes.byref(r),
-                                     code, handle), where)
+    code, device = _dtype(q, "q"), q.get_device()
+    if stream is not None or device != _current_device():
+        with _switched(q, stream):
+            return _turn(where, q, k, inv_freq, positions, position0, interleaved, scale, q_out, k_out, None)
+    r = _rope(q, k, inv_freq, positions, position0, interleaved, scale, device)
+    dtype = q.dtype
+    if q_out is None:
+        q_out = _new(q)
+    ko = ki = None
+    if k is not None:
+        if k_out is None:
+            k_out = _new(k)
+        ko, ki = _heads(k_out, "k_out", dtype, device, k.shape), _heads(k, "k", dtype, device, k.shape)
+    st = getattr(_lib(), where)(_heads(q_out, "q_out", dtype, device, q.shape), ko,
+                                _heads(q, "q", dtype, device, q.shape), ki, r, code, _raw_stream(device))
+    if st:
+        _failed(st, where)
     return q_out, k_out
 
 
@@ -390,18 +409,27 @@ def qk_rmsnorm_rope_fwd(q, k, q_weight, k_weight, inv_freq, q_eps: float = 1e-6,
     """(q_out, k_out): RMSNorm of every head of q and k (weights [head_dim]),
     then rope_fwd, in one pass with one rounding.  k and k_weight may be
     None."""
-    code = _dtype(q, "q")
-    r = _rope(q, k, inv_freq, positions, position0, interleaved, scale)
-    with _On(q.device, stream) as handle:
-        q_out = _out(q_out, q)
-        ko, ki, kw = _NO_HEADS, _NO_HEADS, None
-        if k is not None:
-            k_out = _out(k_out, k)
-            ko, ki = _heads(k_out, q, "k_out", k.shape), _heads(k, q, "k")
-            kw = _flat(k_weight, q, "k_weight", q.shape[3:])
-        _done(_lib().qk_rmsnorm_rope_fwd(
-            _heads(q_out, q, "q_out", q.shape), ko, _heads(q, q, "q"), ki, _flat(q_weight, q, "q_weight", q.shape[3:]),
-            kw, q_eps, k_eps, ctypes.byref(r), code, handle), "qk_rmsnorm_rope_fwd")
+    code, device = _dtype(q, "q"), q.get_device()
+    if stream is not None or device != _current_device():
+        with _switched(q, stream):
+            return qk_rmsnorm_rope_fwd(q, k, q_weight, k_weight, inv_freq, q_eps, k_eps, positions=positions,
+                                       position0=position0, interleaved=interleaved, scale=scale, q_out=q_out,
+                                       k_out=k_out)
+    r = _rope(q, k, inv_freq, positions, position0, interleaved, scale, device)
+    dtype, width = q.dtype, q.shape[3:]
+    if q_out is None:
+        q_out = _new(q)
+    ko = ki = kw = None
+    if k is not None:
+        if k_out is None:
+            k_out = _new(k)
+        ko, ki = _heads(k_out, "k_out", dtype, device, k.shape), _heads(k, "k", dtype, device, k.shape)
+        kw = _flat(k_weight, "k_weight", dtype, device, width)
+    st = _lib().qk_rmsnorm_rope_fwd(
+        _heads(q_out, "q_out", dtype, device, q.shape), ko, _heads(q, "q", dtype, device, q.shape), ki,
+        _flat(q_weight, "q_weight", dtype, device, width), kw, q_eps, k_eps, r, code, _raw_stream(device))
+    if st:
+        _failed(st, "qk_rmsnorm_rope_fwd")
     return q_out, k_out
 
 
@@ -411,31 +439,44 @@ def qk_rmsnorm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, q_ep
                         stream=None):
     """(dq, dk, dq_weight, dk_weight): gradients of qk_rmsnorm_rope_fwd; the
     weights' are fp32, None with weight_grad=False.  dq may be q or dq_out,
-    dk may be k or dk_out."""
-    code = _dtype(q, "q")
-    r = _rope(q, k, inv_freq, positions, position0, interleaved, scale)
+    dk may be k or dk_out.  workspace: a tensor of at least
+    qk_rmsnorm_rope_bwd_workspace_bytes (C ABI); by default one is
+    allocated."""
+    code, device = _dtype(q, "q"), q.get_device()
+    if stream is not None or device != _current_device():
+        with _switched(q, stream):
+            return qk_rmsnorm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, q_eps, k_eps,
+                                       positions=positions, position0=position0, interleaved=interleaved, scale=scale,
+                                       dq=dq, dk=dk, dq_weight=dq_weight, dk_weight=dk_weight, weight_grad=weight_grad,
+                                       workspace=workspace)
     if not weight_grad and (dq_weight is not None or dk_weight is not None):
         raise ValueError("a weight's gradient is given but weight_grad is False")
-    with _On(q.device, stream) as handle:
-        dq = _out(dq, q)
-        kh, kw, dkw = [_NO_HEADS] * 3, None, None
+    r = _rope(q, k, inv_freq, positions, position0, interleaved, scale, device)
+    dtype, width, L = q.dtype, q.shape[3:], _lib()
+    if dq is None:
+        dq = _new(q)
+    dkh = dkoh = kh = kw = None
+    if k is not None:
+        if dk is None:
+            dk = _new(k)
+        dkh, dkoh, kh = (_heads(t, name, dtype, device, k.shape) for t, name in ((dk, "dk"), (dk_out, "dk_out"),
+                                                                               (k, "k")))
+        kw = _flat(k_weight, "k_weight", dtype, device, width)
+    dqw = dkw = wsp = None
+    nbytes = 0
+    if weight_grad:
+        if dq_weight is None:
+            dq_weight = torch.empty(width, dtype=torch.float32, device=q.device)
+        dqw = _flat(dq_weight, "dq_weight", torch.float32, device, width)
         if k is not None:
-            dk = _out(dk, k)
-            kh = [_heads(dk, q, "dk", k.shape), _heads(dk_out, q, "dk_out", k.shape), _heads(k, q, "k")]
-            kw = _flat(k_weight, q, "k_weight", q.shape[3:])
-        work, nbytes, dqw = None, 0, None
-        if weight_grad:
-            if dq_weight is None:
-                dq_weight = torch.empty(q.shape[3], dtype=torch.float32, device=q.device)
-            dqw = _flat(dq_weight, q, "dq_weight", q.shape[3:], torch.float32)
-            if k is not None:
-                if dk_weight is None:
-                    dk_weight = torch.empty(q.shape[3], dtype=torch.float32, device=q.device)
-                dkw = _flat(dk_weight, q, "dk_weight", q.shape[3:], torch.float32)
-            work = _workspace(workspace, _lib().qk_rmsnorm_rope_bwd_workspace_bytes(ctypes.byref(r), code), q)
-            nbytes, work = work.numel() * work.element_size(), work.data_ptr()
-        _done(_lib().qk_rmsnorm_rope_bwd(
-            _heads(dq, q, "dq", q.shape), kh[0], dqw, dkw, _heads(dq_out, q, "dq_out", q.shape), kh[1],
-            _heads(q, q, "q"), kh[2], _flat(q_weight, q, "q_weight", q.shape[3:]), kw, q_eps, k_eps, ctypes.byref(r),
-            code, work, nbytes, handle), "qk_rmsnorm_rope_bwd")
+            if dk_weight is None:
+                dk_weight = torch.empty(width, dtype=torch.float32, device=q.device)
+            dkw = _flat(dk_weight, "dk_weight", torch.float32, device, width)
+        workspace, wsp, nbytes = _workspace(workspace, L.qk_rmsnorm_rope_bwd_workspace_bytes(r, code), q.device)
+    st = L.qk_rmsnorm_rope_bwd(
+        _heads(dq, "dq", dtype, device, q.shape), dkh, dqw, dkw, _heads(dq_out, "dq_out", dtype, device, q.shape), dkoh,
+        _heads(q, "q", dtype, device, q.shape), kh, _flat(q_weight, "q_weight", dtype, device, width), kw, q_eps, k_eps,
+        r, code, wsp, nbytes, _raw_stream(device))
+    if st:
+        _failed(st, "qk_rmsnorm_rope_bwd")
     return dq, dk, dq_weight, dk_weight

@@ -148,7 +148,8 @@ typedef struct dradd_heads {
  * the pair (a, b) becomes scale * (a cos theta - b sin theta,
  * a sin theta + b cos theta); it is columns (i, i + rot_dim / 2) of a head,
  * or (2 i, 2 i + 1) when interleaved.  Columns from rot_dim on pass.
- *   batch, seq, q_heads, k_heads, head_dim  k_heads may be 0 (no k)
+ *   batch, seq, q_heads, k_heads, head_dim  k_heads may be 0: no k, whose
+ *                tensors and weight are then not looked at
  *   rot_dim      even, 2 <= rot_dim <= head_dim
  *   inv_freq     device double[rot_dim / 2], radians per position, finite
  *                (rope_frequencies makes the usual ones)
@@ -177,10 +178,10 @@ typedef struct dradd_rope {
  * only its turning columns are written.  An output must not overlap itself
  * (a stride of 0 with more than one element).
  */
-dradd_status rope_fwd(dradd_heads q_out, dradd_heads k_out, dradd_heads q, dradd_heads k, const dradd_rope* rope,
-                      int dtype, cudaStream_t stream);
-dradd_status rope_bwd(dradd_heads dq, dradd_heads dk, dradd_heads dq_out, dradd_heads dk_out, const dradd_rope* rope,
-                      int dtype, cudaStream_t stream);
+dradd_status rope_fwd(const dradd_heads* q_out, const dradd_heads* k_out, const dradd_heads* q,
+                      const dradd_heads* k, const dradd_rope* rope, int dtype, cudaStream_t stream);
+dradd_status rope_bwd(const dradd_heads* dq, const dradd_heads* dk, const dradd_heads* dq_out,
+                      const dradd_heads* dk_out, const dradd_rope* rope, int dtype, cudaStream_t stream);
 
 /*
  * qk_rmsnorm_rope_fwd -- RMSNorm of every head of q and k (weights
@@ -188,9 +189,9 @@ dradd_status rope_bwd(dradd_heads dq, dradd_heads dk, dradd_heads dq_out, dradd_
  * pass with one rounding: z = (x * inv) * weight in fp32, out = turned z.
  * inv = 1 / sqrt(mean(x^2) + eps) over the head_dim columns.
  */
-dradd_status qk_rmsnorm_rope_fwd(dradd_heads q_out, dradd_heads k_out, dradd_heads q, dradd_heads k,
-                                 const void* q_weight, const void* k_weight, float q_eps, float k_eps,
-                                 const dradd_rope* rope, int dtype, cudaStream_t stream);
+dradd_status qk_rmsnorm_rope_fwd(const dradd_heads* q_out, const dradd_heads* k_out, const dradd_heads* q,
+                                 const dradd_heads* k, const void* q_weight, const void* k_weight, float q_eps,
+                                 float k_eps, const dradd_rope* rope, int dtype, cudaStream_t stream);
 
 /*
  * qk_rmsnorm_rope_bwd -- its gradients from dq_out and dk_out: with
@@ -200,8 +201,9 @@ dradd_status qk_rmsnorm_rope_fwd(dradd_heads q_out, dradd_heads k_out, dradd_hea
  * and the same for k.  dq may be exactly q or dq_out, dk exactly k or
  * dk_out.  dq_weight and dk_weight both NULL: not computed, no workspace.
  */
-dradd_status qk_rmsnorm_rope_bwd(dradd_heads dq, dradd_heads dk, float* dq_weight, float* dk_weight,
-                                 dradd_heads dq_out, dradd_heads dk_out, dradd_heads q, dradd_heads k,
+dradd_status qk_rmsnorm_rope_bwd(const dradd_heads* dq, const dradd_heads* dk, float* dq_weight, float* dk_weight,
+                                 const dradd_heads* dq_out, const dradd_heads* dk_out, const dradd_heads* q,
+                                 const dradd_heads* k,
                                  const void* q_weight, const void* k_weight, float q_eps, float k_eps,
                                  const dradd_rope* rope, int dtype, void* workspace, size_t workspace_bytes,
                                  cudaStream_t stream);

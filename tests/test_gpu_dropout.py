@@ -1,6 +1,7 @@
 """Dropout, dropout + residual add + RMSNorm and its gradients on the GPU:
 the forwards bit for bit against fp32 operations rounded one by one, the
 gradients against fp64 within derived bounds."""
+import ctypes
 import itertools
 
 import numpy as np
@@ -307,13 +308,11 @@ def test_streams_and_pinned_memory():
     assert all(torch.equal(a, b) for got in many for a, b in zip(got, want_bwd))
     # buffers the device reaches over the host link take the direct kernels
     L = dr.lib()
-    import ctypes
-    from deterministic_residual_add_gb300.train import _Dropout
     hx, hr, hw, hd = (t.pin_memory() for t in (x, r, w, dout))
     out, ro, dx, dres = (torch.empty_like(x).pin_memory() for _ in range(4))
     dw = torch.empty(4096, device=cuda())
     ws = torch.empty(L.rmsnorm_bwd_workspace_bytes(64, 4096, 0), dtype=torch.uint8, device=cuda())
-    d = _Dropout(0.1, SEED, 0, None)
+    d = tr.CDropout(0.1, SEED, 0, None)
     s = torch.cuda.current_stream().cuda_stream
     assert L.dropout_add_rmsnorm_fwd(out.data_ptr(), ro.data_ptr(), hx.data_ptr(), hr.data_ptr(), hw.data_ptr(), EPS,
                                      64, 4096, ctypes.byref(d), 0, s) == 0

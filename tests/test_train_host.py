@@ -11,7 +11,7 @@ import torch
 import deterministic_residual_add_gb300 as dr
 import train_refs as tr
 from deterministic_residual_add_gb300 import build as drbuild
-from deterministic_residual_add_gb300.train import _Dropout, _Heads, _Rope
+from train_refs import CDropout as _Dropout, CHeads as _Heads, CRope as _Rope
 
 MB = 1 << 20
 BASE = 1 << 42
@@ -160,8 +160,8 @@ def bshd(data, heads, d=128, s=16):
 
 def rope(L, qo=None, ko=None, q=None, k=None, dtype=0, **kw):
     r = rope_of(**kw)
-    return L.rope_fwd(qo or bshd(A, 4), ko or bshd(B, 2), q or bshd(C, 4), k or bshd(D, 2), ctypes.byref(r), dtype,
-                      None)
+    heads = (qo or bshd(A, 4), ko or bshd(B, 2), q or bshd(C, 4), k or bshd(D, 2))
+    return L.rope_fwd(*map(ctypes.byref, heads), ctypes.byref(r), dtype, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -187,6 +187,18 @@ def packed(data, first, total, d=128, s=16):
     return _Heads(data + first * d * 2, s * total * d, total * d, d)
 
 
+def test_rope_null_structures(L):
+    r, q, none = rope_of(), bshd(A, 4), None
+    assert L.rope_fwd(ctypes.byref(q), ctypes.byref(q), ctypes.byref(q), ctypes.byref(q), none, 0, None) == NULL
+    for i in range(4):
+        heads = [ctypes.byref(bshd(BASE + j * 4096 * MB, 4 if j % 2 == 0 else 2)) for j in range(4)]
+        heads[i] = none
+        assert L.rope_fwd(*heads, ctypes.byref(r), 0, None) == NULL
+    alone = rope_of(k_heads=0)
+    assert reaches_device(L.rope_fwd(ctypes.byref(bshd(A, 4)), none, ctypes.byref(bshd(B, 4)), none,
+                                     ctypes.byref(alone), 0, None))
+
+
 def test_rope_layouts_that_the_checks_pass(L):
     """Launches without a device fail with the CUDA status, after the checks."""
     q, k = packed(A, 0, 8), packed(A, 4, 8)
@@ -206,15 +218,15 @@ def test_rope_layouts_that_the_checks_pass(L):
 
 def norm_rope(L, qw=E, kw_=F, q_eps=1e-6, k_eps=1e-6, **kw):
     r = rope_of(**kw)
-    return L.qk_rmsnorm_rope_fwd(bshd(A, 4), bshd(B, 2), bshd(C, 4), bshd(D, 2), qw, kw_, q_eps, k_eps,
-                                 ctypes.byref(r), 0, None)
+    heads = (bshd(A, 4), bshd(B, 2), bshd(C, 4), bshd(D, 2))
+    return L.qk_rmsnorm_rope_fwd(*map(ctypes.byref, heads), qw, kw_, q_eps, k_eps, ctypes.byref(r), 0, None)
 
 
 def norm_rope_bwd(L, dq=None, dk=None, dqw=None, dkw=None, gq=None, q=None, ws=None, wsb=0, batch=2, k_heads=2):
     r = rope_of(batch=batch, k_heads=k_heads)
-    return L.qk_rmsnorm_rope_bwd(dq or bshd(A, 4), dk or bshd(B, 2), dqw, dkw, gq or bshd(C, 4), bshd(D, 2),
-                                 q or bshd(E, 4), bshd(F, 2), G, G + 4096, 1e-6, 1e-6, ctypes.byref(r), 0, ws, wsb,
-                                 None)
+    h = [ctypes.byref(t) for t in (dq or bshd(A, 4), dk or bshd(B, 2), gq or bshd(C, 4), bshd(D, 2), q or bshd(E, 4),
+                                   bshd(F, 2))]
+    return L.qk_rmsnorm_rope_bwd(*h[:2], dqw, dkw, *h[2:], G, G + 4096, 1e-6, 1e-6, ctypes.byref(r), 0, ws, wsb, None)
 
 
 def test_norm_rope_argument_errors(L):
@@ -276,6 +288,20 @@ def test_binding_refuses_host_tensors_and_types(L):
             call()
     with pytest.raises(TypeError):
         dr.dropout_fwd(x.double(), 0.1, seed=1)
+
+
+def test_packed_structures_match_the_header():
+    """The binding packs dradd_dropout, dradd_heads and dradd_rope as bytes."""
+    from deterministic_residual_add_gb300 import train
+    d = _Dropout.from_buffer_copy(train._pack_dropout(0.25, 2 ** 64 - 1, 7, 0x1234567890))
+    assert (d.p, d.seed, d.offset, d.step) == (0.25, 2 ** 64 - 1, 7, 0x1234567890)
+    h = _Heads.from_buffer_copy(train._pack_heads(0xFFFF000012340000, 5, 6, 7))
+    assert (h.data, h.batch_stride, h.seq_stride, h.head_stride) == (0xFFFF000012340000, 5, 6, 7)
+    packed = train._pack_rope(1, 2, 3, 4, 5, 6, 1, 0x7000, 0x8000, -9, 1.5)
+    assert len(packed) == ctypes.sizeof(_Rope)
+    r = _Rope.from_buffer_copy(packed)
+    assert [getattr(r, f) for f, _ in _Rope._fields_] == [1, 2, 3, 4, 5, 6, 1, 0x7000, 0x8000, -9, 1.5]
+    assert len(train._pack_dropout(0, 0, 0, 0)) == ctypes.sizeof(_Dropout)
 
 
 def test_references_agree_with_autograd():

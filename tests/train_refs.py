@@ -5,8 +5,30 @@ results, bit for bit), everything else in fp64 with bounds on how far the
 fp32 kernels may be from it."""
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import torch
+
+
+class CDropout(ctypes.Structure):
+    """dradd_dropout of include/dradd_train.h."""
+    _fields_ = [("p", ctypes.c_float), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("step", ctypes.c_void_p)]
+
+
+class CHeads(ctypes.Structure):
+    """dradd_heads."""
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("seq_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class CRope(ctypes.Structure):
+    """dradd_rope."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seq", "q_heads", "k_heads", "head_dim", "rot_dim")] + [
+        ("interleaved", ctypes.c_int), ("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("position0", ctypes.c_int64), ("scale", ctypes.c_float)]
+
 
 HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
 # half the spacing of a type's smallest values: what a rounding may add there
