@@ -9,8 +9,10 @@ namespace dradd {
 namespace {
 
 constexpr int kSms = 152;  // a constant, not the device's count: partial sums follow the grid
-constexpr int kAngleBytes = 16 * 1024;
+constexpr int kFwdCtasPerSm = 12;
 constexpr int kBwdCtasPerSm = 2;
+// A token is split among warps until there are this many work items per SM.
+constexpr int kWorkPerSm = 32;
 
 int lanes_for(int units)
 {
@@ -27,24 +29,20 @@ void rope_plan(RopeArgs* a, bool backward, int* grid)
     a->rot_units = (a->rot + 15) / 16;
     a->units = a->rot_units + (a->dim - a->rot + 15) / 16;
     a->group = lanes_for(a->units);
-    // Enough tokens for about four heads a group, so that the angles' cost
-    // is shared, but no fewer CTAs than about six per SM.
-    const int heads = a->q.heads + a->k.heads;
-    const int groups = kRopeThreads / a->group;
-    int64_t step = (4 * groups + heads - 1) / heads;
-    const int64_t room = kAngleBytes / (a->rot_units * 64);
-    const int64_t spread = a->tokens / (6 * kSms);
-    if (step > room)
-        step = room;
-    if (step > spread)
-        step = spread;
-    if (step < 1)
-        step = 1;
-    a->tokens_per_step = static_cast<int>(step);
-    int64_t ctas = (a->tokens + step - 1) / step;
-    if (backward && ctas > kBwdCtasPerSm * kSms)
-        ctas = kBwdCtasPerSm * kSms;
-    *grid = static_cast<int>(ctas);
+    a->heads_per_step = 32 / a->group;
+    a->q_steps = (a->q.heads + a->heads_per_step - 1) / a->heads_per_step;
+    a->k_steps = (a->k.heads + a->heads_per_step - 1) / a->heads_per_step;
+    const int64_t steps = a->q_steps + a->k_steps;
+    int64_t split = (kWorkPerSm * kSms + a->tokens - 1) / a->tokens;
+    if (split > steps)
+        split = steps;
+    a->steps_per_warp = static_cast<int>((steps + split - 1) / split);
+    a->warps_per_token = static_cast<int>((steps + a->steps_per_warp - 1) / a->steps_per_warp);
+    const int64_t work = a->tokens * a->warps_per_token;
+    a->n_work = static_cast<uint32_t>(work);
+    const int64_t ctas = (work + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    const int64_t most = static_cast<int64_t>(backward ? kBwdCtasPerSm : kFwdCtasPerSm) * kSms;
+    *grid = static_cast<int>(ctas < most ? ctas : most);
 }
 
 cudaError_t launch_rope(const RopeArgs& a, int mode, int elem, bool interleaved, bool blocks, int grid,

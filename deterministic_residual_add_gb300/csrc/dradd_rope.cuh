@@ -17,10 +17,12 @@
 // Work layout.  A unit is 16 columns of a head: in the halves layout 8
 // columns and their partners, or 16 that pass; interleaved 16 consecutive
 // ones.  A head's units go to `group` neighbouring lanes (a power of two, so
-// the norm's sums are butterflies within the group); the CTA's groups walk
-// the heads of q and of k of `tokens_per_step` tokens, whose cosines and
-// sines the CTA computes once into shared memory.  Bound by the memory (2
-// elements of traffic an element, the gradient 3).
+// the norm's sums are butterflies within the group), so a warp takes
+// 32 / group heads at a time; one such step is all of q or all of k.  A warp
+// takes a token, computes its cosines and sines once, two or so a lane, into
+// shared memory of its own, and goes through `per_warp` steps of heads with
+// the loads of the next ones in flight; no barrier but the CTA's first.
+// Bound by the memory (2 elements of traffic an element, the gradient 3).
 #pragma once
 
 #include "dradd_elem.cuh"
@@ -79,36 +81,114 @@ __device__ __forceinline__ UnitColumns unit_columns(const RopeArgs& p, int u)
     return c;
 }
 
-// BLOCKS: every run is a whole, 16-byte aligned block of 8.
+// BLOCKS, below: every run is a whole, 16-byte aligned block of 8.
+
+// 16 floats of shared memory as two runs of 8.
+__device__ __forceinline__ void load_shared16(const float* p, float (&a)[8], float (&b)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 va = *reinterpret_cast<const float4*>(p + 4 * i);
+        const float4 vb = *reinterpret_cast<const float4*>(p + 8 + 4 * i);
+        a[4 * i] = va.x; a[4 * i + 1] = va.y; a[4 * i + 2] = va.z; a[4 * i + 3] = va.w;
+        b[4 * i] = vb.x; b[4 * i + 1] = vb.y; b[4 * i + 2] = vb.z; b[4 * i + 3] = vb.w;
+    }
+}
+
+// Turns the unit's first `pairs` pairs by their cosines and sines (cs: 8
+// cosines, then 8 sines); the others stay, whatever they hold.  In the
+// halves layout a unit's pairs all turn or lie outside the head.
+template <bool INTER>
+__device__ __forceinline__ void turn_unit(const float* cs, int pairs, float (&a)[8], float (&b)[8])
+{
+    float c[8], s[8];
+    load_shared16(cs, c, s);
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        // pairs e and e + 1
+        float& x0 = INTER ? (e < 4 ? a[(2 * e) & 7] : b[(2 * e) & 7]) : a[e];
+        float& y0 = INTER ? (e < 4 ? a[(2 * e + 1) & 7] : b[(2 * e + 1) & 7]) : b[e];
+        float& x1 = INTER ? (e < 4 ? a[(2 * e + 2) & 7] : b[(2 * e + 2) & 7]) : a[e + 1];
+        float& y1 = INTER ? (e < 4 ? a[(2 * e + 3) & 7] : b[(2 * e + 3) & 7]) : b[e + 1];
+        float p0, p1, q0, q1;
+        mul2_rn(y0, y1, s[e], s[e + 1], p0, p1);
+        mul2_rn(y0, y1, c[e], c[e + 1], q0, q1);
+        fma2_rn(x0, x1, s[e], s[e + 1], q0, q1, q0, q1);
+        p0 = __fmaf_rn(x0, c[e], -p0);
+        p1 = __fmaf_rn(x1, c[e + 1], -p1);
+        if (!INTER || e < pairs) {
+            x0 = p0;
+            y0 = q0;
+        }
+        if (!INTER || e + 1 < pairs) {
+            x1 = p1;
+            y1 = q1;
+        }
+    }
+}
+
+// The weights of q and of k in fp32, table[side][unit][16] in the order of
+// the unit's columns (0 past the head).
+template <int E, bool INTER>
+__device__ __forceinline__ void fill_weights(const RopeArgs& p, float* table)
+{
+    using T = typename Elem<E>::T;
+    for (int i = threadIdx.x; i < 2 * p.units * 16; i += kRopeThreads) {
+        const int side = i >= p.units * 16;
+        const int r = i - side * p.units * 16;
+        const UnitColumns c = unit_columns<INTER>(p, r >> 4);
+        const int e = r & 7;
+        const bool second = (r & 8) != 0;
+        const T* w = static_cast<const T*>(side ? p.k.weight : p.q.weight);
+        float v = 0.0f;
+        if (w && e < (second ? c.nb : c.na))
+            v = Elem<E>::widen(__ldg(w + (second ? c.b : c.a) + e));
+        table[i] = v;
+    }
+}
+
+// A unit as it comes from memory.
 template <int E, bool BLOCKS>
-__device__ __forceinline__ void load_unit(const void* base, int64_t at, const UnitColumns& c, float (&a)[8],
-                                          float (&b)[8])
+struct RawUnit {
+    typename Elem<E>::Block a, b;
+};
+template <int E>
+struct RawUnit<E, false> {
+    typename Elem<E>::T a[8], b[8];
+};
+
+template <int E, bool BLOCKS>
+__device__ __forceinline__ void load_raw(const void* base, int64_t at, const UnitColumns& c, bool active,
+                                         RawUnit<E, BLOCKS>& r)
 {
     using T = typename Elem<E>::T;
     const T* p = static_cast<const T*>(base) + at;
     if constexpr (BLOCKS) {
-        typename Elem<E>::Block va, vb;
-        if (c.na) {
-            ld_block_stream(p + c.a, 0, va);
-            Elem<E>::unpack(va, a);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                a[e] = 0.0f;
-        }
-        if (c.nb) {
-            ld_block_stream(p + c.b, 0, vb);
-            Elem<E>::unpack(vb, b);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                b[e] = 0.0f;
-        }
+        r.a = r.b = typename Elem<E>::Block{};
+        if (active && c.na)
+            ld_block_stream(p + c.a, 0, r.a);
+        if (active && c.nb)
+            ld_block_stream(p + c.b, 0, r.b);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            a[e] = e < c.na ? Elem<E>::widen(__ldcs(p + c.a + e)) : 0.0f;
-            b[e] = e < c.nb ? Elem<E>::widen(__ldcs(p + c.b + e)) : 0.0f;
+            r.a[e] = active && e < c.na ? __ldcs(p + c.a + e) : T{};
+            r.b[e] = active && e < c.nb ? __ldcs(p + c.b + e) : T{};
+        }
+    }
+}
+
+template <int E, bool BLOCKS>
+__device__ __forceinline__ void widen_unit(const RawUnit<E, BLOCKS>& r, float (&a)[8], float (&b)[8])
+{
+    if constexpr (BLOCKS) {
+        Elem<E>::unpack(r.a, a);
+        Elem<E>::unpack(r.b, b);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            a[e] = Elem<E>::widen(r.a[e]);
+            b[e] = Elem<E>::widen(r.b[e]);
         }
     }
 }
@@ -135,257 +215,282 @@ __device__ __forceinline__ void store_unit(void* base, int64_t at, const UnitCol
     }
 }
 
-// 16 floats of shared memory as two runs of 8.
-__device__ __forceinline__ void load_shared16(const float* p, float (&a)[8], float (&b)[8])
-{
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float4 va = *reinterpret_cast<const float4*>(p + 4 * i);
-        const float4 vb = *reinterpret_cast<const float4*>(p + 8 + 4 * i);
-        a[4 * i] = va.x; a[4 * i + 1] = va.y; a[4 * i + 2] = va.z; a[4 * i + 3] = va.w;
-        b[4 * i] = vb.x; b[4 * i + 1] = vb.y; b[4 * i + 2] = vb.z; b[4 * i + 3] = vb.w;
-    }
-}
-
-// Turns the unit's first `pairs` pairs by their cosines and sines (cs: 8
-// cosines, then 8 sines); the others stay, whatever they hold.  In the
-// halves layout a unit's pairs all turn or lie outside the head.
-template <bool INTER>
-__device__ __forceinline__ void turn_unit(const float* cs, int pairs, float (&a)[8], float (&b)[8])
-{
-    float c[8], s[8];
-    load_shared16(cs, c, s);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float& x = INTER ? (e < 4 ? a[(2 * e) & 7] : b[(2 * e) & 7]) : a[e];
-        float& y = INTER ? (e < 4 ? a[(2 * e + 1) & 7] : b[(2 * e + 1) & 7]) : b[e];
-        const float x1 = __fmaf_rn(x, c[e], -__fmul_rn(y, s[e]));
-        const float y1 = __fmaf_rn(x, s[e], __fmul_rn(y, c[e]));
-        if (!INTER || e < pairs) {
-            x = x1;
-            y = y1;
-        }
-    }
-}
-
-// The weights of q and of k in fp32, table[side][unit][16] in the order of
-// the unit's columns (0 past the head).
-template <int E, bool INTER>
-__device__ __forceinline__ void fill_weights(const RopeArgs& p, float* table)
-{
-    using T = typename Elem<E>::T;
-    for (int i = threadIdx.x; i < 2 * p.units * 16; i += kRopeThreads) {
-        const int side = i >= p.units * 16;
-        const int r = i - side * p.units * 16;
-        const UnitColumns c = unit_columns<INTER>(p, r >> 4);
-        const int e = r & 7;
-        const bool second = (r & 8) != 0;
-        const T* w = static_cast<const T*>(side ? p.k.weight : p.q.weight);
-        float v = 0.0f;
-        if (w && e < (second ? c.nb : c.na))
-            v = Elem<E>::widen(__ldg(w + (second ? c.b : c.a) + e));
-        table[i] = v;
-    }
-}
-
-// The CTA's angles: table[token][unit][8 cosines, 8 sines], for the units
-// that rotate (cosine 1 and sine 0 past rot / 2, never used).
-__device__ __forceinline__ void fill_angles(const RopeArgs& p, float* table, int64_t first, int n_tokens)
-{
-    const int pairs = 8 * p.rot_units;
-    for (int i = threadIdx.x; i < n_tokens * pairs; i += kRopeThreads) {
-        const int j = i / pairs, pair = i - j * pairs;
-        const int64_t token = first + j;
-        float c = 1.0f, s = 0.0f;
-        if (pair < (p.rot >> 1)) {
-            const int64_t pos = p.positions ? __ldg(p.positions + token) : p.position0 + token % p.seq;
-            turn_cos_sin(turn_fraction(__ldg(p.inv_freq + pair)), pos, c, s);
-            c = __fmul_rn(c, p.scale);
-            s = __fmul_rn(s, __fmul_rn(p.scale, p.sign));
-        }
-        float* at = table + (j * p.rot_units + (pair >> 3)) * 16 + (pair & 7);
-        at[0] = c;
-        at[8] = s;
-    }
-}
-
 __device__ __forceinline__ float fold8(const float (&p)[8])
 {
     return __fadd_rn(__fadd_rn(__fadd_rn(p[0], p[1]), __fadd_rn(p[2], p[3])),
                      __fadd_rn(__fadd_rn(p[4], p[5]), __fadd_rn(p[6], p[7])));
 }
 
+// The CTA's shared memory: the pairs' fractions, the weights (norm only),
+// then every warp's cosines and sines, table[unit][8 cosines, 8 sines].
+struct RopeShared {
+    uint64_t* fractions;
+    float* weights;
+    float* table;  // this warp's
+};
+
+template <int E, bool NORM, bool INTER>
+__device__ __forceinline__ RopeShared rope_prologue(const RopeArgs& p, unsigned char* mem)
+{
+    RopeShared sh;
+    sh.fractions = reinterpret_cast<uint64_t*>(mem);
+    sh.weights = reinterpret_cast<float*>(sh.fractions + 8 * p.rot_units);
+    sh.table = sh.weights + (NORM ? 32 * p.units : 0) + (threadIdx.x >> 5) * 16 * p.rot_units;
+    for (int i = threadIdx.x; i < (p.rot >> 1); i += kRopeThreads)
+        sh.fractions[i] = turn_fraction(__ldg(p.inv_freq + i));
+    if constexpr (NORM)
+        fill_weights<E, INTER>(p, sh.weights);
+    __syncthreads();
+    return sh;
+}
+
+// The warp's table for one position.  What lies past rot / 2 is never used.
+__device__ __forceinline__ void fill_angles(const RopeArgs& p, const RopeShared& sh, int64_t position, int lane)
+{
+    __syncwarp();
+    for (int i = lane; i < (p.rot >> 1); i += 32) {
+        float c, s;
+        turn_cos_sin(sh.fractions[i], position, c, s);
+        float* at = sh.table + (i >> 3) * 16 + (i & 7);
+        at[0] = __fmul_rn(c, p.scale);
+        at[8] = __fmul_rn(s, __fmul_rn(p.scale, p.sign));
+    }
+    __syncwarp();
+}
+
+// One step of a warp's work: the heads of q or of k its groups take, and
+// where this lane's head begins.
+struct RopeStep {
+    bool is_k, active;
+    int head;
+};
+
+__device__ __forceinline__ RopeStep rope_step(const RopeArgs& p, int step, int group_in_warp)
+{
+    RopeStep r;
+    r.is_k = step >= p.q_steps;
+    r.head = (step - (r.is_k ? p.q_steps : 0)) * p.heads_per_step + group_in_warp;
+    r.active = r.head < (r.is_k ? p.k.heads : p.q.heads);
+    if (!r.active)
+        r.head = 0;
+    return r;
+}
+
+// The token and the steps of work item w of the call.
+struct RopeWork {
+    int64_t bi, si, position;
+    int first, last;
+};
+
+__device__ __forceinline__ RopeWork rope_work(const RopeArgs& p, uint32_t w)
+{
+    RopeWork r;
+    const uint32_t token = w / static_cast<uint32_t>(p.warps_per_token);
+    const int part = static_cast<int>(w - token * static_cast<uint32_t>(p.warps_per_token));
+    const uint32_t b = token / static_cast<uint32_t>(p.seq);
+    r.bi = b;
+    r.si = token - b * static_cast<uint32_t>(p.seq);
+    r.position = p.positions ? __ldg(p.positions + token) : p.position0 + r.si;
+    r.first = part * p.steps_per_warp;
+    const int steps = p.q_steps + p.k_steps;
+    r.last = r.first + p.steps_per_warp < steps ? r.first + p.steps_per_warp : steps;
+    return r;
+}
+
 // Forward: plain (NORM false; also the inverse) or behind the norm
 //   z = (x * inv) * w, inv = 1 / sqrt(sum x^2 / dim + eps).
 template <int E, bool NORM, bool INTER, bool BLOCKS>
-__global__ void __launch_bounds__(kRopeThreads) rope_fwd_kernel(const RopeArgs p)
+__global__ void __launch_bounds__(kRopeThreads, E == kElemF32 || !BLOCKS ? 2 : 3) rope_fwd_kernel(const RopeArgs p)
 {
-    extern __shared__ __align__(16) float table[];
+    extern __shared__ __align__(16) unsigned char mem[];
     wait_prior_grids();
     allow_next_grid();
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * p.tokens_per_step;
-    const int n_tokens = static_cast<int>(p.tokens - first < p.tokens_per_step ? p.tokens - first : p.tokens_per_step);
-    fill_angles(p, table, first, n_tokens);
-    float* const weights = table + p.tokens_per_step * p.rot_units * 16;
-    if constexpr (NORM)
-        fill_weights<E, INTER>(p, weights);
-    __syncthreads();
-    const int u = threadIdx.x & (p.group - 1);
-    const int groups = kRopeThreads / p.group;
-    const int own = u < p.units ? u : 0;  // lanes past the units carry zeros
+    const RopeShared sh = rope_prologue<E, NORM, INTER>(p, mem);
+    const int lane = threadIdx.x & 31;
+    const int u = lane & (p.group - 1);
+    const int g = lane / p.group;
     const UnitColumns cols = unit_columns<INTER>(p, u);
-    const int heads = p.q.heads + p.k.heads;
-    const int items = n_tokens * heads;
-    // lanes of one warp start together and leave together (the norm's sums
-    // are shuffles of the whole warp)
-    const int mine = threadIdx.x / p.group;
-    const int lead = mine - (threadIdx.x & 31) / p.group;
-    for (int base = 0; lead + base < items; base += groups) {
-        const int item = mine + base;
-        const bool active = item < items;
-        const int j = active ? item / heads : 0;
-        const int head = active ? item - j * heads : 0;
-        const bool is_k = head >= p.q.heads;
-        const RopeSide& side = is_k ? p.k : p.q;
-        const int hd = is_k ? head - p.q.heads : head;
-        const int64_t token = first + j;
-        const int64_t bi = token / p.seq, si = token - bi * p.seq;
-        UnitColumns c = cols;
-        if (!active || (side.skip_rest && c.pairs == 0))
-            c.na = c.nb = 0;
-        float a[8], b[8];
-        load_unit<E, BLOCKS>(side.in, bi * side.in_b + si * side.in_s + hd * side.in_h, c, a, b);
-        if constexpr (NORM) {
-            float sq = __fadd_rn(fold8_squares(a), fold8_squares(b));
-            sq = butterfly_sum(sq, p.group);
-            const float inv = inv_rms(sq, p.dim, p.inv_dim, side.eps);
-            float wa[8], wb[8];
-            load_shared16(weights + ((is_k ? p.units : 0) + own) * 16, wa, wb);
+    const float* const turn = sh.table + (cols.pairs ? u : 0) * 16;
+    const float* const weight = sh.weights + (u < p.units ? u : 0) * 16;
+    const uint32_t warps = gridDim.x * (kRopeThreads / 32);
+    for (uint32_t w = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); w < p.n_work; w += warps) {
+        const RopeWork work = rope_work(p, w);
+        auto load = [&](int step, RawUnit<E, BLOCKS>& raw) {
+            const RopeStep st = rope_step(p, step, g);
+            const RopeSide& side = st.is_k ? p.k : p.q;
+            load_raw<E, BLOCKS>(side.in, work.bi * side.in_b + work.si * side.in_s + st.head * side.in_h, cols,
+                                st.active && step < work.last, raw);
+        };
+        RawUnit<E, BLOCKS> next0, next1;
+        load(work.first, next0);
+        load(work.first + 1, next1);
+        fill_angles(p, sh, work.position, lane);
+        for (int step = work.first; step < work.last; ++step) {
+            float a[8], b[8];
+            widen_unit<E, BLOCKS>(next0, a, b);
+            next0 = next1;
+            load(step + 2, next1);
+            const RopeStep st = rope_step(p, step, g);
+            const RopeSide& side = st.is_k ? p.k : p.q;
+            if constexpr (NORM) {
+                float sq = __fadd_rn(fold8_squares(a), fold8_squares(b));
+                sq = butterfly_sum(sq, p.group);
+                const float inv = inv_rms(sq, p.dim, p.inv_dim, side.eps);
+                float wa[8], wb[8];
+                load_shared16(weight + (st.is_k ? p.units * 16 : 0), wa, wb);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                a[e] = __fmul_rn(__fmul_rn(a[e], inv), wa[e]);
-                b[e] = __fmul_rn(__fmul_rn(b[e], inv), wb[e]);
+                for (int e = 0; e < 8; e += 2) {
+                    mul2_rn(a[e], a[e + 1], inv, inv, a[e], a[e + 1]);
+                    mul2_rn(b[e], b[e + 1], inv, inv, b[e], b[e + 1]);
+                    mul2_rn(a[e], a[e + 1], wa[e], wa[e + 1], a[e], a[e + 1]);
+                    mul2_rn(b[e], b[e + 1], wb[e], wb[e + 1], b[e], b[e + 1]);
+                }
             }
+            if (cols.pairs)
+                turn_unit<INTER>(turn, cols.pairs, a, b);
+            UnitColumns c = cols;
+            if (!st.active || (side.skip_rest && cols.pairs == 0))
+                c.na = c.nb = 0;
+            store_unit<E, BLOCKS>(side.out, work.bi * side.out_b + work.si * side.out_s + st.head * side.out_h, c, a,
+                                  b);
         }
-        if (c.pairs)
-            turn_unit<INTER>(table + (j * p.rot_units + u) * 16, c.pairs, a, b);
-        store_unit<E, BLOCKS>(side.out, bi * side.out_b + si * side.out_s + hd * side.out_h, c, a, b);
     }
 }
 
 // The gradients of the fused call, with g = turn(-theta) dy:
 //   S1 = sum x^2, S2 = sum (g w) x; c = inv (inv (S2 / dim))
 //   dx = inv (g w - x c); dweight += g (x inv), over tokens and heads.
-// A CTA walks its token steps in order, q heads then k heads of each, every
-// group adding its own heads' shares in registers; at the end the groups'
-// sums are added in group order into the CTA's part.
+// Every lane adds the shares of its warp's work in order in registers; at
+// the end a warp's groups are added by butterfly and the CTA's warps in
+// order into the CTA's part.
 template <int E, bool INTER, bool BLOCKS>
-__device__ __forceinline__ void rope_bwd_side(const RopeArgs& p, const RopeSide& side, const float* table, const float* weights,
-                                              int64_t first, int n_tokens, const UnitColumns& cols, int u,
-                                              float (&da)[8], float (&db)[8])
+__global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArgs p)
 {
-    const int groups = kRopeThreads / p.group;
-    const int items = n_tokens * side.heads;
-    const int mine = threadIdx.x / p.group;
-    const int lead = mine - (threadIdx.x & 31) / p.group;
-    for (int base = 0; lead + base < items; base += groups) {
-        const int item = mine + base;
-        const bool active = item < items;
-        const int j = active ? item / side.heads : 0;
-        const int hd = active ? item - j * side.heads : 0;
-        const int64_t token = first + j;
-        const int64_t bi = token / p.seq, si = token - bi * p.seq;
-        UnitColumns c = cols;
-        if (!active)
-            c.na = c.nb = 0;
-        float a[8], b[8], ga[8], gb[8], wa[8], wb[8];
-        load_unit<E, BLOCKS>(side.in, bi * side.in_b + si * side.in_s + hd * side.in_h, c, a, b);
-        load_unit<E, BLOCKS>(side.grad, bi * side.grad_b + si * side.grad_s + hd * side.grad_h, c, ga, gb);
-        if (c.pairs)
-            turn_unit<INTER>(table + (j * p.rot_units + u) * 16, c.pairs, ga, gb);
-        load_shared16(weights + (u < p.units ? u : 0) * 16, wa, wb);
-        float ta[8], tb[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            wa[e] = __fmul_rn(ga[e], wa[e]);
-            wb[e] = __fmul_rn(gb[e], wb[e]);
-            ta[e] = __fmul_rn(wa[e], a[e]);
-            tb[e] = __fmul_rn(wb[e], b[e]);
-        }
-        const float s1 = butterfly_sum(__fadd_rn(fold8_squares(a), fold8_squares(b)), p.group);
-        const float s2 = butterfly_sum(__fadd_rn(fold8(ta), fold8(tb)), p.group);
-        const float inv = inv_rms(s1, p.dim, p.inv_dim, side.eps);
-        const float mean = p.inv_dim != 0.0f ? __fmul_rn(s2, p.inv_dim) : __fdiv_rn(s2, static_cast<float>(p.dim));
-        const float k = __fmul_rn(inv, __fmul_rn(inv, mean));
-        if (active) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                da[e] = __fmaf_rn(ga[e], __fmul_rn(a[e], inv), da[e]);
-                db[e] = __fmaf_rn(gb[e], __fmul_rn(b[e], inv), db[e]);
-                ta[e] = __fmul_rn(inv, __fmaf_rn(-a[e], k, wa[e]));
-                tb[e] = __fmul_rn(inv, __fmaf_rn(-b[e], k, wb[e]));
-            }
-        }
-        store_unit<E, BLOCKS>(side.out, bi * side.out_b + si * side.out_s + hd * side.out_h, c, ta, tb);
-    }
-}
-
-template <int E, bool INTER, bool BLOCKS>
-__global__ void __launch_bounds__(kRopeThreads) rope_bwd_kernel(const RopeArgs p)
-{
-    extern __shared__ __align__(16) float table[];
+    extern __shared__ __align__(16) unsigned char mem[];
     wait_prior_grids();
     allow_next_grid();
-    const int u = threadIdx.x & (p.group - 1);
-    const int group = threadIdx.x / p.group;
-    const int groups = kRopeThreads / p.group;
+    const RopeShared sh = rope_prologue<E, true, INTER>(p, mem);
+    const int lane = threadIdx.x & 31;
+    const int u = lane & (p.group - 1);
+    const int g = lane / p.group;
     const UnitColumns cols = unit_columns<INTER>(p, u);
+    const float* const turn = sh.table + (cols.pairs ? u : 0) * 16;
+    const float* const weight = sh.weights + (u < p.units ? u : 0) * 16;
     float dq[2][8] = {}, dk[2][8] = {};
-    float* const weights = table + p.tokens_per_step * p.rot_units * 16;
-    fill_weights<E, INTER>(p, weights);
-    const int64_t step = static_cast<int64_t>(gridDim.x) * p.tokens_per_step;
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * p.tokens_per_step; first < p.tokens; first += step) {
-        const int n = static_cast<int>(p.tokens - first < p.tokens_per_step ? p.tokens - first : p.tokens_per_step);
-        fill_angles(p, table, first, n);
-        __syncthreads();
-        rope_bwd_side<E, INTER, BLOCKS>(p, p.q, table, weights, first, n, cols, u, dq[0], dq[1]);
-        rope_bwd_side<E, INTER, BLOCKS>(p, p.k, table, weights + p.units * 16, first, n, cols, u, dk[0], dk[1]);
-        __syncthreads();
+    const uint32_t warps = gridDim.x * (kRopeThreads / 32);
+    for (uint32_t w = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); w < p.n_work; w += warps) {
+        const RopeWork work = rope_work(p, w);
+        auto load = [&](int step, RawUnit<E, BLOCKS>& x, RawUnit<E, BLOCKS>& dy) {
+            const RopeStep st = rope_step(p, step, g);
+            const RopeSide& side = st.is_k ? p.k : p.q;
+            const bool active = st.active && step < work.last;
+            load_raw<E, BLOCKS>(side.in, work.bi * side.in_b + work.si * side.in_s + st.head * side.in_h, cols, active,
+                                x);
+            load_raw<E, BLOCKS>(side.grad, work.bi * side.grad_b + work.si * side.grad_s + st.head * side.grad_h, cols,
+                                active, dy);
+        };
+        RawUnit<E, BLOCKS> next_x, next_dy;
+        load(work.first, next_x, next_dy);
+        fill_angles(p, sh, work.position, lane);
+        for (int step = work.first; step < work.last; ++step) {
+            const RopeStep st = rope_step(p, step, g);
+            const RopeSide& side = st.is_k ? p.k : p.q;
+            float a[8], b[8], ga[8], gb[8], wa[8], wb[8], ta[8], tb[8];
+            widen_unit<E, BLOCKS>(next_x, a, b);
+            widen_unit<E, BLOCKS>(next_dy, ga, gb);
+            load(step + 1, next_x, next_dy);
+            if (cols.pairs)
+                turn_unit<INTER>(turn, cols.pairs, ga, gb);
+            load_shared16(weight + (st.is_k ? p.units * 16 : 0), wa, wb);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                mul2_rn(ga[e], ga[e + 1], wa[e], wa[e + 1], wa[e], wa[e + 1]);
+                mul2_rn(gb[e], gb[e + 1], wb[e], wb[e + 1], wb[e], wb[e + 1]);
+                mul2_rn(wa[e], wa[e + 1], a[e], a[e + 1], ta[e], ta[e + 1]);
+                mul2_rn(wb[e], wb[e + 1], b[e], b[e + 1], tb[e], tb[e + 1]);
+            }
+            const float s1 = butterfly_sum(__fadd_rn(fold8_squares(a), fold8_squares(b)), p.group);
+            const float s2 = butterfly_sum(__fadd_rn(fold8(ta), fold8(tb)), p.group);
+            const float inv = inv_rms(s1, p.dim, p.inv_dim, side.eps);
+            const float mean =
+                p.inv_dim != 0.0f ? __fmul_rn(s2, p.inv_dim) : __fdiv_rn(s2, static_cast<float>(p.dim));
+            const float k = -__fmul_rn(inv, __fmul_rn(inv, mean));
+            if (st.active) {
+                float xa[8], xb[8];
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    mul2_rn(a[e], a[e + 1], inv, inv, xa[e], xa[e + 1]);
+                    mul2_rn(b[e], b[e + 1], inv, inv, xb[e], xb[e + 1]);
+                    fma2_rn(a[e], a[e + 1], k, k, wa[e], wa[e + 1], ta[e], ta[e + 1]);
+                    fma2_rn(b[e], b[e + 1], k, k, wb[e], wb[e + 1], tb[e], tb[e + 1]);
+                    mul2_rn(ta[e], ta[e + 1], inv, inv, ta[e], ta[e + 1]);
+                    mul2_rn(tb[e], tb[e + 1], inv, inv, tb[e], tb[e + 1]);
+                }
+                if (st.is_k) {
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        fma2_rn(ga[e], ga[e + 1], xa[e], xa[e + 1], dk[0][e], dk[0][e + 1], dk[0][e], dk[0][e + 1]);
+                        fma2_rn(gb[e], gb[e + 1], xb[e], xb[e + 1], dk[1][e], dk[1][e + 1], dk[1][e], dk[1][e + 1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        fma2_rn(ga[e], ga[e + 1], xa[e], xa[e + 1], dq[0][e], dq[0][e + 1], dq[0][e], dq[0][e + 1]);
+                        fma2_rn(gb[e], gb[e + 1], xb[e], xb[e + 1], dq[1][e], dq[1][e + 1], dq[1][e], dq[1][e + 1]);
+                    }
+                }
+                store_unit<E, BLOCKS>(side.out, work.bi * side.out_b + work.si * side.out_s + st.head * side.out_h,
+                                      cols, ta, tb);
+            }
+        }
     }
     if (!p.partials)
         return;
-    // The table's memory now takes the head's column sums: q, then k.
-    float* part = p.partials + static_cast<int64_t>(blockIdx.x) * 2 * p.dim;
-    for (int side = 0; side < 2; ++side) {
-        for (int g = 0; g < groups; ++g) {
-            if (group == g) {
+    // warp sums [warp][side][unit][16] over the memory used so far
+    float* const sums = reinterpret_cast<float*>(mem);
+    const int stride = 32 * p.units;
+    __syncthreads();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float va = side ? dk[0][e] : dq[0][e], vb = side ? dk[1][e] : dq[1][e];
-                    if (e < cols.na)
-                        table[cols.a + e] = g == 0 ? va : __fadd_rn(table[cols.a + e], va);
-                    if (e < cols.nb)
-                        table[cols.b + e] = g == 0 ? vb : __fadd_rn(table[cols.b + e], vb);
-                }
-            }
-            __syncthreads();
+    for (int side = 0; side < 2; ++side) {
+        float* at = sums + (threadIdx.x >> 5) * stride + (side * p.units + u) * 16;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            float v = side ? dk[e >> 3][e & 7] : dq[e >> 3][e & 7];
+            for (int d = p.group; d < 32; d <<= 1)
+                v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+            if (g == 0 && u < p.units)
+                at[e] = v;
         }
-        for (int i = threadIdx.x; i < p.dim; i += kRopeThreads)
-            part[side * p.dim + i] = table[i];
-        __syncthreads();
+    }
+    __syncthreads();
+    float* part = p.partials + static_cast<int64_t>(blockIdx.x) * 2 * p.dim;
+    for (int i = threadIdx.x; i < stride; i += kRopeThreads) {
+        const int side = i >= 16 * p.units;
+        const int r = i - side * 16 * p.units;
+        const UnitColumns c = unit_columns<INTER>(p, r >> 4);
+        const int e = r & 7;
+        const bool second = (r & 8) != 0;
+        if (e >= (second ? c.nb : c.na))
+            continue;
+        float v = sums[i];
+#pragma unroll
+        for (int k = 1; k < kRopeThreads / 32; ++k)
+            v = __fadd_rn(v, sums[k * stride + i]);
+        part[side * p.dim + (second ? c.b : c.a) + e] = v;
     }
 }
 
 template <int E, bool INTER, bool BLOCKS>
 cudaError_t launch_rope_as(const RopeArgs& p, int mode, int grid, cudaStream_t stream)
 {
-    const size_t angles = static_cast<size_t>(p.tokens_per_step) * p.rot_units * 16 * sizeof(float);
-    const size_t both = angles + static_cast<size_t>(p.units) * 32 * sizeof(float);  // >= dim floats
+    const bool norm = mode != kRopePlain;
+    size_t smem = static_cast<size_t>(p.rot_units) * 64 * (1 + kRopeThreads / 32) + (norm ? p.units * 128 : 0);
+    const size_t sums = static_cast<size_t>(p.units) * 128 * (kRopeThreads / 32);
     if (mode == kRopeNormBwd)
-        return launch(rope_bwd_kernel<E, INTER, BLOCKS>, grid, kRopeThreads, both, false, stream, p);
-    return mode == kRopeNorm
-               ? launch(rope_fwd_kernel<E, true, INTER, BLOCKS>, grid, kRopeThreads, both, false, stream, p)
-               : launch(rope_fwd_kernel<E, false, INTER, BLOCKS>, grid, kRopeThreads, angles, false, stream, p);
+        return launch(rope_bwd_kernel<E, INTER, BLOCKS>, grid, kRopeThreads, smem > sums ? smem : sums, false, stream,
+                      p);
+    return norm ? launch(rope_fwd_kernel<E, true, INTER, BLOCKS>, grid, kRopeThreads, smem, false, stream, p)
+                : launch(rope_fwd_kernel<E, false, INTER, BLOCKS>, grid, kRopeThreads, smem, false, stream, p);
 }
 
 template <int E>

@@ -100,23 +100,26 @@ struct RopeArgs {
     const double* inv_freq;
     const int64_t* positions;  // [batch, seq], or NULL: position0 + s
     int64_t position0;
-    int64_t tokens;  // batch * seq
+    int64_t tokens;  // batch * seq, below 2^31
     int64_t seq;
     int dim, rot;
     int rot_units, units, group;  // 16-element units that rotate, in all; lanes per head (a power of two)
     float inv_dim;                // 1 / dim if a power of two, else 0
     float scale;
     float sign;                   // +1, or -1 for the inverse rotation
-    int tokens_per_step;
-    float* partials;              // gradient: grid x 2 dim sums
+    // A step is the heads of q or of k that a warp takes at a time; a work
+    // item is steps_per_warp steps of one token.
+    int heads_per_step, q_steps, k_steps, steps_per_warp, warps_per_token;
+    uint32_t n_work;
+    float* partials;  // gradient: grid x 2 dim sums
 };
 
 enum RopeMode : int { kRopePlain = 0, kRopeNorm = 1, kRopeNormBwd = 2 };
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxDim = 512;
 
-// Tokens a CTA takes at once, and CTAs; backward: the grid is also the
-// number of partial sums.  A function of the shape alone.
+// Work items and CTAs; backward: the grid is also the number of partial
+// sums.  A function of the shape alone.
 void rope_plan(RopeArgs* a, bool backward, int* grid);
 
 cudaError_t launch_rope(const RopeArgs& a, int mode, int elem, bool interleaved, bool blocks, int grid,
