@@ -11,12 +11,13 @@ namespace {
 constexpr int kSms = 152;  // a constant, not the device's count: partial sums follow the grid
 constexpr int kFwdCtasPerSm = 12;
 constexpr int kBwdCtasPerSm = 2;
-// A token is split among warps until there are this many work items per SM.
-constexpr int kWorkPerSm = 32;
+// A token is split among warps until there are this many work items per SM
+// (4096 tokens of 32 + 8 heads: unsplit 13.6 us, in two 14.4).
+constexpr int kWorkPerSm = 16;
 
 int lanes_for(int units)
 {
-    int g = 1;
+    int g = 4;
     while (g < units)
         g *= 2;
     return g;

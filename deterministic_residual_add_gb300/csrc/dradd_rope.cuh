@@ -20,9 +20,13 @@
 // the norm's sums are butterflies within the group), so a warp takes
 // 32 / group heads at a time; one such step is all of q or all of k.  A warp
 // takes a token, computes its cosines and sines once, two or so a lane, into
-// shared memory of its own, and goes through `per_warp` steps of heads with
-// the loads of the next ones in flight; no barrier but the CTA's first.
-// Bound by the memory (2 elements of traffic an element, the gradient 3).
+// shared memory of its own, and goes through `steps_per_warp` steps; no
+// barrier but the CTA's first.
+//
+// Bound by the memory (2 elements of traffic an element, the gradient 3), so
+// the bytes on their way count: every lane copies its vectors of the next
+// steps, across tokens, into slots of shared memory that only it reads
+// (cp.async, so no barrier and no registers).
 #pragma once
 
 #include "dradd_elem.cuh"
@@ -57,7 +61,7 @@ template <bool INTER>
 __device__ __forceinline__ UnitColumns unit_columns(const RopeArgs& p, int u)
 {
     UnitColumns c;
-    auto clip = [](int n) { return n < 0 ? 0 : n > 8 ? 8 : n; };
+    const auto clip = [](int n) { return n < 0 ? 0 : n > 8 ? 8 : n; };
     if (INTER) {
         c.a = 16 * u;
         c.b = c.a + 8;
@@ -77,32 +81,40 @@ __device__ __forceinline__ UnitColumns unit_columns(const RopeArgs& p, int u)
         c.nb = clip(p.dim - c.b);
     }
     if (u >= p.units)
-        c.na = c.nb = c.pairs = 0;
+        c.a = c.b = c.na = c.nb = c.pairs = 0;
+    if (c.nb == 0)
+        c.b = c.a;  // never used, but inside the head
     return c;
 }
 
 // BLOCKS, below: every run is a whole, 16-byte aligned block of 8.
 
-// 16 floats of shared memory as two runs of 8.
-__device__ __forceinline__ void load_shared16(const float* p, float (&a)[8], float (&b)[8])
+// A table of 16 floats a unit in shared memory, in four planes of one
+// 16-byte quad a unit, so that neighbouring lanes (units) read neighbouring
+// quads without bank conflicts: element i of unit u of n lies at
+// table_at(n, u, i), and `units` below is n.
+__host__ __device__ constexpr int table_at(int n, int u, int i) { return ((i >> 2) * n + u) * 4 + (i & 3); }
+
+// The unit's 16 floats as two runs of 8; p points at its first quad.
+__device__ __forceinline__ void load_table(const float* p, int units, float (&a)[8], float (&b)[8])
 {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const float4 va = *reinterpret_cast<const float4*>(p + 4 * i);
-        const float4 vb = *reinterpret_cast<const float4*>(p + 8 + 4 * i);
+        const float4 va = *reinterpret_cast<const float4*>(p + i * units * 4);
+        const float4 vb = *reinterpret_cast<const float4*>(p + (i + 2) * units * 4);
         a[4 * i] = va.x; a[4 * i + 1] = va.y; a[4 * i + 2] = va.z; a[4 * i + 3] = va.w;
         b[4 * i] = vb.x; b[4 * i + 1] = vb.y; b[4 * i + 2] = vb.z; b[4 * i + 3] = vb.w;
     }
 }
 
-// Turns the unit's first `pairs` pairs by their cosines and sines (cs: 8
-// cosines, then 8 sines); the others stay, whatever they hold.  In the
+// Turns the unit's first `pairs` pairs by their cosines and sines (its table
+// entry: 8 cosines, then 8 sines); the others stay, whatever they hold.  In the
 // halves layout a unit's pairs all turn or lie outside the head.
 template <bool INTER>
-__device__ __forceinline__ void turn_unit(const float* cs, int pairs, float (&a)[8], float (&b)[8])
+__device__ __forceinline__ void turn_unit(const float* entry, int units, int pairs, float (&a)[8], float (&b)[8])
 {
     float c[8], s[8];
-    load_shared16(cs, c, s);
+    load_table(entry, units, c, s);
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
         // pairs e and e + 1
@@ -127,8 +139,8 @@ __device__ __forceinline__ void turn_unit(const float* cs, int pairs, float (&a)
     }
 }
 
-// The weights of q and of k in fp32, table[side][unit][16] in the order of
-// the unit's columns (0 past the head).
+// The weights of q and of k in fp32, a table each, in the order of the
+// unit's columns (0 past the head).
 template <int E, bool INTER>
 __device__ __forceinline__ void fill_weights(const RopeArgs& p, float* table)
 {
@@ -143,7 +155,7 @@ __device__ __forceinline__ void fill_weights(const RopeArgs& p, float* table)
         float v = 0.0f;
         if (w && e < (second ? c.nb : c.na))
             v = Elem<E>::widen(__ldg(w + (second ? c.b : c.a) + e));
-        table[i] = v;
+        table[side * p.units * 16 + table_at(p.units, r >> 4, r & 15)] = v;
     }
 }
 
@@ -157,24 +169,19 @@ struct RawUnit<E, false> {
     typename Elem<E>::T a[8], b[8];
 };
 
-template <int E, bool BLOCKS>
-__device__ __forceinline__ void load_raw(const void* base, int64_t at, const UnitColumns& c, bool active,
-                                         RawUnit<E, BLOCKS>& r)
+// The unit behind p (its first run; the second `second` bytes on), element by
+// element; zeros where the head ends.
+template <int E>
+__device__ __forceinline__ void load_elements(const char* p, int second, const UnitColumns& c, bool active,
+                                              RawUnit<E, false>& r)
 {
     using T = typename Elem<E>::T;
-    const T* p = static_cast<const T*>(base) + at;
-    if constexpr (BLOCKS) {
-        r.a = r.b = typename Elem<E>::Block{};
-        if (active && c.na)
-            ld_block_stream(p + c.a, 0, r.a);
-        if (active && c.nb)
-            ld_block_stream(p + c.b, 0, r.b);
-    } else {
+    const T* a = reinterpret_cast<const T*>(p);
+    const T* b = reinterpret_cast<const T*>(p + second);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            r.a[e] = active && e < c.na ? __ldcs(p + c.a + e) : T{};
-            r.b[e] = active && e < c.nb ? __ldcs(p + c.b + e) : T{};
-        }
+    for (int e = 0; e < 8; ++e) {
+        r.a[e] = active && e < c.na ? __ldcs(a + e) : T{};
+        r.b[e] = active && e < c.nb ? __ldcs(b + e) : T{};
     }
 }
 
@@ -194,54 +201,113 @@ __device__ __forceinline__ void widen_unit(const RawUnit<E, BLOCKS>& r, float (&
 }
 
 template <int E, bool BLOCKS>
-__device__ __forceinline__ void store_unit(void* base, int64_t at, const UnitColumns& c, const float (&a)[8],
-                                           const float (&b)[8])
+__device__ __forceinline__ void store_unit(const char* at, int second, const UnitColumns& c, bool active,
+                                           const float (&a)[8], const float (&b)[8])
 {
     using T = typename Elem<E>::T;
-    T* p = static_cast<T*>(base) + at;
+    T* pa = reinterpret_cast<T*>(const_cast<char*>(at));
+    T* pb = reinterpret_cast<T*>(const_cast<char*>(at) + second);
     if constexpr (BLOCKS) {
-        if (c.na)
-            st_block_stream(p + c.a, 0, Elem<E>::pack(a));
-        if (c.nb)
-            st_block_stream(p + c.b, 0, Elem<E>::pack(b));
+        if (active && c.na)
+            st_block_stream(pa, 0, Elem<E>::pack(a));
+        if (active && c.nb)
+            st_block_stream(pb, 0, Elem<E>::pack(b));
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if (e < c.na)
-                __stcs(p + c.a + e, Elem<E>::narrow(a[e]));
-            if (e < c.nb)
-                __stcs(p + c.b + e, Elem<E>::narrow(b[e]));
+            if (active && e < c.na)
+                __stcs(pa + e, Elem<E>::narrow(a[e]));
+            if (active && e < c.nb)
+                __stcs(pb + e, Elem<E>::narrow(b[e]));
         }
     }
 }
 
-__device__ __forceinline__ float fold8(const float (&p)[8])
+// The lane's share of sum x y over its two runs: four chains of fused
+// multiply-adds, two to an instruction, then their sum.
+__device__ __forceinline__ float unit_dot(const float (&xa)[8], const float (&xb)[8], const float (&ya)[8],
+                                          const float (&yb)[8])
 {
-    return __fadd_rn(__fadd_rn(__fadd_rn(p[0], p[1]), __fadd_rn(p[2], p[3])),
-                     __fadd_rn(__fadd_rn(p[4], p[5]), __fadd_rn(p[6], p[7])));
+    float a0, a1, b0, b1;
+    mul2_rn(xa[0], xa[1], ya[0], ya[1], a0, a1);
+    mul2_rn(xb[0], xb[1], yb[0], yb[1], b0, b1);
+#pragma unroll
+    for (int e = 2; e < 8; e += 2) {
+        fma2_rn(xa[e], xa[e + 1], ya[e], ya[e + 1], a0, a1, a0, a1);
+        fma2_rn(xb[e], xb[e + 1], yb[e], yb[e + 1], b0, b1, b0, b1);
+    }
+    add2_rn(a0, a1, b0, b1, a0, a1);
+    return __fadd_rn(a0, a1);
 }
 
-// The CTA's shared memory: the pairs' fractions, the weights (norm only),
-// then every warp's cosines and sines, table[unit][8 cosines, 8 sines].
+// 1 / sqrt(v): the reciprocal square root approximation (within 2^-22.9)
+// with one Newton step, r + r (1/2 - v/2 r r), which leaves less than 2^-23
+// relative.  v = 0 and v = inf keep the approximation's inf and 0.
+__device__ __forceinline__ float inv_sqrt(float v)
+{
+    float r;
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    const float h = __fmul_rn(-0.5f, v);
+    const float e = __fmaf_rn(__fmul_rn(h, r), r, 0.5f);
+    const float n = __fmaf_rn(r, e, r);
+    return v > 0.0f && v < __int_as_float(0x7f800000) ? n : r;
+}
+
+// The mean over a head of a sum over it.
+__device__ __forceinline__ float head_mean(const RopeArgs& p, float sum)
+{
+    return __fmul_rn(sum, p.inv_dim);
+}
+
+// A lane's ring of shared memory: kSlots steps, one being computed while the
+// others are on their way; a step is the 16-byte pieces of N tensors' runs,
+// then the position.  Two steps ahead measured best: q and k of 8192 tokens
+// behind the norm 29.7 us, one ahead 30.3, three 30.4, four 31.5 (more
+// shared memory leaves less of it as cache).
+template <int E, int N>
+struct RopeRing {
+    static constexpr int kVec = E == kElemF32 ? 2 : 1;  // pieces of a run
+    static constexpr int kPieces = 2 * N * kVec;
+    static constexpr int kPosition = kPieces * 512;
+    static constexpr int kStepBytes = kPosition + 256;
+    static constexpr int kSlots = 3;
+    static constexpr int kBytes = kSlots * kStepBytes * (kRopeThreads / 32);
+    static __device__ __forceinline__ uint32_t after(uint32_t slot, uint32_t ring)
+    {
+        return slot == ring + (kSlots - 1) * kStepBytes ? ring : slot + kStepBytes;
+    }
+};
+
+// The CTA's shared memory: the warps' rings (BLOCKS only), the pairs'
+// fractions, the weights (norm only), then every warp's table of cosines and
+// sines.
 struct RopeShared {
+    unsigned char* ring;  // this warp's
     uint64_t* fractions;
     float* weights;
     float* table;  // this warp's
 };
 
-template <int E, bool NORM, bool INTER>
-__device__ __forceinline__ RopeShared rope_prologue(const RopeArgs& p, unsigned char* mem)
+template <bool NORM>
+__device__ __forceinline__ RopeShared rope_shared(const RopeArgs& p, unsigned char* mem, int ring_bytes)
 {
+    const int warp = threadIdx.x >> 5;
     RopeShared sh;
-    sh.fractions = reinterpret_cast<uint64_t*>(mem);
+    sh.ring = mem + warp * (ring_bytes / (kRopeThreads / 32));
+    sh.fractions = reinterpret_cast<uint64_t*>(mem + ring_bytes);
     sh.weights = reinterpret_cast<float*>(sh.fractions + 8 * p.rot_units);
-    sh.table = sh.weights + (NORM ? 32 * p.units : 0) + (threadIdx.x >> 5) * 16 * p.rot_units;
+    sh.table = sh.weights + (NORM ? 32 * p.units : 0) + warp * 16 * p.rot_units;
+    return sh;
+}
+
+template <int E, bool NORM, bool INTER>
+__device__ __forceinline__ void rope_prologue(const RopeArgs& p, const RopeShared& sh)
+{
     for (int i = threadIdx.x; i < (p.rot >> 1); i += kRopeThreads)
         sh.fractions[i] = turn_fraction(__ldg(p.inv_freq + i));
     if constexpr (NORM)
         fill_weights<E, INTER>(p, sh.weights);
     __syncthreads();
-    return sh;
 }
 
 // The warp's table for one position.  What lies past rot / 2 is never used.
@@ -251,93 +317,263 @@ __device__ __forceinline__ void fill_angles(const RopeArgs& p, const RopeShared&
     for (int i = lane; i < (p.rot >> 1); i += 32) {
         float c, s;
         turn_cos_sin(sh.fractions[i], position, c, s);
-        float* at = sh.table + (i >> 3) * 16 + (i & 7);
-        at[0] = __fmul_rn(c, p.scale);
-        at[8] = __fmul_rn(s, __fmul_rn(p.scale, p.sign));
+        sh.table[table_at(p.rot_units, i >> 3, i & 7)] = __fmul_rn(c, p.scale);
+        sh.table[table_at(p.rot_units, i >> 3, 8 + (i & 7))] = __fmul_rn(s, __fmul_rn(p.scale, p.sign));
     }
     __syncwarp();
 }
 
-// One step of a warp's work: the heads of q or of k its groups take, and
-// where this lane's head begins.
-struct RopeStep {
-    bool is_k, active;
-    int head;
+// One lane's way through the steps of a work item in the tensors W: first
+// its heads of q, then those of k.  Everything but the addresses and `left`
+// is uniform over the warp.
+template <int... W>
+struct HeadWalk {
+    static constexpr int N = sizeof...(W);
+    const char* at[N];  // the lane's first column in its head of this step
+    int steps;          // left of the work item, this one included
+    int side_steps;     // left of q, or of k
+    int left;           // heads of this side from the lane's on; <= 0: none
+    bool is_k;
+    uint32_t b, s;
+
+    __device__ __forceinline__ int64_t token(const RopeArgs& p) const { return b * p.seq + s; }
+    __device__ __forceinline__ void side(const RopeArgs& p, const RopeSide& sd, int step, int per_step, int g,
+                                         int first_byte)
+    {
+        constexpr int which[N] = {W...};
+        const int head = step * per_step + g;
+        left = sd.heads - head;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const HeadsView& v = sd.t[which[i]];
+            at[i] = v.data + b * v.batch + s * v.seq + head * v.head + first_byte;
+        }
+    }
+    __device__ __forceinline__ void begin(const RopeArgs& p, uint32_t w, int per_step, int g, int first_byte)
+    {
+        const uint32_t token = p.warps_per_token == 1 ? w : w / static_cast<uint32_t>(p.warps_per_token);
+        const int first = static_cast<int>(w - token * static_cast<uint32_t>(p.warps_per_token)) * p.steps_per_warp;
+        b = token / static_cast<uint32_t>(p.seq);
+        s = token - b * static_cast<uint32_t>(p.seq);
+        const int all = p.q_steps + p.k_steps - first;
+        steps = all < p.steps_per_warp ? all : p.steps_per_warp;
+        side_steps = p.q_steps - first;
+        is_k = side_steps <= 0;
+        if (is_k)
+            side(p, p.k, -side_steps, per_step, g, first_byte);
+        else
+            side(p, p.q, first, per_step, g, first_byte);
+    }
+    __device__ __forceinline__ bool active() const { return left > 0; }
+    // On to the next step; false when this one was the work item's last.
+    __device__ __forceinline__ bool advance(const RopeArgs& p, int per_step, int g, int first_byte)
+    {
+        if (--steps == 0)
+            return false;
+        if (--side_steps == 0) {
+            is_k = true;
+            side(p, p.k, 0, per_step, g, first_byte);
+            return true;
+        }
+        constexpr int which[N] = {W...};
+        left -= per_step;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            at[i] += is_k ? p.k.t[which[i]].step : p.q.t[which[i]].step;
+        return true;
+    }
 };
 
-__device__ __forceinline__ RopeStep rope_step(const RopeArgs& p, int step, int group_in_warp)
+// 16 and 8 bytes from global to this lane's shared memory.
+__device__ __forceinline__ void copy_ahead16(uint32_t dst, const void* src)
 {
-    RopeStep r;
-    r.is_k = step >= p.q_steps;
-    r.head = (step - (r.is_k ? p.q_steps : 0)) * p.heads_per_step + group_in_warp;
-    r.active = r.head < (r.is_k ? p.k.heads : p.q.heads);
-    if (!r.active)
-        r.head = 0;
-    return r;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_ahead8(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_ahead_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_ahead_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ int64_t lds8(uint32_t at)
+{
+    int64_t v;
+    asm volatile("ld.shared.s64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
+    return v;
 }
 
-// The token and the steps of work item w of the call.
-struct RopeWork {
-    int64_t bi, si, position;
-    int first, last;
+// The copies ahead of the computation: the tensors W of the warp's work
+// items, step by step, into the lane's slots.  A run the lane's head does
+// not have is never copied (its slot keeps the zeros it starts with); a head
+// the step does not have leaves what was there, which nobody uses.
+template <int E, int... W>
+struct RopeAhead {
+    static constexpr int N = sizeof...(W);
+    using Ring = RopeRing<E, N>;
+    HeadWalk<W...> walk;
+    uint32_t w, warps, slot;
+    bool first;  // the walk stands at its work item's first step
+
+    __device__ __forceinline__ void begin(const RopeArgs& p, uint32_t ring, uint32_t w0, uint32_t n_warps,
+                                          int per_step, int g, int first_byte)
+    {
+        w = w0;
+        warps = n_warps;
+        slot = ring;
+        first = true;
+        if (w < p.n_work)
+            walk.begin(p, w, per_step, g, first_byte);
+    }
+    // Copies one step into the next slot, or nothing when no work is left.
+    // ring: the first slot, where the lane's 16-byte pieces begin.
+    __device__ __forceinline__ void issue(const RopeArgs& p, uint32_t ring, int lane, int per_step, int g,
+                                          int first_byte, int second, bool has_a, bool has_b)
+    {
+        if (w < p.n_work) {
+            if (walk.active()) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+#pragma unroll
+                    for (int v = 0; v < Ring::kVec; ++v) {
+                        const uint32_t dst = slot + (2 * i * Ring::kVec + v) * 512;
+                        if (has_a)
+                            copy_ahead16(dst, walk.at[i] + 16 * v);
+                        if (has_b)
+                            copy_ahead16(dst + Ring::kVec * 512, walk.at[i] + second + 16 * v);
+                    }
+                }
+            }
+            if (first && p.positions)
+                copy_ahead8(slot + Ring::kPosition - 8 * lane, p.positions + walk.token(p));
+            first = false;
+            if (!walk.advance(p, per_step, g, first_byte)) {
+                w += warps;
+                first = true;
+                if (w < p.n_work)
+                    walk.begin(p, w, per_step, g, first_byte);
+            }
+        }
+        copy_ahead_commit();
+        slot = Ring::after(slot, ring);
+    }
 };
 
-__device__ __forceinline__ RopeWork rope_work(const RopeArgs& p, uint32_t w)
+template <int E, int N>
+__device__ __forceinline__ void read_slot(uint32_t slot, int i, RawUnit<E, true>& r)
 {
-    RopeWork r;
-    const uint32_t token = w / static_cast<uint32_t>(p.warps_per_token);
-    const int part = static_cast<int>(w - token * static_cast<uint32_t>(p.warps_per_token));
-    const uint32_t b = token / static_cast<uint32_t>(p.seq);
-    r.bi = b;
-    r.si = token - b * static_cast<uint32_t>(p.seq);
-    r.position = p.positions ? __ldg(p.positions + token) : p.position0 + r.si;
-    r.first = part * p.steps_per_warp;
-    const int steps = p.q_steps + p.k_steps;
-    r.last = r.first + p.steps_per_warp < steps ? r.first + p.steps_per_warp : steps;
-    return r;
+    using Ring = RopeRing<E, N>;
+    const uint32_t at = slot + 2 * i * Ring::kVec * 512;
+    if constexpr (Ring::kVec == 1) {
+        r.a = lds16(at);
+        r.b = lds16(at + 512);
+    } else {
+        r.a.lo = lds16(at);
+        r.a.hi = lds16(at + 512);
+        r.b.lo = lds16(at + 1024);
+        r.b.hi = lds16(at + 1536);
+    }
+}
+
+template <typename Ring>
+__device__ __forceinline__ void clear_ring(unsigned char* ring, int lane)
+{
+    for (int i = lane; i < Ring::kSlots * Ring::kStepBytes / 16; i += 32)
+        reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncwarp();
+}
+
+// G: lanes per head, or 0 for p.group (element-wise kernels, which have
+// more to do than a butterfly's branches).
+template <int G>
+__device__ __forceinline__ float head_sum(float v, int group)
+{
+    return butterfly_sum(v, G ? G : group);
 }
 
 // Forward: plain (NORM false; also the inverse) or behind the norm
 //   z = (x * inv) * w, inv = 1 / sqrt(sum x^2 / dim + eps).
-template <int E, bool NORM, bool INTER, bool BLOCKS>
-__global__ void __launch_bounds__(kRopeThreads, E == kElemF32 || !BLOCKS ? 2 : 3) rope_fwd_kernel(const RopeArgs p)
+template <int E, bool NORM, bool INTER, int G>
+__global__ void __launch_bounds__(kRopeThreads, E == kElemF32 ? 3 : 4) rope_fwd_kernel(const RopeArgs p)
 {
+    constexpr bool BLOCKS = G != 0;
+    using T = typename Elem<E>::T;
+    using Ring = RopeRing<E, 1>;
     extern __shared__ __align__(16) unsigned char mem[];
+    const RopeShared sh = rope_shared<NORM>(p, mem, BLOCKS ? Ring::kBytes : 0);
+    const int lane = threadIdx.x & 31;
+    const int group = G ? G : p.group;
+    const int per_step = G ? 32 / (G ? G : 1) : p.heads_per_step;
+    const int u = lane & (group - 1);
+    const int g = lane / group;
+    const UnitColumns cols = unit_columns<INTER>(p, u);
+    const bool has_a = cols.na != 0, has_b = cols.nb != 0;
+    const int first_byte = cols.a * static_cast<int>(sizeof(T));
+    const int second = (cols.b - cols.a) * static_cast<int>(sizeof(T));
+    const uint32_t warps = gridDim.x * (kRopeThreads / 32);
+    uint32_t w = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t ring = smem_u32(sh.ring) + lane * 16;
     wait_prior_grids();
     allow_next_grid();
-    const RopeShared sh = rope_prologue<E, NORM, INTER>(p, mem);
-    const int lane = threadIdx.x & 31;
-    const int u = lane & (p.group - 1);
-    const int g = lane / p.group;
-    const UnitColumns cols = unit_columns<INTER>(p, u);
-    const float* const turn = sh.table + (cols.pairs ? u : 0) * 16;
-    const float* const weight = sh.weights + (u < p.units ? u : 0) * 16;
-    const uint32_t warps = gridDim.x * (kRopeThreads / 32);
-    for (uint32_t w = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); w < p.n_work; w += warps) {
-        const RopeWork work = rope_work(p, w);
-        auto load = [&](int step, RawUnit<E, BLOCKS>& raw) {
-            const RopeStep st = rope_step(p, step, g);
-            const RopeSide& side = st.is_k ? p.k : p.q;
-            load_raw<E, BLOCKS>(side.in, work.bi * side.in_b + work.si * side.in_s + st.head * side.in_h, cols,
-                                st.active && step < work.last, raw);
-        };
-        RawUnit<E, BLOCKS> next0, next1;
-        load(work.first, next0);
-        load(work.first + 1, next1);
-        fill_angles(p, sh, work.position, lane);
-        for (int step = work.first; step < work.last; ++step) {
+    RopeAhead<E, kRopeIn> ahead;
+    if constexpr (BLOCKS) {
+        clear_ring<Ring>(sh.ring, lane);
+        ahead.begin(p, ring, w, warps, per_step, g, first_byte);
+#pragma unroll
+        for (int i = 0; i < Ring::kSlots - 1; ++i)
+            ahead.issue(p, ring, lane, per_step, g, first_byte, second, has_a, has_b);
+    }
+    rope_prologue<E, NORM, INTER>(p, sh);
+    const float* const turn = sh.table + (cols.pairs ? u : 0) * 4;
+    const float* const weight = sh.weights + (u < p.units ? u : 0) * 4;
+    const bool rest = cols.pairs == 0;
+    const bool skip_q = rest && p.q.skip_rest, skip_k = rest && p.k.skip_rest;
+    uint32_t slot = ring;
+    for (; w < p.n_work; w += warps) {
+        // out, and x where it is not copied ahead
+        HeadWalk<kRopeOut, kRopeIn> walk;
+        walk.begin(p, w, per_step, g, first_byte);
+        bool fresh = true;
+        do {
+            if constexpr (BLOCKS) {
+                ahead.issue(p, ring, lane, per_step, g, first_byte, second, has_a, has_b);
+                copy_ahead_wait<Ring::kSlots - 1>();
+            }
+            if (fresh) {
+                int64_t position = p.position0 + walk.s;
+                if (p.positions)
+                    position = BLOCKS ? lds8(slot + Ring::kPosition - 8 * lane) : __ldg(p.positions + walk.token(p));
+                fill_angles(p, sh, position, lane);
+                fresh = false;
+            }
+            const float eps = walk.is_k ? p.k.eps : p.q.eps;
+            const float* const w_side = weight + (walk.is_k ? p.units * 16 : 0);
+            const bool skip = walk.is_k ? skip_k : skip_q;
+            const bool active = walk.active();
+            RawUnit<E, BLOCKS> x;
+            if constexpr (BLOCKS)
+                read_slot<E, 1>(slot, 0, x);
+            else
+                load_elements<E>(walk.at[1], second, cols, active, x);
             float a[8], b[8];
-            widen_unit<E, BLOCKS>(next0, a, b);
-            next0 = next1;
-            load(step + 2, next1);
-            const RopeStep st = rope_step(p, step, g);
-            const RopeSide& side = st.is_k ? p.k : p.q;
+            widen_unit<E, BLOCKS>(x, a, b);
             if constexpr (NORM) {
-                float sq = __fadd_rn(fold8_squares(a), fold8_squares(b));
-                sq = butterfly_sum(sq, p.group);
-                const float inv = inv_rms(sq, p.dim, p.inv_dim, side.eps);
+                const float sq = head_sum<G>(unit_dot(a, b, a, b), group);
+                const float inv = inv_sqrt(__fadd_rn(head_mean(p, sq), eps));
                 float wa[8], wb[8];
-                load_shared16(weight + (st.is_k ? p.units * 16 : 0), wa, wb);
+                load_table(w_side, p.units, wa, wb);
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
                     mul2_rn(a[e], a[e + 1], inv, inv, a[e], a[e + 1]);
@@ -346,14 +582,11 @@ __global__ void __launch_bounds__(kRopeThreads, E == kElemF32 || !BLOCKS ? 2 : 3
                     mul2_rn(b[e], b[e + 1], wb[e], wb[e + 1], b[e], b[e + 1]);
                 }
             }
-            if (cols.pairs)
-                turn_unit<INTER>(turn, cols.pairs, a, b);
-            UnitColumns c = cols;
-            if (!st.active || (side.skip_rest && cols.pairs == 0))
-                c.na = c.nb = 0;
-            store_unit<E, BLOCKS>(side.out, work.bi * side.out_b + work.si * side.out_s + st.head * side.out_h, c, a,
-                                  b);
-        }
+            if (!rest)
+                turn_unit<INTER>(turn, p.rot_units, cols.pairs, a, b);
+            store_unit<E, BLOCKS>(walk.at[0], second, cols, active && !skip, a, b);
+            slot = Ring::after(slot, ring);
+        } while (walk.advance(p, per_step, g, first_byte));
     }
 }
 
@@ -363,90 +596,115 @@ __global__ void __launch_bounds__(kRopeThreads, E == kElemF32 || !BLOCKS ? 2 : 3
 // Every lane adds the shares of its warp's work in order in registers; at
 // the end a warp's groups are added by butterfly and the CTA's warps in
 // order into the CTA's part.
-template <int E, bool INTER, bool BLOCKS>
+template <int E, bool INTER, int G>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArgs p)
 {
+    constexpr bool BLOCKS = G != 0;
+    using T = typename Elem<E>::T;
+    using Ring = RopeRing<E, 2>;
     extern __shared__ __align__(16) unsigned char mem[];
+    const RopeShared sh = rope_shared<true>(p, mem, BLOCKS ? Ring::kBytes : 0);
+    const int lane = threadIdx.x & 31;
+    const int group = G ? G : p.group;
+    const int per_step = G ? 32 / (G ? G : 1) : p.heads_per_step;
+    const int u = lane & (group - 1);
+    const int g = lane / group;
+    const UnitColumns cols = unit_columns<INTER>(p, u);
+    const bool has_a = cols.na != 0, has_b = cols.nb != 0;
+    const int first_byte = cols.a * static_cast<int>(sizeof(T));
+    const int second = (cols.b - cols.a) * static_cast<int>(sizeof(T));
+    const uint32_t warps = gridDim.x * (kRopeThreads / 32);
+    uint32_t w = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t ring = smem_u32(sh.ring) + lane * 16;
     wait_prior_grids();
     allow_next_grid();
-    const RopeShared sh = rope_prologue<E, true, INTER>(p, mem);
-    const int lane = threadIdx.x & 31;
-    const int u = lane & (p.group - 1);
-    const int g = lane / p.group;
-    const UnitColumns cols = unit_columns<INTER>(p, u);
-    const float* const turn = sh.table + (cols.pairs ? u : 0) * 16;
-    const float* const weight = sh.weights + (u < p.units ? u : 0) * 16;
+    RopeAhead<E, kRopeIn, kRopeGrad> ahead;
+    if constexpr (BLOCKS) {
+        clear_ring<Ring>(sh.ring, lane);
+        ahead.begin(p, ring, w, warps, per_step, g, first_byte);
+#pragma unroll
+        for (int i = 0; i < Ring::kSlots - 1; ++i)
+            ahead.issue(p, ring, lane, per_step, g, first_byte, second, has_a, has_b);
+    }
+    rope_prologue<E, true, INTER>(p, sh);
+    const float* const turn = sh.table + (cols.pairs ? u : 0) * 4;
+    const float* const weight = sh.weights + (u < p.units ? u : 0) * 4;
     float dq[2][8] = {}, dk[2][8] = {};
-    const uint32_t warps = gridDim.x * (kRopeThreads / 32);
-    for (uint32_t w = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); w < p.n_work; w += warps) {
-        const RopeWork work = rope_work(p, w);
-        auto load = [&](int step, RawUnit<E, BLOCKS>& x, RawUnit<E, BLOCKS>& dy) {
-            const RopeStep st = rope_step(p, step, g);
-            const RopeSide& side = st.is_k ? p.k : p.q;
-            const bool active = st.active && step < work.last;
-            load_raw<E, BLOCKS>(side.in, work.bi * side.in_b + work.si * side.in_s + st.head * side.in_h, cols, active,
-                                x);
-            load_raw<E, BLOCKS>(side.grad, work.bi * side.grad_b + work.si * side.grad_s + st.head * side.grad_h, cols,
-                                active, dy);
-        };
-        RawUnit<E, BLOCKS> next_x, next_dy;
-        load(work.first, next_x, next_dy);
-        fill_angles(p, sh, work.position, lane);
-        for (int step = work.first; step < work.last; ++step) {
-            const RopeStep st = rope_step(p, step, g);
-            const RopeSide& side = st.is_k ? p.k : p.q;
-            float a[8], b[8], ga[8], gb[8], wa[8], wb[8], ta[8], tb[8];
-            widen_unit<E, BLOCKS>(next_x, a, b);
-            widen_unit<E, BLOCKS>(next_dy, ga, gb);
-            load(step + 1, next_x, next_dy);
+    uint32_t slot = ring;
+    for (; w < p.n_work; w += warps) {
+        HeadWalk<kRopeOut, kRopeIn, kRopeGrad> walk;
+        walk.begin(p, w, per_step, g, first_byte);
+        bool fresh = true;
+        do {
+            if constexpr (BLOCKS) {
+                ahead.issue(p, ring, lane, per_step, g, first_byte, second, has_a, has_b);
+                copy_ahead_wait<Ring::kSlots - 1>();
+            }
+            if (fresh) {
+                int64_t position = p.position0 + walk.s;
+                if (p.positions)
+                    position = BLOCKS ? lds8(slot + Ring::kPosition - 8 * lane) : __ldg(p.positions + walk.token(p));
+                fill_angles(p, sh, position, lane);
+                fresh = false;
+            }
+            const float eps = walk.is_k ? p.k.eps : p.q.eps;
+            const float* const w_side = weight + (walk.is_k ? p.units * 16 : 0);
+            const bool active = walk.active();
+            RawUnit<E, BLOCKS> x, dy;
+            if constexpr (BLOCKS) {
+                read_slot<E, 2>(slot, 0, x);
+                read_slot<E, 2>(slot, 1, dy);
+            } else {
+                load_elements<E>(walk.at[1], second, cols, active, x);
+                load_elements<E>(walk.at[2], second, cols, active, dy);
+            }
+            float a[8], b[8], ga[8], gb[8], wa[8], wb[8];
+            widen_unit<E, BLOCKS>(x, a, b);
+            widen_unit<E, BLOCKS>(dy, ga, gb);
             if (cols.pairs)
-                turn_unit<INTER>(turn, cols.pairs, ga, gb);
-            load_shared16(weight + (st.is_k ? p.units * 16 : 0), wa, wb);
+                turn_unit<INTER>(turn, p.rot_units, cols.pairs, ga, gb);
+            load_table(w_side, p.units, wa, wb);
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 mul2_rn(ga[e], ga[e + 1], wa[e], wa[e + 1], wa[e], wa[e + 1]);
                 mul2_rn(gb[e], gb[e + 1], wb[e], wb[e + 1], wb[e], wb[e + 1]);
-                mul2_rn(wa[e], wa[e + 1], a[e], a[e + 1], ta[e], ta[e + 1]);
-                mul2_rn(wb[e], wb[e + 1], b[e], b[e + 1], tb[e], tb[e + 1]);
             }
-            const float s1 = butterfly_sum(__fadd_rn(fold8_squares(a), fold8_squares(b)), p.group);
-            const float s2 = butterfly_sum(__fadd_rn(fold8(ta), fold8(tb)), p.group);
-            const float inv = inv_rms(s1, p.dim, p.inv_dim, side.eps);
-            const float mean =
-                p.inv_dim != 0.0f ? __fmul_rn(s2, p.inv_dim) : __fdiv_rn(s2, static_cast<float>(p.dim));
-            const float k = -__fmul_rn(inv, __fmul_rn(inv, mean));
-            if (st.active) {
-                float xa[8], xb[8];
+            const float s1 = head_sum<G>(unit_dot(a, b, a, b), group);
+            const float s2 = head_sum<G>(unit_dot(a, b, wa, wb), group);
+            const float inv = inv_sqrt(__fadd_rn(head_mean(p, s1), eps));
+            const float c = -__fmul_rn(inv, __fmul_rn(inv, head_mean(p, s2)));
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    mul2_rn(a[e], a[e + 1], inv, inv, xa[e], xa[e + 1]);
-                    mul2_rn(b[e], b[e + 1], inv, inv, xb[e], xb[e + 1]);
-                    fma2_rn(a[e], a[e + 1], k, k, wa[e], wa[e + 1], ta[e], ta[e + 1]);
-                    fma2_rn(b[e], b[e + 1], k, k, wb[e], wb[e + 1], tb[e], tb[e + 1]);
-                    mul2_rn(ta[e], ta[e + 1], inv, inv, ta[e], ta[e + 1]);
-                    mul2_rn(tb[e], tb[e + 1], inv, inv, tb[e], tb[e + 1]);
-                }
-                if (st.is_k) {
+            for (int e = 0; e < 8; e += 2) {
+                fma2_rn(a[e], a[e + 1], c, c, wa[e], wa[e + 1], wa[e], wa[e + 1]);
+                fma2_rn(b[e], b[e + 1], c, c, wb[e], wb[e + 1], wb[e], wb[e + 1]);
+                mul2_rn(wa[e], wa[e + 1], inv, inv, wa[e], wa[e + 1]);
+                mul2_rn(wb[e], wb[e + 1], inv, inv, wb[e], wb[e + 1]);
+                mul2_rn(a[e], a[e + 1], inv, inv, a[e], a[e + 1]);
+                mul2_rn(b[e], b[e + 1], inv, inv, b[e], b[e + 1]);
+            }
+            if (active) {  // a lane without a head adds nothing
+                if (walk.is_k) {
 #pragma unroll
                     for (int e = 0; e < 8; e += 2) {
-                        fma2_rn(ga[e], ga[e + 1], xa[e], xa[e + 1], dk[0][e], dk[0][e + 1], dk[0][e], dk[0][e + 1]);
-                        fma2_rn(gb[e], gb[e + 1], xb[e], xb[e + 1], dk[1][e], dk[1][e + 1], dk[1][e], dk[1][e + 1]);
+                        fma2_rn(ga[e], ga[e + 1], a[e], a[e + 1], dk[0][e], dk[0][e + 1], dk[0][e], dk[0][e + 1]);
+                        fma2_rn(gb[e], gb[e + 1], b[e], b[e + 1], dk[1][e], dk[1][e + 1], dk[1][e], dk[1][e + 1]);
                     }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; e += 2) {
-                        fma2_rn(ga[e], ga[e + 1], xa[e], xa[e + 1], dq[0][e], dq[0][e + 1], dq[0][e], dq[0][e + 1]);
-                        fma2_rn(gb[e], gb[e + 1], xb[e], xb[e + 1], dq[1][e], dq[1][e + 1], dq[1][e], dq[1][e + 1]);
+                        fma2_rn(ga[e], ga[e + 1], a[e], a[e + 1], dq[0][e], dq[0][e + 1], dq[0][e], dq[0][e + 1]);
+                        fma2_rn(gb[e], gb[e + 1], b[e], b[e + 1], dq[1][e], dq[1][e + 1], dq[1][e], dq[1][e + 1]);
                     }
                 }
-                store_unit<E, BLOCKS>(side.out, work.bi * side.out_b + work.si * side.out_s + st.head * side.out_h,
-                                      cols, ta, tb);
             }
-        }
+            store_unit<E, BLOCKS>(walk.at[0], second, cols, active, wa, wb);
+            slot = Ring::after(slot, ring);
+        } while (walk.advance(p, per_step, g, first_byte));
     }
     if (!p.partials)
         return;
     // warp sums [warp][side][unit][16] over the memory used so far
+    copy_ahead_wait<0>();
     float* const sums = reinterpret_cast<float*>(mem);
     const int stride = 32 * p.units;
     __syncthreads();
@@ -456,7 +714,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArg
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             float v = side ? dk[e >> 3][e & 7] : dq[e >> 3][e & 7];
-            for (int d = p.group; d < 32; d <<= 1)
+            for (int d = group; d < 32; d <<= 1)
                 v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
             if (g == 0 && u < p.units)
                 at[e] = v;
@@ -469,38 +727,69 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArg
         const int r = i - side * 16 * p.units;
         const UnitColumns c = unit_columns<INTER>(p, r >> 4);
         const int e = r & 7;
-        const bool second = (r & 8) != 0;
-        if (e >= (second ? c.nb : c.na))
+        const bool upper = (r & 8) != 0;
+        if (e >= (upper ? c.nb : c.na))
             continue;
         float v = sums[i];
 #pragma unroll
         for (int k = 1; k < kRopeThreads / 32; ++k)
             v = __fadd_rn(v, sums[k * stride + i]);
-        part[side * p.dim + (second ? c.b : c.a) + e] = v;
+        part[side * p.dim + (upper ? c.b : c.a) + e] = v;
     }
 }
 
-template <int E, bool INTER, bool BLOCKS>
+// ------------------------------------------------------------------- launch
+template <typename F>
+cudaError_t launch_rope_kernel(F fn, const RopeArgs& p, int grid, size_t smem, cudaStream_t stream)
+{
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(smem));
+        if (e != cudaSuccess)
+            return e;
+    }
+    return launch(fn, grid, kRopeThreads, smem, false, stream, p);
+}
+
+template <int E, bool INTER, int G>
 cudaError_t launch_rope_as(const RopeArgs& p, int mode, int grid, cudaStream_t stream)
 {
+    constexpr bool BLOCKS = G != 0;
     const bool norm = mode != kRopePlain;
-    size_t smem = static_cast<size_t>(p.rot_units) * 64 * (1 + kRopeThreads / 32) + (norm ? p.units * 128 : 0);
-    const size_t sums = static_cast<size_t>(p.units) * 128 * (kRopeThreads / 32);
-    if (mode == kRopeNormBwd)
-        return launch(rope_bwd_kernel<E, INTER, BLOCKS>, grid, kRopeThreads, smem > sums ? smem : sums, false, stream,
-                      p);
-    return norm ? launch(rope_fwd_kernel<E, true, INTER, BLOCKS>, grid, kRopeThreads, smem, false, stream, p)
-                : launch(rope_fwd_kernel<E, false, INTER, BLOCKS>, grid, kRopeThreads, smem, false, stream, p);
+    const size_t tables = static_cast<size_t>(p.rot_units) * 64 * (1 + kRopeThreads / 32) + (norm ? p.units * 128 : 0);
+    if (mode == kRopeNormBwd) {
+        const size_t all = tables + (BLOCKS ? RopeRing<E, 2>::kBytes : 0);
+        const size_t sums = static_cast<size_t>(p.units) * 128 * (kRopeThreads / 32);
+        return launch_rope_kernel(rope_bwd_kernel<E, INTER, G>, p, grid, all > sums ? all : sums, stream);
+    }
+    const size_t all = tables + (BLOCKS ? RopeRing<E, 1>::kBytes : 0);
+    return norm ? launch_rope_kernel(rope_fwd_kernel<E, true, INTER, G>, p, grid, all, stream)
+                : launch_rope_kernel(rope_fwd_kernel<E, false, INTER, G>, p, grid, all, stream);
+}
+
+template <int E, bool INTER>
+cudaError_t launch_rope_layout(const RopeArgs& p, int mode, bool blocks, int grid, cudaStream_t stream)
+{
+    if (!blocks)
+        return launch_rope_as<E, INTER, 0>(p, mode, grid, stream);
+    switch (p.group) {
+    case 4:
+        return launch_rope_as<E, INTER, 4>(p, mode, grid, stream);
+    case 8:
+        return launch_rope_as<E, INTER, 8>(p, mode, grid, stream);
+    case 16:
+        return launch_rope_as<E, INTER, 16>(p, mode, grid, stream);
+    default:
+        return launch_rope_as<E, INTER, 32>(p, mode, grid, stream);
+    }
 }
 
 template <int E>
 cudaError_t launch_rope_of(const RopeArgs& p, int mode, bool interleaved, bool blocks, int grid, cudaStream_t stream)
 {
-    if (interleaved)
-        return blocks ? launch_rope_as<E, true, true>(p, mode, grid, stream)
-                      : launch_rope_as<E, true, false>(p, mode, grid, stream);
-    return blocks ? launch_rope_as<E, false, true>(p, mode, grid, stream)
-                  : launch_rope_as<E, false, false>(p, mode, grid, stream);
+    return interleaved ? launch_rope_layout<E, true>(p, mode, blocks, grid, stream)
+                       : launch_rope_layout<E, false>(p, mode, blocks, grid, stream);
 }
 
 }  // namespace dradd

@@ -246,7 +246,7 @@ dradd_status rope_shape(const dradd_rope* r, int dtype, RopeArgs* a, bool backwa
     a->seq = r->seq;
     a->dim = static_cast<int>(r->head_dim);
     a->rot = static_cast<int>(r->rot_dim);
-    a->inv_dim = inverse_if_pow2(r->head_dim);
+    a->inv_dim = 1.0f / static_cast<float>(r->head_dim);
     a->q.heads = static_cast<int>(r->q_heads);
     a->k.heads = static_cast<int>(r->k_heads);
     a->inv_freq = r->inv_freq;
@@ -334,22 +334,18 @@ dradd_status rope_check(const dradd_rope& r, const RopeSideArgs (&sides)[2], boo
     return check_views(outs, n_out, ins, n_in);
 }
 
-void fill_side(RopeSide* s, const RopeSideArgs& t, float eps)
+HeadsView heads_bytes(const dradd_heads& t, int64_t eb, int per_step)
 {
-    s->out = t.out->data;
-    s->out_b = t.out->batch_stride;
-    s->out_s = t.out->seq_stride;
-    s->out_h = t.out->head_stride;
-    s->in = t.in->data;
-    s->in_b = t.in->batch_stride;
-    s->in_s = t.in->seq_stride;
-    s->in_h = t.in->head_stride;
-    if (t.grad) {
-        s->grad = t.grad->data;
-        s->grad_b = t.grad->batch_stride;
-        s->grad_s = t.grad->seq_stride;
-        s->grad_h = t.grad->head_stride;
-    }
+    return {static_cast<char*>(t.data), t.batch_stride * eb, t.seq_stride * eb, t.head_stride * eb,
+            t.head_stride * eb * per_step};
+}
+
+void fill_side(RopeSide* s, const RopeSideArgs& t, float eps, int64_t eb, int per_step)
+{
+    s->t[kRopeIn] = heads_bytes(*t.in, eb, per_step);
+    s->t[kRopeOut] = heads_bytes(*t.out, eb, per_step);
+    if (t.grad)
+        s->t[kRopeGrad] = heads_bytes(*t.grad, eb, per_step);
     s->weight = t.weight;
     s->eps = eps;
 }
@@ -373,12 +369,12 @@ dradd_status run_rope(const dradd_heads* q_out, const dradd_heads* k_out, const 
     if (st != DRADD_OK)
         return st;
     a.sign = sign;
-    fill_side(&a.q, sides[0], q_eps);
+    fill_side(&a.q, sides[0], q_eps, elem_bytes(dtype), a.heads_per_step);
     if (r->k_heads > 0)
-        fill_side(&a.k, sides[1], k_eps);
+        fill_side(&a.k, sides[1], k_eps, elem_bytes(dtype), a.heads_per_step);
     if (!norm) {
-        a.q.skip_rest = a.q.out == a.q.in;
-        a.k.skip_rest = a.k.out == a.k.in;
+        a.q.skip_rest = a.q.t[kRopeOut].data == a.q.t[kRopeIn].data;
+        a.k.skip_rest = a.k.t[kRopeOut].data == a.k.t[kRopeIn].data;
     }
     return launch_rope(a, norm ? kRopeNorm : kRopePlain, dtype, r->interleaved != 0, blocks, grid, stream) ==
                    cudaSuccess
@@ -533,9 +529,9 @@ dradd_status qk_rmsnorm_rope_bwd(const dradd_heads* dq, const dradd_heads* dk, f
     if (st != DRADD_OK)
         return st;
     a.sign = -1.0f;
-    fill_side(&a.q, sides[0], q_eps);
+    fill_side(&a.q, sides[0], q_eps, elem_bytes(dtype), a.heads_per_step);
     if (has_k)
-        fill_side(&a.k, sides[1], k_eps);
+        fill_side(&a.k, sides[1], k_eps, elem_bytes(dtype), a.heads_per_step);
     a.partials = sums ? static_cast<float*>(workspace) : nullptr;
     if (launch_rope(a, kRopeNormBwd, dtype, rope->interleaved != 0, blocks, grid, stream) != cudaSuccess)
         return DRADD_ERR_CUDA;

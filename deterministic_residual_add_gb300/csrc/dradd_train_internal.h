@@ -81,15 +81,19 @@ cudaError_t launch_column_sums(const float* partials, int parts, int cols, float
                                cudaStream_t stream);
 
 // ------------------------------------------------------------------- rotary
-// One of q and k.  Strides in elements (batch, sequence, head).
+// Tensors of heads: element (b, s, head, 0) at data + b * batch + s * seq +
+// head * head_stride, in bytes; step: from a lane's head to its next one.
+struct HeadsView {
+    char* data;
+    int64_t batch, seq, head, step;
+};
+
+enum RopeTensor : int { kRopeIn = 0, kRopeGrad = 1, kRopeOut = 2 };
+
+// One of q and k: x, the gradient's dy, and what is written.
 struct RopeSide {
-    void* out;
-    const void* in;        // forward: x; gradient of the fused call: x
-    const void* grad;      // gradient of the fused call: dy
-    const void* weight;    // fused call
-    int64_t out_b, out_s, out_h;
-    int64_t in_b, in_s, in_h;
-    int64_t grad_b, grad_s, grad_h;
+    HeadsView t[3];
+    const void* weight;  // behind the norm
     int heads;
     float eps;
     int skip_rest;  // in place without a norm: the columns past rot_dim stay
@@ -103,8 +107,8 @@ struct RopeArgs {
     int64_t tokens;  // batch * seq, below 2^31
     int64_t seq;
     int dim, rot;
-    int rot_units, units, group;  // 16-element units that rotate, in all; lanes per head (a power of two)
-    float inv_dim;                // 1 / dim if a power of two, else 0
+    int rot_units, units, group;  // 16-element units that rotate, in all; lanes per head (4, 8, 16 or 32)
+    float inv_dim;                // 1 / dim
     float scale;
     float sign;                   // +1, or -1 for the inverse rotation
     // A step is the heads of q or of k that a warp takes at a time; a work

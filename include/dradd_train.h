@@ -187,7 +187,8 @@ dradd_status rope_bwd(const dradd_heads* dq, const dradd_heads* dk, const dradd_
  * qk_rmsnorm_rope_fwd -- RMSNorm of every head of q and k (weights
  * [head_dim], shared by the heads of one side), then the rotation, in one
  * pass with one rounding: z = (x * inv) * weight in fp32, out = turned z.
- * inv = 1 / sqrt(mean(x^2) + eps) over the head_dim columns.
+ * inv = 1 / sqrt(mean(x^2) + eps) over the head_dim columns, within a few
+ * fp32 roundings (not the correctly rounded one of dradd.h's rows).
  */
 dradd_status qk_rmsnorm_rope_fwd(const dradd_heads* q_out, const dradd_heads* k_out, const dradd_heads* q,
                                  const dradd_heads* k, const void* q_weight, const void* k_weight, float q_eps,
