@@ -8,9 +8,9 @@
 //
 // Backward from h = residual_out (the rounded sum is what a training step
 // keeps), with g = dout * w:
-//   S1 = sum h^2, S2 = sum g h, both in the canonical tree
-//   inv from S1; c = (inv * (inv * (S2 / hidden)))
-//   d = dresidual_out + inv * (g - h * c)
+//   S1 = sum h^2, S2 = sum g h, in a fixed order
+//   inv from S1; c = -inv * (inv * (S2 / hidden))
+//   d = dresidual_out + inv * (g + h * c)
 //   dresidual = E(d); dx = E(kept ? d scale : 0)
 //   dweight[i] = sum over rows of dout * (h * inv), in fp32: every CTA (part)
 //   adds its rows in order and a second kernel adds the parts in a fixed
@@ -34,7 +34,7 @@ namespace dradd {
 // ------------------------------------------------------------- block helpers
 // acc of one block; the residual sum is stored.
 template <int E>
-__device__ __forceinline__ void fwd_block(const DropNormArgs& a, const DropKey& key,
+__device__ __forceinline__ void fwd_block(const DropNormArgs& a, const uint2& offset,
                                           const typename Elem<E>::Block& xv, const typename Elem<E>::Block& rv,
                                           int64_t row, int b, float (&acc)[8])
 {
@@ -42,8 +42,8 @@ __device__ __forceinline__ void fwd_block(const DropNormArgs& a, const DropKey& 
     float r[8];
     Elem<E>::unpack(xv, acc);
     Elem<E>::unpack(rv, r);
-    if (key.threshold)
-        drop8(acc, key, static_cast<uint32_t>(b), static_cast<uint32_t>(row));
+    if (a.drop.drops)
+        drop8(acc, a.drop, offset, static_cast<uint32_t>(b), static_cast<uint32_t>(row));
 #pragma unroll
     for (int e = 0; e < 8; e += 2)
         add2_rn(acc[e], acc[e + 1], r[e], r[e + 1], acc[e], acc[e + 1]);
@@ -66,13 +66,8 @@ __device__ __forceinline__ void fwd_finish(const DropNormArgs& a, float (&acc)[8
     st_block_stream(static_cast<T*>(a.out) + row * a.hidden, b, Elem<E>::pack(acc));
 }
 
-// The block's parts of sum g h (as fold8_squares adds the squares).
-__device__ __forceinline__ float fold8_products(const float (&p)[8])
-{
-    return __fadd_rn(__fadd_rn(__fadd_rn(p[0], p[1]), __fadd_rn(p[2], p[3])),
-                     __fadd_rn(__fadd_rn(p[4], p[5]), __fadd_rn(p[6], p[7])));
-}
-
+// The block's parts of sum h^2 and sum g h (g = dout w): two chains of fused
+// multiply-adds each, two to an instruction, then their sum.
 template <int E>
 __device__ __forceinline__ void bwd_sums(const typename Elem<E>::Block& hv, const typename Elem<E>::Block& gv,
                                          const typename Elem<E>::Block& wv, float& s1, float& s2)
@@ -81,16 +76,24 @@ __device__ __forceinline__ void bwd_sums(const typename Elem<E>::Block& hv, cons
     Elem<E>::unpack(hv, h);
     Elem<E>::unpack(gv, g);
     Elem<E>::unpack(wv, w);
-    s1 = fold8_squares(h);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        g[e] = __fmul_rn(__fmul_rn(g[e], w[e]), h[e]);
-    s2 = fold8_products(g);
+    for (int e = 0; e < 8; e += 2)
+        mul2_rn(g[e], g[e + 1], w[e], w[e + 1], g[e], g[e + 1]);
+    float a0, a1, b0, b1;
+    mul2_rn(h[0], h[1], h[0], h[1], a0, a1);
+    mul2_rn(h[0], h[1], g[0], g[1], b0, b1);
+#pragma unroll
+    for (int e = 2; e < 8; e += 2) {
+        fma2_rn(h[e], h[e + 1], h[e], h[e + 1], a0, a1, a0, a1);
+        fma2_rn(h[e], h[e + 1], g[e], g[e + 1], b0, b1, b0, b1);
+    }
+    s1 = __fadd_rn(a0, a1);
+    s2 = __fadd_rn(b0, b1);
 }
 
 // The gradients of one block, and its rows' share of dweight.
 template <int E>
-__device__ __forceinline__ void bwd_finish(const DropNormArgs& a, const DropKey& key,
+__device__ __forceinline__ void bwd_finish(const DropNormArgs& a, const uint2& offset,
                                            const typename Elem<E>::Block& hv, const typename Elem<E>::Block& gv,
                                            const typename Elem<E>::Block& wv, const typename Elem<E>::Block& dv,
                                            float inv, float c, int64_t row, int b, float (&dw)[8])
@@ -102,25 +105,28 @@ __device__ __forceinline__ void bwd_finish(const DropNormArgs& a, const DropKey&
     Elem<E>::unpack(wv, w);
     Elem<E>::unpack(dv, d);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        dw[e] = __fmaf_rn(g[e], __fmul_rn(h[e], inv), dw[e]);
-        const float t = __fmaf_rn(-h[e], c, __fmul_rn(g[e], w[e]));
-        d[e] = __fmaf_rn(inv, t, d[e]);
+    for (int e = 0; e < 8; e += 2) {
+        float x0, x1;
+        mul2_rn(h[e], h[e + 1], inv, inv, x0, x1);
+        fma2_rn(g[e], g[e + 1], x0, x1, dw[e], dw[e + 1], dw[e], dw[e + 1]);
+        mul2_rn(g[e], g[e + 1], w[e], w[e + 1], g[e], g[e + 1]);
+        fma2_rn(h[e], h[e + 1], c, c, g[e], g[e + 1], g[e], g[e + 1]);
+        fma2_rn(g[e], g[e + 1], inv, inv, d[e], d[e + 1], d[e], d[e + 1]);
     }
     st_block_stream(static_cast<T*>(a.dresidual) + row * a.hidden, b, Elem<E>::pack(d));
     if (a.dx) {
-        if (key.threshold)
-            drop8(d, key, static_cast<uint32_t>(b), static_cast<uint32_t>(row));
+        if (a.drop.drops)
+            drop8(d, a.drop, offset, static_cast<uint32_t>(b), static_cast<uint32_t>(row));
         st_block_stream(static_cast<T*>(a.dx) + row * a.hidden, b, Elem<E>::pack(d));
     }
 }
 
-// c of the row: inv^2 S2 / hidden.
+// c of the row: -inv^2 S2 / hidden.
 __device__ __forceinline__ float bwd_coefficient(const DropNormArgs& a, float s2, float inv)
 {
     const float mean = a.inv_hidden != 0.0f ? __fmul_rn(s2, a.inv_hidden)
                                             : __fdiv_rn(s2, static_cast<float>(a.hidden));
-    return __fmul_rn(inv, __fmul_rn(inv, mean));
+    return -__fmul_rn(inv, __fmul_rn(inv, mean));
 }
 
 // ------------------------------------------------------------- narrow rows
@@ -137,7 +143,7 @@ __global__ void __launch_bounds__(kNarrowThreads) drop_norm_fwd_narrow(const Dro
     const int nblocks = a.hidden >> 3;
     wait_prior_grids();
     allow_next_grid();
-    const DropKey key = make_drop_key(a.drop);
+    const uint2 offset = drop_offset(a.drop);
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kNarrowThreads / L);
     const int64_t first = static_cast<int64_t>(blockIdx.x) * (kNarrowThreads / L) + threadIdx.x / L;
     // rows of one warp start together, so every lane of it makes the same
@@ -162,7 +168,7 @@ __global__ void __launch_bounds__(kNarrowThreads) drop_norm_fwd_narrow(const Dro
             const int b = t + j * L;
             part[j] = 0.0f;
             if (active && b < nblocks) {
-                fwd_block<E>(a, key, xv[j], rv[j], row, b, acc[j]);
+                fwd_block<E>(a, offset, xv[j], rv[j], row, b, acc[j]);
                 part[j] = fold8_squares(acc[j]);
             }
             part[j] = butterfly_sum(part[j], L);
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(kNarrowThreads) drop_norm_bwd_narrow(const Dro
     const int nblocks = a.hidden >> 3;
     wait_prior_grids();
     allow_next_grid();
-    const DropKey key = make_drop_key(a.drop);
+    const uint2 offset = drop_offset(a.drop);
     float dw[K][8] = {};
     const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kGroups + group;
@@ -225,7 +231,7 @@ __global__ void __launch_bounds__(kNarrowThreads) drop_norm_bwd_narrow(const Dro
         for (int j = 0; j < K; ++j) {
             const int b = t + j * L;
             if (active && b < nblocks)
-                bwd_finish<E>(a, key, hv[j], gv[j], wv[j], dv[j], inv, c, row, b, dw[j]);
+                bwd_finish<E>(a, offset, hv[j], gv[j], wv[j], dv[j], inv, c, row, b, dw[j]);
         }
     }
     if (!a.partials)
@@ -343,7 +349,7 @@ __global__ void __launch_bounds__(T, wide_min_blocks(T, K)) drop_norm_fwd_wide(c
                 ring.issue(s, blockIdx.x + s * stride);
         }
     }
-    const DropKey key = make_drop_key(a.drop);
+    const uint2 offset = drop_offset(a.drop);
     V wv[K];
 #pragma unroll
     for (int j = 0; j < K; ++j) {
@@ -373,7 +379,7 @@ __global__ void __launch_bounds__(T, wide_min_blocks(T, K)) drop_norm_fwd_wide(c
                 V xv, rv;
                 ld_block(xs, b, xv);
                 ld_block(rs, b, rv);
-                fwd_block<E>(a, key, xv, rv, row, b, acc[j]);
+                fwd_block<E>(a, offset, xv, rv, row, b, acc[j]);
                 part[j] = fold8_squares(acc[j]);
             }
         }
@@ -450,7 +456,7 @@ __global__ void __launch_bounds__(T, wide_min_blocks(T, K)) drop_norm_bwd_wide(c
                 ring.issue(s, blockIdx.x + s * stride);
         }
     }
-    const DropKey key = make_drop_key(a.drop);
+    const uint2 offset = drop_offset(a.drop);
     const X* wrow = static_cast<const X*>(a.weight);
     float dw[K][8] = {};
     int s = 0, buf = 0;
@@ -521,7 +527,7 @@ __global__ void __launch_bounds__(T, wide_min_blocks(T, K)) drop_norm_bwd_wide(c
                 ld_block(wrow, b, wv);
                 if (a.dresidual_out)
                     ld_block(ds, b, dv);
-                bwd_finish<E>(a, key, hv, gv, wv, dv, inv, c, row, b, dw[j]);
+                bwd_finish<E>(a, offset, hv, gv, wv, dv, inv, c, row, b, dw[j]);
             }
         }
         buf ^= 1;

@@ -28,12 +28,8 @@ dradd_status drop_params(const dradd_dropout* d, DropParams* out)
     if (d->step && !aligned(d->step, 8))
         return DRADD_ERR_MISALIGNED;
     const uint32_t t = static_cast<uint32_t>(std::nearbyint(static_cast<double>(d->p) * 65536.0));
-    out->seed_lo = static_cast<uint32_t>(d->seed);
-    out->seed_hi = static_cast<uint32_t>(d->seed >> 32);
-    out->offset = d->offset;
-    out->step = d->step;
-    out->threshold = t;
-    out->scale = t < 65536 ? static_cast<float>(65536.0 / (65536.0 - t)) : 0.0f;
+    *out = make_drop_params(d->seed, d->offset, d->step, t,
+                            t < 65536 ? static_cast<float>(65536.0 / (65536.0 - t)) : 0.0f);
     return DRADD_OK;
 }
 
@@ -59,7 +55,7 @@ dradd_status run_dropout(void* out, int64_t out_stride, const void* x, int64_t x
     dradd_status st = drop_params(drop, &a.drop);
     if (st != DRADD_OK)
         return st;
-    if (n_rows < 0 || n_rows > 0xFFFFFFFFll || hidden <= 0 || hidden > 0x7FFFFFFFll)
+    if (n_rows < 0 || n_rows > 0x7FFFFFFFll || hidden <= 0 || hidden > 0x7FFFFFFFll)
         return DRADD_ERR_BAD_SHAPE;
     if (n_rows == 0)
         return DRADD_OK;
@@ -102,7 +98,7 @@ dradd_status run_dropout(void* out, int64_t out_stride, const void* x, int64_t x
 // ------------------------------------- dropout + residual add + RMSNorm
 dradd_status norm_shape(int64_t n_rows, int64_t hidden)
 {
-    if (n_rows < 0 || n_rows > 0xFFFFFFFFll || hidden <= 0)
+    if (n_rows < 0 || n_rows > 0x7FFFFFFFll || hidden <= 0)
         return DRADD_ERR_BAD_SHAPE;
     if (hidden % 8 != 0 || hidden > DRADD_MAX_HIDDEN)
         return DRADD_ERR_UNSUPPORTED_HIDDEN;

@@ -67,9 +67,9 @@ typedef struct dradd_dropout {
  * dropout_fwd -- out = dropout(x), n_rows x hidden with row strides in
  * elements (unit column stride).  It is its own gradient: dx = dropout(dy)
  * with the same mask.
- *   1 <= hidden < 2^31 (any, multiple of 8 or not), n_rows < 2^32, strides >= hidden,
- *   pointers aligned to the element.  Rows of whole 16-byte vectors (hidden
- *   % 8 == 0, 16-byte aligned rows) take the fast path.
+ *   1 <= hidden < 2^31 (a multiple of 8 or not), n_rows < 2^31, strides >=
+ *   hidden, pointers aligned to the element.  Rows of whole 16-byte vectors
+ *   (hidden % 8 == 0, 16-byte aligned rows) take the fast path.
  *   out may be exactly x.
  */
 dradd_status dropout_fwd(void* out, int64_t out_stride, const void* x, int64_t x_stride, int64_t n_rows,
@@ -91,7 +91,7 @@ dradd_status dropout_add_fwd(void* residual_out, int64_t out_stride, const void*
  *     out          = rne((acc * inv) * fp32(weight)),  inv as in dradd.h
  * With p = 0 and bf16 the results are add_rmsnorm_fwd's, bit for bit.
  * Tensors are contiguous, hidden a multiple of 8 up to DRADD_MAX_HIDDEN,
- * pointers 16-byte aligned, n_rows < 2^32.  out and residual_out may each be
+ * pointers 16-byte aligned, n_rows < 2^31.  out and residual_out may each be
  * exactly x or residual.
  */
 dradd_status dropout_add_rmsnorm_fwd(void* out, void* residual_out, const void* x, const void* residual,

@@ -70,7 +70,7 @@ def drop_add(L, out=A, os=64, x=B, xs=64, r=C, rs=64, n=4, h=64, p=0.1, dtype=0)
 
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=3), ARG), (dict(dtype=-1), ARG), (dict(p=-0.1), ARG), (dict(p=1.5), ARG), (dict(p=math.nan), ARG),
-    (dict(none=True), NULL), (dict(n=-1), SHAPE), (dict(n=1 << 32), SHAPE), (dict(h=0), SHAPE),
+    (dict(none=True), NULL), (dict(n=-1), SHAPE), (dict(n=1 << 31), SHAPE), (dict(h=0), SHAPE),
     (dict(h=1 << 31), SHAPE), (dict(xs=63), SHAPE), (dict(os=10), SHAPE), (dict(out=0), NULL), (dict(x=0), NULL),
     (dict(out=A + 1), ALIGN), (dict(x=B + 2, dtype=2), ALIGN), (dict(step=D + 4), ALIGN), (dict(n=0), OK),
     (dict(n=0, out=0, x=0), OK), (dict(out=B + 2), ALIAS), (dict(out=B + 128), ALIAS),
@@ -103,7 +103,7 @@ def bwd(L, dx=A, dres=B, dw=C, dout=D, dro=E, h_=F, w=G, eps=1e-6, n=4, h=1024, 
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(dtype=9), ARG), (dict(p=2.0), ARG), (dict(n=-1), SHAPE), (dict(n=1 << 32), SHAPE), (dict(h=0), SHAPE),
+    (dict(dtype=9), ARG), (dict(p=2.0), ARG), (dict(n=-1), SHAPE), (dict(n=1 << 31), SHAPE), (dict(h=0), SHAPE),
     (dict(h=1001), HIDDEN), (dict(h=32776), HIDDEN), (dict(eps=-1.0), EPS), (dict(eps=math.inf), EPS),
     (dict(n=0, out=0, x=0), OK), (dict(out=0), NULL), (dict(ro=0), NULL), (dict(x=0), NULL), (dict(r=0), NULL),
     (dict(w=0), NULL), (dict(out=A + 8), ALIGN), (dict(w=E + 2), ALIGN), (dict(out=B), ALIAS),
