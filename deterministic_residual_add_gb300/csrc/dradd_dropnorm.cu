@@ -30,19 +30,25 @@ DropNormPlan drop_norm_plan(int64_t n_rows, int hidden, int elem, bool backward,
         p.threads = 256;
         const int rows = p.threads / p.lanes;
         units = (n_rows + rows - 1) / rows;
-        per_sm = 4;
+        per_sm = 2;
+        p.smem = narrow_ring_bytes(elem, backward ? 3 : 2, p.K);
+        const size_t sums = static_cast<size_t>(P) * 4 * (p.threads / 32);
+        if (backward && p.smem < sums)
+            p.smem = sums;
     } else {
         p.K = P <= 2048 ? 1 : P <= 8192 ? 2 : P / 4096;
         p.threads = P / 8 / p.K;
         units = n_rows;
-        // As many CTAs per SM as leave each of them enough slots (the
-        // backward pass refills a slot one row later, so it wants one more).
+        // As many CTAs per SM as the registers allow (1024 threads, or 512
+        // for the kernels of 128 registers) and as leave each of them enough
+        // slots: two, or three where a slot is refilled a row later.
         const int64_t slot = static_cast<int64_t>(hidden) * (elem == kElemF32 ? 4 : 2) * (backward ? 3 : 2);
+        const int least = backward && p.K > 2 ? 3 : 2;
         int stages = 0;
-        for (per_sm = p.K <= 2 ? 1024 / p.threads : 1;; per_sm /= 2) {
+        for (per_sm = (p.K <= (backward ? 1 : 2) ? 1024 : 512) / p.threads;; per_sm /= 2) {
             const int64_t room = kSmemPerSm / per_sm - 4096;  // less the system's share and the kernel's own
             stages = static_cast<int>(room / slot);
-            if (stages >= (backward ? 3 : 2) || per_sm == 1)
+            if (stages >= least || per_sm == 1)
                 break;
         }
         if (stages > kMaxStages)

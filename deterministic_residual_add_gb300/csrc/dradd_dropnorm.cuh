@@ -66,19 +66,17 @@ __device__ __forceinline__ void fwd_finish(const DropNormArgs& a, float (&acc)[8
     st_block_stream(static_cast<T*>(a.out) + row * a.hidden, b, Elem<E>::pack(acc));
 }
 
-// The block's parts of sum h^2 and sum g h (g = dout w): two chains of fused
+// The block's parts of sum h^2 and sum (dout w) h: two chains of fused
 // multiply-adds each, two to an instruction, then their sum.
 template <int E>
-__device__ __forceinline__ void bwd_sums(const typename Elem<E>::Block& hv, const typename Elem<E>::Block& gv,
+__device__ __forceinline__ void bwd_sums(const float (&h)[8], const float (&dout)[8],
                                          const typename Elem<E>::Block& wv, float& s1, float& s2)
 {
-    float h[8], g[8], w[8];
-    Elem<E>::unpack(hv, h);
-    Elem<E>::unpack(gv, g);
-    Elem<E>::unpack(wv, w);
+    float g[8];
+    Elem<E>::unpack(wv, g);
 #pragma unroll
     for (int e = 0; e < 8; e += 2)
-        mul2_rn(g[e], g[e + 1], w[e], w[e + 1], g[e], g[e + 1]);
+        mul2_rn(dout[e], dout[e + 1], g[e], g[e + 1], g[e], g[e + 1]);
     float a0, a1, b0, b1;
     mul2_rn(h[0], h[1], h[0], h[1], a0, a1);
     mul2_rn(h[0], h[1], g[0], g[1], b0, b1);
@@ -91,17 +89,25 @@ __device__ __forceinline__ void bwd_sums(const typename Elem<E>::Block& hv, cons
     s2 = __fadd_rn(b0, b1);
 }
 
-// The gradients of one block, and its rows' share of dweight.
 template <int E>
-__device__ __forceinline__ void bwd_finish(const DropNormArgs& a, const uint2& offset,
-                                           const typename Elem<E>::Block& hv, const typename Elem<E>::Block& gv,
-                                           const typename Elem<E>::Block& wv, const typename Elem<E>::Block& dv,
-                                           float inv, float c, int64_t row, int b, float (&dw)[8])
+__device__ __forceinline__ void bwd_sums(const typename Elem<E>::Block& hv, const typename Elem<E>::Block& gv,
+                                         const typename Elem<E>::Block& wv, float& s1, float& s2)
 {
-    using T = typename Elem<E>::T;
-    float h[8], g[8], w[8], d[8];
+    float h[8], g[8];
     Elem<E>::unpack(hv, h);
     Elem<E>::unpack(gv, g);
+    bwd_sums<E>(h, g, wv, s1, s2);
+}
+
+// The gradients of one block, and its rows' share of dweight (g: dout).
+template <int E>
+__device__ __forceinline__ void bwd_finish(const DropNormArgs& a, const uint2& offset, const float (&h)[8],
+                                           const float (&g)[8], const typename Elem<E>::Block& wv,
+                                           const typename Elem<E>::Block& dv, float inv, float c, int64_t row, int b,
+                                           float (&dw)[8])
+{
+    using T = typename Elem<E>::T;
+    float w[8], d[8];
     Elem<E>::unpack(wv, w);
     Elem<E>::unpack(dv, d);
 #pragma unroll
@@ -109,9 +115,9 @@ __device__ __forceinline__ void bwd_finish(const DropNormArgs& a, const uint2& o
         float x0, x1;
         mul2_rn(h[e], h[e + 1], inv, inv, x0, x1);
         fma2_rn(g[e], g[e + 1], x0, x1, dw[e], dw[e + 1], dw[e], dw[e + 1]);
-        mul2_rn(g[e], g[e + 1], w[e], w[e + 1], g[e], g[e + 1]);
-        fma2_rn(h[e], h[e + 1], c, c, g[e], g[e + 1], g[e], g[e + 1]);
-        fma2_rn(g[e], g[e + 1], inv, inv, d[e], d[e + 1], d[e], d[e + 1]);
+        mul2_rn(g[e], g[e + 1], w[e], w[e + 1], w[e], w[e + 1]);
+        fma2_rn(h[e], h[e + 1], c, c, w[e], w[e + 1], w[e], w[e + 1]);
+        fma2_rn(w[e], w[e + 1], inv, inv, d[e], d[e + 1], d[e], d[e + 1]);
     }
     st_block_stream(static_cast<T*>(a.dresidual) + row * a.hidden, b, Elem<E>::pack(d));
     if (a.dx) {
@@ -119,6 +125,18 @@ __device__ __forceinline__ void bwd_finish(const DropNormArgs& a, const uint2& o
             drop8(d, a.drop, offset, static_cast<uint32_t>(b), static_cast<uint32_t>(row));
         st_block_stream(static_cast<T*>(a.dx) + row * a.hidden, b, Elem<E>::pack(d));
     }
+}
+
+template <int E>
+__device__ __forceinline__ void bwd_finish(const DropNormArgs& a, const uint2& offset,
+                                           const typename Elem<E>::Block& hv, const typename Elem<E>::Block& gv,
+                                           const typename Elem<E>::Block& wv, const typename Elem<E>::Block& dv,
+                                           float inv, float c, int64_t row, int b, float (&dw)[8])
+{
+    float h[8], g[8];
+    Elem<E>::unpack(hv, h);
+    Elem<E>::unpack(gv, g);
+    bwd_finish<E>(a, offset, h, g, wv, dv, inv, c, row, b, dw);
 }
 
 // c of the row: -inv^2 S2 / hidden.
@@ -131,44 +149,99 @@ __device__ __forceinline__ float bwd_coefficient(const DropNormArgs& a, float s2
 
 // ------------------------------------------------------------- narrow rows
 // L lanes a row (8, 16 or 32), K blocks of 8 a lane: P = 8 L K <= 1024.  A
-// CTA takes (warps x 32 / L) rows at a time.
+// CTA takes (threads x 32 / L) rows at a time.  Every thread copies its
+// blocks of the next rows into a ring of shared memory that only it reads.
 constexpr int kNarrowThreads = 256;
+
+// N tensors, K blocks each: slots of the ring, and its bytes.
+template <int E, int N, int K>
+struct NarrowRing {
+    static constexpr uint32_t kPiece = kNarrowThreads * 16;
+    static constexpr int kVec = E == kElemF32 ? 2 : 1;
+    static constexpr uint32_t kSlotBytes = N * K * kVec * kPiece;
+    static constexpr int kSlots = narrow_slots(E, N, K);
+    static constexpr uint32_t kBytes = kSlots * kSlotBytes;
+    static_assert(kBytes == narrow_ring_bytes(E, N, K), "the host sizes the same ring");
+    static __device__ __forceinline__ uint32_t at(uint32_t slot, int tensor, int j)
+    {
+        return slot + (tensor * K + j) * kVec * kPiece;
+    }
+    static __device__ __forceinline__ uint32_t after(uint32_t slot, uint32_t ring)
+    {
+        return slot == ring + (kSlots - 1) * kSlotBytes ? ring : slot + kSlotBytes;
+    }
+};
+
+// Copies row `row` of the tensors into a slot, or nothing past the last row.
+template <int E, int N, int L, int K>
+__device__ __forceinline__ void narrow_issue(const void* const (&src)[N], int64_t row, const DropNormArgs& a,
+                                             uint32_t slot, int t)
+{
+    using T = typename Elem<E>::T;
+    using Ring = NarrowRing<E, N, K>;
+    if (row < a.n_rows) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (!src[i])
+                continue;
+            const T* p = static_cast<const T*>(src[i]) + row * a.hidden + t * 8;
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if (8 * (t + j * L) < a.hidden)
+                    copy_ahead_block(Ring::at(slot, i, j), Ring::kPiece, p + j * L * 8);
+        }
+    }
+    copy_ahead_commit();
+}
 
 template <int E, int L, int K>
 __global__ void __launch_bounds__(kNarrowThreads) drop_norm_fwd_narrow(const DropNormArgs a)
 {
     using T = typename Elem<E>::T;
     using V = typename Elem<E>::Block;
+    using Ring = NarrowRing<E, 2, K>;
+    extern __shared__ __align__(128) unsigned char stage_mem[];
     const int t = threadIdx.x & (L - 1);
     const int nblocks = a.hidden >> 3;
-    wait_prior_grids();
-    allow_next_grid();
-    const uint2 offset = drop_offset(a.drop);
+    const uint32_t ring = smem_u32(stage_mem) + threadIdx.x * 16;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kNarrowThreads / L);
     const int64_t first = static_cast<int64_t>(blockIdx.x) * (kNarrowThreads / L) + threadIdx.x / L;
     // rows of one warp start together, so every lane of it makes the same
     // number of steps and takes part in the shuffles
     const int64_t lead = first - (threadIdx.x & 31) / L;
+    wait_prior_grids();
+    allow_next_grid();
+    const void* const src[2] = {a.x, a.residual};
+    uint32_t in = ring, slot = ring;
+#pragma unroll
+    for (int i = 0; i < Ring::kSlots - 1; ++i) {
+        narrow_issue<E, 2, L, K>(src, first + i * step, a, in, t);
+        in = Ring::after(in, ring);
+    }
+    const uint2 offset = drop_offset(a.drop);
+    V wv[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        wv[j] = V{};
+        if (t + j * L < nblocks)
+            ld_block(static_cast<const T*>(a.weight), t + j * L, wv[j]);
+    }
     for (int64_t base = 0; lead + base < a.n_rows; base += step) {
         const int64_t row = first + base;
         const bool active = row < a.n_rows;
-        V xv[K], rv[K], wv[K];
-#pragma unroll
-        for (int j = 0; j < K; ++j) {
-            const int b = t + j * L;
-            if (active && b < nblocks) {
-                ld_block_stream(static_cast<const T*>(a.x) + row * a.hidden, b, xv[j]);
-                ld_block_stream(static_cast<const T*>(a.residual) + row * a.hidden, b, rv[j]);
-                ld_block(static_cast<const T*>(a.weight), b, wv[j]);
-            }
-        }
+        narrow_issue<E, 2, L, K>(src, row + (Ring::kSlots - 1) * step, a, in, t);
+        in = Ring::after(in, ring);
+        copy_ahead_wait<Ring::kSlots - 1>();
         float acc[K][8], part[K];
 #pragma unroll
         for (int j = 0; j < K; ++j) {
             const int b = t + j * L;
             part[j] = 0.0f;
             if (active && b < nblocks) {
-                fwd_block<E>(a, offset, xv[j], rv[j], row, b, acc[j]);
+                V xv, rv;
+                lds_block(Ring::at(slot, 0, j), Ring::kPiece, xv);
+                lds_block(Ring::at(slot, 1, j), Ring::kPiece, rv);
+                fwd_block<E>(a, offset, xv, rv, row, b, acc[j]);
                 part[j] = fold8_squares(acc[j]);
             }
             part[j] = butterfly_sum(part[j], L);
@@ -180,78 +253,97 @@ __global__ void __launch_bounds__(kNarrowThreads) drop_norm_fwd_narrow(const Dro
             if (active && b < nblocks)
                 fwd_finish<E>(a, acc[j], inv, wv[j], row, b);
         }
+        slot = Ring::after(slot, ring);
     }
 }
 
 template <int E, int L, int K>
-__global__ void __launch_bounds__(kNarrowThreads) drop_norm_bwd_narrow(const DropNormArgs a)
+__global__ void __launch_bounds__(kNarrowThreads, 2) drop_norm_bwd_narrow(const DropNormArgs a)
 {
     using T = typename Elem<E>::T;
     using V = typename Elem<E>::Block;
-    constexpr int kGroups = kNarrowThreads / L;
-    __shared__ float sums[L * K * 8];
+    using Ring = NarrowRing<E, 3, K>;
+    extern __shared__ __align__(128) unsigned char stage_mem[];
     const int t = threadIdx.x & (L - 1);
-    const int group = threadIdx.x / L;
     const int nblocks = a.hidden >> 3;
+    const uint32_t ring = smem_u32(stage_mem) + threadIdx.x * 16;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kNarrowThreads / L);
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (kNarrowThreads / L) + threadIdx.x / L;
+    const int64_t lead = first - (threadIdx.x & 31) / L;  // as in the forward
     wait_prior_grids();
     allow_next_grid();
+    const void* const src[3] = {a.h, a.dout, a.dresidual_out};
+    uint32_t in = ring, slot = ring;
+#pragma unroll
+    for (int i = 0; i < Ring::kSlots - 1; ++i) {
+        narrow_issue<E, 3, L, K>(src, first + i * step, a, in, t);
+        in = Ring::after(in, ring);
+    }
     const uint2 offset = drop_offset(a.drop);
     float dw[K][8] = {};
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * kGroups + group;
-    const int64_t lead = first - (threadIdx.x & 31) / L;  // as in the forward
     for (int64_t base = 0; lead + base < a.n_rows; base += step) {
         const int64_t row = first + base;
         const bool active = row < a.n_rows;
-        V hv[K], gv[K], wv[K], dv[K];
-#pragma unroll
-        for (int j = 0; j < K; ++j) {
-            const int b = t + j * L;
-            dv[j] = V{};
-            if (active && b < nblocks) {
-                ld_block_stream(static_cast<const T*>(a.h) + row * a.hidden, b, hv[j]);
-                ld_block_stream(static_cast<const T*>(a.dout) + row * a.hidden, b, gv[j]);
-                if (a.dresidual_out)
-                    ld_block_stream(static_cast<const T*>(a.dresidual_out) + row * a.hidden, b, dv[j]);
-                ld_block(static_cast<const T*>(a.weight), b, wv[j]);
-            }
-        }
+        narrow_issue<E, 3, L, K>(src, row + (Ring::kSlots - 1) * step, a, in, t);
+        in = Ring::after(in, ring);
+        copy_ahead_wait<Ring::kSlots - 1>();
         float p1[K], p2[K];
 #pragma unroll
         for (int j = 0; j < K; ++j) {
             p1[j] = p2[j] = 0.0f;
-            if (active && t + j * L < nblocks)
-                bwd_sums<E>(hv[j], gv[j], wv[j], p1[j], p2[j]);
-            p1[j] = butterfly_sum(p1[j], L);
-            p2[j] = butterfly_sum(p2[j], L);
+            if (active && t + j * L < nblocks) {
+                V hv, gv, wv;
+                lds_block(Ring::at(slot, 0, j), Ring::kPiece, hv);
+                lds_block(Ring::at(slot, 1, j), Ring::kPiece, gv);
+                ld_block(static_cast<const T*>(a.weight), t + j * L, wv);
+                bwd_sums<E>(hv, gv, wv, p1[j], p2[j]);
+            }
         }
-        const float inv = inv_rms(fold_k<K>(p1), a.hidden, a.inv_hidden, a.eps);
-        const float c = bwd_coefficient(a, fold_k<K>(p2), inv);
+        const float inv =
+            inv_rms(butterfly_sum(fold_k<K>(p1), L), a.hidden, a.inv_hidden, a.eps);
+        const float c = bwd_coefficient(a, butterfly_sum(fold_k<K>(p2), L), inv);
 #pragma unroll
         for (int j = 0; j < K; ++j) {
             const int b = t + j * L;
-            if (active && b < nblocks)
-                bwd_finish<E>(a, offset, hv[j], gv[j], wv[j], dv[j], inv, c, row, b, dw[j]);
+            if (active && b < nblocks) {
+                V hv, gv, wv, dv = V{};
+                lds_block(Ring::at(slot, 0, j), Ring::kPiece, hv);
+                lds_block(Ring::at(slot, 1, j), Ring::kPiece, gv);
+                if (a.dresidual_out)
+                    lds_block(Ring::at(slot, 2, j), Ring::kPiece, dv);
+                ld_block(static_cast<const T*>(a.weight), b, wv);
+                bwd_finish<E>(a, offset, hv, gv, wv, dv, inv, c, row, b, dw[j]);
+            }
         }
+        slot = Ring::after(slot, ring);
     }
     if (!a.partials)
         return;
-    // the CTA's part: its groups' sums, added in group order
-    for (int g = 0; g < kGroups; ++g) {
-        if (group == g) {
+    // the CTA's part: a warp's groups by butterfly, then the warps in order
+    copy_ahead_wait<0>();
+    __syncthreads();
+    float* const sums = reinterpret_cast<float*>(stage_mem);
+    constexpr int P = 8 * L * K;
 #pragma unroll
-            for (int j = 0; j < K; ++j) {
+    for (int j = 0; j < K; ++j) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float& s = sums[(t + j * L) * 8 + e];
-                    s = g == 0 ? dw[j][e] : __fadd_rn(s, dw[j][e]);
-                }
-            }
+        for (int e = 0; e < 8; ++e) {
+            float v = dw[j][e];
+#pragma unroll
+            for (int d = L; d < 32; d <<= 1)
+                v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+            if ((threadIdx.x & 31) < L)
+                sums[(threadIdx.x >> 5) * P + (t + j * L) * 8 + e] = v;
         }
-        __syncthreads();
     }
-    for (int i = threadIdx.x; i < a.hidden; i += kNarrowThreads)
-        a.partials[static_cast<int64_t>(blockIdx.x) * a.hidden + i] = sums[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.hidden; i += kNarrowThreads) {
+        float v = sums[i];
+#pragma unroll
+        for (int k = 1; k < kNarrowThreads / 32; ++k)
+            v = __fadd_rn(v, sums[k * P + i]);
+        a.partials[static_cast<int64_t>(blockIdx.x) * a.hidden + i] = v;
+    }
 }
 
 // --------------------------------------------------------------- wide rows
@@ -260,8 +352,12 @@ __global__ void __launch_bounds__(kNarrowThreads) drop_norm_bwd_narrow(const Dro
 // (buffers that are not device memory, rows of which two do not fit).
 
 // Resident CTAs per SM the kernels are compiled for: 1024 threads of 64
-// registers up to two blocks a thread, else one CTA of 512 threads.
-constexpr int wide_min_blocks(int T, int K) { return K <= 2 ? 1024 / T : 1; }
+// registers, or 512 of 128.  The backward pass of up to two blocks a thread
+// holds h and dout in registers between its two passes; beyond that it reads
+// them from the stage again.
+constexpr int fwd_min_blocks(int T, int K) { return K <= 2 ? 1024 / T : 512 / T; }
+__host__ __device__ constexpr bool bwd_holds(int K) { return K <= 2; }
+constexpr int bwd_min_blocks(int T, int K) { return K == 1 ? 1024 / T : 512 / T; }
 
 // N arrays of rows staged in turn: a ring of `stages` slots, each one row of
 // every array, filled by thread 0.
@@ -277,6 +373,16 @@ struct RowRing {
     __device__ __forceinline__ const unsigned char* slot(int s) const
     {
         return mem + static_cast<size_t>(s) * N * row_bytes;
+    }
+    // The row's lines into L2, while the previous grid finishes: a hint that
+    // moves nothing to the SM, so the copies issued after the wait still read
+    // what the memory holds then.
+    __device__ __forceinline__ void prefetch(int64_t row) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (src[i])
+                prefetch_l2(src[i] + row * static_cast<int64_t>(row_bytes), row_bytes);
     }
     __device__ __forceinline__ void issue(int s, int64_t row) const
     {
@@ -315,7 +421,7 @@ __device__ __forceinline__ void give_up(const DropNormArgs& a, uint64_t* bars, i
 }
 
 template <int E, int T, int K, bool STAGED>
-__global__ void __launch_bounds__(T, wide_min_blocks(T, K)) drop_norm_fwd_wide(const DropNormArgs a)
+__global__ void __launch_bounds__(T, fwd_min_blocks(T, K)) drop_norm_fwd_wide(const DropNormArgs a)
 {
     using X = typename Elem<E>::T;
     using V = typename Elem<E>::Block;
@@ -335,6 +441,7 @@ __global__ void __launch_bounds__(T, wide_min_blocks(T, K)) drop_norm_fwd_wide(c
         ring.src[1] = static_cast<const unsigned char*>(a.residual);
         ring.policy = l2_policy_evict_first();
         if (tid == 0) {
+            ring.prefetch(blockIdx.x);
             for (int s = 0; s < a.stages; ++s)
                 mbar_init(&ring.bars[s], 1);
             fence_mbar_init();
@@ -421,7 +528,7 @@ __global__ void __launch_bounds__(T, wide_min_blocks(T, K)) drop_norm_fwd_wide(c
 }
 
 template <int E, int T, int K, bool STAGED>
-__global__ void __launch_bounds__(T, wide_min_blocks(T, K)) drop_norm_bwd_wide(const DropNormArgs a)
+__global__ void __launch_bounds__(T, bwd_min_blocks(T, K)) drop_norm_bwd_wide(const DropNormArgs a)
 {
     using X = typename Elem<E>::T;
     using V = typename Elem<E>::Block;
@@ -442,6 +549,7 @@ __global__ void __launch_bounds__(T, wide_min_blocks(T, K)) drop_norm_bwd_wide(c
         ring.src[2] = static_cast<const unsigned char*>(a.dresidual_out);
         ring.policy = l2_policy_evict_first();
         if (tid == 0) {
+            ring.prefetch(blockIdx.x);
             for (int s = 0; s < a.stages; ++s)
                 mbar_init(&ring.bars[s], 1);
             fence_mbar_init();
@@ -474,17 +582,31 @@ __global__ void __launch_bounds__(T, wide_min_blocks(T, K)) drop_norm_bwd_wide(c
             gs = static_cast<const X*>(a.dout) + row * a.hidden;
             ds = static_cast<const X*>(a.dresidual_out) + row * a.hidden;
         }
-        float p1[K], p2[K];
+        constexpr bool HOLD = bwd_holds(K);
+        constexpr int H = HOLD ? K : 1;
+        float p1[K], p2[K], h[H][8], g[H][8];
+        V wv[H], dv[H];
 #pragma unroll
         for (int j = 0; j < K; ++j) {
             const int b = tid + j * T;
             p1[j] = p2[j] = 0.0f;
             if (block_in_row<K>(j, b, nblocks)) {
-                V hv, gv, wv;
+                V hv, gv;
                 ld_block(hs, b, hv);
                 ld_block(gs, b, gv);
-                ld_block(wrow, b, wv);
-                bwd_sums<E>(hv, gv, wv, p1[j], p2[j]);
+                if constexpr (HOLD) {
+                    ld_block(wrow, b, wv[j]);
+                    dv[j] = V{};
+                    if (a.dresidual_out)
+                        ld_block(ds, b, dv[j]);
+                    Elem<E>::unpack(hv, h[j]);
+                    Elem<E>::unpack(gv, g[j]);
+                    bwd_sums<E>(h[j], g[j], wv[j], p1[j], p2[j]);
+                } else {
+                    V w;
+                    ld_block(wrow, b, w);
+                    bwd_sums<E>(hv, gv, w, p1[j], p2[j]);
+                }
             }
         }
         int jsub;
@@ -497,20 +619,28 @@ __global__ void __launch_bounds__(T, wide_min_blocks(T, K)) drop_norm_bwd_wide(c
         if constexpr (STAGED) {
             if (__syncthreads_or(!ok)) {
                 if (tid == 0) {
-                    // filled and not taken: this row's slot and those after
-                    // it, short of the slot of the row before (not refilled)
+                    // filled and not taken: this row's slot and those after it;
+                    // without HOLD, short of the row before's (not refilled yet)
                     const int64_t left = (a.n_rows - row + stride - 1) / stride;
-                    const int64_t filled = row == blockIdx.x ? a.stages : a.stages - 1;
+                    const int64_t filled = HOLD || row == blockIdx.x ? a.stages : a.stages - 1;
                     give_up(a, ring.bars, s, parity, left < filled ? left : filled);
                 }
                 return;
             }
-            // Past this barrier every thread is done with the row before
-            // this one, so its slot takes the next row: no second barrier a
-            // row, at the price of one slot's depth.
-            if (tid == 0 && row != blockIdx.x && row + (a.stages - 1) * stride < a.n_rows) {
-                fence_proxy_async_smem();
-                ring.issue(s == 0 ? a.stages - 1 : s - 1, row + (a.stages - 1) * stride);
+            if constexpr (HOLD) {
+                // every thread has taken this row into registers
+                if (tid == 0 && row + a.stages * stride < a.n_rows) {
+                    fence_proxy_async_smem();
+                    ring.issue(s, row + a.stages * stride);
+                }
+            } else {
+                // Past this barrier every thread is done with the row before
+                // this one, so its slot takes the next row: no second barrier
+                // a row, at the price of one slot's depth.
+                if (tid == 0 && row != blockIdx.x && row + (a.stages - 1) * stride < a.n_rows) {
+                    fence_proxy_async_smem();
+                    ring.issue(s == 0 ? a.stages - 1 : s - 1, row + (a.stages - 1) * stride);
+                }
             }
         } else {
             __syncthreads();
@@ -521,13 +651,17 @@ __global__ void __launch_bounds__(T, wide_min_blocks(T, K)) drop_norm_bwd_wide(c
         for (int j = 0; j < K; ++j) {
             const int b = tid + j * T;
             if (block_in_row<K>(j, b, nblocks)) {
-                V hv, gv, wv, dv = V{};
-                ld_block(hs, b, hv);
-                ld_block(gs, b, gv);
-                ld_block(wrow, b, wv);
-                if (a.dresidual_out)
-                    ld_block(ds, b, dv);
-                bwd_finish<E>(a, offset, hv, gv, wv, dv, inv, c, row, b, dw[j]);
+                if constexpr (HOLD) {
+                    bwd_finish<E>(a, offset, h[j], g[j], wv[j], dv[j], inv, c, row, b, dw[j]);
+                } else {
+                    V hv, gv, w, d = V{};
+                    ld_block(hs, b, hv);
+                    ld_block(gs, b, gv);
+                    ld_block(wrow, b, w);
+                    if (a.dresidual_out)
+                        ld_block(ds, b, d);
+                    bwd_finish<E>(a, offset, hv, gv, w, d, inv, c, row, b, dw[j]);
+                }
             }
         }
         buf ^= 1;

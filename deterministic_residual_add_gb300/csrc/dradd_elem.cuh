@@ -108,4 +108,57 @@ __device__ __forceinline__ void st_block_stream(float* p, int64_t i, const F32Bl
     st_stream(reinterpret_cast<uint4*>(p) + 2 * i + 1, b.hi);
 }
 
+// ------------------------------------------------- lane-private copies ahead
+// Asynchronous copies from global memory into shared memory that only the
+// copying thread reads again, so that waiting for its own groups is all the
+// synchronisation there is.  Ordinary loads to the memory system: any
+// address a load could take.
+__device__ __forceinline__ void copy_ahead16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_ahead8(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_ahead_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_ahead_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ int64_t lds8(uint32_t at)
+{
+    int64_t v;
+    asm volatile("ld.shared.s64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// A block of 8 elements in such memory: its 16-byte pieces `stride` bytes
+// apart.
+__device__ __forceinline__ void copy_ahead_block(uint32_t dst, uint32_t stride, const uint16_t* src)
+{
+    copy_ahead16(dst, src);
+}
+__device__ __forceinline__ void copy_ahead_block(uint32_t dst, uint32_t stride, const float* src)
+{
+    copy_ahead16(dst, src);
+    copy_ahead16(dst + stride, src + 4);
+}
+__device__ __forceinline__ void lds_block(uint32_t at, uint32_t stride, uint4& b) { b = lds16(at); }
+__device__ __forceinline__ void lds_block(uint32_t at, uint32_t stride, F32Block& b)
+{
+    b.lo = lds16(at);
+    b.hi = lds16(at + stride);
+}
+
 }  // namespace dradd

@@ -384,37 +384,6 @@ struct HeadWalk {
     }
 };
 
-// 16 and 8 bytes from global to this lane's shared memory.
-__device__ __forceinline__ void copy_ahead16(uint32_t dst, const void* src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_ahead8(uint32_t dst, const void* src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_ahead_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_ahead_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint4 lds16(uint32_t at)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(at)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ int64_t lds8(uint32_t at)
-{
-    int64_t v;
-    asm volatile("ld.shared.s64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
-    return v;
-}
-
 // The copies ahead of the computation: the tensors W of the warp's work
 // items, step by step, into the lane's slots.  A run the lane's head does
 // not have is never copied (its slot keeps the zeros it starts with); a head

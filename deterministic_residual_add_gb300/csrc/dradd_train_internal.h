@@ -54,6 +54,23 @@ struct DropNormArgs {
     uint64_t wait_limit_ns;
 };
 
+// The rings of the narrow-row kernels: N tensors, K blocks of 8 a lane, 256
+// threads.  Slots: as many as two CTAs an SM have room for, at most three
+// rows ahead.
+constexpr uint32_t narrow_slot_bytes(int elem, int n, int K)
+{
+    return static_cast<uint32_t>(n * K * (elem == 2 ? 2 : 1)) * 256u * 16u;
+}
+constexpr int narrow_slots(int elem, int n, int K)
+{
+    const int fit = static_cast<int>(110u * 1024u / narrow_slot_bytes(elem, n, K));
+    return fit > 4 ? 4 : fit < 2 ? 2 : fit;
+}
+constexpr uint32_t narrow_ring_bytes(int elem, int n, int K)
+{
+    return narrow_slots(elem, n, K) * narrow_slot_bytes(elem, n, K);
+}
+
 // How a call's rows are spread: a function of (n_rows, hidden, element type,
 // direction, memory) alone.
 struct DropNormPlan {
