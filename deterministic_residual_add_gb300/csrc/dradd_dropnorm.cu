@@ -30,25 +30,32 @@ DropNormPlan drop_norm_plan(int64_t n_rows, int hidden, int elem, bool backward,
         p.threads = 256;
         const int rows = p.threads / p.lanes;
         units = (n_rows + rows - 1) / rows;
-        per_sm = 2;
+        per_sm = narrow_ctas(elem, backward ? 3 : 2, p.K);
         p.smem = narrow_ring_bytes(elem, backward ? 3 : 2, p.K);
         const size_t sums = static_cast<size_t>(P) * 4 * (p.threads / 32);
         if (backward && p.smem < sums)
             p.smem = sums;
     } else {
         p.K = P <= 2048 ? 1 : P <= 8192 ? 2 : P / 4096;
-        p.threads = P / 8 / p.K;
+        p.threads = backward ? (hidden / 8 + 32 * p.K - 1) / (32 * p.K) * 32 : P / 8 / p.K;
         units = n_rows;
-        // As many CTAs per SM as the registers allow (1024 threads, or 512
-        // for the kernels of 128 registers) and as leave each of them enough
-        // slots: two, or three where a slot is refilled a row later.
+        // As many CTAs per SM as the registers allow (dradd_dropnorm.cuh) and
+        // as leave each of them enough slots: two, or three where a slot is
+        // refilled a row later.
         const int64_t slot = static_cast<int64_t>(hidden) * (elem == kElemF32 ? 4 : 2) * (backward ? 3 : 2);
-        const int least = backward && p.K > 2 ? 3 : 2;
+        const bool later = backward && p.K > 2;
+        const int resident = !backward ? (p.K <= 2 ? 1024 : 512)
+                             : p.K == 1 ? 1024
+                             : p.K == 2 ? 2 * bwd_pair_threads(elem)
+                                        : 512;
         int stages = 0;
-        for (per_sm = (p.K <= (backward ? 1 : 2) ? 1024 : 512) / p.threads;; per_sm /= 2) {
+        per_sm = resident / p.threads;
+        if (per_sm > 4)
+            per_sm = 4;
+        for (;; --per_sm) {
             const int64_t room = kSmemPerSm / per_sm - 4096;  // less the system's share and the kernel's own
             stages = static_cast<int>(room / slot);
-            if (stages >= least || per_sm == 1)
+            if (stages >= (later ? 3 : 2) || per_sm <= 1)
                 break;
         }
         if (stages > kMaxStages)
@@ -78,6 +85,8 @@ cudaError_t launch_drop_norm_bwd(const DropNormArgs& a, const DropNormPlan& p, i
                               : launch_drop_norm_f32(a, p, true, stream);
 }
 
+constexpr int kColumnLoads = 10;
+
 // Warp w of a CTA adds parts w, w + 32, ... of its 32 columns in order; the
 // 32 warps' sums are then added in warp order.
 __global__ void __launch_bounds__(1024) column_sums_kernel(const float* partials, int parts, int cols, float* out0,
@@ -91,9 +100,15 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const float* partials
     float s = 0.0f;
     if (col < cols) {
         const float* p = partials + col;
-#pragma unroll 4
-        for (int i = warp; i < parts; i += 32)
-            s = __fadd_rn(s, __ldcs(p + static_cast<int64_t>(i) * cols));
+        for (int i = warp; i < parts; i += 32 * kColumnLoads) {
+            float v[kColumnLoads];  // on their way together
+#pragma unroll
+            for (int k = 0; k < kColumnLoads; ++k)
+                v[k] = i + 32 * k < parts ? __ldcs(p + static_cast<int64_t>(i + 32 * k) * cols) : 0.0f;
+#pragma unroll
+            for (int k = 0; k < kColumnLoads; ++k)
+                s = __fadd_rn(s, v[k]);
+        }
     }
     sums[warp][lane] = s;
     __syncthreads();

@@ -66,7 +66,7 @@ __device__ __forceinline__ void fwd_finish(const DropNormArgs& a, float (&acc)[8
     st_block_stream(static_cast<T*>(a.out) + row * a.hidden, b, Elem<E>::pack(acc));
 }
 
-// The block's parts of sum h^2 and sum (dout w) h: two chains of fused
+// The block's parts of sum h^2 and sum g h (g = dout w): two chains of fused
 // multiply-adds each, two to an instruction, then their sum.
 template <int E>
 __device__ __forceinline__ void bwd_sums(const float (&h)[8], const float (&dout)[8],
@@ -89,20 +89,10 @@ __device__ __forceinline__ void bwd_sums(const float (&h)[8], const float (&dout
     s2 = __fadd_rn(b0, b1);
 }
 
-template <int E>
-__device__ __forceinline__ void bwd_sums(const typename Elem<E>::Block& hv, const typename Elem<E>::Block& gv,
-                                         const typename Elem<E>::Block& wv, float& s1, float& s2)
-{
-    float h[8], g[8];
-    Elem<E>::unpack(hv, h);
-    Elem<E>::unpack(gv, g);
-    bwd_sums<E>(h, g, wv, s1, s2);
-}
-
-// The gradients of one block, and its rows' share of dweight (g: dout).
+// The gradients of one block, and its rows' share of dweight.
 template <int E>
 __device__ __forceinline__ void bwd_finish(const DropNormArgs& a, const uint2& offset, const float (&h)[8],
-                                           const float (&g)[8], const typename Elem<E>::Block& wv,
+                                           const float (&dout)[8], const typename Elem<E>::Block& wv,
                                            const typename Elem<E>::Block& dv, float inv, float c, int64_t row, int b,
                                            float (&dw)[8])
 {
@@ -114,8 +104,8 @@ __device__ __forceinline__ void bwd_finish(const DropNormArgs& a, const uint2& o
     for (int e = 0; e < 8; e += 2) {
         float x0, x1;
         mul2_rn(h[e], h[e + 1], inv, inv, x0, x1);
-        fma2_rn(g[e], g[e + 1], x0, x1, dw[e], dw[e + 1], dw[e], dw[e + 1]);
-        mul2_rn(g[e], g[e + 1], w[e], w[e + 1], w[e], w[e + 1]);
+        fma2_rn(dout[e], dout[e + 1], x0, x1, dw[e], dw[e + 1], dw[e], dw[e + 1]);
+        mul2_rn(dout[e], dout[e + 1], w[e], w[e + 1], w[e], w[e + 1]);
         fma2_rn(h[e], h[e + 1], c, c, w[e], w[e + 1], w[e], w[e + 1]);
         fma2_rn(w[e], w[e + 1], inv, inv, d[e], d[e + 1], d[e], d[e + 1]);
     }
@@ -125,18 +115,6 @@ __device__ __forceinline__ void bwd_finish(const DropNormArgs& a, const uint2& o
             drop8(d, a.drop, offset, static_cast<uint32_t>(b), static_cast<uint32_t>(row));
         st_block_stream(static_cast<T*>(a.dx) + row * a.hidden, b, Elem<E>::pack(d));
     }
-}
-
-template <int E>
-__device__ __forceinline__ void bwd_finish(const DropNormArgs& a, const uint2& offset,
-                                           const typename Elem<E>::Block& hv, const typename Elem<E>::Block& gv,
-                                           const typename Elem<E>::Block& wv, const typename Elem<E>::Block& dv,
-                                           float inv, float c, int64_t row, int b, float (&dw)[8])
-{
-    float h[8], g[8];
-    Elem<E>::unpack(hv, h);
-    Elem<E>::unpack(gv, g);
-    bwd_finish<E>(a, offset, h, g, wv, dv, inv, c, row, b, dw);
 }
 
 // c of the row: -inv^2 S2 / hidden.
@@ -280,6 +258,14 @@ __global__ void __launch_bounds__(kNarrowThreads, 2) drop_norm_bwd_narrow(const 
         in = Ring::after(in, ring);
     }
     const uint2 offset = drop_offset(a.drop);
+    __shared__ V weights[L * K];
+    for (int i = threadIdx.x; i < L * K; i += kNarrowThreads) {
+        V v = V{};
+        if (i < nblocks)
+            ld_block(static_cast<const T*>(a.weight), i, v);
+        weights[i] = v;
+    }
+    __syncthreads();
     float dw[K][8] = {};
     for (int64_t base = 0; lead + base < a.n_rows; base += step) {
         const int64_t row = first + base;
@@ -290,14 +276,17 @@ __global__ void __launch_bounds__(kNarrowThreads, 2) drop_norm_bwd_narrow(const 
         float p1[K], p2[K];
 #pragma unroll
         for (int j = 0; j < K; ++j) {
-            p1[j] = p2[j] = 0.0f;
-            if (active && t + j * L < nblocks) {
-                V hv, gv, wv;
-                lds_block(Ring::at(slot, 0, j), Ring::kPiece, hv);
-                lds_block(Ring::at(slot, 1, j), Ring::kPiece, gv);
-                ld_block(static_cast<const T*>(a.weight), t + j * L, wv);
-                bwd_sums<E>(hv, gv, wv, p1[j], p2[j]);
-            }
+            // a slot that was not filled is read all the same and counts nothing
+            V hv, gv;
+            lds_block(Ring::at(slot, 0, j), Ring::kPiece, hv);
+            lds_block(Ring::at(slot, 1, j), Ring::kPiece, gv);
+            float h[8], g[8];
+            Elem<E>::unpack(hv, h);
+            Elem<E>::unpack(gv, g);
+            bwd_sums<E>(h, g, weights[t + j * L], p1[j], p2[j]);
+            const bool in_row = active && t + j * L < nblocks;
+            p1[j] = in_row ? p1[j] : 0.0f;
+            p2[j] = in_row ? p2[j] : 0.0f;
         }
         const float inv =
             inv_rms(butterfly_sum(fold_k<K>(p1), L), a.hidden, a.inv_hidden, a.eps);
@@ -306,13 +295,15 @@ __global__ void __launch_bounds__(kNarrowThreads, 2) drop_norm_bwd_narrow(const 
         for (int j = 0; j < K; ++j) {
             const int b = t + j * L;
             if (active && b < nblocks) {
-                V hv, gv, wv, dv = V{};
+                V hv, gv, dv = V{};
                 lds_block(Ring::at(slot, 0, j), Ring::kPiece, hv);
                 lds_block(Ring::at(slot, 1, j), Ring::kPiece, gv);
                 if (a.dresidual_out)
                     lds_block(Ring::at(slot, 2, j), Ring::kPiece, dv);
-                ld_block(static_cast<const T*>(a.weight), b, wv);
-                bwd_finish<E>(a, offset, hv, gv, wv, dv, inv, c, row, b, dw[j]);
+                float h[8], g[8];
+                Elem<E>::unpack(hv, h);
+                Elem<E>::unpack(gv, g);
+                bwd_finish<E>(a, offset, h, g, weights[b], dv, inv, c, row, b, dw[j]);
             }
         }
         slot = Ring::after(slot, ring);
@@ -351,13 +342,18 @@ __global__ void __launch_bounds__(kNarrowThreads, 2) drop_norm_bwd_narrow(const 
 // through stages of shared memory (STAGED) or straight from global memory
 // (buffers that are not device memory, rows of which two do not fit).
 
-// Resident CTAs per SM the kernels are compiled for: 1024 threads of 64
-// registers, or 512 of 128.  The backward pass of up to two blocks a thread
-// holds h and dout in registers between its two passes; beyond that it reads
-// them from the stage again.
+// The forward's T threads cover the padded row exactly, as the canonical
+// tree wants; the backward pass, whose sums have no such order to keep,
+// takes as many whole warps as the row has work for.
+//
+// Resident CTAs per SM the kernels are compiled for: forward 1024 threads of
+// 64 registers, or 512 of 128; backward likewise, and 640 of about 100 for
+// two blocks a thread in CTAs of 256 to 320 threads (2-byte types).
 constexpr int fwd_min_blocks(int T, int K) { return K <= 2 ? 1024 / T : 512 / T; }
+// Between its two passes the backward kernel holds h and dout in registers,
+// widened; more than two blocks a thread it reads from the stage again (held
+// as they came, four blocks: 61.8 us against 57.8 at 2048 x 16384 bf16).
 __host__ __device__ constexpr bool bwd_holds(int K) { return K <= 2; }
-constexpr int bwd_min_blocks(int T, int K) { return K == 1 ? 1024 / T : 512 / T; }
 
 // N arrays of rows staged in turn: a ring of `stages` slots, each one row of
 // every array, filled by thread 0.
@@ -527,14 +523,17 @@ __global__ void __launch_bounds__(T, fwd_min_blocks(T, K)) drop_norm_fwd_wide(co
     }
 }
 
-template <int E, int T, int K, bool STAGED>
-__global__ void __launch_bounds__(T, bwd_min_blocks(T, K)) drop_norm_bwd_wide(const DropNormArgs a)
+// MAXT threads at most, MINB CTAs an SM.
+template <int E, int K, int MAXT, int MINB, bool STAGED>
+__global__ void __launch_bounds__(MAXT, MINB) drop_norm_bwd_wide(const DropNormArgs a)
 {
     using X = typename Elem<E>::T;
     using V = typename Elem<E>::Block;
-    constexpr int W = T / 32;
+    constexpr bool HOLD = bwd_holds(K);
+    constexpr int H = HOLD ? K : 1;
     extern __shared__ __align__(128) unsigned char stage_mem[];
-    __shared__ float red1[2][K * W], red2[2][K * W];
+    __shared__ float red1[2][16], red2[2][16];
+    const int T = blockDim.x, W = T >> 5;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nblocks = a.hidden >> 3;
     const int64_t stride = gridDim.x;
@@ -582,39 +581,41 @@ __global__ void __launch_bounds__(T, bwd_min_blocks(T, K)) drop_norm_bwd_wide(co
             gs = static_cast<const X*>(a.dout) + row * a.hidden;
             ds = static_cast<const X*>(a.dresidual_out) + row * a.hidden;
         }
-        constexpr bool HOLD = bwd_holds(K);
-        constexpr int H = HOLD ? K : 1;
-        float p1[K], p2[K], h[H][8], g[H][8];
+        float h[H][8], g[H][8];
         V wv[H], dv[H];
+        const auto load = [&](int b, int i) {
+            V v;
+            ld_block(hs, b, v);
+            Elem<E>::unpack(v, h[i]);
+            ld_block(gs, b, v);
+            Elem<E>::unpack(v, g[i]);
+            ld_block(wrow, b, wv[i]);
+        };
+        // T is nblocks / K rounded up to whole warps, so only the last of a
+        // thread's blocks may lie past the row; it is then read from the last
+        // block and counts nothing, which keeps the loads free of branches.
+        float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int j = 0; j < K; ++j) {
-            const int b = tid + j * T;
-            p1[j] = p2[j] = 0.0f;
-            if (block_in_row<K>(j, b, nblocks)) {
-                V hv, gv;
-                ld_block(hs, b, hv);
-                ld_block(gs, b, gv);
-                if constexpr (HOLD) {
-                    ld_block(wrow, b, wv[j]);
-                    dv[j] = V{};
-                    if (a.dresidual_out)
-                        ld_block(ds, b, dv[j]);
-                    Elem<E>::unpack(hv, h[j]);
-                    Elem<E>::unpack(gv, g[j]);
-                    bwd_sums<E>(h[j], g[j], wv[j], p1[j], p2[j]);
-                } else {
-                    V w;
-                    ld_block(wrow, b, w);
-                    bwd_sums<E>(hv, gv, w, p1[j], p2[j]);
-                }
+            const int i = HOLD ? j : 0;
+            const bool in_row = j < K - 1 || tid + j * T < nblocks;
+            const int b = in_row ? tid + j * T : nblocks - 1;
+            load(b, i);
+            if constexpr (HOLD) {
+                dv[i] = V{};
+                if (a.dresidual_out)
+                    ld_block(ds, b, dv[i]);
             }
+            float p1, p2;
+            bwd_sums<E>(h[i], g[i], wv[i], p1, p2);
+            s1 = __fadd_rn(s1, in_row ? p1 : 0.0f);
+            s2 = __fadd_rn(s2, in_row ? p2 : 0.0f);
         }
-        int jsub;
-        const float v1 = warp_halving_sum<K>(p1, lane, jsub);
-        const float v2 = warp_halving_sum<K>(p2, lane, jsub);
-        if (lane < K) {
-            red1[buf][jsub * W + warp] = v1;
-            red2[buf][jsub * W + warp] = v2;
+        s1 = butterfly_sum(s1, 32);
+        s2 = butterfly_sum(s2, 32);
+        if (lane == 0) {
+            red1[buf][warp] = s1;
+            red2[buf][warp] = s2;
         }
         if constexpr (STAGED) {
             if (__syncthreads_or(!ok)) {
@@ -645,23 +646,22 @@ __global__ void __launch_bounds__(T, bwd_min_blocks(T, K)) drop_norm_bwd_wide(co
         } else {
             __syncthreads();
         }
-        const float inv = inv_rms(cross_warp_sum<K, W>(red1[buf], lane), a.hidden, a.inv_hidden, a.eps);
-        const float c = bwd_coefficient(a, cross_warp_sum<K, W>(red2[buf], lane), inv);
+        s1 = butterfly_sum((lane & 15) < W ? red1[buf][lane & 15] : 0.0f, 16);
+        s2 = butterfly_sum((lane & 15) < W ? red2[buf][lane & 15] : 0.0f, 16);
+        const float inv = inv_rms(s1, a.hidden, a.inv_hidden, a.eps);
+        const float c = bwd_coefficient(a, s2, inv);
 #pragma unroll
         for (int j = 0; j < K; ++j) {
             const int b = tid + j * T;
-            if (block_in_row<K>(j, b, nblocks)) {
-                if constexpr (HOLD) {
-                    bwd_finish<E>(a, offset, h[j], g[j], wv[j], dv[j], inv, c, row, b, dw[j]);
-                } else {
-                    V hv, gv, w, d = V{};
-                    ld_block(hs, b, hv);
-                    ld_block(gs, b, gv);
-                    ld_block(wrow, b, w);
+            const int i = HOLD ? j : 0;
+            if (j < K - 1 || b < nblocks) {
+                if constexpr (!HOLD) {
+                    load(b, i);
+                    dv[i] = V{};
                     if (a.dresidual_out)
-                        ld_block(ds, b, d);
-                    bwd_finish<E>(a, offset, hv, gv, w, d, inv, c, row, b, dw[j]);
+                        ld_block(ds, b, dv[i]);
                 }
+                bwd_finish<E>(a, offset, h[i], g[i], wv[i], dv[i], inv, c, row, b, dw[j]);
             }
         }
         buf ^= 1;
@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(T, bwd_min_blocks(T, K)) drop_norm_bwd_wide(co
 #pragma unroll
     for (int j = 0; j < K; ++j) {
         const int b = tid + j * T;
-        if (block_in_row<K>(j, b, nblocks)) {
+        if (j < K - 1 || b < nblocks) {
             float4* p = reinterpret_cast<float4*>(part) + 2 * b;
             p[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
             p[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(T, bwd_min_blocks(T, K)) drop_norm_bwd_wide(co
 template <typename F>
 cudaError_t launch_sized(F fn, const DropNormArgs& a, const DropNormPlan& p, cudaStream_t stream)
 {
-    if (p.smem > 48 * 1024) {
+    if (p.smem > 40 * 1024) {  // with the kernels' own shared memory, past the 48 KB of a plain launch
         const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(p.smem));
@@ -701,13 +701,17 @@ cudaError_t launch_sized(F fn, const DropNormArgs& a, const DropNormPlan& p, cud
 }
 
 template <int E, int T, int K>
-cudaError_t launch_wide(const DropNormArgs& a, const DropNormPlan& p, bool backward, cudaStream_t stream)
+cudaError_t launch_fwd_wide(const DropNormArgs& a, const DropNormPlan& p, cudaStream_t stream)
 {
-    if (p.staged)
-        return backward ? launch_sized(drop_norm_bwd_wide<E, T, K, true>, a, p, stream)
-                        : launch_sized(drop_norm_fwd_wide<E, T, K, true>, a, p, stream);
-    return backward ? launch_sized(drop_norm_bwd_wide<E, T, K, false>, a, p, stream)
+    return p.staged ? launch_sized(drop_norm_fwd_wide<E, T, K, true>, a, p, stream)
                     : launch_sized(drop_norm_fwd_wide<E, T, K, false>, a, p, stream);
+}
+
+template <int E, int K, int MAXT, int MINB>
+cudaError_t launch_bwd_wide(const DropNormArgs& a, const DropNormPlan& p, cudaStream_t stream)
+{
+    return p.staged ? launch_sized(drop_norm_bwd_wide<E, K, MAXT, MINB, true>, a, p, stream)
+                    : launch_sized(drop_norm_bwd_wide<E, K, MAXT, MINB, false>, a, p, stream);
 }
 
 template <int E, int L, int K>
@@ -728,19 +732,32 @@ cudaError_t launch_drop_norm_of(const DropNormArgs& a, const DropNormPlan& p, bo
         return p.K == 2 ? launch_narrow<E, 32, 2>(a, p, backward, stream)
                         : launch_narrow<E, 32, 4>(a, p, backward, stream);
     }
+    if (backward) {
+        switch (p.K) {
+        case 1:
+            return launch_bwd_wide<E, 1, 256, 4>(a, p, stream);
+        case 2:
+            if (p.threads <= 256)
+                return launch_bwd_wide<E, 2, 256, 2>(a, p, stream);
+            return p.threads <= bwd_pair_threads(E) ? launch_bwd_wide<E, 2, 320, 2>(a, p, stream)
+                                                    : launch_bwd_wide<E, 2, 512, 1>(a, p, stream);
+        case 4:
+            return launch_bwd_wide<E, 4, 512, 1>(a, p, stream);
+        default:
+            return launch_bwd_wide<E, 8, 512, 1>(a, p, stream);
+        }
+    }
     switch (p.threads * 8 * p.K) {
     case 2048:
-        return launch_wide<E, 256, 1>(a, p, backward, stream);
+        return launch_fwd_wide<E, 256, 1>(a, p, stream);
     case 4096:
-        return launch_wide<E, 256, 2>(a, p, backward, stream);
+        return launch_fwd_wide<E, 256, 2>(a, p, stream);
     case 8192:
-        return launch_wide<E, 512, 2>(a, p, backward, stream);
+        return launch_fwd_wide<E, 512, 2>(a, p, stream);
     case 16384:
-        return launch_wide<E, 512, 4>(a, p, backward, stream);
-    case 32768:
-        return launch_wide<E, 512, 8>(a, p, backward, stream);
+        return launch_fwd_wide<E, 512, 4>(a, p, stream);
     default:
-        return cudaErrorInvalidValue;
+        return launch_fwd_wide<E, 512, 8>(a, p, stream);
     }
 }
 

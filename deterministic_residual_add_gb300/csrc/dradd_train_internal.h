@@ -54,22 +54,34 @@ struct DropNormArgs {
     uint64_t wait_limit_ns;
 };
 
-// The rings of the narrow-row kernels: N tensors, K blocks of 8 a lane, 256
-// threads.  Slots: as many as two CTAs an SM have room for, at most three
-// rows ahead.
+// The rings of the narrow-row kernels: N tensors (forward 2, backward 3), K
+// blocks of 8 a lane, 256 threads.  CTAs an SM, and slots: as many as those
+// CTAs have room for, two to four.
 constexpr uint32_t narrow_slot_bytes(int elem, int n, int K)
 {
     return static_cast<uint32_t>(n * K * (elem == 2 ? 2 : 1)) * 256u * 16u;
 }
+constexpr int narrow_ctas(int elem, int n, int K)
+{
+    const uint32_t two = 2 * narrow_slot_bytes(elem, n, K);
+    const int most = n == 2 ? (K == 4 ? 3 : 4) : 2;  // what the registers allow
+    const int fit = static_cast<int>(220u * 1024u / two);
+    return fit < most ? fit : most;
+}
 constexpr int narrow_slots(int elem, int n, int K)
 {
-    const int fit = static_cast<int>(110u * 1024u / narrow_slot_bytes(elem, n, K));
-    return fit > 4 ? 4 : fit < 2 ? 2 : fit;
+    const int fit =
+        static_cast<int>(220u * 1024u / (narrow_ctas(elem, n, K) * narrow_slot_bytes(elem, n, K)));
+    return fit > 4 ? 4 : fit;
 }
 constexpr uint32_t narrow_ring_bytes(int elem, int n, int K)
 {
     return narrow_slots(elem, n, K) * narrow_slot_bytes(elem, n, K);
 }
+
+// Backward, two blocks a thread: CTAs of up to this many threads run two to
+// an SM.
+constexpr int bwd_pair_threads(int elem) { return elem == 2 ? 256 : 320; }
 
 // How a call's rows are spread: a function of (n_rows, hidden, element type,
 // direction, memory) alone.
