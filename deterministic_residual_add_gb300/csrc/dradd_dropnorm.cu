@@ -11,7 +11,12 @@ namespace {
 
 constexpr int kSms = 152;  // a constant, not the device's count: the parts of dweight follow the grid
 constexpr int kSmemPerSm = 227 * 1024;
-constexpr int kMaxStages = 4;
+// Rows the busiest CTA takes with `ctas` per SM.
+int64_t rounds(int64_t n_rows, int ctas)
+{
+    const int64_t grid = static_cast<int64_t>(kSms) * ctas;
+    return (n_rows + grid - 1) / grid;
+}
 
 }  // namespace
 
@@ -23,7 +28,9 @@ DropNormPlan drop_norm_plan(int64_t n_rows, int hidden, int elem, bool backward,
         P *= 2;
     int per_sm;
     int64_t units;
-    if (P <= 1024) {
+    // Narrow kernels: backward wins up to 1024 for 2-byte types (16384 x 1024
+    // 29.3 us, one CTA a row 32.3 to 43.3), not for fp32 (4096 x 1024 25.3, 19.5).
+    if (P <= (backward && elem != kElemF32 ? 1024 : 256)) {
         p.warp = true;
         p.lanes = P / 8 < 32 ? P / 8 : 32;
         p.K = P / 8 / p.lanes;
@@ -36,30 +43,49 @@ DropNormPlan drop_norm_plan(int64_t n_rows, int hidden, int elem, bool backward,
         if (backward && p.smem < sums)
             p.smem = sums;
     } else {
-        p.K = P <= 2048 ? 1 : P <= 8192 ? 2 : P / 4096;
-        p.threads = backward ? (hidden / 8 + 32 * p.K - 1) / (32 * p.K) * 32 : P / 8 / p.K;
+        if (backward) {
+            p.K = P <= 2048 ? 1 : P <= 8192 ? 2 : P / 4096;
+            p.threads = (hidden / 8 + 32 * p.K - 1) / (32 * p.K) * 32;
+        } else {
+            // Many small CTAs: with one warp a row of 512 or 1024 and four
+            // warps one of 2048 and 4096, the rows' barriers and sums hide
+            // behind each other (8192 x 2048 bf16: 256 threads of one block
+            // 23.8 us, 128 of two 16.3; 16384 x 1024: 128 of one 24.4, 64 of
+            // two 17.5, 32 of four 16.4).  fp32 blocks are twice the bytes:
+            // below 2048 one a thread (4096 x 1024: 10.6 us, two 12.0, four 13.3).
+            p.K = P <= 1024 && elem == kElemF32 ? 1 : P == 512 || P == 2048 ? 2 : P <= 8192 ? 4 : P / 4096;
+            p.threads = P / 8 / p.K;
+        }
         units = n_rows;
-        // As many CTAs per SM as the registers allow (dradd_dropnorm.cuh) and
+        // CTAs per SM: as many as the registers allow (dradd_dropnorm.cuh) and
         // as leave each of them enough slots: two, or three where a slot is
         // refilled a row later.
         const int64_t slot = static_cast<int64_t>(hidden) * (elem == kElemF32 ? 4 : 2) * (backward ? 3 : 2);
-        const bool later = backward && p.K > 2;
-        const int resident = !backward ? (p.K <= 2 ? 1024 : 512)
-                             : p.K == 1 ? 1024
-                             : p.K == 2 ? 2 * bwd_pair_threads(elem)
-                                        : 512;
-        int stages = 0;
+        const int least = backward && p.K > 2 ? 3 : 2;
+        const int resident =
+            backward ? (p.K == 1 ? 1024 : p.K == 2 ? 2 * bwd_pair_threads(elem) : 512)
+                     : p.K <= 2 && p.threads > 32 ? 1024 : 512;
+        const auto slots_of = [&](int ctas) {
+            return static_cast<int>((kSmemPerSm / ctas - 4096) / slot);  // less the system's share and the kernel's own
+        };
         per_sm = resident / p.threads;
-        if (per_sm > 4)
-            per_sm = 4;
-        for (;; --per_sm) {
-            const int64_t room = kSmemPerSm / per_sm - 4096;  // less the system's share and the kernel's own
-            stages = static_cast<int>(room / slot);
-            if (stages >= (later ? 3 : 2) || per_sm <= 1)
-                break;
+        if (backward && per_sm > 4)
+            per_sm = 4;  // more would only make more partial sums
+        while (per_sm > 1 && slots_of(per_sm) < least)
+            --per_sm;
+        // Several forward CTAs an SM do best with two slots each (16384 x 4096
+        // bf16 88.7 us, with three 90.0; 16384 x 512 9.6, with four 13.8).
+        int stages = slots_of(per_sm);
+        const int most_stages = backward || per_sm == 1 ? 4 : 2;
+        if (stages > most_stages)
+            stages = most_stages;
+        // One CTA with more slots keeps an SM busy too where a row is long
+        // enough, and deals rows out evenly where two would leave the last
+        // round half empty: 4096 x 8192 bf16 40.8 us against 43.9.
+        if (!backward && per_sm == 2 && slot >= 32 * 1024 && rounds(n_rows, 1) < 2 * rounds(n_rows, 2)) {
+            per_sm = 1;
+            stages = slots_of(1) < 4 ? slots_of(1) : 4;
         }
-        if (stages > kMaxStages)
-            stages = kMaxStages;
         if (device_memory && stages >= 2) {
             p.staged = true;
             p.stages = stages;

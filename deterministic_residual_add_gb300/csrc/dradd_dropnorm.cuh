@@ -17,7 +17,8 @@
 //   order, so the bits depend on the shape and the element type alone.
 //
 // Bound by the memory: 4 elements of traffic an element forward, 5 backward.
-// Rows of P >= 2048 (P: hidden rounded up to a power of two) go through
+// Rows of P > 256 (P: hidden rounded up to a power of two), backward P > 1024
+// for 2-byte types, go through
 // shared memory, one CTA a row, staged `stages` rows ahead by bulk copies;
 // the backward pass needs h and dout twice, before and after the row's sums,
 // and takes them from the stage both times.  Narrower rows are loaded
@@ -126,8 +127,8 @@ __device__ __forceinline__ float bwd_coefficient(const DropNormArgs& a, float s2
 }
 
 // ------------------------------------------------------------- narrow rows
-// L lanes a row (8, 16 or 32), K blocks of 8 a lane: P = 8 L K <= 1024.  A
-// CTA takes (threads x 32 / L) rows at a time.  Every thread copies its
+// L lanes a row (8, 16 or 32), K blocks of 8 a lane: P = 8 L K, up to 256
+// (K = 1), backward up to 1024 for 2-byte types.  A CTA takes (threads x 32 / L) rows at a time.  Every thread copies its
 // blocks of the next rows into a ring of shared memory that only it reads.
 constexpr int kNarrowThreads = 256;
 
@@ -172,12 +173,12 @@ __device__ __forceinline__ void narrow_issue(const void* const (&src)[N], int64_
     copy_ahead_commit();
 }
 
-template <int E, int L, int K>
+template <int E, int L>
 __global__ void __launch_bounds__(kNarrowThreads) drop_norm_fwd_narrow(const DropNormArgs a)
 {
     using T = typename Elem<E>::T;
     using V = typename Elem<E>::Block;
-    using Ring = NarrowRing<E, 2, K>;
+    using Ring = NarrowRing<E, 2, 1>;
     extern __shared__ __align__(128) unsigned char stage_mem[];
     const int t = threadIdx.x & (L - 1);
     const int nblocks = a.hidden >> 3;
@@ -193,44 +194,30 @@ __global__ void __launch_bounds__(kNarrowThreads) drop_norm_fwd_narrow(const Dro
     uint32_t in = ring, slot = ring;
 #pragma unroll
     for (int i = 0; i < Ring::kSlots - 1; ++i) {
-        narrow_issue<E, 2, L, K>(src, first + i * step, a, in, t);
+        narrow_issue<E, 2, L, 1>(src, first + i * step, a, in, t);
         in = Ring::after(in, ring);
     }
     const uint2 offset = drop_offset(a.drop);
-    V wv[K];
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-        wv[j] = V{};
-        if (t + j * L < nblocks)
-            ld_block(static_cast<const T*>(a.weight), t + j * L, wv[j]);
-    }
+    V wv = V{};
+    if (t < nblocks)
+        ld_block(static_cast<const T*>(a.weight), t, wv);
     for (int64_t base = 0; lead + base < a.n_rows; base += step) {
         const int64_t row = first + base;
-        const bool active = row < a.n_rows;
-        narrow_issue<E, 2, L, K>(src, row + (Ring::kSlots - 1) * step, a, in, t);
+        narrow_issue<E, 2, L, 1>(src, row + (Ring::kSlots - 1) * step, a, in, t);
         in = Ring::after(in, ring);
         copy_ahead_wait<Ring::kSlots - 1>();
-        float acc[K][8], part[K];
-#pragma unroll
-        for (int j = 0; j < K; ++j) {
-            const int b = t + j * L;
-            part[j] = 0.0f;
-            if (active && b < nblocks) {
-                V xv, rv;
-                lds_block(Ring::at(slot, 0, j), Ring::kPiece, xv);
-                lds_block(Ring::at(slot, 1, j), Ring::kPiece, rv);
-                fwd_block<E>(a, offset, xv, rv, row, b, acc[j]);
-                part[j] = fold8_squares(acc[j]);
-            }
-            part[j] = butterfly_sum(part[j], L);
+        const bool in_row = row < a.n_rows && t < nblocks;
+        float acc[8], part = 0.0f;
+        if (in_row) {
+            V xv, rv;
+            lds_block(Ring::at(slot, 0, 0), Ring::kPiece, xv);
+            lds_block(Ring::at(slot, 1, 0), Ring::kPiece, rv);
+            fwd_block<E>(a, offset, xv, rv, row, t, acc);
+            part = fold8_squares(acc);
         }
-        const float inv = inv_rms(fold_k<K>(part), a.hidden, a.inv_hidden, a.eps);
-#pragma unroll
-        for (int j = 0; j < K; ++j) {
-            const int b = t + j * L;
-            if (active && b < nblocks)
-                fwd_finish<E>(a, acc[j], inv, wv[j], row, b);
-        }
+        const float inv = inv_rms(butterfly_sum(part, L), a.hidden, a.inv_hidden, a.eps);
+        if (in_row)
+            fwd_finish<E>(a, acc, inv, wv, row, t);
         slot = Ring::after(slot, ring);
     }
 }
@@ -714,23 +701,25 @@ cudaError_t launch_bwd_wide(const DropNormArgs& a, const DropNormPlan& p, cudaSt
                     : launch_sized(drop_norm_bwd_wide<E, K, MAXT, MINB, false>, a, p, stream);
 }
 
-template <int E, int L, int K>
+template <int E, int L>
 cudaError_t launch_narrow(const DropNormArgs& a, const DropNormPlan& p, bool backward, cudaStream_t stream)
 {
-    return backward ? launch_sized(drop_norm_bwd_narrow<E, L, K>, a, p, stream)
-                    : launch_sized(drop_norm_fwd_narrow<E, L, K>, a, p, stream);
+    return backward ? launch_sized(drop_norm_bwd_narrow<E, L, 1>, a, p, stream)
+                    : launch_sized(drop_norm_fwd_narrow<E, L>, a, p, stream);
 }
 
 template <int E>
 cudaError_t launch_drop_norm_of(const DropNormArgs& a, const DropNormPlan& p, bool backward, cudaStream_t stream)
 {
     if (p.warp) {
-        if (p.K == 1)
-            return p.lanes == 8    ? launch_narrow<E, 8, 1>(a, p, backward, stream)
-                   : p.lanes == 16 ? launch_narrow<E, 16, 1>(a, p, backward, stream)
-                                   : launch_narrow<E, 32, 1>(a, p, backward, stream);
-        return p.K == 2 ? launch_narrow<E, 32, 2>(a, p, backward, stream)
-                        : launch_narrow<E, 32, 4>(a, p, backward, stream);
+        if constexpr (E != kElemF32) {
+            if (p.K > 1)
+                return p.K == 2 ? launch_sized(drop_norm_bwd_narrow<E, 32, 2>, a, p, stream)
+                                : launch_sized(drop_norm_bwd_narrow<E, 32, 4>, a, p, stream);
+        }
+        return p.lanes == 8    ? launch_narrow<E, 8>(a, p, backward, stream)
+               : p.lanes == 16 ? launch_narrow<E, 16>(a, p, backward, stream)
+                               : launch_narrow<E, 32>(a, p, backward, stream);
     }
     if (backward) {
         switch (p.K) {
@@ -747,13 +736,18 @@ cudaError_t launch_drop_norm_of(const DropNormArgs& a, const DropNormPlan& p, bo
             return launch_bwd_wide<E, 8, 512, 1>(a, p, stream);
         }
     }
+    constexpr bool wide_type = E == kElemF32;
     switch (p.threads * 8 * p.K) {
+    case 512:
+        return launch_fwd_wide<E, wide_type ? 64 : 32, wide_type ? 1 : 2>(a, p, stream);
+    case 1024:
+        return launch_fwd_wide<E, wide_type ? 128 : 32, wide_type ? 1 : 4>(a, p, stream);
     case 2048:
-        return launch_fwd_wide<E, 256, 1>(a, p, stream);
+        return launch_fwd_wide<E, 128, 2>(a, p, stream);
     case 4096:
-        return launch_fwd_wide<E, 256, 2>(a, p, stream);
+        return launch_fwd_wide<E, 128, 4>(a, p, stream);
     case 8192:
-        return launch_fwd_wide<E, 512, 2>(a, p, stream);
+        return launch_fwd_wide<E, 256, 4>(a, p, stream);
     case 16384:
         return launch_fwd_wide<E, 512, 4>(a, p, stream);
     default:

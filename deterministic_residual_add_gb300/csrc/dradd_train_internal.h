@@ -64,7 +64,7 @@ constexpr uint32_t narrow_slot_bytes(int elem, int n, int K)
 constexpr int narrow_ctas(int elem, int n, int K)
 {
     const uint32_t two = 2 * narrow_slot_bytes(elem, n, K);
-    const int most = n == 2 ? (K == 4 ? 3 : 4) : 2;  // what the registers allow
+    const int most = n == 2 ? 4 : 2;  // what the registers allow
     const int fit = static_cast<int>(220u * 1024u / two);
     return fit < most ? fit : most;
 }
@@ -86,7 +86,7 @@ constexpr int bwd_pair_threads(int elem) { return elem == 2 ? 256 : 320; }
 // How a call's rows are spread: a function of (n_rows, hidden, element type,
 // direction, memory) alone.
 struct DropNormPlan {
-    bool warp;     // several rows a warp, or a warp a row (P <= 1024)
+    bool warp;     // several rows a warp, or a warp a row
     bool staged;   // rows staged through shared memory by bulk copies
     int lanes;     // warp: lanes per row
     int threads;   // threads per CTA
