@@ -92,7 +92,13 @@ dradd_status run_dropout(void* out, int64_t out_stride, const void* x, int64_t x
     };
     const bool blocks = hidden % 8 == 0 && rows_aligned(out, out_stride) && rows_aligned(x, x_stride) &&
                         (!add || rows_aligned(residual, residual_stride));
-    return launch_dropout(a, dtype, blocks, L.sm_count, stream) == cudaSuccess ? DRADD_OK : DRADD_ERR_CUDA;
+    auto one_run = [&](const void* p, int64_t stride) {
+        return aligned(p, 16) && (n_rows == 1 || stride == hidden);
+    };
+    const bool flat = hidden >= kFlatHidden && one_run(out, out_stride) && one_run(x, x_stride) &&
+                      (!add || one_run(residual, residual_stride));
+    const DropoutLayout layout = blocks ? kDropoutBlocks : flat ? kDropoutFlat : kDropoutRagged;
+    return launch_dropout(a, dtype, layout, L.sm_count, stream) == cudaSuccess ? DRADD_OK : DRADD_ERR_CUDA;
 }
 
 // ------------------------------------- dropout + residual add + RMSNorm

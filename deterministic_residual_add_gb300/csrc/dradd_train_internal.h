@@ -26,9 +26,12 @@ constexpr int kDropoutThreads = 256;
 // CTAs launched per SM at most: eight waves of the eight that fit at once.
 constexpr int kDropoutCtasPerSm = 64;
 
-// blocks: hidden, strides and addresses let every row move as aligned blocks
-// of 8 elements.
-cudaError_t launch_dropout(const DropoutArgs& a, int elem, bool blocks, int sm_count, cudaStream_t stream);
+// Blocks: hidden, strides and addresses let every row move as aligned blocks
+// of 8 elements.  Flat: contiguous 16-byte aligned tensors, at least
+// kFlatHidden wide.  Ragged: anything.
+enum DropoutLayout : int { kDropoutBlocks = 0, kDropoutFlat = 1, kDropoutRagged = 2 };
+constexpr int64_t kFlatHidden = 8;
+cudaError_t launch_dropout(const DropoutArgs& a, int elem, DropoutLayout layout, int sm_count, cudaStream_t stream);
 
 // ------------------------------------- dropout + residual add + RMSNorm
 struct DropNormArgs {

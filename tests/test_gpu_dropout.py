@@ -43,6 +43,21 @@ def test_dropout_bits(rows, cols, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cols", [8, 9, 15, 17, 63, 65, 71, 100, 127, 250, 254, 257, 511, 1023])
+def test_dropout_of_widths_no_vector_divides(cols, dtype):
+    """Contiguous rows back to back: vectors across one or more row ends, at
+    every phase, in more than one round of the grid for the narrow ones."""
+    for rows in (1, 2, 7, 1000):
+        x = normal((rows, cols), dtype, rows + cols)
+        got = dr.dropout_fwd(x.to(cuda()), 0.4, seed=SEED, offset=OFFSET)
+        tr.assert_same_bits(got, tr.dropped32(x, 0.4, SEED, OFFSET).to(dtype), f"{rows} rows")
+    x = normal((40009, 257), dtype, 3)  # 40 MB of fp32: several rounds of the largest grid
+    xd = x.to(cuda())
+    got = dr.dropout_add_fwd(xd, xd, 0.4, seed=SEED, offset=OFFSET, residual_out=xd)
+    tr.assert_same_bits(got, (x.float() + tr.dropped32(x, 0.4, SEED, OFFSET)).to(dtype), "in place")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_dropout_strided_rows_and_neighbours(dtype):
     """Row-strided and unaligned views: the mask follows (row, column) of the
     view, and nothing outside it is written."""
