@@ -293,9 +293,9 @@ dradd_status rope_check(const dradd_rope& r, const RopeSideArgs (&sides)[2], boo
             const View v = heads_view(*t[i], r, heads[s], eb);
             if (!view_fits(v))
                 return DRADD_ERR_BAD_SHAPE;
-            vec = vec && aligned(t[i]->data, 16);
-            for (int d = 0; d < v.nd; ++d)
-                vec = vec && (v.stride[d] == 1 || v.stride[d] * eb % 16 == 0);
+            const auto whole = [&](int64_t n, int64_t stride) { return n == 1 || stride * eb % 16 == 0; };
+            vec = vec && aligned(t[i]->data, 16) && whole(r.batch, t[i]->batch_stride) &&
+                  whole(r.seq, t[i]->seq_stride) && whole(heads[s], t[i]->head_stride);
             if (i == 0)
                 outs[n_out++] = v;
             else

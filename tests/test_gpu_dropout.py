@@ -337,4 +337,25 @@ def test_streams_and_pinned_memory():
     torch.cuda.synchronize()
     for a, b in zip((out, ro, dx, dres, dw), (*want, *want_bwd)):
         assert torch.equal(a.cpu(), b.cpu())
+    # narrow rows, and dropout alone
+    for n, h in ((50, 200), (50, 1000)):
+        hx, hr, hw = (normal(sh, torch.bfloat16, 5 + i).pin_memory() for i, sh in enumerate(((n, h), (n, h), (h,))))
+        out, ro, dx, dres = (torch.empty_like(hx).pin_memory() for _ in range(4))
+        dw = torch.empty(h, device=cuda())
+        want = dr.dropout_add_rmsnorm_fwd(hx.to(cuda()), hr.to(cuda()), hw.to(cuda()), 0.1, EPS, seed=SEED)
+        want_bwd = dr.dropout_add_rmsnorm_bwd(hx.to(cuda()), None, want[1], hw.to(cuda()), 0.1, EPS, seed=SEED)
+        assert L.dropout_add_rmsnorm_fwd(out.data_ptr(), ro.data_ptr(), hx.data_ptr(), hr.data_ptr(), hw.data_ptr(),
+                                         EPS, n, h, ctypes.byref(d), 0, s) == 0
+        assert L.dropout_add_rmsnorm_bwd(dx.data_ptr(), dres.data_ptr(), dw.data_ptr(), hx.data_ptr(), None,
+                                         ro.data_ptr(), hw.data_ptr(), EPS, n, h, ctypes.byref(d), 0, ws.data_ptr(),
+                                         ws.numel(), s) == 0
+        torch.cuda.synchronize()
+        for a, b in zip((out, ro, dx, dres, dw), (*want, *want_bwd)):
+            assert torch.equal(a.cpu(), b.cpu())
+        for cols in (h, h - 1):
+            x = hx[:, :cols].contiguous().pin_memory()
+            got = torch.empty_like(x).pin_memory()
+            assert L.dropout_fwd(got.data_ptr(), cols, x.data_ptr(), cols, n, cols, ctypes.byref(d), 0, s) == 0
+            torch.cuda.synchronize()
+            tr.assert_same_bits(got, tr.dropped32(x, 0.1, SEED).to(x.dtype), "pinned dropout")
     assert dr.device_status() == 0

@@ -1,5 +1,6 @@
 """Rotary positions of q and k, plain and behind their RMSNorm, and the
 gradients, on the GPU against fp64 within derived bounds."""
+import ctypes
 import itertools
 from fractions import Fraction
 
@@ -123,6 +124,29 @@ def test_layouts_in_place_and_neighbours():
             dr.rope_fwd(q.to(cuda()), None, freq, q_out=one)
         with pytest.raises(dr.DraddError):
             dr.rope_fwd(dev[:, :, :4], dev[:, :, 4:6], freq, q_out=dev[:, :, 1:5])
+
+
+def test_overlapping_inputs_and_pinned_memory():
+    """Inputs whose rows overlap by all but one element, whatever that does to
+    their alignment, and buffers the device reaches over the host link."""
+    freq = dr.rope_frequencies(64).to(cuda())
+    w = normal(64, torch.bfloat16, 2, 0.1, 1.0).to(cuda())
+    for dtype, strides in itertools.product(DTYPES, ((0, 1, 64, 1), (64, 64, 1, 1), (1, 8, 64, 1), (3, 0, 2, 1))):
+        room = normal((4096,), dtype, 5).to(cuda())
+        q = room.as_strided((2, 9, 4, 64), strides)
+        assert torch.equal(dr.rope_fwd(q, None, freq)[0], dr.rope_fwd(q.contiguous(), None, freq)[0])
+        a = dr.qk_rmsnorm_rope_fwd(q, None, w.to(dtype), None, freq)[0]
+        assert torch.equal(a, dr.qk_rmsnorm_rope_fwd(q.contiguous(), None, w.to(dtype), None, freq)[0])
+    L = dr.lib()
+    q = normal((2, 9, 4, 64), torch.bfloat16, 6)
+    want = dr.rope_fwd(q.to(cuda()), None, freq, position0=7)[0]
+    host, out = q.pin_memory(), torch.empty_like(q).pin_memory()
+    heads = [tr.CHeads(t.data_ptr(), 9 * 256, 256, 64) for t in (out, host)]
+    r = tr.CRope(2, 9, 4, 0, 64, 64, 0, freq.data_ptr(), None, 7, 1.0)
+    assert L.rope_fwd(ctypes.byref(heads[0]), None, ctypes.byref(heads[1]), None, ctypes.byref(r), 0,
+                      torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(out, want.cpu())
 
 
 def test_columns_that_pass_hold_anything():
