@@ -465,8 +465,6 @@ def qk_rmsnorm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, q_ep
     dqw = dkw = wsp = None
     nbytes = 0
     if weight_grad:
-        if dq_weight is None and dk_weight is None and k is not None:
-            dq_weight, dk_weight = torch.empty(2, *width, dtype=torch.float32, device=q.device).unbind(0)
         if dq_weight is None:
             dq_weight = torch.empty(width, dtype=torch.float32, device=q.device)
         dqw = _flat(dq_weight, "dq_weight", torch.float32, device, width)
