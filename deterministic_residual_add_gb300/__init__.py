@@ -12,6 +12,9 @@ every call fails loudly if the library cannot be loaded.
 The operation is rmsnorm2d_fwd_with_add as defined on the ROCm/aiter issue
 #5151 page ("Steps to Reproduce", reference()), with round-to-nearest-even
 bf16 stores and a reduction order that never depends on the launch.
+
+train.py adds dropout, the gradients, and rotary positions of q and k; its
+functions are exported here too.
 """
 from __future__ import annotations
 

@@ -17,12 +17,19 @@
 //   order, so the bits depend on the shape and the element type alone.
 //
 // Bound by the memory: 4 elements of traffic an element forward, 5 backward.
-// Rows of P > 256 (P: hidden rounded up to a power of two), backward P > 1024
-// for 2-byte types, go through
-// shared memory, one CTA a row, staged `stages` rows ahead by bulk copies;
-// the backward pass needs h and dout twice, before and after the row's sums,
-// and takes them from the stage both times.  Narrower rows are loaded
-// straight into registers, a warp (or 8 or 16 lanes) a row.
+// Rows of P > 256 (P: hidden rounded up to a power of two; backward, 2-byte
+// types, P > 1024) go through shared memory, one CTA a row, staged `stages`
+// rows ahead by bulk copies.  The forward keeps acc in registers between its
+// two passes; the backward pass keeps h and dout there up to two blocks of 8
+// a thread, so that the slot is refilled at once, and reads longer rows from
+// the slot again.  Narrower rows take a warp (or 8 or 16 lanes) each, with
+// the next rows on their way into shared memory that only their lane reads.
+//
+// Measured on GB300 (device time; share of the 6.79 TB/s a copy reaches):
+// forward bf16 4096 x 8192 41.9 us (94 %), 16384 x 4096 88.8 (89 %), 4096 x
+// 1024 5.9 (84 %), fp32 1999 x 5120 25.3 (95 %); backward bf16 8192 x 8192
+// 108.5 us (91 %), 4096 x 4096 30.6 (81 %), 4096 x 1024 12.3 (50 %; the sums
+// of dweight's parts are 3 us of any call), fp32 1999 x 5120 38.4 (78 %).
 #pragma once
 
 #include "dradd_elem.cuh"
