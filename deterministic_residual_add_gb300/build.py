@@ -1,8 +1,9 @@
-"""Build libdradd.so in-tree with nvcc for sm_103a.
+"""Build libdradd.so in-tree with nvcc for sm_103a, and _binding.so, the
+compiled part of the Python binding, with the host compiler.
 
 Each .cu translation unit is compiled in parallel, then linked into a shared
 library next to this file.  `python -m deterministic_residual_add_gb300.build`
-builds it from the command line.
+builds both from the command line.
 """
 from __future__ import annotations
 
@@ -10,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import threading
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
@@ -20,6 +22,8 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 BUILD = PKG / "_build"
 LIB = PKG / "libdradd.so"
+BINDING = PKG / "_binding.so"
+BINDING_SRC = CSRC / "dradd_binding.cpp"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # No fast math: IEEE division and square root, no flush to zero, and no
@@ -46,14 +50,52 @@ def _deps():
 
 
 def stale() -> bool:
-    if not LIB.exists():
+    if not LIB.exists() or not BINDING.exists():
         return True
     t = LIB.stat().st_mtime
-    return any(p.stat().st_mtime > t for p in _deps())
+    if any(p.stat().st_mtime > t for p in _deps()):
+        return True
+    t = BINDING.stat().st_mtime
+    return any(p.stat().st_mtime > t for p in [BINDING_SRC, *INCLUDE.glob("*.h")])
+
+
+def _binding_flags():
+    """Compiler flags against the installed torch and Python."""
+    import torch
+
+    root = Path(torch.__file__).resolve().parent
+    inc = [root / "include", root / "include/torch/csrc/api/include", Path(nvcc()).resolve().parents[1] / "include",
+           Path(sysconfig.get_paths()["include"]), INCLUDE]
+    return ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in inc)], root / "lib"
+
+
+def _run(cmd, what: str):
+    r = subprocess.run([str(c) for c in cmd], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_binding() -> Path:
+    flags, _ = _binding_flags()
+    obj = BUILD / "dradd_binding.o"
+    _run(["g++", *flags, "-c", BINDING_SRC, "-o", obj], "compiling the binding")
+    return obj
+
+
+def _link_binding(obj: Path):
+    """Against libdradd.so beside it; torch's libraries are loaded already
+    when the module is imported."""
+    _, libs = _binding_flags()
+    tmp = BINDING.with_suffix(f".so.tmp{os.getpid()}")
+    _run(["g++", "-shared", obj, "-o", tmp, f"-L{PKG}", "-ldradd", "-Wl,-rpath,$ORIGIN", f"-L{libs}", "-lc10",
+          "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"], "linking the binding")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> Path:
-    """Compile and link libdradd.so if it is missing or older than a source."""
+    """Compile and link libdradd.so and _binding.so if one is missing or older
+    than a source."""
     with _lock:
         if not force and not stale():
             return LIB
@@ -71,14 +113,17 @@ def build(force: bool = False, verbose: bool = False) -> Path:
             return obj
 
         srcs = _sources()
-        with ThreadPoolExecutor(len(srcs)) as ex:
+        with ThreadPoolExecutor(len(srcs) + 1) as ex:
+            binding = ex.submit(_compile_binding)
             objs = list(ex.map(compile_one, srcs))
+            binding_obj = binding.result()
         tmp = LIB.with_suffix(f".so.tmp{os.getpid()}")
         cmd = [cc, *ARCH, "-shared", "-o", str(tmp), *map(str, objs)]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+        _link_binding(binding_obj)
         if verbose:
             for f in sorted(BUILD.glob("*.ptxas.txt")):
                 print(f.read_text())

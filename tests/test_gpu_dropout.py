@@ -323,6 +323,8 @@ def test_streams_and_pinned_memory():
     assert all(torch.equal(a, b) for got in many for a, b in zip(got, want_bwd))
     # buffers the device reaches over the host link take the direct kernels
     L = dr.lib()
+    for name in ("dropout_fwd", "dropout_add_rmsnorm_fwd", "dropout_add_rmsnorm_bwd"):
+        tr.c_entry(L, name)
     hx, hr, hw, hd = (t.pin_memory() for t in (x, r, w, dout))
     out, ro, dx, dres = (torch.empty_like(x).pin_memory() for _ in range(4))
     dw = torch.empty(4096, device=cuda())

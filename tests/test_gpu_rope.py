@@ -143,7 +143,7 @@ def test_overlapping_inputs_and_pinned_memory():
     host, out = q.pin_memory(), torch.empty_like(q).pin_memory()
     heads = [tr.CHeads(t.data_ptr(), 9 * 256, 256, 64) for t in (out, host)]
     r = tr.CRope(2, 9, 4, 0, 64, 64, 0, freq.data_ptr(), None, 7, 1.0)
-    assert L.rope_fwd(ctypes.byref(heads[0]), None, ctypes.byref(heads[1]), None, ctypes.byref(r), 0,
+    assert tr.c_entry(L, "rope_fwd")(ctypes.byref(heads[0]), None, ctypes.byref(heads[1]), None, ctypes.byref(r), 0,
                       torch.cuda.current_stream().cuda_stream) == 0
     torch.cuda.synchronize()
     assert torch.equal(out, want.cpu())

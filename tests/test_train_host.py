@@ -27,7 +27,11 @@ def reaches_device(status):
 @pytest.fixture(scope="module")
 def L():
     drbuild.build()
-    return dr.lib()
+    L = dr.lib()
+    for name in ("dropout_fwd", "dropout_add_fwd", "dropout_add_rmsnorm_fwd", "dropout_add_rmsnorm_bwd",
+                 "add_rmsnorm_bwd", "rope_fwd", "rope_bwd", "qk_rmsnorm_rope_fwd", "qk_rmsnorm_rope_bwd"):
+        tr.c_entry(L, name)
+    return L
 
 
 @pytest.mark.parametrize("rounds,counter,key,out", [
@@ -290,18 +294,17 @@ def test_binding_refuses_host_tensors_and_types(L):
         dr.dropout_fwd(x.double(), 0.1, seed=1)
 
 
-def test_packed_structures_match_the_header():
-    """The binding packs dradd_dropout, dradd_heads and dradd_rope as bytes."""
-    from deterministic_residual_add_gb300 import train
-    d = _Dropout.from_buffer_copy(train._pack_dropout(0.25, 2 ** 64 - 1, 7, 0x1234567890))
-    assert (d.p, d.seed, d.offset, d.step) == (0.25, 2 ** 64 - 1, 7, 0x1234567890)
-    h = _Heads.from_buffer_copy(train._pack_heads(0xFFFF000012340000, 5, 6, 7))
-    assert (h.data, h.batch_stride, h.seq_stride, h.head_stride) == (0xFFFF000012340000, 5, 6, 7)
-    packed = train._pack_rope(1, 2, 3, 4, 5, 6, 1, 0x7000, 0x8000, -9, 1.5)
-    assert len(packed) == ctypes.sizeof(_Rope)
-    r = _Rope.from_buffer_copy(packed)
-    assert [getattr(r, f) for f, _ in _Rope._fields_] == [1, 2, 3, 4, 5, 6, 1, 0x7000, 0x8000, -9, 1.5]
-    assert len(train._pack_dropout(0, 0, 0, 0)) == ctypes.sizeof(_Dropout)
+def test_binding_checks_types_before_anything_else(L):
+    """Arguments that are not tensors or numbers, and a wrong number of them."""
+    from deterministic_residual_add_gb300 import _binding, train
+    x = torch.zeros(4, 64)
+    for call in (lambda: dr.dropout_fwd(None, 0.1, seed=1), lambda: dr.dropout_fwd([1.0], 0.1, seed=1),
+                 lambda: dr.dropout_add_fwd(x, None, 0.1, seed=1), lambda: dr.rope_fwd("q", None, None),
+                 lambda: dr.dropout_add_rmsnorm_fwd(x, x, None, 0.1, seed=1),
+                 lambda: _binding.dropout(x), lambda: _binding.rope()):
+        with pytest.raises(TypeError):
+            call()
+    assert train._C is _binding
 
 
 def test_references_agree_with_autograd():

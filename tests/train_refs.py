@@ -30,6 +30,26 @@ class CRope(ctypes.Structure):
         ("position0", ctypes.c_int64), ("scale", ctypes.c_float)]
 
 
+def c_entry(L, name):
+    """An entry point of dradd_train.h for the C structures above: pointers
+    by ctypes.byref, the rest converted by these argument types."""
+    vp, i64, f32, i32, size = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int, ctypes.c_size_t
+    f = getattr(L, name)
+    f.argtypes = {
+        "dropout_fwd": [vp, i64, vp, i64, i64, i64, vp, i32, vp],
+        "dropout_add_fwd": [vp, i64, vp, i64, vp, i64, i64, i64, vp, i32, vp],
+        "dropout_add_rmsnorm_fwd": [vp] * 5 + [f32, i64, i64, vp, i32, vp],
+        "dropout_add_rmsnorm_bwd": [vp] * 7 + [f32, i64, i64, vp, i32, vp, size, vp],
+        "add_rmsnorm_bwd": [vp] * 6 + [f32, i64, i64, i32, vp, size, vp],
+        "rope_fwd": [vp] * 5 + [i32, vp],
+        "rope_bwd": [vp] * 5 + [i32, vp],
+        "qk_rmsnorm_rope_fwd": [vp] * 6 + [f32, f32, vp, i32, vp],
+        "qk_rmsnorm_rope_bwd": [vp] * 10 + [f32, f32, vp, i32, vp, size, vp],
+    }[name]
+    f.restype = i32
+    return f
+
+
 HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
 # half the spacing of a type's smallest values: what a rounding may add there
 TINY = {torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25, torch.float32: 2.0 ** -150}
