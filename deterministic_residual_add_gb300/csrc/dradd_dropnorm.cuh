@@ -28,8 +28,8 @@
 // Measured on GB300 (device time; share of the 6.79 TB/s a copy reaches):
 // forward bf16 4096 x 8192 41.9 us (94 %), 16384 x 4096 88.8 (89 %), 4096 x
 // 1024 5.9 (84 %), fp32 1999 x 5120 25.3 (95 %); backward bf16 8192 x 8192
-// 108.5 us (91 %), 4096 x 4096 30.6 (81 %), 4096 x 1024 12.3 (50 %; the sums
-// of dweight's parts are 3 us of any call), fp32 1999 x 5120 38.4 (78 %).
+// 108.5 us (91 %), 4096 x 4096 30.6 (81 %), 4096 x 1024 12.2 (50 %; the sums
+// of dweight's parts are 3 us of any call), fp32 1999 x 5120 37.4 (81 %).
 #pragma once
 
 #include "dradd_elem.cuh"
@@ -559,6 +559,17 @@ __global__ void __launch_bounds__(MAXT, MINB) drop_norm_bwd_wide(const DropNormA
     }
     const uint2 offset = drop_offset(a.drop);
     const X* wrow = static_cast<const X*>(a.weight);
+    // fp32 weights stay in registers too where the row does: shared memory
+    // leaves the L1 cache too small for them (2048 x 4096 31.6 us, read again
+    // every row 33.5); 2-byte ones fit, and the registers do more elsewhere
+    // (16384 x 4096 bf16 110 us, held 117).
+    constexpr bool HOLD_WEIGHTS = HOLD && E == kElemF32;
+    V wv[H];
+    if constexpr (HOLD_WEIGHTS) {
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            ld_block(wrow, j < K - 1 || tid + j * T < nblocks ? tid + j * T : nblocks - 1, wv[j]);
+    }
     float dw[K][8] = {};
     int s = 0, buf = 0;
     uint32_t parity = 0;
@@ -576,14 +587,15 @@ __global__ void __launch_bounds__(MAXT, MINB) drop_norm_bwd_wide(const DropNormA
             ds = static_cast<const X*>(a.dresidual_out) + row * a.hidden;
         }
         float h[H][8], g[H][8];
-        V wv[H], dv[H];
+        V dv[H];
         const auto load = [&](int b, int i) {
             V v;
             ld_block(hs, b, v);
             Elem<E>::unpack(v, h[i]);
             ld_block(gs, b, v);
             Elem<E>::unpack(v, g[i]);
-            ld_block(wrow, b, wv[i]);
+            if constexpr (!HOLD_WEIGHTS)
+                ld_block(wrow, b, wv[i]);
         };
         // T is nblocks / K rounded up to whole warps, so only the last of a
         // thread's blocks may lie past the row; it is then read from the last
@@ -735,8 +747,11 @@ cudaError_t launch_drop_norm_of(const DropNormArgs& a, const DropNormPlan& p, bo
         case 2:
             if (p.threads <= 256)
                 return launch_bwd_wide<E, 2, 256, 2>(a, p, stream);
-            return p.threads <= bwd_pair_threads(E) ? launch_bwd_wide<E, 2, 320, 2>(a, p, stream)
-                                                    : launch_bwd_wide<E, 2, 512, 1>(a, p, stream);
+            if constexpr (bwd_pair_threads(E) > 256) {
+                if (p.threads <= bwd_pair_threads(E))
+                    return launch_bwd_wide<E, 2, bwd_pair_threads(E), 2>(a, p, stream);
+            }
+            return launch_bwd_wide<E, 2, 512, 1>(a, p, stream);
         case 4:
             return launch_bwd_wide<E, 4, 512, 1>(a, p, stream);
         default:
