@@ -18,9 +18,10 @@
 // columns and their partners, or 16 that pass; interleaved 16 consecutive
 // ones.  A head's units go to `group` neighbouring lanes (a power of two, so
 // the norm's sums are butterflies within the group), so a warp takes
-// 32 / group heads at a time; one such step is all of q or all of k.  A warp
-// takes a token, computes its cosines and sines once, two or so a lane, into
-// shared memory of its own, and goes through `steps_per_warp` steps; no
+// 32 / group heads at a time: of one token, or, where that would leave lanes
+// idle, one head each of several tokens.  One such step is all of q or all of
+// k.  A warp computes its tokens' cosines and sines once, two or so a lane,
+// into shared memory of its own, and goes through `steps_per_warp` steps; no
 // barrier but the CTA's first.
 //
 // Bound by the memory (2 elements of traffic an element, the gradient 3), so
@@ -30,7 +31,7 @@
 //
 // Measured on GB300 (device time; share of the 6.79 TB/s a copy reaches), 32
 // + 8 heads of 128, bf16: rotation of 4096 tokens 13.3 us (93 %), behind the
-// norm of 8192 tokens 29.5 us (84 %), its gradient for 4096 tokens 28.2 us
+// norm of 8192 tokens 29.3 us (84 %), its gradient for 4096 tokens 28.2 us
 // (66 %).  What holds the last two back is instructions: 248 and 287 a warp
 // and step against 154 for the rotation alone, at an issue rate of 73 % with
 // 32 warps an SM and 50 % with the gradient's 16 (128 registers: the 32 sums
@@ -290,7 +291,7 @@ struct RopeRing {
 };
 
 // The CTA's shared memory: the warps' rings (BLOCKS only), the pairs'
-// fractions, the weights (norm only), then every warp's table of cosines and
+// fractions, the weights (norm only), then every warp's tables of cosines and
 // sines.
 struct RopeShared {
     unsigned char* ring;  // this warp's
@@ -299,7 +300,14 @@ struct RopeShared {
     float* table;  // this warp's
 };
 
-template <bool NORM>
+// Tables of cosines and sines a warp keeps.
+template <bool TOK>
+__host__ __device__ __forceinline__ int rope_tables(const RopeArgs& p)
+{
+    return TOK ? 32 / p.group : 1;
+}
+
+template <bool NORM, bool TOK>
 __device__ __forceinline__ RopeShared rope_shared(const RopeArgs& p, unsigned char* mem, int ring_bytes)
 {
     const int warp = threadIdx.x >> 5;
@@ -307,7 +315,7 @@ __device__ __forceinline__ RopeShared rope_shared(const RopeArgs& p, unsigned ch
     sh.ring = mem + warp * (ring_bytes / (kRopeThreads / 32));
     sh.fractions = reinterpret_cast<uint64_t*>(mem + ring_bytes);
     sh.weights = reinterpret_cast<float*>(sh.fractions + 8 * p.rot_units);
-    sh.table = sh.weights + (NORM ? 32 * p.units : 0) + warp * 16 * p.rot_units;
+    sh.table = sh.weights + (NORM ? 32 * p.units : 0) + warp * rope_tables<TOK>(p) * 16 * p.rot_units;
     return sh;
 }
 
@@ -321,23 +329,27 @@ __device__ __forceinline__ void rope_prologue(const RopeArgs& p, const RopeShare
     __syncthreads();
 }
 
-// The warp's table for one position.  What lies past rot / 2 is never used.
-__device__ __forceinline__ void fill_angles(const RopeArgs& p, const RopeShared& sh, int64_t position, int lane)
+// The table of the lane's token, filled by the warp together, or by each
+// lane group for its own token.  What lies past rot / 2 is never used.
+template <bool TOK>
+__device__ __forceinline__ void fill_angles(const RopeArgs& p, const RopeShared& sh, int64_t position, int lane,
+                                            int group)
 {
+    float* const table = sh.table + (TOK ? (lane / group) * 16 * p.rot_units : 0);
     __syncwarp();
-    for (int i = lane; i < (p.rot >> 1); i += 32) {
+    for (int i = TOK ? lane & (group - 1) : lane; i < (p.rot >> 1); i += TOK ? group : 32) {
         float c, s;
         turn_cos_sin(sh.fractions[i], position, c, s);
-        sh.table[table_at(p.rot_units, i >> 3, i & 7)] = __fmul_rn(c, p.scale);
-        sh.table[table_at(p.rot_units, i >> 3, 8 + (i & 7))] = __fmul_rn(s, __fmul_rn(p.scale, p.sign));
+        table[table_at(p.rot_units, i >> 3, i & 7)] = __fmul_rn(c, p.scale);
+        table[table_at(p.rot_units, i >> 3, 8 + (i & 7))] = __fmul_rn(s, __fmul_rn(p.scale, p.sign));
     }
     __syncwarp();
 }
 
 // One lane's way through the steps of a work item in the tensors W: first
 // its heads of q, then those of k.  Everything but the addresses and `left`
-// is uniform over the warp.
-template <int... W>
+// is uniform over the warp; with TOK the token is the lane group's own.
+template <bool TOK, int... W>
 struct HeadWalk {
     static constexpr int N = sizeof...(W);
     const char* at[N];  // the lane's first column in its head of this step
@@ -345,15 +357,16 @@ struct HeadWalk {
     int side_steps;     // left of q, or of k
     int left;           // heads of this side from the lane's on; <= 0: none
     bool is_k;
-    uint32_t b, s;
+    bool real;          // TOK: the lane's token is one of the call's
+    uint32_t b, s;      // the lane's token
 
     __device__ __forceinline__ int64_t token(const RopeArgs& p) const { return b * p.seq + s; }
     __device__ __forceinline__ void side(const RopeArgs& p, const RopeSide& sd, int step, int per_step, int g,
                                          int first_byte)
     {
         constexpr int which[N] = {W...};
-        const int head = step * per_step + g;
-        left = sd.heads - head;
+        const int head = step * per_step + (TOK ? 0 : g);
+        left = !TOK || real ? sd.heads - head : 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const HeadsView& v = sd.t[which[i]];
@@ -362,8 +375,16 @@ struct HeadWalk {
     }
     __device__ __forceinline__ void begin(const RopeArgs& p, uint32_t w, int per_step, int g, int first_byte)
     {
-        const uint32_t token = p.warps_per_token == 1 ? w : w / static_cast<uint32_t>(p.warps_per_token);
-        const int first = static_cast<int>(w - token * static_cast<uint32_t>(p.warps_per_token)) * p.steps_per_warp;
+        const uint32_t item = p.warps_per_item == 1 ? w : w / static_cast<uint32_t>(p.warps_per_item);
+        const int first = static_cast<int>(w - item * static_cast<uint32_t>(p.warps_per_item)) * p.steps_per_warp;
+        uint32_t token = item;
+        real = true;
+        if constexpr (TOK) {
+            token = item * (32u / p.group) + g;
+            real = token < p.tokens;
+            if (!real)
+                token = item * (32u / p.group);  // not read, but an address inside the tensor
+        }
         b = token / static_cast<uint32_t>(p.seq);
         s = token - b * static_cast<uint32_t>(p.seq);
         const int all = p.q_steps + p.k_steps - first;
@@ -399,11 +420,11 @@ struct HeadWalk {
 // items, step by step, into the lane's slots.  A run the lane's head does
 // not have is never copied (its slot keeps the zeros it starts with); a head
 // the step does not have leaves what was there, which nobody uses.
-template <int E, int... W>
+template <int E, bool TOK, int... W>
 struct RopeAhead {
     static constexpr int N = sizeof...(W);
     using Ring = RopeRing<E, N>;
-    HeadWalk<W...> walk;
+    HeadWalk<TOK, W...> walk;
     uint32_t w, warps, slot;
     bool first;  // the walk stands at its work item's first step
 
@@ -485,17 +506,17 @@ __device__ __forceinline__ float head_sum(float v, int group)
 
 // Forward: plain (NORM false; also the inverse) or behind the norm
 //   z = (x * inv) * w, inv = 1 / sqrt(sum x^2 / dim + eps).
-template <int E, bool NORM, bool INTER, int G>
+template <int E, bool NORM, bool INTER, int G, bool TOK>
 __global__ void __launch_bounds__(kRopeThreads, E == kElemF32 ? 3 : 4) rope_fwd_kernel(const RopeArgs p)
 {
     constexpr bool BLOCKS = G != 0;
     using T = typename Elem<E>::T;
     using Ring = RopeRing<E, 1>;
     extern __shared__ __align__(16) unsigned char mem[];
-    const RopeShared sh = rope_shared<NORM>(p, mem, BLOCKS ? Ring::kBytes : 0);
+    const RopeShared sh = rope_shared<NORM, TOK>(p, mem, BLOCKS ? Ring::kBytes : 0);
     const int lane = threadIdx.x & 31;
     const int group = G ? G : p.group;
-    const int per_step = G ? 32 / (G ? G : 1) : p.heads_per_step;
+    const int per_step = TOK ? 1 : G ? 32 / (G ? G : 1) : p.heads_per_step;
     const int u = lane & (group - 1);
     const int g = lane / group;
     const UnitColumns cols = unit_columns<INTER>(p, u);
@@ -507,7 +528,7 @@ __global__ void __launch_bounds__(kRopeThreads, E == kElemF32 ? 3 : 4) rope_fwd_
     const uint32_t ring = smem_u32(sh.ring) + lane * 16;
     wait_prior_grids();
     allow_next_grid();
-    RopeAhead<E, kRopeIn> ahead;
+    RopeAhead<E, TOK, kRopeIn> ahead;
     if constexpr (BLOCKS) {
         clear_ring<Ring>(sh.ring, lane);
         ahead.begin(p, ring, w, warps, per_step, g, first_byte);
@@ -516,14 +537,14 @@ __global__ void __launch_bounds__(kRopeThreads, E == kElemF32 ? 3 : 4) rope_fwd_
             ahead.issue(p, ring, lane, per_step, g, first_byte, second, has_a, has_b);
     }
     rope_prologue<E, NORM, INTER>(p, sh);
-    const float* const turn = sh.table + (cols.pairs ? u : 0) * 4;
+    const float* const turn = sh.table + (TOK ? g * 16 * p.rot_units : 0) + (cols.pairs ? u : 0) * 4;
     const float* const weight = sh.weights + (u < p.units ? u : 0) * 4;
     const bool rest = cols.pairs == 0;
     const bool skip_q = rest && p.q.skip_rest, skip_k = rest && p.k.skip_rest;
     uint32_t slot = ring;
     for (; w < p.n_work; w += warps) {
         // out, and x where it is not copied ahead
-        HeadWalk<kRopeOut, kRopeIn> walk;
+        HeadWalk<TOK, kRopeOut, kRopeIn> walk;
         walk.begin(p, w, per_step, g, first_byte);
         bool fresh = true;
         do {
@@ -535,7 +556,7 @@ __global__ void __launch_bounds__(kRopeThreads, E == kElemF32 ? 3 : 4) rope_fwd_
                 int64_t position = p.position0 + walk.s;
                 if (p.positions)
                     position = BLOCKS ? lds8(slot + Ring::kPosition - 8 * lane) : __ldg(p.positions + walk.token(p));
-                fill_angles(p, sh, position, lane);
+                fill_angles<TOK>(p, sh, position, lane, group);
                 fresh = false;
             }
             const float eps = walk.is_k ? p.k.eps : p.q.eps;
@@ -576,17 +597,17 @@ __global__ void __launch_bounds__(kRopeThreads, E == kElemF32 ? 3 : 4) rope_fwd_
 // Every lane adds the shares of its warp's work in order in registers; at
 // the end a warp's groups are added by butterfly and the CTA's warps in
 // order into the CTA's part.
-template <int E, bool INTER, int G>
+template <int E, bool INTER, int G, bool TOK>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArgs p)
 {
     constexpr bool BLOCKS = G != 0;
     using T = typename Elem<E>::T;
     using Ring = RopeRing<E, 2>;
     extern __shared__ __align__(16) unsigned char mem[];
-    const RopeShared sh = rope_shared<true>(p, mem, BLOCKS ? Ring::kBytes : 0);
+    const RopeShared sh = rope_shared<true, TOK>(p, mem, BLOCKS ? Ring::kBytes : 0);
     const int lane = threadIdx.x & 31;
     const int group = G ? G : p.group;
-    const int per_step = G ? 32 / (G ? G : 1) : p.heads_per_step;
+    const int per_step = TOK ? 1 : G ? 32 / (G ? G : 1) : p.heads_per_step;
     const int u = lane & (group - 1);
     const int g = lane / group;
     const UnitColumns cols = unit_columns<INTER>(p, u);
@@ -598,7 +619,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArg
     const uint32_t ring = smem_u32(sh.ring) + lane * 16;
     wait_prior_grids();
     allow_next_grid();
-    RopeAhead<E, kRopeIn, kRopeGrad> ahead;
+    RopeAhead<E, TOK, kRopeIn, kRopeGrad> ahead;
     if constexpr (BLOCKS) {
         clear_ring<Ring>(sh.ring, lane);
         ahead.begin(p, ring, w, warps, per_step, g, first_byte);
@@ -607,12 +628,12 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArg
             ahead.issue(p, ring, lane, per_step, g, first_byte, second, has_a, has_b);
     }
     rope_prologue<E, true, INTER>(p, sh);
-    const float* const turn = sh.table + (cols.pairs ? u : 0) * 4;
+    const float* const turn = sh.table + (TOK ? g * 16 * p.rot_units : 0) + (cols.pairs ? u : 0) * 4;
     const float* const weight = sh.weights + (u < p.units ? u : 0) * 4;
     float dq[2][8] = {}, dk[2][8] = {};
     uint32_t slot = ring;
     for (; w < p.n_work; w += warps) {
-        HeadWalk<kRopeOut, kRopeIn, kRopeGrad> walk;
+        HeadWalk<TOK, kRopeOut, kRopeIn, kRopeGrad> walk;
         walk.begin(p, w, per_step, g, first_byte);
         bool fresh = true;
         do {
@@ -624,7 +645,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArg
                 int64_t position = p.position0 + walk.s;
                 if (p.positions)
                     position = BLOCKS ? lds8(slot + Ring::kPosition - 8 * lane) : __ldg(p.positions + walk.token(p));
-                fill_angles(p, sh, position, lane);
+                fill_angles<TOK>(p, sh, position, lane, group);
                 fresh = false;
             }
             const float eps = walk.is_k ? p.k.eps : p.q.eps;
@@ -732,36 +753,45 @@ cudaError_t launch_rope_kernel(F fn, const RopeArgs& p, int grid, size_t smem, c
     return launch(fn, grid, kRopeThreads, smem, false, stream, p);
 }
 
-template <int E, bool INTER, int G>
+template <int E, bool INTER, int G, bool TOK>
 cudaError_t launch_rope_as(const RopeArgs& p, int mode, int grid, cudaStream_t stream)
 {
     constexpr bool BLOCKS = G != 0;
     const bool norm = mode != kRopePlain;
-    const size_t tables = static_cast<size_t>(p.rot_units) * 64 * (1 + kRopeThreads / 32) + (norm ? p.units * 128 : 0);
+    const int per_cta = 1 + rope_tables<TOK>(p) * (kRopeThreads / 32);  // the fractions, the tables
+    const size_t tables = static_cast<size_t>(p.rot_units) * 64 * per_cta + (norm ? p.units * 128 : 0);
     if (mode == kRopeNormBwd) {
         const size_t all = tables + (BLOCKS ? RopeRing<E, 2>::kBytes : 0);
         const size_t sums = static_cast<size_t>(p.units) * 128 * (kRopeThreads / 32);
-        return launch_rope_kernel(rope_bwd_kernel<E, INTER, G>, p, grid, all > sums ? all : sums, stream);
+        return launch_rope_kernel(rope_bwd_kernel<E, INTER, G, TOK>, p, grid, all > sums ? all : sums, stream);
     }
     const size_t all = tables + (BLOCKS ? RopeRing<E, 1>::kBytes : 0);
-    return norm ? launch_rope_kernel(rope_fwd_kernel<E, true, INTER, G>, p, grid, all, stream)
-                : launch_rope_kernel(rope_fwd_kernel<E, false, INTER, G>, p, grid, all, stream);
+    return norm ? launch_rope_kernel(rope_fwd_kernel<E, true, INTER, G, TOK>, p, grid, all, stream)
+                : launch_rope_kernel(rope_fwd_kernel<E, false, INTER, G, TOK>, p, grid, all, stream);
+}
+
+// With 32 lanes a head a warp has one lane group, so TOK does not arise.
+template <int E, bool INTER, int G>
+cudaError_t launch_rope_group(const RopeArgs& p, int mode, int grid, cudaStream_t stream)
+{
+    return p.by_token ? launch_rope_as<E, INTER, G, true>(p, mode, grid, stream)
+                      : launch_rope_as<E, INTER, G, false>(p, mode, grid, stream);
 }
 
 template <int E, bool INTER>
 cudaError_t launch_rope_layout(const RopeArgs& p, int mode, bool blocks, int grid, cudaStream_t stream)
 {
     if (!blocks)
-        return launch_rope_as<E, INTER, 0>(p, mode, grid, stream);
+        return launch_rope_group<E, INTER, 0>(p, mode, grid, stream);
     switch (p.group) {
     case 4:
-        return launch_rope_as<E, INTER, 4>(p, mode, grid, stream);
+        return launch_rope_group<E, INTER, 4>(p, mode, grid, stream);
     case 8:
-        return launch_rope_as<E, INTER, 8>(p, mode, grid, stream);
+        return launch_rope_group<E, INTER, 8>(p, mode, grid, stream);
     case 16:
-        return launch_rope_as<E, INTER, 16>(p, mode, grid, stream);
+        return launch_rope_group<E, INTER, 16>(p, mode, grid, stream);
     default:
-        return launch_rope_as<E, INTER, 32>(p, mode, grid, stream);
+        return launch_rope_as<E, INTER, 32, false>(p, mode, grid, stream);
     }
 }
 

@@ -256,7 +256,7 @@ dradd_status rope_shape(const dradd_rope* r, int dtype, RopeArgs* a, bool backwa
     a->position0 = r->position0;
     a->scale = r->scale;
     if (a->tokens > 0)
-        rope_plan(a, backward, grid);
+        rope_plan(a, dtype, backward, grid);
     return DRADD_OK;
 }
 

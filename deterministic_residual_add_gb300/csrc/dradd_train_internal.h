@@ -146,9 +146,11 @@ struct RopeArgs {
     float inv_dim;                // 1 / dim
     float scale;
     float sign;                   // +1, or -1 for the inverse rotation
-    // A step is the heads of q or of k that a warp takes at a time; a work
-    // item is steps_per_warp steps of one token.
-    int heads_per_step, q_steps, k_steps, steps_per_warp, warps_per_token;
+    // A warp has 32 / group lane groups.  They take as many heads of one
+    // token a step (by_token 0), or one head each of as many tokens (1).  A
+    // work item is steps_per_warp steps of its token or tokens.
+    int by_token;
+    int heads_per_step, q_steps, k_steps, steps_per_warp, warps_per_item;
     uint32_t n_work;
     float* partials;  // gradient: grid x 2 dim sums
 };
@@ -158,8 +160,8 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxDim = 512;
 
 // Work items and CTAs; backward: the grid is also the number of partial
-// sums.  A function of the shape alone.
-void rope_plan(RopeArgs* a, bool backward, int* grid);
+// sums.  A function of the shape and the element type alone.
+void rope_plan(RopeArgs* a, int elem, bool backward, int* grid);
 
 cudaError_t launch_rope(const RopeArgs& a, int mode, int elem, bool interleaved, bool blocks, int grid,
                         cudaStream_t stream);

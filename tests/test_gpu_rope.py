@@ -80,6 +80,27 @@ def test_rope(shape, inter, dtype):
     check_rope(*shape, inter, dtype, positions=pos, grad=True, scale=0.75)
 
 
+# many tokens of few heads: (batch, seq, q heads, k heads, head dim, rotary dim)
+MANY = [(1, 9731, 2, 2, 128, 32), (3, 3301, 4, 1, 128, 128), (1, 19467, 7, 1, 32, 32), (2, 4999, 1, 3, 80, 80),
+        (1, 5003, 3, 1, 256, 128), (7, 2800, 1, 1, 64, 64), (1, 20001, 1, 1, 24, 6)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("shape", MANY)
+def test_rope_many_tokens_of_few_heads(shape, inter, dtype):
+    check_rope(*shape, inter, dtype, position0=3)
+    b, s = shape[:2]
+    pos = torch.randint(0, 5000, (b, s), generator=torch.Generator().manual_seed(4))
+    check_rope(*shape, inter, dtype, positions=pos, grad=True, scale=0.75)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("shape", MANY)
+def test_norm_rope_many_tokens_of_few_heads(shape, inter):
+    check_norm_rope(shape, inter, torch.bfloat16)
+
+
 def test_far_positions():
     """Positions up to 2^40 and of either sign: the angle modulo one turn in
     exact rational arithmetic."""
@@ -202,6 +223,10 @@ def norm_bounds(x, w, eps):
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("shape", SHAPES)
 def test_norm_rope(shape, inter, dtype):
+    check_norm_rope(shape, inter, dtype)
+
+
+def check_norm_rope(shape, inter, dtype):
     b, s, hq, hk, d, rot = shape
     packed, q, k = case(b, s, hq, hk, d, dtype)
     dev = packed.to(cuda())
