@@ -34,8 +34,23 @@ struct ErrorSet {};
     throw ErrorSet{};
 }
 
-void check_status(dradd_status status, const char* where)
+// The interpreter's lock is free while one lives: a launch or an allocation
+// may wait for the device, and the device for a host function in the
+// interpreter.
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// Makes a call into the library; `f` must not touch Python.
+template <typename F>
+void run(const char* where, F f)
 {
+    dradd_status status;
+    {
+        const Unlocked unlocked;
+        status = f();
+    }
     if (status == DRADD_OK)
         return;
     PyObject* package = PyImport_ImportModule("deterministic_residual_add_gb300");
@@ -143,6 +158,7 @@ void* flat(const at::Tensor& t, const char* name, at::ScalarType type, c10::Devi
 
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, c10::Device device)
 {
+    const Unlocked unlocked;
     return at::empty(shape, at::TensorOptions().dtype(type).device(device));
 }
 
@@ -245,12 +261,14 @@ PyObject* dropout(PyObject* const* a)
     if (residual) {
         const Rows r(*residual, "residual", shape, c);
         if (xr.cols)
-            check_status(dropout_add_fwd(o.data, o.stride, xr.data, xr.stride, r.data, r.stride, xr.n, xr.cols, &d,
-                                         c.dtype, c.stream),
-                         "dropout_add_fwd");
+            run("dropout_add_fwd", [&] {
+                return dropout_add_fwd(o.data, o.stride, xr.data, xr.stride, r.data, r.stride, xr.n, xr.cols, &d,
+                                       c.dtype, c.stream);
+            });
     } else if (xr.cols) {
-        check_status(dropout_fwd(o.data, o.stride, xr.data, xr.stride, xr.n, xr.cols, &d, c.dtype, c.stream),
-                     "dropout_fwd");
+        run("dropout_fwd", [&] {
+            return dropout_fwd(o.data, o.stride, xr.data, xr.stride, xr.n, xr.cols, &d, c.dtype, c.stream);
+        });
     }
     return THPVariable_Wrap(out);
 }
@@ -278,10 +296,12 @@ PyObject* drop_norm_fwd(PyObject* const* a)
     const at::Tensor out = output(a[8], "out", shape, c);
     const at::Tensor residual_out = output(a[9], "residual_out", shape, c);
     const dradd_dropout d = dropout_of(a[3], a[5], a[6], a[7], c);
-    check_status(dropout_add_rmsnorm_fwd(flat(out, "out", c.type, c.device, shape),
-                                         flat(residual_out, "residual_out", c.type, c.device, shape), xp, rp, wp,
-                                         static_cast<float>(number(a[4])), n, hidden, &d, c.dtype, c.stream),
-                 "dropout_add_rmsnorm_fwd");
+    void* op = flat(out, "out", c.type, c.device, shape);
+    void* hp = flat(residual_out, "residual_out", c.type, c.device, shape);
+    const float eps = static_cast<float>(number(a[4]));
+    run("dropout_add_rmsnorm_fwd", [&] {
+        return dropout_add_rmsnorm_fwd(op, hp, xp, rp, wp, eps, n, hidden, &d, c.dtype, c.stream);
+    });
     return tuple_of({&out, &residual_out});
 }
 
@@ -326,12 +346,14 @@ PyObject* drop_norm_bwd(PyObject* const* a)
     const float eps = static_cast<float>(number(a[6]));
     if (drop) {
         const dradd_dropout d = dropout_of(a[5], a[7], a[8], a[9], c);
-        check_status(dropout_add_rmsnorm_bwd(xp, op, sp, gp, dp, hp, wp, eps, n, hidden, &d, c.dtype, ws, bytes,
-                                             c.stream),
-                     "dropout_add_rmsnorm_bwd");
+        run("dropout_add_rmsnorm_bwd", [&] {
+            return dropout_add_rmsnorm_bwd(xp, op, sp, gp, dp, hp, wp, eps, n, hidden, &d, c.dtype, ws, bytes,
+                                           c.stream);
+        });
     } else {
-        check_status(add_rmsnorm_bwd(op, sp, gp, dp, hp, wp, eps, n, hidden, c.dtype, ws, bytes, c.stream),
-                     "add_rmsnorm_bwd");
+        run("add_rmsnorm_bwd", [&] {
+            return add_rmsnorm_bwd(op, sp, gp, dp, hp, wp, eps, n, hidden, c.dtype, ws, bytes, c.stream);
+        });
     }
     return tuple_of({&dx, &dresidual, &dweight});
 }
@@ -403,8 +425,9 @@ PyObject* rope(PyObject* const* a)
         ko = sk.to;
         ki = sk.from;
     }
-    check_status((inverse ? rope_bwd : rope_fwd)(&sq.to, &ko, &sq.from, &ki, &r, c.dtype, c.stream),
-                 inverse ? "rope_bwd" : "rope_fwd");
+    run(inverse ? "rope_bwd" : "rope_fwd", [&] {
+        return (inverse ? rope_bwd : rope_fwd)(&sq.to, &ko, &sq.from, &ki, &r, c.dtype, c.stream);
+    });
     return tuple_of({&sq.out, &k_out});
 }
 
@@ -428,9 +451,10 @@ PyObject* norm_rope_fwd(PyObject* const* a)
         ko = sk.to;
         ki = sk.from;
     }
-    check_status(qk_rmsnorm_rope_fwd(&sq.to, &ko, &sq.from, &ki, qw, kw, static_cast<float>(number(a[4])),
-                                     static_cast<float>(number(a[5])), &r, c.dtype, c.stream),
-                 "qk_rmsnorm_rope_fwd");
+    const float q_eps = static_cast<float>(number(a[4])), k_eps = static_cast<float>(number(a[5]));
+    run("qk_rmsnorm_rope_fwd", [&] {
+        return qk_rmsnorm_rope_fwd(&sq.to, &ko, &sq.from, &ki, qw, kw, q_eps, k_eps, &r, c.dtype, c.stream);
+    });
     return tuple_of({&sq.out, &k_out});
 }
 
@@ -476,10 +500,11 @@ PyObject* norm_rope_bwd(PyObject* const* a)
         ws = w.data;
         bytes = w.bytes;
     }
-    check_status(qk_rmsnorm_rope_bwd(&sq.to, &ko, qs, ks, &gq, &gk, &sq.from, &ki, qw, kw,
-                                     static_cast<float>(number(a[6])), static_cast<float>(number(a[7])), &r, c.dtype,
-                                     ws, bytes, c.stream),
-                 "qk_rmsnorm_rope_bwd");
+    const float q_eps = static_cast<float>(number(a[6])), k_eps = static_cast<float>(number(a[7]));
+    run("qk_rmsnorm_rope_bwd", [&] {
+        return qk_rmsnorm_rope_bwd(&sq.to, &ko, qs, ks, &gq, &gk, &sq.from, &ki, qw, kw, q_eps, k_eps, &r, c.dtype, ws,
+                                   bytes, c.stream);
+    });
     return tuple_of({&sq.out, &dk, &dqw, &dkw});
 }
 
