@@ -27,9 +27,9 @@
 //
 // Measured on GB300 (device time; share of the 6.79 TB/s a copy reaches):
 // forward bf16 4096 x 8192 41.9 us (94 %), 16384 x 4096 88.8 (89 %), 4096 x
-// 1024 5.9 (84 %), fp32 1999 x 5120 25.3 (95 %); backward bf16 8192 x 8192
+// 1024 5.9 (84 %), fp32 8192 x 4096 85.4 (93 %); backward bf16 8192 x 8192
 // 108.5 us (91 %), 4096 x 4096 30.6 (81 %), 4096 x 1024 12.2 (50 %; the sums
-// of dweight's parts are 3 us of any call), fp32 1999 x 5120 37.4 (81 %).
+// of dweight's parts are 3 us of any call), fp32 1999 x 5120 35.5 (85 %).
 #pragma once
 
 #include "dradd_elem.cuh"

@@ -20,9 +20,9 @@
 // the norm's sums are butterflies within the group), so a warp takes
 // 32 / group heads at a time: of one token, or, where that would leave lanes
 // idle, one head each of several tokens.  One such step is all of q or all of
-// k.  A warp computes its tokens' cosines and sines once, two or so a lane,
-// into shared memory of its own, and goes through `steps_per_warp` steps; no
-// barrier but the CTA's first.
+// k.  A warp takes steps_per_warp steps in a row, across tokens, and computes
+// the cosines and sines of the tokens it comes to, two or so a lane, into
+// shared memory of its own; no barrier but the CTA's first.
 //
 // Bound by the memory (2 elements of traffic an element, the gradient 3), so
 // the bytes on their way count: every lane copies its vectors of the next
@@ -30,12 +30,12 @@
 // (cp.async, so no barrier and no registers).
 //
 // Measured on GB300 (device time; share of the 6.79 TB/s a copy reaches), 32
-// + 8 heads of 128, bf16: rotation of 4096 tokens 13.3 us (93 %), behind the
-// norm of 8192 tokens 29.3 us (84 %), its gradient for 4096 tokens 28.2 us
-// (66 %).  What holds the last two back is instructions: 248 and 287 a warp
-// and step against 154 for the rotation alone, at an issue rate of 73 % with
-// 32 warps an SM and 50 % with the gradient's 16 (128 registers: the 32 sums
-// of both weights' gradients live there).  Three CTAs of 80 registers spill
+// + 8 heads of 128, bf16: rotation of 4096 tokens 13.0 us (95 %), behind the
+// norm of 8192 tokens 29.3 us (84 %), its gradient for 4096 tokens 25.6 us
+// (72 %).  What holds the last two back is instructions: about 250 and 290 a
+// warp and step against 160 for the rotation alone, at an issue rate of 73 %
+// with 32 warps an SM and 56 % with the gradient's 16 (128 registers: the 32
+// sums of both weights' gradients live there).  Three CTAs of 80 registers spill
 // (62.6 us); a chunk of two steps with one look at the walk took fewer
 // instructions and more time; so did one walk for loads and stores, whose
 // notes of the steps between cost more than a second walk.
@@ -288,6 +288,10 @@ struct RopeRing {
     {
         return slot == ring + (kSlots - 1) * kStepBytes ? ring : slot + kStepBytes;
     }
+    static __device__ __forceinline__ uint32_t before(uint32_t slot, uint32_t ring)
+    {
+        return slot == ring ? ring + (kSlots - 1) * kStepBytes : slot - kStepBytes;
+    }
 };
 
 // The CTA's shared memory: the warps' rings (BLOCKS only), the pairs'
@@ -346,14 +350,34 @@ __device__ __forceinline__ void fill_angles(const RopeArgs& p, const RopeShared&
     __syncwarp();
 }
 
-// One lane's way through the steps of a work item in the tensors W: first
+// A warp's steps: `count` of them from step `first` of item `item` on.
+struct WarpRange {
+    uint32_t item;
+    int first, count;
+};
+
+__device__ __forceinline__ WarpRange warp_range(const RopeArgs& p, uint32_t warp)
+{
+    const int64_t from = static_cast<int64_t>(warp) * p.steps_per_warp;
+    const int64_t left = p.n_steps - from;
+    const uint32_t steps = static_cast<uint32_t>(p.q_steps + p.k_steps);
+    WarpRange r = {0, 0, 0};
+    if (left > 0) {
+        r.count = left < p.steps_per_warp ? static_cast<int>(left) : p.steps_per_warp;
+        r.item = p.n_steps >> 32 ? static_cast<uint32_t>(from / steps) : static_cast<uint32_t>(from) / steps;
+        r.first = static_cast<int>(from - static_cast<int64_t>(r.item) * steps);
+    }
+    return r;
+}
+
+// One lane's way through the steps of an item in the tensors W: first
 // its heads of q, then those of k.  Everything but the addresses and `left`
 // is uniform over the warp; with TOK the token is the lane group's own.
 template <bool TOK, int... W>
 struct HeadWalk {
     static constexpr int N = sizeof...(W);
     const char* at[N];  // the lane's first column in its head of this step
-    int steps;          // left of the work item, this one included
+    int steps;          // left of the item, this one included
     int side_steps;     // left of q, or of k
     int left;           // heads of this side from the lane's on; <= 0: none
     bool is_k;
@@ -373,12 +397,11 @@ struct HeadWalk {
             at[i] = v.data + b * v.batch + s * v.seq + head * v.head + first_byte;
         }
     }
-    __device__ __forceinline__ void begin(const RopeArgs& p, uint32_t w, int per_step, int g, int first_byte)
+    // To step `first` of an item, for `most` steps or to its end.
+    __device__ __forceinline__ void begin(const RopeArgs& p, uint32_t item, int first, int most, int per_step, int g,
+                                          int first_byte)
     {
-        const uint32_t item = p.warps_per_item == 1 ? w : w / static_cast<uint32_t>(p.warps_per_item);
-        const int first = static_cast<int>(w - item * static_cast<uint32_t>(p.warps_per_item)) * p.steps_per_warp;
         uint32_t token = item;
-        real = true;
         if constexpr (TOK) {
             token = item * (32u / p.group) + g;
             real = token < p.tokens;
@@ -388,7 +411,7 @@ struct HeadWalk {
         b = token / static_cast<uint32_t>(p.seq);
         s = token - b * static_cast<uint32_t>(p.seq);
         const int all = p.q_steps + p.k_steps - first;
-        steps = all < p.steps_per_warp ? all : p.steps_per_warp;
+        steps = all < most ? all : most;
         side_steps = p.q_steps - first;
         is_k = side_steps <= 0;
         if (is_k)
@@ -397,7 +420,7 @@ struct HeadWalk {
             side(p, p.q, first, per_step, g, first_byte);
     }
     __device__ __forceinline__ bool active() const { return left > 0; }
-    // On to the next step; false when this one was the work item's last.
+    // On to the next step; false when this one was the last.
     __device__ __forceinline__ bool advance(const RopeArgs& p, int per_step, int g, int first_byte)
     {
         if (--steps == 0)
@@ -416,8 +439,8 @@ struct HeadWalk {
     }
 };
 
-// The copies ahead of the computation: the tensors W of the warp's work
-// items, step by step, into the lane's slots.  A run the lane's head does
+// The copies ahead of the computation: the tensors W of the warp's steps,
+// one by one, into the lane's slots.  A run the lane's head does
 // not have is never copied (its slot keeps the zeros it starts with); a head
 // the step does not have leaves what was there, which nobody uses.
 template <int E, bool TOK, int... W>
@@ -425,25 +448,23 @@ struct RopeAhead {
     static constexpr int N = sizeof...(W);
     using Ring = RopeRing<E, N>;
     HeadWalk<TOK, W...> walk;
-    uint32_t w, warps, slot;
-    bool first;  // the walk stands at its work item's first step
+    uint32_t item;
+    bool fresh;  // the walk stands at an item's first step for this warp
 
-    __device__ __forceinline__ void begin(const RopeArgs& p, uint32_t ring, uint32_t w0, uint32_t n_warps,
-                                          int per_step, int g, int first_byte)
+    __device__ __forceinline__ void begin(const RopeArgs& p, const WarpRange& r, int per_step, int g,
+                                          int first_byte)
     {
-        w = w0;
-        warps = n_warps;
-        slot = ring;
-        first = true;
-        if (w < p.n_work)
-            walk.begin(p, w, per_step, g, first_byte);
+        item = r.item;
+        fresh = true;
+        if (r.count > 0)
+            walk.begin(p, item, r.first, r.count, per_step, g, first_byte);
     }
-    // Copies one step into the next slot, or nothing when no work is left.
-    // ring: the first slot, where the lane's 16-byte pieces begin.
-    __device__ __forceinline__ void issue(const RopeArgs& p, uint32_t ring, int lane, int per_step, int g,
+    // Copies one step into a slot, or nothing when no work is left.  rest:
+    // the warp's steps from this one on; slot: of the lane's 16-byte pieces.
+    __device__ __forceinline__ void issue(const RopeArgs& p, int rest, uint32_t slot, int lane, int per_step, int g,
                                           int first_byte, int second, bool has_a, bool has_b)
     {
-        if (w < p.n_work) {
+        if (rest > 0) {
             if (walk.active()) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
@@ -457,18 +478,13 @@ struct RopeAhead {
                     }
                 }
             }
-            if (first && p.positions)
+            if (fresh && p.positions)
                 copy_ahead8(slot + Ring::kPosition - 8 * lane, p.positions + walk.token(p));
-            first = false;
-            if (!walk.advance(p, per_step, g, first_byte)) {
-                w += warps;
-                first = true;
-                if (w < p.n_work)
-                    walk.begin(p, w, per_step, g, first_byte);
-            }
+            fresh = !walk.advance(p, per_step, g, first_byte);
+            if (fresh && rest > 1)
+                walk.begin(p, ++item, 0, rest - 1, per_step, g, first_byte);
         }
         copy_ahead_commit();
-        slot = Ring::after(slot, ring);
     }
 };
 
@@ -523,18 +539,17 @@ __global__ void __launch_bounds__(kRopeThreads, E == kElemF32 ? 3 : 4) rope_fwd_
     const bool has_a = cols.na != 0, has_b = cols.nb != 0;
     const int first_byte = cols.a * static_cast<int>(sizeof(T));
     const int second = (cols.b - cols.a) * static_cast<int>(sizeof(T));
-    const uint32_t warps = gridDim.x * (kRopeThreads / 32);
-    uint32_t w = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+    WarpRange range = warp_range(p, blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5));
     const uint32_t ring = smem_u32(sh.ring) + lane * 16;
     wait_prior_grids();
     allow_next_grid();
     RopeAhead<E, TOK, kRopeIn> ahead;
     if constexpr (BLOCKS) {
         clear_ring<Ring>(sh.ring, lane);
-        ahead.begin(p, ring, w, warps, per_step, g, first_byte);
+        ahead.begin(p, range, per_step, g, first_byte);
 #pragma unroll
         for (int i = 0; i < Ring::kSlots - 1; ++i)
-            ahead.issue(p, ring, lane, per_step, g, first_byte, second, has_a, has_b);
+            ahead.issue(p, range.count - i, ring + i * Ring::kStepBytes, lane, per_step, g, first_byte, second, has_a, has_b);
     }
     rope_prologue<E, NORM, INTER>(p, sh);
     const float* const turn = sh.table + (TOK ? g * 16 * p.rot_units : 0) + (cols.pairs ? u : 0) * 4;
@@ -542,14 +557,19 @@ __global__ void __launch_bounds__(kRopeThreads, E == kElemF32 ? 3 : 4) rope_fwd_
     const bool rest = cols.pairs == 0;
     const bool skip_q = rest && p.q.skip_rest, skip_k = rest && p.k.skip_rest;
     uint32_t slot = ring;
-    for (; w < p.n_work; w += warps) {
-        // out, and x where it is not copied ahead
-        HeadWalk<TOK, kRopeOut, kRopeIn> walk;
-        walk.begin(p, w, per_step, g, first_byte);
+    // The slot to fill, the one before `slot`: kept behind the norm (8192
+    // tokens of 32 + 8 heads 29.3 us, computed 30.4), computed without it
+    // (4096 tokens 13.0, kept 14.2: a register spills).
+    uint32_t into = ring + (Ring::kSlots - 1) * Ring::kStepBytes;
+    HeadWalk<TOK, kRopeOut, kRopeIn> walk;  // out, and x where it is not copied ahead
+    while (range.count > 0) {
+        walk.begin(p, range.item, range.first, range.count, per_step, g, first_byte);
         bool fresh = true;
         do {
             if constexpr (BLOCKS) {
-                ahead.issue(p, ring, lane, per_step, g, first_byte, second, has_a, has_b);
+                ahead.issue(p, range.count - (Ring::kSlots - 1), NORM ? into : Ring::before(slot, ring), lane, per_step, g,
+                            first_byte, second, has_a, has_b);
+                into = Ring::after(into, ring);
                 copy_ahead_wait<Ring::kSlots - 1>();
             }
             if (fresh) {
@@ -587,7 +607,10 @@ __global__ void __launch_bounds__(kRopeThreads, E == kElemF32 ? 3 : 4) rope_fwd_
                 turn_unit<INTER>(turn, p.rot_units, cols.pairs, a, b);
             store_unit<E, BLOCKS>(walk.at[0], second, cols, active && !skip, a, b);
             slot = Ring::after(slot, ring);
+            --range.count;
         } while (walk.advance(p, per_step, g, first_byte));
+        ++range.item;
+        range.first = 0;
     }
 }
 
@@ -614,31 +637,31 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArg
     const bool has_a = cols.na != 0, has_b = cols.nb != 0;
     const int first_byte = cols.a * static_cast<int>(sizeof(T));
     const int second = (cols.b - cols.a) * static_cast<int>(sizeof(T));
-    const uint32_t warps = gridDim.x * (kRopeThreads / 32);
-    uint32_t w = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+    WarpRange range = warp_range(p, blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5));
     const uint32_t ring = smem_u32(sh.ring) + lane * 16;
     wait_prior_grids();
     allow_next_grid();
     RopeAhead<E, TOK, kRopeIn, kRopeGrad> ahead;
     if constexpr (BLOCKS) {
         clear_ring<Ring>(sh.ring, lane);
-        ahead.begin(p, ring, w, warps, per_step, g, first_byte);
+        ahead.begin(p, range, per_step, g, first_byte);
 #pragma unroll
         for (int i = 0; i < Ring::kSlots - 1; ++i)
-            ahead.issue(p, ring, lane, per_step, g, first_byte, second, has_a, has_b);
+            ahead.issue(p, range.count - i, ring + i * Ring::kStepBytes, lane, per_step, g, first_byte, second, has_a, has_b);
     }
     rope_prologue<E, true, INTER>(p, sh);
     const float* const turn = sh.table + (TOK ? g * 16 * p.rot_units : 0) + (cols.pairs ? u : 0) * 4;
     const float* const weight = sh.weights + (u < p.units ? u : 0) * 4;
     float dq[2][8] = {}, dk[2][8] = {};
     uint32_t slot = ring;
-    for (; w < p.n_work; w += warps) {
-        HeadWalk<TOK, kRopeOut, kRopeIn, kRopeGrad> walk;
-        walk.begin(p, w, per_step, g, first_byte);
+    HeadWalk<TOK, kRopeOut, kRopeIn, kRopeGrad> walk;
+    while (range.count > 0) {
+        walk.begin(p, range.item, range.first, range.count, per_step, g, first_byte);
         bool fresh = true;
         do {
             if constexpr (BLOCKS) {
-                ahead.issue(p, ring, lane, per_step, g, first_byte, second, has_a, has_b);
+                ahead.issue(p, range.count - (Ring::kSlots - 1), Ring::before(slot, ring), lane, per_step, g, first_byte,
+                            second, has_a, has_b);
                 copy_ahead_wait<Ring::kSlots - 1>();
             }
             if (fresh) {
@@ -700,7 +723,10 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArg
             }
             store_unit<E, BLOCKS>(walk.at[0], second, cols, active, wa, wb);
             slot = Ring::after(slot, ring);
+            --range.count;
         } while (walk.advance(p, per_step, g, first_byte));
+        ++range.item;
+        range.first = 0;
     }
     if (!p.partials)
         return;

@@ -147,11 +147,12 @@ struct RopeArgs {
     float scale;
     float sign;                   // +1, or -1 for the inverse rotation
     // A warp has 32 / group lane groups.  They take as many heads of one
-    // token a step (by_token 0), or one head each of as many tokens (1).  A
-    // work item is steps_per_warp steps of its token or tokens.
+    // token a step (by_token 0), or one head each of as many tokens (1).  An
+    // item is that token or those tokens, q_steps + k_steps steps; a warp
+    // takes steps_per_warp of all n_steps, in order.
     int by_token;
-    int heads_per_step, q_steps, k_steps, steps_per_warp, warps_per_item;
-    uint32_t n_work;
+    int heads_per_step, q_steps, k_steps, steps_per_warp;
+    int64_t n_steps;
     float* partials;  // gradient: grid x 2 dim sums
 };
 
@@ -159,7 +160,7 @@ enum RopeMode : int { kRopePlain = 0, kRopeNorm = 1, kRopeNormBwd = 2 };
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxDim = 512;
 
-// Work items and CTAs; backward: the grid is also the number of partial
+// Steps and CTAs; backward: the grid is also the number of partial
 // sums.  A function of the shape and the element type alone.
 void rope_plan(RopeArgs* a, int elem, bool backward, int* grid);
 

@@ -150,6 +150,7 @@ typedef struct dradd_heads {
  * or (2 i, 2 i + 1) when interleaved.  Columns from rot_dim on pass.
  *   batch, seq, q_heads, k_heads, head_dim  k_heads may be 0: no k, whose
  *                tensors and weight are then not looked at
+ *                (batch * seq < 2^31, at most 65536 heads a side)
  *   rot_dim      even, 2 <= rot_dim <= head_dim
  *   inv_freq     device double[rot_dim / 2], radians per position, finite
  *                (rope_frequencies makes the usual ones)

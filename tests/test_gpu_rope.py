@@ -85,20 +85,26 @@ MANY = [(1, 9731, 2, 2, 128, 32), (3, 3301, 4, 1, 128, 128), (1, 19467, 7, 1, 32
         (1, 5003, 3, 1, 256, 128), (7, 2800, 1, 1, 64, 64), (1, 20001, 1, 1, 24, 6)]
 
 
+# tokens shared between warps unevenly, and several tokens a warp
+SHARED = [(3, 499, 32, 8, 128, 128), (1, 1499, 32, 8, 64, 32), (2, 2903, 9, 5, 96, 96), (1, 20011, 30, 30, 8, 8),
+          (1, 5003, 17, 4, 40, 10)]
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("inter", [False, True])
-@pytest.mark.parametrize("shape", MANY)
-def test_rope_many_tokens_of_few_heads(shape, inter, dtype):
+@pytest.mark.parametrize("shape", MANY + SHARED)
+def test_rope_many_tokens(shape, inter, dtype):
     check_rope(*shape, inter, dtype, position0=3)
     b, s = shape[:2]
     pos = torch.randint(0, 5000, (b, s), generator=torch.Generator().manual_seed(4))
     check_rope(*shape, inter, dtype, positions=pos, grad=True, scale=0.75)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("inter", [False, True])
-@pytest.mark.parametrize("shape", MANY)
-def test_norm_rope_many_tokens_of_few_heads(shape, inter):
-    check_norm_rope(shape, inter, torch.bfloat16)
+@pytest.mark.parametrize("shape", MANY + SHARED)
+def test_norm_rope_many_tokens(shape, inter, dtype):
+    check_norm_rope(shape, inter, dtype)
 
 
 def test_far_positions():
