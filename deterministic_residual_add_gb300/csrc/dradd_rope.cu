@@ -53,7 +53,7 @@ void rope_plan(RopeArgs* a, int elem, bool backward, int* grid)
     int64_t share = a->by_token ? share_groups : share_whole;
     // A share that saves no more than a step of a token's is not worth the
     // angles of two tokens: bf16 2048 tokens of 8 + 1 heads 4.4 us against
-    // 6.3, 4096 of 32 + 8 13.7 against 14.1.  Over several tokens a lane
+    // 6.3, 4096 of 32 + 8 13.0 against 13.1.  Over several tokens a lane
     // group it is: 13036 of 2 + 2 8.4 against 9.9.
     if (share < steps && share + 1 >= steps && !a->by_token)
         share = steps;
