@@ -1,4 +1,4 @@
-"""Several of the training and rotary calls at once: threads on streams of
+"""The training and rotary calls in company: threads on streams of
 their own, and captured graphs replayed side by side.  Every result has to
 have the bits of the same call made alone."""
 import threading
@@ -91,3 +91,49 @@ def test_captured_graphs_side_by_side():
         torch.cuda.synchronize()
         for o, w in zip(outs, want):
             assert same(o, w)
+
+
+def test_fp32_tensors_on_16_byte_boundaries():
+    """fp32 blocks at 32-byte boundaries move in one store, others in two:
+    the same bits, and the neighbours stay."""
+    dev = torch.device("cuda", 0)
+    g = torch.Generator().manual_seed(3)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g).to(dev)
+
+    def moved(shape):
+        """A contiguous fp32 tensor 16 bytes past a 32-byte boundary, inside a buffer of NaN."""
+        n = torch.Size(shape).numel()
+        buf = torch.full((n + 16,), float("nan"), device=dev)
+        return buf, buf[4:4 + n].view(shape)
+
+    def put(t):
+        m = moved(t.shape)[1]
+        assert m.data_ptr() % 32 == 16
+        return m.copy_(t)
+
+    for rows, hidden in ((37, 264), (300, 1024), (500, 4096)):
+        x, r, d, w = normal(rows, hidden), normal(rows, hidden), normal(rows, hidden), normal(hidden)
+        want = [dr.dropout_fwd(x, 0.3, seed=1), dr.dropout_add_fwd(x, r, 0.3, seed=1),
+                *dr.dropout_add_rmsnorm_fwd(x, r, w, 0.3, seed=1)]
+        want += dr.dropout_add_rmsnorm_bwd(d, r, want[3], w, 0.3, seed=1)[:2]
+        bufs, o = zip(*(moved((rows, hidden)) for _ in want))
+        dr.dropout_fwd(put(x), 0.3, seed=1, out=o[0])
+        dr.dropout_add_fwd(put(x), put(r), 0.3, seed=1, residual_out=o[1])
+        dr.dropout_add_rmsnorm_fwd(put(x), put(r), put(w), 0.3, seed=1, out=o[2], residual_out=o[3])
+        dr.dropout_add_rmsnorm_bwd(put(d), put(r), o[3], put(w), 0.3, seed=1, dx=o[4], dresidual=o[5])
+        for b, got, t in zip(bufs, o, want):
+            assert same([got], [t]) and b[:4].isnan().all() and b[-12:].isnan().all()
+    # heads 100 elements apart: every other one on a 32-byte boundary
+    freq = dr.rope_frequencies(96, device=dev)
+    q, dq, w = normal(2, 41, 6, 96), normal(2, 41, 6, 96), normal(96)
+    want = [dr.rope_fwd(q, None, freq)[0], dr.qk_rmsnorm_rope_fwd(q, None, w, None, freq)[0],
+            dr.qk_rmsnorm_rope_bwd(dq, None, q, None, w, None, freq)[0]]
+    bufs = [torch.full((2, 41, 6, 100), float("nan"), device=dev) for _ in want]
+    o = [b[..., :96] for b in bufs]
+    dr.rope_fwd(q, None, freq, q_out=o[0])
+    dr.qk_rmsnorm_rope_fwd(q, None, w, None, freq, q_out=o[1])
+    dr.qk_rmsnorm_rope_bwd(dq, None, q, None, w, None, freq, dq=o[2])
+    for b, got, t in zip(bufs, o, want):
+        assert same([got.contiguous()], [t]) and b[..., 96:].isnan().all()
