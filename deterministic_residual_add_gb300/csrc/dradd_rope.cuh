@@ -121,7 +121,9 @@ __device__ __forceinline__ void load_table(const float* p, int units, float (&a)
 
 // Turns the unit's first `pairs` pairs by their cosines and sines (its table
 // entry: 8 cosines, then 8 sines); the others stay, whatever they hold.  In the
-// halves layout a unit's pairs all turn or lie outside the head.
+// halves layout a unit's pairs all turn or lie outside the head: those are
+// turned by what the table holds past rot / 2, and come out finite only where
+// that is.
 template <bool INTER>
 __device__ __forceinline__ void turn_unit(const float* entry, int units, int pairs, float (&a)[8], float (&b)[8])
 {
@@ -333,8 +335,19 @@ __device__ __forceinline__ void rope_prologue(const RopeArgs& p, const RopeShare
     __syncthreads();
 }
 
+// Zeros in all of the warp's tables, for a kernel whose sums take in the
+// columns outside the head too (after turn_unit in the halves layout, where
+// rot / 2 is no multiple of 8): shared memory may hold NaN, and 0 * NaN would
+// reach every column of the head.
+template <bool TOK>
+__device__ __forceinline__ void clear_tables(const RopeArgs& p, const RopeShared& sh, int lane)
+{
+    for (int i = lane; i < rope_tables<TOK>(p) * 16 * p.rot_units; i += 32)
+        sh.table[i] = 0.0f;
+}
+
 // The table of the lane's token, filled by the warp together, or by each
-// lane group for its own token.  What lies past rot / 2 is never used.
+// lane group for its own token.  What lies past rot / 2 is left as it is.
 template <bool TOK>
 __device__ __forceinline__ void fill_angles(const RopeArgs& p, const RopeShared& sh, int64_t position, int lane,
                                             int group)
@@ -649,6 +662,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArg
         for (int i = 0; i < Ring::kSlots - 1; ++i)
             ahead.issue(p, range.count - i, ring + i * Ring::kStepBytes, lane, per_step, g, first_byte, second, has_a, has_b);
     }
+    if constexpr (!BLOCKS && !INTER)
+        clear_tables<TOK>(p, sh, lane);
     rope_prologue<E, true, INTER>(p, sh);
     const float* const turn = sh.table + (TOK ? g * 16 * p.rot_units : 0) + (cols.pairs ? u : 0) * 4;
     const float* const weight = sh.weights + (u < p.units ? u : 0) * 4;
