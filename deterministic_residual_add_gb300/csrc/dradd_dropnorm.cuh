@@ -693,38 +693,36 @@ __global__ void __launch_bounds__(MAXT, MINB) drop_norm_bwd_wide(const DropNormA
 }
 
 // ------------------------------------------------------------------- launch
-template <typename F>
-cudaError_t launch_sized(F fn, const DropNormArgs& a, const DropNormPlan& p, cudaStream_t stream)
+template <auto FN>
+cudaError_t launch_sized(const DropNormArgs& a, const DropNormPlan& p, cudaStream_t stream)
 {
     if (p.smem > 40 * 1024) {  // with the kernels' own shared memory, past the 48 KB of a plain launch
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(p.smem));
+        const cudaError_t e = allow_all_shared<FN>();
         if (e != cudaSuccess)
             return e;
     }
-    return launch(fn, p.grid, p.threads, p.smem, false, stream, a);
+    return launch(FN, p.grid, p.threads, p.smem, false, stream, a);
 }
 
 template <int E, int T, int K>
 cudaError_t launch_fwd_wide(const DropNormArgs& a, const DropNormPlan& p, cudaStream_t stream)
 {
-    return p.staged ? launch_sized(drop_norm_fwd_wide<E, T, K, true>, a, p, stream)
-                    : launch_sized(drop_norm_fwd_wide<E, T, K, false>, a, p, stream);
+    return p.staged ? launch_sized<drop_norm_fwd_wide<E, T, K, true>>(a, p, stream)
+                    : launch_sized<drop_norm_fwd_wide<E, T, K, false>>(a, p, stream);
 }
 
 template <int E, int K, int MAXT, int MINB>
 cudaError_t launch_bwd_wide(const DropNormArgs& a, const DropNormPlan& p, cudaStream_t stream)
 {
-    return p.staged ? launch_sized(drop_norm_bwd_wide<E, K, MAXT, MINB, true>, a, p, stream)
-                    : launch_sized(drop_norm_bwd_wide<E, K, MAXT, MINB, false>, a, p, stream);
+    return p.staged ? launch_sized<drop_norm_bwd_wide<E, K, MAXT, MINB, true>>(a, p, stream)
+                    : launch_sized<drop_norm_bwd_wide<E, K, MAXT, MINB, false>>(a, p, stream);
 }
 
 template <int E, int L>
 cudaError_t launch_narrow(const DropNormArgs& a, const DropNormPlan& p, bool backward, cudaStream_t stream)
 {
-    return backward ? launch_sized(drop_norm_bwd_narrow<E, L, 1>, a, p, stream)
-                    : launch_sized(drop_norm_fwd_narrow<E, L>, a, p, stream);
+    return backward ? launch_sized<drop_norm_bwd_narrow<E, L, 1>>(a, p, stream)
+                    : launch_sized<drop_norm_fwd_narrow<E, L>>(a, p, stream);
 }
 
 template <int E>
@@ -733,8 +731,8 @@ cudaError_t launch_drop_norm_of(const DropNormArgs& a, const DropNormPlan& p, bo
     if (p.warp) {
         if constexpr (E != kElemF32) {
             if (p.K > 1)
-                return p.K == 2 ? launch_sized(drop_norm_bwd_narrow<E, 32, 2>, a, p, stream)
-                                : launch_sized(drop_norm_bwd_narrow<E, 32, 4>, a, p, stream);
+                return p.K == 2 ? launch_sized<drop_norm_bwd_narrow<E, 32, 2>>(a, p, stream)
+                                : launch_sized<drop_norm_bwd_narrow<E, 32, 4>>(a, p, stream);
         }
         return p.lanes == 8    ? launch_narrow<E, 8>(a, p, backward, stream)
                : p.lanes == 16 ? launch_narrow<E, 16>(a, p, backward, stream)

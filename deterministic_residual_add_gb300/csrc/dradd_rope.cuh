@@ -781,17 +781,15 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const RopeArg
 }
 
 // ------------------------------------------------------------------- launch
-template <typename F>
-cudaError_t launch_rope_kernel(F fn, const RopeArgs& p, int grid, size_t smem, cudaStream_t stream)
+template <auto FN>
+cudaError_t launch_rope_kernel(const RopeArgs& p, int grid, size_t smem, cudaStream_t stream)
 {
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
+        const cudaError_t e = allow_all_shared<FN>();
         if (e != cudaSuccess)
             return e;
     }
-    return launch(fn, grid, kRopeThreads, smem, false, stream, p);
+    return launch(FN, grid, kRopeThreads, smem, false, stream, p);
 }
 
 template <int E, bool INTER, int G, bool TOK>
@@ -804,11 +802,11 @@ cudaError_t launch_rope_as(const RopeArgs& p, int mode, int grid, cudaStream_t s
     if (mode == kRopeNormBwd) {
         const size_t all = tables + (BLOCKS ? RopeRing<E, 2>::kBytes : 0);
         const size_t sums = static_cast<size_t>(p.units) * 128 * (kRopeThreads / 32);
-        return launch_rope_kernel(rope_bwd_kernel<E, INTER, G, TOK>, p, grid, all > sums ? all : sums, stream);
+        return launch_rope_kernel<rope_bwd_kernel<E, INTER, G, TOK>>(p, grid, all > sums ? all : sums, stream);
     }
     const size_t all = tables + (BLOCKS ? RopeRing<E, 1>::kBytes : 0);
-    return norm ? launch_rope_kernel(rope_fwd_kernel<E, true, INTER, G, TOK>, p, grid, all, stream)
-                : launch_rope_kernel(rope_fwd_kernel<E, false, INTER, G, TOK>, p, grid, all, stream);
+    return norm ? launch_rope_kernel<rope_fwd_kernel<E, true, INTER, G, TOK>>(p, grid, all, stream)
+                : launch_rope_kernel<rope_fwd_kernel<E, false, INTER, G, TOK>>(p, grid, all, stream);
 }
 
 // With 32 lanes a head a warp has one lane group, so TOK does not arise.

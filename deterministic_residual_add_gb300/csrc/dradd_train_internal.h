@@ -3,6 +3,7 @@
 // Not part of the public interface.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -10,6 +11,38 @@
 #include "dradd_philox.cuh"
 
 namespace dradd {
+
+// Lets kernel FN use all the dynamic shared memory a CTA may have on the
+// current device, once per kernel and device.  The limit belongs to the
+// kernel, which serves calls of many sizes from many threads: set to what
+// one call needs, it would refuse a larger call made at the same time.
+template <auto FN>
+cudaError_t allow_all_shared()
+{
+    static std::atomic<uint64_t> done{0};  // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit)
+        return cudaSuccess;
+    int optin = 0;
+    e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e != cudaSuccess)
+        return e;
+    const void* const fn = reinterpret_cast<const void*>(FN);
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, fn);
+    if (e != cudaSuccess)
+        return e;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             optin - static_cast<int>(attr.sharedSizeBytes));
+    if (e != cudaSuccess)
+        return e;
+    done.fetch_or(bit, std::memory_order_acq_rel);
+    return cudaSuccess;
+}
 
 // ------------------------------------------------------------------ dropout
 // Row strides in elements.  residual NULL: plain dropout.

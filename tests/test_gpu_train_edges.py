@@ -1,5 +1,8 @@
 """The training and rotary calls where something outside the call could show
-in its results."""
+in its results: what earlier kernels left in shared memory, and calls of
+other sizes made by other threads at the same time."""
+import threading
+
 import pytest
 import torch
 
@@ -53,3 +56,66 @@ def test_rotary_calls_whatever_shared_memory_holds(tokens, hq, hk, dim, rot, int
         torch.cuda.synchronize()
         assert all(bool(torch.isfinite(t).all()) for t in got), f"call {i}: not finite"
         assert same(got, want), f"call {i}: other bits"
+
+
+# ------------------------------------------------- other sizes at the same time
+def norm_calls(rows, hidden, dtype):
+    x, r, g = (normal((rows, hidden), dtype, i) for i in range(3))
+    w = normal(hidden, dtype, 4, 0.1, 1.0)
+    return (lambda: list(dr.dropout_add_rmsnorm_fwd(x, r, w, 0.25, seed=1)),
+            lambda: list(dr.dropout_add_rmsnorm_bwd(g, r, x, w, 0.25, seed=1)))
+
+
+def rope_calls(rot, dim, dtype):
+    q, k, gq, gk = (normal((1, 64, h, dim), dtype, i) for i, h in enumerate((4, 2, 4, 2)))
+    qw, kw = normal(dim, dtype, 5, 0.1, 1.0), normal(dim, dtype, 6, 0.1, 1.0)
+    freq = dr.rope_frequencies(rot, device=cuda())
+    return (lambda: list(dr.qk_rmsnorm_rope_fwd(q, k, qw, kw, freq)),
+            lambda: list(dr.qk_rmsnorm_rope_bwd(gq, gk, q, k, qw, kw, freq)))
+
+
+# (call 0 or 1, makers): sizes that one kernel serves with different amounts of shared memory
+SIDE_BY_SIDE = {
+    "norm, 100 and 304 rows of 8192 bf16": (0, lambda: norm_calls(100, 8192, torch.bfloat16),
+                                            lambda: norm_calls(304, 8192, torch.bfloat16)),
+    "norm, rows of 8192 and 4104 bf16": (0, lambda: norm_calls(100, 8192, torch.bfloat16),
+                                         lambda: norm_calls(100, 4104, torch.bfloat16)),
+    "norm gradient, rows of 8192 and 6000 fp32": (1, lambda: norm_calls(50, 8192, torch.float32),
+                                                  lambda: norm_calls(50, 6000, torch.float32)),
+    "norm gradient, rows of 4096 and 2056 fp16": (1, lambda: norm_calls(50, 4096, torch.float16),
+                                                  lambda: norm_calls(50, 2056, torch.float16)),
+    "rotary gradient, 128 and 32 of 128 bf16": (1, lambda: rope_calls(128, 128, torch.bfloat16),
+                                                lambda: rope_calls(32, 128, torch.bfloat16)),
+    "rotary, 128 and 32 of 128 fp32": (0, lambda: rope_calls(128, 128, torch.float32),
+                                       lambda: rope_calls(32, 128, torch.float32)),
+}
+
+
+@pytest.mark.parametrize("name", SIDE_BY_SIDE)
+def test_threads_with_other_sizes(name):
+    which, *makers = SIDE_BY_SIDE[name]
+    programs = [m()[which] for m in makers] * 2
+    want = [p() for p in programs]
+    torch.cuda.synchronize()
+    failed = []
+    start = threading.Barrier(len(programs))
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            start.wait(60)
+            with torch.cuda.stream(stream):
+                for _ in range(10):
+                    results = [programs[i]() for _ in range(150)]
+                    stream.synchronize()
+            if not all(same(r, want[i]) for r in results):
+                failed.append(f"thread {i}: other bits")
+        except Exception as e:  # reported by the main thread
+            failed.append(f"thread {i}: {e!r}")
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(programs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    assert not failed and not any(t.is_alive() for t in threads), failed
