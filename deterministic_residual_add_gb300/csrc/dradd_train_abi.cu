@@ -508,9 +508,8 @@ dradd_status qk_rmsnorm_rope_bwd(const dradd_heads* dq, const dradd_heads* dk, f
     const bool has_k = rope->k_heads > 0;
     if (!eps_ok(q_eps) || (has_k && !eps_ok(k_eps)))
         return DRADD_ERR_BAD_EPS;
-    if (!has_k)
-        dk_weight = nullptr;
-    const bool sums = dq_weight || dk_weight;
+    float* const dk_sums = has_k ? dk_weight : nullptr;  // a sum over no heads is zeros, below
+    const bool sums = dq_weight || dk_sums;
     if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4))
         return DRADD_ERR_MISALIGNED;
     if (a.tokens == 0) {
@@ -537,8 +536,9 @@ dradd_status qk_rmsnorm_rope_bwd(const dradd_heads* dq, const dradd_heads* dk, f
     a.partials = sums ? static_cast<float*>(workspace) : nullptr;
     if (launch_rope(a, kRopeNormBwd, dtype, rope->interleaved != 0, blocks, grid, stream) != cudaSuccess)
         return DRADD_ERR_CUDA;
-    if (sums &&
-        launch_column_sums(a.partials, grid, 2 * a.dim, dq_weight, a.dim, dk_weight, stream) != cudaSuccess)
+    if (sums && launch_column_sums(a.partials, grid, 2 * a.dim, dq_weight, a.dim, dk_sums, stream) != cudaSuccess)
+        return DRADD_ERR_CUDA;
+    if (dk_weight && !has_k && cudaMemsetAsync(dk_weight, 0, static_cast<size_t>(a.dim) * 4, stream) != cudaSuccess)
         return DRADD_ERR_CUDA;
     return DRADD_OK;
 }

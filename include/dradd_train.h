@@ -202,6 +202,7 @@ dradd_status qk_rmsnorm_rope_fwd(const dradd_heads* q_out, const dradd_heads* k_
  *   dq_weight = sum over tokens and heads of g * xh, [head_dim] fp32
  * and the same for k.  dq may be exactly q or dq_out, dk exactly k or
  * dk_out.  dq_weight and dk_weight both NULL: not computed, no workspace.
+ * With k_heads == 0 a dk_weight is set to zeros.
  */
 dradd_status qk_rmsnorm_rope_bwd(const dradd_heads* dq, const dradd_heads* dk, float* dq_weight, float* dk_weight,
                                  const dradd_heads* dq_out, const dradd_heads* dk_out, const dradd_heads* q,

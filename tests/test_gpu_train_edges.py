@@ -1,6 +1,6 @@
 """The training and rotary calls where something outside the call could show
 in its results: what earlier kernels left in shared memory, and calls of
-other sizes made by other threads at the same time."""
+other sizes made by other threads at the same time.  And k without heads."""
 import threading
 
 import pytest
@@ -119,3 +119,23 @@ def test_threads_with_other_sizes(name):
     for t in threads:
         t.join(120)
     assert not failed and not any(t.is_alive() for t in threads), failed
+
+
+# --------------------------------------------------------------- no k heads
+@pytest.mark.parametrize("batch", [2, 0])
+def test_k_of_no_heads(batch):
+    """A sum over no heads is zero: k's weight gradient, given or not."""
+    q, gq = normal((batch, 7, 4, 64), torch.bfloat16, 1), normal((batch, 7, 4, 64), torch.bfloat16, 2)
+    k = q[:, :, :0]
+    w = normal(64, torch.bfloat16, 3, 0.1, 1.0)
+    freq = dr.rope_frequencies(64, device=cuda())
+    alone = dr.qk_rmsnorm_rope_bwd(gq, None, q, None, w, None, freq)
+    for _ in range(3):
+        torch.full((64,), float("nan"), device=cuda())  # what the next allocation of this size may find
+        got = dr.qk_rmsnorm_rope_bwd(gq, k, q, k, w, w, freq)
+        assert same([got[0], got[2]], [alone[0], alone[2]]) and got[1].shape == k.shape
+        assert bool((got[3] == 0).all())
+    mine = torch.full((64,), float("nan"), device=cuda())
+    got = dr.qk_rmsnorm_rope_bwd(gq, k, q, k, w, w, freq, dk_weight=mine)
+    assert got[3] is mine and bool((mine == 0).all()) and same([got[0], got[2]], [alone[0], alone[2]])
+    assert dr.qk_rmsnorm_rope_bwd(gq, k, q, k, w, w, freq, weight_grad=False)[2:] == (None, None)

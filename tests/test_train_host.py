@@ -253,6 +253,16 @@ def test_norm_rope_argument_errors(L):
     assert L.qk_rmsnorm_rope_bwd_workspace_bytes(ctypes.byref(rope_of(rot_dim=3)), 0) == 0
 
 
+def test_norm_rope_gradient_without_k_heads(L):
+    """dk_weight is an output there too (zeros), so its checks hold; it needs
+    no workspace."""
+    assert norm_rope_bwd(L, dkw=I + 2, k_heads=0) == ALIGN
+    assert norm_rope_bwd(L, dkw=A, k_heads=0) == ALIAS and norm_rope_bwd(L, dkw=E, k_heads=0) == ALIAS
+    assert reaches_device(norm_rope_bwd(L, dkw=I, k_heads=0))
+    assert reaches_device(norm_rope_bwd(L, dkw=B, k_heads=0))  # k's tensors are not looked at
+    assert norm_rope_bwd(L, dqw=I, dkw=I + 1024, k_heads=0) == WORK
+
+
 def test_rope_frequencies(L):
     i = np.arange(32)
     f = 500.0 ** (-2.0 * i / 64)
