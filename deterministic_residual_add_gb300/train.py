@@ -11,7 +11,9 @@ A dropout mask is a function of (seed, offset, row, column), row and column
 those of the tensor seen as [rows, last dimension]; forward and backward
 take the same seed and offset.  `step` is an optional device int64 that the
 kernel adds to the offset, so that a captured graph draws a new mask at
-every replay when the program advances it in between.
+every replay when the program advances it in between.  Calls of equal
+offset + step have one mask, so with layers at the offsets 0 .. L - 1 it has
+to advance by L a replay (or the offsets lie 2^32 apart).
 
 Checks, allocations and calls are one compiled function each
 (csrc/dradd_binding.cpp): a decode step's kernels take two or three

@@ -48,7 +48,10 @@ enum { DRADD_BF16 = 0, DRADD_F16 = 1, DRADD_F32 = 2 };
  *   step    NULL, or a device int64 added to offset (mod 2^64) when the
  *           kernel runs, so a captured graph draws a new mask at every
  *           replay if the program changes the value in between (8-byte
- *           aligned)
+ *           aligned).  Calls of equal offset + step have one mask: where
+ *           layers take the offsets 0 .. L - 1, let the value advance by L
+ *           a replay, or space the offsets 2^32 apart; advancing by one
+ *           would give a layer the mask its neighbour just had.
  * The element in (row, column) is kept when
  *     u >= t,  u = 16 bits (column % 8) of Philox4x32-7 with the counter
  *     (column / 8, row, offset low, offset high) and the key seed,

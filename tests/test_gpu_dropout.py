@@ -136,6 +136,33 @@ def test_step_in_a_captured_graph():
         assert int(step) == k + 1
 
 
+def test_step_and_the_offsets_of_layers():
+    """The step is added to the offset: layers at neighbouring offsets have
+    masks of their own in every replay when it advances by their number, and
+    share them when it advances by one."""
+    layers, p = 3, 0.5
+    x = torch.ones(8, 256, dtype=torch.bfloat16, device=cuda())
+    step = torch.zeros(1, dtype=torch.int64, device=cuda())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = [dr.dropout_fwd(x, p, seed=SEED, offset=i, step=step) for i in range(layers)]
+
+    def masks(advance):
+        got = []
+        for replay in range(4):
+            step.fill_(replay * advance)
+            g.replay()
+            got += [(h != 0).cpu() for h in held]
+        return got
+
+    for advance in (layers, 1):
+        for i, m in enumerate(masks(advance)):
+            offset = i // layers * advance + i % layers
+            assert torch.equal(m, tr.keep_mask(8, 256, p, SEED, offset))
+    assert len({m.numpy().tobytes() for m in masks(layers)}) == 4 * layers
+    assert len({m.numpy().tobytes() for m in masks(1)}) == layers + 3
+
+
 # ------------------------------------- dropout + residual add + RMSNorm
 HIDDENS = [8, 64, 72, 128, 200, 256, 504, 512, 1000, 1024, 1032, 2048, 4096, 5000, 8192, 8200, 16384, 32768]
 
