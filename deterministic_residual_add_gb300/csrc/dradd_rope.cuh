@@ -10,9 +10,10 @@
 // fraction of a turn; position times it modulo 2^64 is then the angle modulo
 // one turn, exact up to the fraction's own rounding (below position * 2^-53
 // turns for frequencies up to one radian), for positions of either sign.
-// Its top 32 bits go to sincospif.  fp32 angles would lose far positions:
-// at 2^20 they are off by 2^-5 radians.  Three integer multiplies and no
-// fp64 outside the one conversion a CTA makes.
+// Its top 32 bits (2^-32 turns), rounded to fp32 (2^-26 turns at most), go to
+// sincospif.  fp32 angles would lose far positions: at 2^20 they are off by
+// 2^-5 radians.  Three integer multiplies and no fp64 outside the one
+// conversion a CTA makes.
 //
 // Work layout.  A unit is 16 columns of a head: in the halves layout 8
 // columns and their partners, or 16 that pass; interleaved 16 consecutive

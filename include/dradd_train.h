@@ -161,10 +161,13 @@ typedef struct dradd_heads {
  *                of (b, s) is position0 + s
  *   scale        finite
  * head_dim <= 512, and ceil(rot_dim / 16) + ceil((head_dim - rot_dim) / 16)
- * <= 32 (every head_dim <= 496).  Angles are exact to about position * 2^-53
- * turns.  Heads of whole 16-byte vectors (8 divides head_dim, the strides
- * and, in the halves layout, rot_dim / 2; 16-byte aligned tensors) take the
- * fast path.
+ * <= 32 (every head_dim <= 496).
+ * An angle, reduced to half a turn either way, is off by at most |position| *
+ * 2^-53 turns (where |inv_freq| <= 1) plus 2^-32, and is then rounded to fp32
+ * (2^-26 turns at most).  The first two are absolute: the sine of an angle
+ * next to zero does not have fp32's relative precision.
+ * Heads of whole 16-byte vectors (8 divides head_dim, the strides and, in the
+ * halves layout, rot_dim / 2; 16-byte aligned tensors) take the fast path.
  */
 typedef struct dradd_rope {
     int64_t batch, seq, q_heads, k_heads, head_dim, rot_dim;

@@ -125,6 +125,27 @@ def test_far_positions():
         tr.assert_close(got[0, i, 0], want, err, f"position {p}")
 
 
+@pytest.mark.parametrize("base", [100.0, 1e4, 1e9])
+def test_angles_within_their_stated_bound(base):
+    """|position| 2^-53 and 2^-32 turns, then fp32's rounding: near zero, for
+    pairs that turn by less than fp32 holds of a turn, and far out.  The
+    cosine and sine add an ulp and two roundings (4 half steps) of their own
+    size."""
+    freq = dr.rope_frequencies(128, base)
+    pos = torch.tensor([[0, 1, -1, 2, 5, 37, -1000, 4095, 100003, 2 ** 24 + 1, -(2 ** 31) + 7]])
+    q = torch.zeros(1, pos.shape[1], 1, 128)
+    q[..., :64] = 1.0
+    got = dr.rope_fwd(q.to(cuda()), None, freq.to(cuda()), pos.to(cuda()))[0][0, :, 0].double().cpu()
+    for i, p in enumerate(pos[0].tolist()):
+        turns = [(Fraction(f) * p * INV_TAU) % 1 for f in freq.tolist()]
+        turns = torch.tensor([float(t - 1 if 2 * t >= 1 else t) for t in turns], dtype=torch.float64)
+        ang = turns * (2 * np.pi)
+        off = 2 * np.pi * (abs(p) * 2.0 ** -53 + 2.0 ** -32) + ang.abs() * 2.0 ** -24
+        for name, value, j in (("cos", torch.cos(ang), 0), ("sin", torch.sin(ang), 64)):
+            d = (got[i, j:j + 64] - value).abs()
+            assert bool((d <= off + 4 * tr.EPS32 * value.abs()).all()), (name, p, float(d.max()))
+
+
 def test_layouts_in_place_and_neighbours():
     """Packed, expanded, transposed and element-aligned tensors; what is not
     part of q and k stays as it was."""
