@@ -164,7 +164,7 @@ struct RopeSide {
     const void* weight;  // behind the norm
     int heads;
     float eps;
-    int skip_rest;  // in place without a norm: the columns past rot_dim stay
+    int skip_rest;  // in place without a norm: the units that do not turn stay
 };
 
 struct RopeArgs {

@@ -150,7 +150,8 @@ typedef struct dradd_heads {
  * How q and k turn.  With theta = position * inv_freq[i], i < rot_dim / 2,
  * the pair (a, b) becomes scale * (a cos theta - b sin theta,
  * a sin theta + b cos theta); it is columns (i, i + rot_dim / 2) of a head,
- * or (2 i, 2 i + 1) when interleaved.  Columns from rot_dim on pass.
+ * or (2 i, 2 i + 1) when interleaved.  Columns from rot_dim on pass (a NaN as
+ * some NaN).
  *   batch, seq, q_heads, k_heads, head_dim  k_heads may be 0: no k, whose
  *                tensors and weight are then not looked at
  *                (batch * seq < 2^31, at most 65536 heads a side)
@@ -182,8 +183,9 @@ typedef struct dradd_rope {
  * rope_fwd -- q_out = turned q, k_out = turned k.  rope_bwd turns by -theta:
  * the gradient of rope_fwd, given the gradients of q_out and k_out (and its
  * inverse when scale is 1).  An output may be exactly its own input; then
- * only its turning columns are written.  An output must not overlap itself
- * (a stride of 0 with more than one element).
+ * the columns from rot_dim on are not written (interleaved: those from the
+ * next multiple of 16 on; between, they are written with what they hold).  An
+ * output must not overlap itself (a stride of 0 with more than one element).
  */
 dradd_status rope_fwd(const dradd_heads* q_out, const dradd_heads* k_out, const dradd_heads* q,
                       const dradd_heads* k, const dradd_rope* rope, int dtype, cudaStream_t stream);

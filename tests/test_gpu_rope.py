@@ -208,6 +208,23 @@ def test_columns_that_pass_hold_anything():
         assert bool(torch.isnan(got[..., 24:30]).all()) and bool((got[..., 30:] == float("inf")).all())
 
 
+@pytest.mark.parametrize("dim,rot", [(64, 24), (64, 32), (64, 4), (100, 36), (33, 6), (128, 64)])
+def test_columns_not_written_in_place(dim, rot):
+    """In place, bits that a copy through fp32 would not keep (a signalling
+    NaN) stay: in the halves layout past rot, interleaved past the next
+    multiple of 16; between, a NaN stays a NaN."""
+    for inter in (False, True):
+        x = normal((2, 37, 3, dim), torch.bfloat16, 1)
+        x.view(torch.int16)[..., rot:] = 0x7F81
+        on = x.to(cuda())
+        freq = dr.rope_frequencies(rot).to(cuda())
+        want = dr.rope_fwd(on, None, freq, position0=4, interleaved=inter)[0]
+        got = dr.rope_fwd(on, None, freq, position0=4, interleaved=inter, q_out=on)[0]
+        assert torch.equal(got[..., :rot], want[..., :rot]) and bool(torch.isnan(got[..., rot:]).all())
+        kept = -(-rot // 16) * 16 if inter else rot
+        assert bool((got.view(torch.int16)[..., kept:] == 0x7F81).all())
+
+
 def test_refusals_and_empty():
     q = torch.zeros(2, 3, 4, 64, device=cuda(), dtype=torch.bfloat16)
     f = dr.rope_frequencies(64).to(cuda())
