@@ -4,6 +4,11 @@ compiled part of the Python binding, with the host compiler.
 Each .cu translation unit is compiled in parallel, then linked into a shared
 library next to this file.  `python -m deterministic_residual_add_gb300.build`
 builds both from the command line.
+
+The library needs nothing but nvcc and its host compiler.  The binding, which
+only the calls of train.py use, needs g++, Python's headers and a torch with
+CUDA; where one of them is missing it is left out with a warning, and those
+calls say so.
 """
 from __future__ import annotations
 
@@ -13,6 +18,7 @@ import subprocess
 import sys
 import sysconfig
 import threading
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -24,6 +30,7 @@ BUILD = PKG / "_build"
 LIB = PKG / "libdradd.so"
 BINDING = PKG / "_binding.so"
 BINDING_SRC = CSRC / "dradd_binding.cpp"
+BINDING_FOR = "binding_for.txt"  # in BUILD: the Python and torch that _binding.so was built for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # No fast math: IEEE division and square root, no flush to zero, and no
@@ -49,14 +56,51 @@ def _deps():
     return _sources() + sorted(CSRC.glob("*.cuh")) + sorted(CSRC.glob("*.h")) + sorted(INCLUDE.glob("*.h"))
 
 
-def stale() -> bool:
-    if not LIB.exists() or not BINDING.exists():
+def lib_stale() -> bool:
+    if not LIB.exists():
         return True
     t = LIB.stat().st_mtime
-    if any(p.stat().st_mtime > t for p in _deps()):
+    return any(p.stat().st_mtime > t for p in _deps())
+
+
+def binding_stale() -> bool:
+    """Missing, older than its sources, or built for another Python or torch
+    (whose interfaces a compiled module is bound to)."""
+    if not BINDING.exists():
         return True
     t = BINDING.stat().st_mtime
-    return any(p.stat().st_mtime > t for p in [BINDING_SRC, *INCLUDE.glob("*.h")])
+    if any(p.stat().st_mtime > t for p in [BINDING_SRC, *INCLUDE.glob("*.h")]):
+        return True
+    tag = BUILD / BINDING_FOR
+    return not tag.exists() or tag.read_text() != _binding_for()
+
+
+def stale() -> bool:
+    return lib_stale() or (binding_stale() and not binding_lacks())
+
+
+def _binding_for() -> str:
+    try:
+        import torch
+    except ImportError:
+        return f"{sys.version}\nno torch"
+    return f"{sys.version}\ntorch {torch.__version__} at {Path(torch.__file__).parent}"
+
+
+def binding_lacks() -> str:
+    """What the binding needs and this machine does not have, or ""."""
+    if not shutil.which("g++"):
+        return "g++"
+    if not (Path(sysconfig.get_paths()["include"]) / "Python.h").exists():
+        return "Python's headers"
+    try:
+        import torch
+    except ImportError:
+        return "torch"
+    root = Path(torch.__file__).resolve().parent
+    if not (root / "include/c10/cuda/CUDAStream.h").exists() or not (root / "lib/libc10_cuda.so").exists():
+        return "a torch with CUDA"
+    return ""
 
 
 def _binding_flags():
@@ -76,6 +120,25 @@ def _run(cmd, what: str):
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
+def _build_lib(ex: ThreadPoolExecutor):
+    cc = nvcc()
+
+    def compile_one(src: Path) -> Path:
+        obj = BUILD / (src.stem + ".o")
+        cmd = [cc, *ARCH, *NVCC_FLAGS, "-I", str(INCLUDE), "-I", str(CSRC), "-c", str(src),
+               "-o", str(obj)]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        (BUILD / (src.stem + ".ptxas.txt")).write_text(r.stdout + r.stderr)
+        if r.returncode != 0:
+            raise RuntimeError(f"nvcc failed for {src.name}:\n{r.stdout}\n{r.stderr}")
+        return obj
+
+    objs = list(ex.map(compile_one, _sources()))
+    tmp = LIB.with_suffix(f".so.tmp{os.getpid()}")
+    _run([cc, *ARCH, "-shared", "-o", tmp, *objs], "linking the library")
+    os.replace(tmp, LIB)
+
+
 def _compile_binding() -> Path:
     flags, _ = _binding_flags()
     obj = BUILD / "dradd_binding.o"
@@ -88,45 +151,32 @@ def _link_binding(obj: Path):
     when the module is imported."""
     _, libs = _binding_flags()
     tmp = BINDING.with_suffix(f".so.tmp{os.getpid()}")
-    _run(["g++", "-shared", obj, "-o", tmp, f"-L{PKG}", "-ldradd", "-Wl,-rpath,$ORIGIN", f"-L{libs}", "-lc10",
+    _run(["g++", "-shared", obj, "-o", tmp, f"-L{LIB.parent}", "-ldradd", "-Wl,-rpath,$ORIGIN", f"-L{libs}", "-lc10",
           "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"], "linking the binding")
     os.replace(tmp, BINDING)
+    (BUILD / BINDING_FOR).write_text(_binding_for())
 
 
 def build(force: bool = False, verbose: bool = False) -> Path:
-    """Compile and link libdradd.so and _binding.so if one is missing or older
-    than a source."""
+    """Compile and link what is missing or older than its sources: libdradd.so,
+    then _binding.so."""
     with _lock:
-        if not force and not stale():
-            return LIB
         BUILD.mkdir(exist_ok=True)
-        cc = nvcc()
-
-        def compile_one(src: Path) -> Path:
-            obj = BUILD / (src.stem + ".o")
-            cmd = [cc, *ARCH, *NVCC_FLAGS, "-I", str(INCLUDE), "-I", str(CSRC), "-c", str(src),
-                   "-o", str(obj)]
-            r = subprocess.run(cmd, capture_output=True, text=True)
-            (BUILD / (src.stem + ".ptxas.txt")).write_text(r.stdout + r.stderr)
-            if r.returncode != 0:
-                raise RuntimeError(f"nvcc failed for {src.name}:\n{r.stdout}\n{r.stderr}")
-            return obj
-
-        srcs = _sources()
-        with ThreadPoolExecutor(len(srcs) + 1) as ex:
-            binding = ex.submit(_compile_binding)
-            objs = list(ex.map(compile_one, srcs))
-            binding_obj = binding.result()
-        tmp = LIB.with_suffix(f".so.tmp{os.getpid()}")
-        cmd = [cc, *ARCH, "-shared", "-o", str(tmp), *map(str, objs)]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, LIB)
-        _link_binding(binding_obj)
-        if verbose:
-            for f in sorted(BUILD.glob("*.ptxas.txt")):
-                print(f.read_text())
+        lacks = binding_lacks()
+        want_lib = force or lib_stale()
+        want_binding = not lacks and (force or binding_stale())
+        with ThreadPoolExecutor(len(_sources()) + 1) as ex:
+            binding = ex.submit(_compile_binding) if want_binding else None
+            if want_lib:
+                _build_lib(ex)
+                if verbose:
+                    for f in sorted(BUILD.glob("*.ptxas.txt")):
+                        print(f.read_text())
+            if binding:
+                _link_binding(binding.result())
+        if lacks and binding_stale():
+            warnings.warn(f"{LIB.name} is built; {BINDING.name} is not, for want of {lacks}: dropout, the gradients and "
+                          "the rotary calls will not load", stacklevel=2)
     return LIB
 
 

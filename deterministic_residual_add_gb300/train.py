@@ -35,7 +35,12 @@ def _load():
     global _C
     from . import lib
     lib()  # says how to build where nothing is built
-    from . import _binding
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise RuntimeError("the compiled binding does not load: build it with `python -m "
+                           "deterministic_residual_add_gb300.build` (needs g++, Python's headers and a torch with "
+                           f"CUDA): {e}") from e
     _C = _binding
     return _C
 
