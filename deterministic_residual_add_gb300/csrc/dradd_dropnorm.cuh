@@ -25,11 +25,13 @@
 // the slot again.  Narrower rows take a warp (or 8 or 16 lanes) each, with
 // the next rows on their way into shared memory that only their lane reads.
 //
-// Measured on GB300 (device time; share of the 6.79 TB/s a copy reaches):
-// forward bf16 4096 x 8192 41.9 us (94 %), 16384 x 4096 88.8 (89 %), 4096 x
-// 1024 5.9 (84 %), fp32 8192 x 4096 85.4 (93 %); backward bf16 8192 x 8192
-// 108.5 us (91 %), 4096 x 4096 30.6 (81 %), 4096 x 1024 12.2 (50 %; the sums
-// of dweight's parts are 3 us of any call), fp32 1999 x 5120 35.5 (85 %).
+// Measured on GB300 (device time, inputs and outputs of every pass its own;
+// share of the 6.79 TB/s a copy reaches): forward bf16 4096 x 8192 42.2 us (94
+// %), 16384 x 4096 88.0 (90 %), 4096 x 1024 6.5 (76 %), fp32 8192 x 4096 84.5
+// (93 %); backward bf16 8192 x 8192 109.8 us (90 %), 4096 x 4096 33.2 (74 %),
+// 4096 x 1024 13.0 (47 %; the sums of dweight's parts are 3 us of any call),
+// fp32 1999 x 5120 37.9 (80 %).  The sweeps noted in the code shared their
+// outputs between passes, which reads up to 3 us lower.
 #pragma once
 
 #include "dradd_elem.cuh"

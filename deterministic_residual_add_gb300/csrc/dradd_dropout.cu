@@ -4,9 +4,13 @@
 //
 // Bound by the memory: 2 (3) elements of traffic an element, and one
 // generator call for 8 of them (dradd_philox.cuh).  Measured on GB300 (device
-// time; share of the 6.79 TB/s a copy reaches): 8192 x 4096 bf16 21.7 us (91
-// %); 15322 x 2315 fp16 31.4 us (67 %, the flat kernel: 1.25 generator calls
-// and about 25 instructions of shifting a vector), with the residual 36.0 (87 %).
+// time, inputs and outputs of every pass its own; share of the 6.79 TB/s a
+// copy reaches): 8192 x 4096 bf16 22.6 us (87 %), with the residual 31.0 (95
+// %); 15322 x 2315 fp16 31.6 us (66 %, the flat kernel: 1.25 generator calls
+// and about 25 instructions of shifting a vector), with the residual 36.4 (86
+// %); 8192 x 4096 bf16 in unaligned rows 4099 apart 42.4 us (47 %, the ragged
+// kernel), with the residual 46.9 (63 %).  The sweeps noted in the code shared
+// their outputs between passes, which reads about a microsecond lower.
 #include "dradd_elem.cuh"
 #include "dradd_internal.h"
 #include "dradd_philox.cuh"

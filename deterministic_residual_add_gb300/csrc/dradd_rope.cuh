@@ -30,16 +30,20 @@
 // steps, across tokens, into slots of shared memory that only it reads
 // (cp.async, so no barrier and no registers).
 //
-// Measured on GB300 (device time; share of the 6.79 TB/s a copy reaches), 32
-// + 8 heads of 128, bf16: rotation of 4096 tokens 13.0 us (95 %), behind the
-// norm of 8192 tokens 29.3 us (84 %), its gradient for 4096 tokens 25.6 us
-// (72 %).  What holds the last two back is instructions: about 250 and 290 a
+// Measured on GB300 (device time, inputs and outputs of every pass its own;
+// share of the 6.79 TB/s a copy reaches), 32 + 8 heads of 128, bf16: rotation
+// of 4096 tokens 16.4 us (75 %), of 8192 28.9 (85 %), behind the norm of 8192
+// tokens 29.9 us (83 %), its gradient for 4096 tokens 26.6 us (70 %); fp32
+// 38.3 (64 %), 69.2 (71 %) and, the gradient, 72.7 (51 %).  The sweeps noted
+// in the code shared their outputs between passes, which reads 1 to 3 us
+// lower.  What holds the norm's kernels back: about 250 and 290 instructions a
 // warp and step against 160 for the rotation alone, at an issue rate of 73 %
-// with 32 warps an SM and 56 % with the gradient's 16 (128 registers: the 32
-// sums of both weights' gradients live there).  Three CTAs of 80 registers spill
-// (62.6 us); a chunk of two steps with one look at the walk took fewer
-// instructions and more time; so did one walk for loads and stores, whose
-// notes of the steps between cost more than a second walk.
+// with 32 warps an SM; 56 % with the gradient's 16 (128 registers: the 32 sums
+// of both weights' gradients live there; fp32 spills 56 to 76 bytes), which do
+// not cover their latency.  Three CTAs of 80 registers spill (62.6 us); a
+// chunk of two steps with one look at the walk took fewer instructions and
+// more time; so did one walk for loads and stores, whose notes of the steps
+// between cost more than a second walk.
 #pragma once
 
 #include "dradd_elem.cuh"

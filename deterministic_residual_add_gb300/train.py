@@ -15,6 +15,9 @@ every replay when the program advances it in between.  Calls of equal
 offset + step have one mask, so with layers at the offsets 0 .. L - 1 it has
 to advance by L a replay (or the offsets lie 2^32 apart).
 
+Results carry no autograd graph, whatever their inputs require: a program's
+own torch.autograd.Function calls a forward and its gradient.
+
 Checks, allocations and calls are one compiled function each
 (csrc/dradd_binding.cpp): a decode step's kernels take two or three
 microseconds, less than the same in Python.
@@ -138,8 +141,9 @@ def add_rmsnorm_bwd(dout, dresidual_out, residual_out, weight, eps: float = 1e-6
 
 
 def rmsnorm_bwd(dout, x, weight, eps: float = 1e-6, **kw):
-    """(dx, dweight): gradients of rmsnorm_fwd.  Keywords as in
-    add_rmsnorm_bwd."""
+    """(dx, dweight): gradients of rmsnorm_fwd, and in fp16 and fp32, which
+    that call does not take, of dropout_add_rmsnorm_fwd with p = 0 and a
+    residual of zeros.  Keywords as in add_rmsnorm_bwd."""
     return add_rmsnorm_bwd(dout, None, x, weight, eps, **kw)
 
 

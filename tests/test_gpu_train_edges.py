@@ -1,6 +1,7 @@
 """The training and rotary calls where something outside the call could show
 in its results: what earlier kernels left in shared memory, and calls of
-other sizes made by other threads at the same time.  And k without heads."""
+other sizes made by other threads at the same time.  And k without heads,
+inputs that require gradients, and the forward that goes with rmsnorm_bwd."""
 import threading
 
 import pytest
@@ -139,3 +140,51 @@ def test_k_of_no_heads(batch):
     got = dr.qk_rmsnorm_rope_bwd(gq, k, q, k, w, w, freq, dk_weight=mine)
     assert got[3] is mine and bool((mine == 0).all()) and same([got[0], got[2]], [alone[0], alone[2]])
     assert dr.qk_rmsnorm_rope_bwd(gq, k, q, k, w, w, freq, weight_grad=False)[2:] == (None, None)
+
+
+# ----------------------------------------------------------------- autograd
+class DropNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, p, seed):
+        out, h = dr.dropout_add_rmsnorm_fwd(x, residual, weight, p, seed=seed)
+        ctx.save_for_backward(h, weight)
+        ctx.how = p, seed
+        return out, h
+
+    @staticmethod
+    def backward(ctx, dout, dh):
+        h, weight = ctx.saved_tensors
+        p, seed = ctx.how
+        dx, dres, dw = dr.dropout_add_rmsnorm_bwd(dout.contiguous(), dh.contiguous(), h, weight, p, seed=seed)
+        return dx, dres, dw.to(weight.dtype), None, None
+
+
+def test_inputs_that_require_gradients():
+    """A call's results carry no graph; inside a program's own Function the
+    gradients are those of the calls."""
+    x, r, g, gh = (normal((40, 512), torch.float32, i) for i in range(4))
+    w = normal(512, torch.float32, 5, 0.1, 1.0)
+    leaves = [t.clone().requires_grad_() for t in (x, r, w)]
+    out, h = dr.dropout_add_rmsnorm_fwd(*leaves, 0.2, seed=7)
+    assert not out.requires_grad and not h.requires_grad
+    freq = dr.rope_frequencies(64, device=cuda())
+    q = normal((1, 40, 8, 64), torch.float32, 6).requires_grad_()
+    assert not dr.rope_fwd(q, None, freq)[0].requires_grad
+    out2, h2 = DropNorm.apply(*leaves, 0.2, 7)
+    assert same([out2.detach(), h2.detach()], [out, h])
+    got = torch.autograd.grad([out2, h2], leaves, [g, gh])
+    assert same(got, dr.dropout_add_rmsnorm_bwd(g, gh, h, w, 0.2, seed=7))
+
+
+@pytest.mark.parametrize("hidden", [200, 4096])
+def test_norm_forward_without_a_residual(hidden):
+    """With p = 0 and a residual of zeros the forward is the plain norm's, and
+    rmsnorm_bwd its gradient: the same bits as from its residual_out."""
+    w, zeros = normal(hidden, torch.bfloat16, 5, 0.1, 1.0), torch.zeros(30, hidden, dtype=torch.bfloat16, device=cuda())
+    x, g = normal((30, hidden), torch.bfloat16, 1), normal((30, hidden), torch.bfloat16, 2)
+    out, h = dr.dropout_add_rmsnorm_fwd(x, zeros, w, 0.0, seed=1)
+    assert same([out, h], [dr.rmsnorm_fwd(x, w), x])
+    for dtype in (torch.bfloat16, torch.float16, torch.float32):
+        x, g, z, v = (t.to(dtype) for t in (x, g, zeros, w))
+        h = dr.dropout_add_rmsnorm_fwd(x, z, v, 0.0, seed=1)[1]
+        assert same(dr.rmsnorm_bwd(g, x, v), dr.add_rmsnorm_bwd(g, None, h, v))
