@@ -27,8 +27,6 @@ from __future__ import annotations
 import contextlib
 import ctypes
 
-import torch
-
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
 
 _C = None  # the compiled part, loaded with the first call
@@ -63,6 +61,7 @@ def _bind(L):
 def _on(x, stream):
     """The launch stream current; a call launches on the current stream of
     its tensors' device."""
+    import torch  # here, as elsewhere in the package: the library and its build do without
     if not x.is_cuda:
         raise ValueError("tensors must be CUDA tensors")
     if isinstance(stream, int):
@@ -156,6 +155,7 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "non
     "by_parts" (pairs that make more than `high` turns within
     original_length stay, those that make fewer than `low` are divided by
     factor, those between are blended)."""
+    import torch
     from . import DraddError, lib
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")

@@ -67,6 +67,17 @@ def test_calls_say_that_the_binding_is_missing(monkeypatch):
     assert dr.abi_version() == 1  # the other calls do without it
 
 
+def test_package_and_library_without_torch():
+    """Configurations and the C ABI are there where torch is not."""
+    drbuild.build()
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "import deterministic_residual_add_gb300 as dr\n"
+            "from deterministic_residual_add_gb300 import build\n"
+            "print(dr.abi_version(), dr.resolve_config(4096, 4096).threads_per_row, build.binding_lacks())")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=drbuild.ROOT)
+    assert r.returncode == 0 and r.stdout.split() == ["1", "128", "torch"], r.stderr
+
+
 def test_command_line():
     r = subprocess.run([sys.executable, "-m", "deterministic_residual_add_gb300.build"], capture_output=True, text=True,
                        cwd=drbuild.ROOT)
