@@ -59,6 +59,49 @@ def test_rotary_calls_whatever_shared_memory_holds(tokens, hq, hk, dim, rot, int
         assert same(got, want), f"call {i}: other bits"
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tokens,hq,hk,dim,rot", [(9001, 2, 1, 64, 64), (300, 7, 3, 96, 96), (300, 7, 3, 40, 10),
+                                                  (40, 32, 8, 128, 64)])
+def test_a_head_of_nan_reaches_no_other(tokens, hq, hk, dim, rot, dtype):
+    """Steps with fewer heads than lane groups, several tokens a step: what
+    one head or token holds stays its own (but for the weights' gradients)."""
+    q, k, gq, gk = (normal((1, tokens, h, dim), dtype, i) for i, h in enumerate((hq, hk, hq, hk)))
+    qw, kw = normal(dim, dtype, 5, 0.1, 1.0), normal(dim, dtype, 6, 0.1, 1.0)
+    freq = dr.rope_frequencies(rot, device=cuda())
+    bad = torch.zeros(1, tokens, hq, 1, dtype=torch.bool, device=cuda())
+    bad[:, ::5, hq - 1] = True
+    bad[:, 3::7, 0] = True
+
+    def calls(q, gq):
+        return (dr.rope_fwd(q, k, freq), dr.qk_rmsnorm_rope_fwd(q, k, qw, kw, freq),
+                dr.qk_rmsnorm_rope_bwd(gq, gk, q, k, qw, kw, freq))
+
+    want = calls(q, gq)
+    for nq, ng in ((q.masked_fill(bad, float("nan")), gq), (q, gq.masked_fill(bad, float("inf")))):
+        for i, (got, w) in enumerate(zip(calls(nq, ng), want)):
+            assert same([got[0].masked_fill(bad, 0), got[1]], [w[0].masked_fill(bad, 0), w[1]]), i
+    assert same(calls(nq, ng)[2][3:], want[2][3:])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("hidden", [8, 72, 200, 504, 1000, 2056, 5000, 9000])
+def test_norm_calls_whatever_shared_memory_holds(hidden, dtype):
+    """Lanes and slots without a row, columns past the row's last."""
+    for rows in (1, 5, 307):
+        x, r, g = (normal((rows, hidden), dtype, i) for i in range(3))
+        w = normal(hidden, dtype, 4, 0.1, 1.0)
+        for call in (lambda: list(dr.dropout_add_rmsnorm_fwd(x, r, w, 0.25, seed=1)),
+                     lambda: list(dr.dropout_add_rmsnorm_bwd(g, r, x, w, 0.25, seed=1)),
+                     lambda: list(dr.add_rmsnorm_bwd(g, None, x, w))):
+            leave_in_shared_memory(0)
+            want = call()
+            torch.cuda.synchronize()
+            leave_in_shared_memory(-1)
+            got = call()
+            torch.cuda.synchronize()
+            assert all(bool(torch.isfinite(t).all()) for t in got) and same(got, want), rows
+
+
 # ------------------------------------------------- other sizes at the same time
 def norm_calls(rows, hidden, dtype):
     x, r, g = (normal((rows, hidden), dtype, i) for i in range(3))
