@@ -13,8 +13,9 @@ The operation is rmsnorm2d_fwd_with_add as defined on the ROCm/aiter issue
 #5151 page ("Steps to Reproduce", reference()), with round-to-nearest-even
 bf16 stores and a reduction order that never depends on the launch.
 
-train.py adds dropout, the gradients, and rotary positions of q and k; its
-functions are exported here too.
+train.py adds dropout, the gradients, and rotary positions of q and k;
+linear.py matrix products with bias, activation and residual, and the losses
+behind the last norm.  Their functions are exported here too.
 """
 from __future__ import annotations
 
@@ -31,6 +32,8 @@ __all__ = [
     "dropout_fwd", "dropout_add_fwd", "dropout_add_rmsnorm_fwd", "dropout_add_rmsnorm_bwd", "add_rmsnorm_bwd",
     "rmsnorm_bwd", "rope_fwd", "rope_bwd", "qk_rmsnorm_rope_fwd", "qk_rmsnorm_rope_bwd", "rope_frequencies",
     "ROPE_SCALINGS",
+    "linear_act_add_fwd", "linear_act_add_bwd", "linear_cross_entropy_fwd", "linear_cross_entropy_bwd",
+    "linear_distill_fwd", "linear_distill_bwd", "ACTIVATIONS",
     "LaunchConfig", "DraddError", "resolve_config",
     "device_status", "last_device_status", "bf16_convert_range", "status_string", "abi_version", "lib",
     "library_path", "VARIANT_AUTO", "VARIANT_ROWS", "VARIANT_STAGED", "VARIANT_SPLIT", "VARIANT_WARP",
@@ -635,6 +638,9 @@ def bf16_convert_range(out, first: int, count: int, method: int = 0, stream=None
     return out
 
 
+from .linear import (  # noqa: E402
+    ACTIVATIONS, linear_act_add_bwd, linear_act_add_fwd, linear_cross_entropy_bwd, linear_cross_entropy_fwd,
+    linear_distill_bwd, linear_distill_fwd)
 from .train import (  # noqa: E402  (train uses the helpers above)
     ROPE_SCALINGS, add_rmsnorm_bwd, dropout_add_fwd, dropout_add_rmsnorm_bwd, dropout_add_rmsnorm_fwd, dropout_fwd,
     qk_rmsnorm_rope_bwd, qk_rmsnorm_rope_fwd, rmsnorm_bwd, rope_bwd, rope_frequencies, rope_fwd)

@@ -1,17 +1,20 @@
-// dradd_binding.cpp -- the Python binding of include/dradd_train.h: checks
-// of tensors, allocation of outputs, and the call, in one C function each.
+// dradd_binding.cpp -- the Python binding of include/dradd_train.h and
+// include/dradd_linear.h: checks of tensors, allocation of outputs, and the
+// call, in one C function each.
 //
 // A decode step's kernels take two or three microseconds.  With the same
 // checks and allocations in Python, a call through ctypes took 15 to 40 us on
 // the GPU's host (rotation of 8 tokens 15.7, the norm + rotation gradient
 // 39); from here 5.1 and 12.8.  The functions take every argument by
-// position; train.py gives them their names, defaults and documentation.
+// position; train.py and linear.py give them their names, defaults and
+// documentation.
 #include <Python.h>
 
 #include <cstdint>
 #include <initializer_list>
 #include <sstream>
 #include <string>
+#include <vector>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
@@ -21,6 +24,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include "dradd_linear.h"
 #include "dradd_train.h"
 
 namespace {
@@ -508,6 +512,257 @@ PyObject* norm_rope_bwd(PyObject* const* a)
     return tuple_of({&sq.out, &dk, &dqw, &dkw});
 }
 
+// ---------------------------------------------------------- matrix products
+// The call's type, one of the 16-bit ones.
+Call product_call(const at::Tensor& x)
+{
+    if (x.scalar_type() != at::kBFloat16 && x.scalar_type() != at::kHalf)
+        fail(PyExc_TypeError,
+             std::string("x must be bfloat16 or float16 (got ") + c10::toString(x.scalar_type()) + ")");
+    return Call(x, "x");
+}
+
+int64_t inner_of(const at::Tensor& x)
+{
+    if (x.dim() == 0 || x.size(-1) == 0)
+        fail(PyExc_ValueError, "x must have a last dimension that is not empty");
+    return x.size(-1);
+}
+
+// A 2-D weight [anything, inner].
+const at::Tensor& weight_of(PyObject* o, int64_t inner)
+{
+    const at::Tensor& w = tensor(o, "weight");
+    if (w.dim() != 2 || w.size(1) != inner) {
+        std::ostringstream s;
+        s << "weight has shape " << w.sizes() << ", expected [*, " << inner << "]";
+        fail(PyExc_ValueError, s.str());
+    }
+    return w;
+}
+
+dradd_matrix matrix(const Rows& r) { return {r.data, r.stride}; }
+
+std::vector<int64_t> with_last(at::IntArrayRef shape, int64_t n)
+{
+    std::vector<int64_t> v(shape.begin(), shape.end());
+    v.back() = n;
+    return v;
+}
+
+// linear_fwd(x, weight, bias | None, residual | None, act, out | None, workspace | None)
+PyObject* linear_fwd(PyObject* const* a)
+{
+    const at::Tensor& x = tensor(a[0], "x");
+    const Call c = product_call(x);
+    const int64_t inner = inner_of(x);
+    const at::Tensor& weight = weight_of(a[1], inner);
+    const int64_t cols = weight.size(0);
+    const at::Tensor* bias = optional_tensor(a[2], "bias");
+    const at::Tensor* residual = optional_tensor(a[3], "residual");
+    const int act = static_cast<int>(bits64(a[4]));
+    const std::vector<int64_t> shape = with_last(x.sizes(), cols);
+    const Rows xr(x, "x", x.sizes(), c), wr(weight, "weight", weight.sizes(), c);
+    const void* bp = bias ? flat(*bias, "bias", c.type, c.device, {cols}) : nullptr;
+    dradd_matrix rm = {nullptr, 0};
+    if (residual)
+        rm = matrix(Rows(*residual, "residual", shape, c));
+    const at::Tensor out = output(a[5], "out", shape, c);
+    const Rows o(out, "out", shape, c);
+    const dradd_matrix om = matrix(o), xm = matrix(xr), wm = matrix(wr);
+    const size_t need = linear_act_add_fwd_workspace_bytes(xr.n, inner, cols);
+    void* ws = nullptr;
+    size_t bytes = 0;
+    at::Tensor keep;
+    if (need) {
+        const Workspace w(a[6], need, c);
+        keep = w.keep;
+        ws = w.data;
+        bytes = w.bytes;
+    }
+    run("linear_act_add_fwd", [&] {
+        return linear_act_add_fwd(&om, &xm, &wm, bp, &rm, act, xr.n, inner, cols, c.dtype, ws, bytes, c.stream);
+    });
+    return THPVariable_Wrap(out);
+}
+
+// linear_bwd(dout, x, weight, bias | None, act, dx, dweight, dbias, input_grad, weight_grad, workspace)
+PyObject* linear_bwd(PyObject* const* a)
+{
+    const at::Tensor& dout = tensor(a[0], "dout");
+    const at::Tensor& x = tensor(a[1], "x");
+    const Call c = product_call(x);
+    const int64_t inner = inner_of(x);
+    const at::Tensor& weight = weight_of(a[2], inner);
+    const int64_t cols = weight.size(0);
+    const at::Tensor* bias = optional_tensor(a[3], "bias");
+    const int act = static_cast<int>(bits64(a[4]));
+    const bool want_x = truth(a[8]), want_w = truth(a[9]), want_b = want_w && bias;
+    if ((!want_x && a[5] != Py_None) || (!want_w && a[6] != Py_None) || (!want_b && a[7] != Py_None))
+        fail(PyExc_ValueError, "an output is given for a gradient that is not asked for");
+    const std::vector<int64_t> shape = with_last(x.sizes(), cols);
+    const Rows xr(x, "x", x.sizes(), c), wr(weight, "weight", weight.sizes(), c), gr(dout, "dout", shape, c);
+    const void* bp = bias ? flat(*bias, "bias", c.type, c.device, {cols}) : nullptr;
+    at::Tensor dx, dw, db;
+    if (want_x)
+        dx = output(a[5], "dx", x.sizes(), c);
+    if (want_w)
+        dw = output(a[6], "dweight", weight.sizes(), c);
+    if (want_b)
+        db = output(a[7], "dbias", {cols}, c);
+    void* xp = want_x ? flat(dx, "dx", c.type, c.device, x.sizes()) : nullptr;
+    void* wp = want_w ? flat(dw, "dweight", c.type, c.device, weight.sizes()) : nullptr;
+    void* dbp = want_b ? flat(db, "dbias", c.type, c.device, {cols}) : nullptr;
+    const dradd_matrix gm = matrix(gr), xm = matrix(xr), wm = matrix(wr);
+    const Workspace w(a[10], linear_act_add_bwd_workspace_bytes(xr.n, inner, cols, act, want_x, want_w, want_b), c);
+    run("linear_act_add_bwd", [&] {
+        return linear_act_add_bwd(xp, wp, dbp, &gm, &xm, &wm, bp, act, xr.n, inner, cols, c.dtype, w.data, w.bytes,
+                                  c.stream);
+    });
+    return tuple_of({&dx, &dw, &db});
+}
+
+// A row's words: int64 targets, or a teacher's index and logits.
+struct LossWords {
+    const int64_t* target = nullptr;
+    int64_t ignore_index = 0;
+    dradd_teacher teacher = {};
+    bool distill = false;
+
+    // a: target | index, teacher logits | None, ignore_index, temperature
+    LossWords(PyObject* const* a, at::IntArrayRef rows, const Call& c)
+    {
+        const at::Tensor* logits = optional_tensor(a[1], "teacher_logits");
+        distill = logits != nullptr;
+        if (!distill) {
+            const at::Tensor& t = tensor(a[0], "target");
+            target = static_cast<const int64_t*>(flat(t, "target", at::kLong, c.device, rows));
+            ignore_index = static_cast<int64_t>(bits64(a[2]));
+            return;
+        }
+        const at::Tensor& t = tensor(a[0], "teacher_index");
+        if (t.dim() == 0)
+            fail(PyExc_ValueError, "teacher_index must have a last dimension: the entries of a row");
+        std::vector<int64_t> shape(rows.begin(), rows.end());
+        shape.push_back(t.size(-1));
+        teacher.index = static_cast<const int64_t*>(flat(t, "teacher_index", at::kLong, c.device, shape));
+        switch (logits->scalar_type()) {
+        case at::kBFloat16: teacher.logits_dtype = DRADD_BF16; break;
+        case at::kHalf: teacher.logits_dtype = DRADD_F16; break;
+        case at::kFloat: teacher.logits_dtype = DRADD_F32; break;
+        default: fail(PyExc_TypeError, "teacher_logits must be bfloat16, float16 or float32");
+        }
+        teacher.logits = flat(*logits, "teacher_logits", logits->scalar_type(), c.device, shape);
+        teacher.top = t.size(-1);
+        teacher.temperature = static_cast<float>(number(a[3]));
+    }
+};
+
+// A row's fp32 number: contiguous, or one value for all rows.
+struct RowNumbers {
+    const float* data;
+    int64_t stride;
+
+    RowNumbers(const at::Tensor& t, const char* name, at::IntArrayRef rows, const Call& c)
+    {
+        bool one = true;
+        for (int64_t i = 0; i < t.dim(); ++i)
+            one = one && (t.stride(i) == 0 || t.size(i) == 1);
+        check(t, name, at::kFloat, c.device, t.dim() == 0 ? t.sizes() : rows);
+        if (!one && !t.is_contiguous())
+            fail(PyExc_ValueError, std::string(name) + " must be contiguous, or one value for all rows");
+        data = static_cast<const float*>(t.data_ptr());
+        stride = one ? 0 : 1;
+    }
+};
+
+// loss_fwd(x, weight, target | index, teacher_logits | None, ignore_index, temperature, loss, lse, workspace)
+PyObject* loss_fwd(PyObject* const* a)
+{
+    const at::Tensor& x = tensor(a[0], "x");
+    const Call c = product_call(x);
+    const int64_t hidden = inner_of(x);
+    const at::Tensor& weight = weight_of(a[1], hidden);
+    const int64_t vocab = weight.size(0);
+    const at::IntArrayRef rows = x.sizes().slice(0, x.dim() - 1);
+    const Rows xr(x, "x", x.sizes(), c), wr(weight, "weight", weight.sizes(), c);
+    const LossWords words(a + 2, rows, c);
+    const auto numbers = [&](PyObject* o, const char* name) {
+        const at::Tensor* t = optional_tensor(o, name);
+        return t ? *t : fresh(rows, at::kFloat, c.device);
+    };
+    const at::Tensor loss = numbers(a[6], "loss"), lse = numbers(a[7], "lse");
+    float* lp = static_cast<float*>(flat(loss, "loss", at::kFloat, c.device, rows));
+    float* ep = static_cast<float*>(flat(lse, "lse", at::kFloat, c.device, rows));
+    const Workspace w(a[8],
+                      words.distill ? linear_distill_fwd_workspace_bytes(xr.n, hidden, vocab, words.teacher.top)
+                                    : linear_cross_entropy_fwd_workspace_bytes(xr.n, hidden, vocab),
+                      c);
+    const dradd_matrix xm = matrix(xr), wm = matrix(wr);
+    if (words.distill)
+        run("linear_distill_fwd", [&] {
+            return linear_distill_fwd(lp, ep, &xm, &wm, &words.teacher, xr.n, hidden, vocab, c.dtype, w.data, w.bytes,
+                                      c.stream);
+        });
+    else
+        run("linear_cross_entropy_fwd", [&] {
+            return linear_cross_entropy_fwd(lp, ep, &xm, &wm, words.target, words.ignore_index, xr.n, hidden, vocab,
+                                            c.dtype, w.data, w.bytes, c.stream);
+        });
+    return tuple_of({&loss, &lse});
+}
+
+// loss_bwd(dloss, dlse | None, x, weight, target | index, teacher_logits | None, ignore_index, temperature, lse, dx,
+//          dweight, input_grad, weight_grad, workspace)
+PyObject* loss_bwd(PyObject* const* a)
+{
+    const at::Tensor& x = tensor(a[2], "x");
+    const Call c = product_call(x);
+    const int64_t hidden = inner_of(x);
+    const at::Tensor& weight = weight_of(a[3], hidden);
+    const int64_t vocab = weight.size(0);
+    const at::IntArrayRef rows = x.sizes().slice(0, x.dim() - 1);
+    const Rows xr(x, "x", x.sizes(), c), wr(weight, "weight", weight.sizes(), c);
+    const LossWords words(a + 4, rows, c);
+    const RowNumbers dloss(tensor(a[0], "dloss"), "dloss", rows, c);
+    const at::Tensor* given = optional_tensor(a[1], "dlse");
+    const float* dlse = nullptr;
+    int64_t dlse_stride = 0;
+    if (given) {
+        const RowNumbers n(*given, "dlse", rows, c);
+        dlse = n.data;
+        dlse_stride = n.stride;
+    }
+    const float* lse = static_cast<const float*>(flat(tensor(a[8], "lse"), "lse", at::kFloat, c.device, rows));
+    const bool want_x = truth(a[11]), want_w = truth(a[12]);
+    if ((!want_x && a[9] != Py_None) || (!want_w && a[10] != Py_None))
+        fail(PyExc_ValueError, "an output is given for a gradient that is not asked for");
+    at::Tensor dx, dw;
+    if (want_x)
+        dx = output(a[9], "dx", x.sizes(), c);
+    if (want_w)
+        dw = output(a[10], "dweight", weight.sizes(), c);
+    void* xp = want_x ? flat(dx, "dx", c.type, c.device, x.sizes()) : nullptr;
+    void* wp = want_w ? flat(dw, "dweight", c.type, c.device, weight.sizes()) : nullptr;
+    const Workspace w(a[13],
+                      words.distill ? linear_distill_bwd_workspace_bytes(xr.n, hidden, vocab, words.teacher.top)
+                                    : linear_cross_entropy_bwd_workspace_bytes(xr.n, hidden, vocab),
+                      c);
+    const dradd_matrix xm = matrix(xr), wm = matrix(wr);
+    if (words.distill)
+        run("linear_distill_bwd", [&] {
+            return linear_distill_bwd(xp, wp, dloss.data, dloss.stride, dlse, dlse_stride, &xm, &wm, &words.teacher,
+                                      lse, xr.n, hidden, vocab, c.dtype, w.data, w.bytes, c.stream);
+        });
+    else
+        run("linear_cross_entropy_bwd", [&] {
+            return linear_cross_entropy_bwd(xp, wp, dloss.data, dloss.stride, dlse, dlse_stride, &xm, &wm,
+                                            words.target, words.ignore_index, lse, xr.n, hidden, vocab, c.dtype,
+                                            w.data, w.bytes, c.stream);
+        });
+    return tuple_of({&dx, &dw});
+}
+
 // ------------------------------------------------------------------- module
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n)
@@ -537,6 +792,10 @@ PyMethodDef methods[] = {method<dropout, 7>("dropout"),
                          method<rope, 10>("rope"),
                          method<norm_rope_fwd, 13>("norm_rope_fwd"),
                          method<norm_rope_bwd, 19>("norm_rope_bwd"),
+                         method<linear_fwd, 7>("linear_fwd"),
+                         method<linear_bwd, 11>("linear_bwd"),
+                         method<loss_fwd, 9>("loss_fwd"),
+                         method<loss_bwd, 14>("loss_bwd"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

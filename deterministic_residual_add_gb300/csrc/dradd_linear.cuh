@@ -1,0 +1,381 @@
+// dradd_linear.cuh -- the matrix product kernel of dradd_linear.h.
+//
+// C[m, n] = sum over k of A[m, k] B[n, k] in 16-bit operands and fp32 sums.
+// A persistent grid of CTAs (CG = 1) or CTA pairs (CG = 2) walks the tiles.
+// In a CTA one thread copies operands through a ring in shared memory, one
+// thread (CG = 2: of the pair's first CTA) issues the products into one of
+// two accumulators in tensor memory, and eight warps turn the other one into
+// the call's results, so that the epilogue runs beside the next tile's
+// products.  What the epilogue does is the template's argument E.
+#pragma once
+
+#include "dradd_elem.cuh"
+#include "dradd_internal.h"
+#include "dradd_linear_internal.h"
+#include "dradd_mma.cuh"
+#include "dradd_train_internal.h"
+
+namespace dradd {
+
+constexpr int kProductThreads = 384;  // a copying warp, an issuing one, two spare, eight for the epilogue
+constexpr int kEpiWarps = 8;
+constexpr uint32_t kBoxBytes = 64 * 64 * 2;  // 64 rows of 128 bytes
+
+__host__ __device__ constexpr uint32_t product_stage_bytes(int CG) { return (2u + 4u / CG) * kBoxBytes; }
+__host__ __device__ constexpr int product_stages(int CG) { return static_cast<int>(200u * 1024u / product_stage_bytes(CG)); }
+constexpr uint32_t product_smem(int CG) { return product_stages(CG) * product_stage_bytes(CG) + 1024u; }
+
+// Waits that have given up end every role's loop; the CTA then drains what
+// it has in flight and returns.
+struct ProductBars {
+    uint64_t full[8], empty[8], acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+};
+
+struct TileAt {
+    int problem, m, n, split, k0, k1;
+};
+
+// The i-th tile of a worker, or -1 behind its last.  The first problem's
+// tiles go round the workers; where they do not come out even, the workers
+// that got one less first take as many tiles of the second problem as one of
+// the first is worth.
+template <class K>
+__device__ __forceinline__ int tile_of(const ProductArgs<K>& a, int worker, int workers, int i)
+{
+    int t = worker + i * workers;
+    if constexpr (K::kProblems == 1)
+        return t < a.tiles ? t : -1;
+    if (t < a.tiles0)
+        return t;
+    const int odd = a.tiles0 % workers;
+    i -= a.tiles0 / workers + (worker < odd);
+    t = worker + i * workers;
+    if (odd > 0) {
+        const int rest = workers - odd;
+        if (worker >= odd) {
+            t = i < a.worth ? worker - odd + i * rest : rest * a.worth + worker + (i - a.worth) * workers;
+        } else {
+            t += rest * a.worth;
+        }
+    }
+    t += a.tiles0;
+    return t < a.tiles ? t : -1;
+}
+
+// Tiles of one problem: splits outermost, then bands of 8 tile rows that are
+// walked down column by column, so that the tiles at work at one time share
+// few rows and columns.
+template <class K>
+__device__ __forceinline__ TileAt tile_at(const ProductArgs<K>& a, int t)
+{
+    constexpr int kBand = 8;
+    TileAt r;
+    r.problem = K::kProblems > 1 && t >= a.tiles0 ? 1 : 0;
+    if (r.problem)
+        t -= a.tiles0;
+    const ProductShape& s = a.shape[K::kProblems > 1 ? r.problem : 0];
+    const int per = s.tiles_m * s.tiles_n;
+    r.split = t / per;
+    t -= r.split * per;
+    const int band_tiles = kBand * s.tiles_n;
+    const int band = t / band_tiles;
+    t -= band * band_tiles;
+    const int high = min(kBand, s.tiles_m - band * kBand);
+    r.n = t / high;
+    r.m = band * kBand + t - r.n * high;
+    const int each = (s.k_blocks + s.splits - 1) / s.splits;
+    r.k0 = r.split * each;
+    r.k1 = min(r.k0 + each, s.k_blocks);
+    return r;
+}
+
+template <int CG, class E>
+__global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __grid_constant__ ProductArgs<typename E::Kind> a)
+{
+    constexpr int kStages = product_stages(CG);
+    constexpr uint32_t kStageBytes = product_stage_bytes(CG);
+    constexpr uint32_t kBytesA = 2 * kBoxBytes;
+    constexpr int kRowsB = kTileCols / CG;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ ProductBars bars;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? cluster_ctarank() : 0;
+    const int worker = static_cast<int>(blockIdx.x) / CG, workers = static_cast<int>(gridDim.x) / CG;
+
+    if (warp == 0 && lane == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&bars.full[i], 1);
+            mbar_init(&bars.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.acc_full[i], 1);
+            mbar_init(&bars.acc_empty[i], kEpiWarps * CG);
+        }
+        mbar_init(&bars.drain, 1);
+        fence_mbar_init();
+        for (int i = 0; i < E::Kind::kProblems && (i == 0 || a.tiles > a.tiles0); ++i) {
+            prefetch_map(&a.shape[i].a);
+            prefetch_map(&a.shape[i].b);
+        }
+    }
+    if (warp == 2)
+        tmem_alloc<CG>(&bars.tmem, 512);
+    tmem_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2)
+        cluster_sync_all();
+    tmem_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
+    wait_prior_grids();
+    allow_next_grid();
+
+    const auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (mbar_wait_bounded(bar, parity, a.wait_limit_ns))
+            return true;
+        atomicOr(a.status, kDeviceStatusTimeout);
+        return false;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            int64_t steps = 0;
+            for (int i = 0, t; ok && (t = tile_of(a, worker, workers, i)) >= 0; ++i) {
+                const TileAt at = tile_at(a, t);
+                const ProductShape& s = a.shape[E::Kind::kProblems > 1 ? at.problem : 0];
+                const int row = (at.m * CG + static_cast<int>(rank)) * kTileRows;
+                const int col = at.n * kTileCols + static_cast<int>(rank) * kRowsB;
+                for (int k = at.k0; k < at.k1; ++k) {
+                    ok = wait(&bars.empty[stage], phase ^ 1u);
+                    if (!ok)
+                        break;
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(&bars.full[stage], CG * kStageBytes);
+                    const uint32_t to = ring + stage * kStageBytes;
+                    uint64_t* bar = &bars.full[stage];
+                    if (s.a_mn) {
+#pragma unroll
+                        for (int j = 0; j < kTileRows / 64; ++j)
+                            copy_box<CG>(to + j * kBoxBytes, &s.a, row + j * 64, k * kTileDepth, bar);
+                    } else {
+                        copy_box<CG>(to, &s.a, k * kTileDepth, row, bar);
+                    }
+                    if (s.b_mn) {
+#pragma unroll
+                        for (int j = 0; j < kRowsB / 64; ++j)
+                            copy_box<CG>(to + kBytesA + j * kBoxBytes, &s.b, col + j * 64, k * kTileDepth, bar);
+                    } else {
+                        copy_box<CG>(to + kBytesA, &s.b, k * kTileDepth, col, bar);
+                    }
+                    ++steps;
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // The last products have let go of every slot: nothing arrives
+            // on this CTA's barriers after it has gone.
+            for (int j = 0; ok && j < kStages && j < steps; ++j) {
+                if (--stage < 0) {
+                    stage = kStages - 1;
+                    phase ^= 1u;
+                }
+                ok = wait(&bars.empty[stage], phase);
+            }
+            // Copies of this CTA (of the pair, where the barriers are) that
+            // may still be in flight after a wait gave up.
+            if (!ok && rank == 0) {
+                for (int j = 0; j < kStages && j < steps; ++j) {
+                    if (--stage < 0) {
+                        stage = kStages - 1;
+                        phase ^= 1u;
+                    }
+                    if (!mbar_wait_bounded(&bars.full[stage], phase, a.wait_limit_ns))
+                        atomicOr(a.status, kDeviceStatusUndrained);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true;
+            for (int i = 0, t; ok && (t = tile_of(a, worker, workers, i)) >= 0; ++i) {
+                const TileAt at = tile_at(a, t);
+                const ProductShape& s = a.shape[E::Kind::kProblems > 1 ? at.problem : 0];
+                const uint32_t desc = product_desc(a.bf16, s.a_mn, s.b_mn, kTileRows * CG, kTileCols);
+                // 16 of the summed dimension: 32 bytes along a row, or 16 rows
+                const uint64_t step_a = s.a_mn ? 16 * 128 >> 4 : 32 >> 4, step_b = s.b_mn ? 16 * 128 >> 4 : 32 >> 4;
+                ok = wait(&bars.acc_empty[acc], acc_phase ^ 1u);
+                if (!ok)
+                    break;
+                tmem_fence_after();
+                const uint32_t d = tmem + acc * kTileCols;
+                for (int k = at.k0; k < at.k1; ++k) {
+                    ok = wait(&bars.full[stage], phase);
+                    if (!ok)
+                        break;
+                    tmem_fence_after();
+                    const uint32_t from = ring + stage * kStageBytes;
+                    const uint64_t da = operand_desc(from, kBoxBytes), db = operand_desc(from + kBytesA, kBoxBytes);
+#pragma unroll
+                    for (int j = 0; j < kTileDepth / 16; ++j)
+                        mma_f16<CG>(d, da + j * step_a, db + j * step_b, desc, k > at.k0 || j > 0);
+                    mma_commit<CG>(&bars.empty[stage]);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok)
+                    break;
+                mma_commit<CG>(&bars.acc_full[acc]);
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            }
+            if (!ok) {
+                mma_commit<CG>(&bars.drain);
+                if (!mbar_wait_bounded(&bars.drain, 0, a.wait_limit_ns))
+                    atomicOr(a.status, kDeviceStatusUndrained);
+            }
+        }
+    } else if (warp >= 4) {
+        const int quadrant = warp & 3, half = (warp - 4) >> 2;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int i = 0, t; (t = tile_of(a, worker, workers, i)) >= 0; ++i) {
+            const TileAt at = tile_at(a, t);
+            const int row = (at.m * CG + static_cast<int>(rank)) * kTileRows + quadrant * 32 + lane;
+            const int col = at.n * kTileCols + half * kHalfCols;
+            E epi(a.epi[E::Kind::kProblems > 1 ? at.problem : 0], a.bf16, row, col, at.split);
+            if (!__all_sync(0xffffffffu, wait(&bars.acc_full[acc], acc_phase)))
+                break;
+            tmem_fence_after();
+            const uint32_t from = tmem + (static_cast<uint32_t>(quadrant * 32) << 16) + acc * kTileCols +
+                                  half * kHalfCols;
+#pragma unroll 1
+            for (int c = 0; c < kHalfCols; c += 32) {
+                uint32_t bits[32];
+                tmem_load32(from + c, bits);
+                tmem_wait_loads();
+                if (c + 32 == kHalfCols) {
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_at(&bars.acc_empty[acc], 0);
+                }
+                epi.columns(bits, c);
+            }
+            epi.end();
+            if (++acc == 2) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2)
+        cluster_sync_all();
+    tmem_fence_after();
+    if (warp == 2)
+        tmem_free<CG>(tmem, 512);
+}
+
+template <int CG, class E>
+cudaError_t launch_product_group(const ProductArgs<typename E::Kind>& a, int sm_count, cudaStream_t stream)
+{
+    constexpr auto fn = &product_kernel<CG, E>;
+    cudaError_t e = allow_all_shared<product_kernel<CG, E>>();
+    if (e != cudaSuccess)
+        return e;
+    const int workers = a.tiles < sm_count / CG ? a.tiles : sm_count / CG;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(workers * CG));
+    cfg.blockDim = dim3(kProductThreads);
+    cfg.dynamicSmemBytes = product_smem(CG);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, fn, a);
+}
+
+template <class E>
+cudaError_t launch_with(const ProductArgs<typename E::Kind>& a, int cta_group, int sm_count, cudaStream_t stream)
+{
+    return cta_group == 2 ? launch_product_group<2, E>(a, sm_count, stream)
+                          : launch_product_group<1, E>(a, sm_count, stream);
+}
+
+// 32 consecutive values of a 16-bit row, `n` of them inside it (a multiple of
+// 8): stored in whole 32-byte sectors where the address allows.
+__device__ __forceinline__ void pack32(const float (&f)[32], bool bf16, uint32_t (&w)[16])
+{
+    if (bf16) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            w[i] = pack_rne(f[2 * i], f[2 * i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            w[i] = Elem<kElemF16>::pack2(f[2 * i], f[2 * i + 1]);
+    }
+}
+
+__device__ __forceinline__ void store32(uint16_t* p, const uint32_t (&w)[16], int n)
+{
+    if (n >= 32 && (reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 16 * i), "r"(w[8 * i]),
+                         "r"(w[8 * i + 1]), "r"(w[8 * i + 2]), "r"(w[8 * i + 3]), "r"(w[8 * i + 4]),
+                         "r"(w[8 * i + 5]), "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
+                         : "memory");
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (8 * i < n)
+            reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+__device__ __forceinline__ void unpack2(uint32_t w, bool bf16, float& lo, float& hi)
+{
+    if (bf16) {
+        lo = bf16_lo(w);
+        hi = bf16_hi(w);
+    } else {
+        lo = Elem<kElemF16>::widen(static_cast<uint16_t>(w & 0xFFFFu));
+        hi = Elem<kElemF16>::widen(static_cast<uint16_t>(w >> 16));
+    }
+}
+
+// 32 consecutive values of a 16-bit row, zeros past the n inside it.
+__device__ __forceinline__ void load32(const uint16_t* p, int n, uint32_t (&w)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (8 * i < n)
+            v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+    }
+}
+
+}  // namespace dradd

@@ -1,0 +1,903 @@
+// dradd_linear_abi.cu -- the C entry points of include/dradd_linear.h:
+// argument checks, how a call is tiled and split, and its launches.  Every
+// check is made before any GPU work.
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "dradd_linear.h"
+
+#include "dradd_host.h"
+#include "dradd_internal.h"
+#include "dradd_linear_internal.h"
+#include "dradd_train_internal.h"
+
+namespace dradd {
+
+bool make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t stride, int box_rows)
+{
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static std::atomic<void*> entry{nullptr};
+    void* fn = entry.load(std::memory_order_acquire);
+    if (!fn) {
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess || !fn)
+            return false;
+        entry.store(fn, std::memory_order_release);
+    }
+    const cuuint64_t sizes[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t steps[2] = {1, 1};
+    return reinterpret_cast<Encode>(fn)(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), sizes, strides,
+                                        box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
+constexpr int64_t kMaxInner = 1 << 24;
+constexpr int64_t kMaxVocab = 1 << 30;
+constexpr int64_t kMaxRows = 0x7FFFFFFF;
+constexpr int64_t kMaxTop = 1024;
+// What plans count on, whatever device the call runs on: they decide the
+// order of sums.
+constexpr int kPlanSms = 152;
+
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+int64_t parts_of(int64_t n, int64_t each) { return (n + each - 1) / each; }
+
+// ------------------------------------------------------------------- plans
+// A product of m x n with k summed: its tiles, pairs of CTAs from more than
+// 128 rows on, and the parts that k is split into.
+struct Plan {
+    int group, tiles_m, tiles_n, k_blocks, splits;
+    int64_t tiles() const { return static_cast<int64_t>(tiles_m) * tiles_n; }
+    int64_t units() const { return tiles() * k_blocks; }
+    void split(int64_t most_blocks, int most_splits)
+    {
+        int64_t s = parts_of(k_blocks, most_blocks < 1 ? 1 : most_blocks);
+        s = s < most_splits ? s : most_splits;
+        splits = static_cast<int>(parts_of(k_blocks, parts_of(k_blocks, s)));  // none empty
+    }
+};
+
+Plan plan_of(int64_t m, int64_t n, int64_t k, int group)
+{
+    Plan p;
+    p.group = group;
+    p.tiles_m = static_cast<int>(parts_of(m, kTileRows * group));
+    p.tiles_n = static_cast<int>(parts_of(n, kTileCols));
+    p.k_blocks = static_cast<int>(parts_of(k, kTileDepth));
+    p.splits = 1;
+    return p;
+}
+
+int group_for(int64_t m) { return m <= kTileRows ? 1 : 2; }
+
+// The split of one product that runs alone: as many parts as fill the
+// workers once, of at least kLeastBlocks steps.
+constexpr int kLeastBlocks = 8;
+constexpr int kMostSplits = 32;
+void split_alone(Plan* p)
+{
+    const int64_t workers = kPlanSms / p->group, tiles = p->tiles();
+    if (tiles * 2 > workers)
+        return;
+    const int64_t parts = workers / tiles;
+    const int64_t each = parts_of(p->k_blocks, parts);
+    p->split(each < kLeastBlocks ? kLeastBlocks : each, kMostSplits);
+}
+
+// Two products in one launch (either may be absent: no tiles): no tile longer than a
+// quarter of a worker's share.
+void split_pair(Plan* p, Plan* q)
+{
+    const int64_t workers = kPlanSms / p->group, all = p->units() + q->units();
+    int64_t most = all / (4 * workers);
+    most = most < 2 * kLeastBlocks ? 2 * kLeastBlocks : most;
+    p->split(most, kMostSplits);
+    q->split(most, kMostSplits);
+}
+
+int64_t partial_bytes(const Plan& p, int64_t m, int64_t n) { return p.splits > 1 ? p.splits * m * n * 4 : 0; }
+
+// Parts of a call's workspace, each on 256 bytes.
+struct Carver {
+    char* base;
+    int64_t used = 0;
+    explicit Carver(void* p) : base(static_cast<char*>(p)) {}
+    template <class T = void>
+    T* take(int64_t bytes)
+    {
+        char* at = base ? base + used : nullptr;
+        used += up(bytes, 256);
+        return bytes ? reinterpret_cast<T*>(at) : nullptr;
+    }
+};
+
+// ------------------------------------------------------------------ checks
+bool dtype_ok(int dtype) { return dtype == DRADD_BF16 || dtype == DRADD_F16; }
+
+View matrix_view(const void* p, int64_t rows, int64_t cols, int64_t stride, int64_t elem)
+{
+    View v;
+    v.base = reinterpret_cast<uintptr_t>(p);
+    v.elem = elem;
+    v.add(rows, stride);
+    v.add(cols, 1);
+    return v;
+}
+View flat(const void* p, int64_t n, int64_t elem) { return matrix_view(p, 1, n, n, elem); }
+
+struct Checks {
+    View outs[4], ins[8];
+    int n_out = 0, n_in = 0;
+    bool exact_ok[8] = {};  // in: an output may be exactly this
+    dradd_status st = DRADD_OK;
+
+    void fail(dradd_status s)
+    {
+        if (st == DRADD_OK)
+            st = s;
+    }
+    // A 16-bit matrix.
+    void matrix(const dradd_matrix* m, int64_t rows, int64_t cols, bool out, bool exact = false)
+    {
+        if (!m || !m->data)
+            return fail(DRADD_ERR_NULL_PTR);
+        if (!aligned(m->data, 16) || (rows > 1 && m->stride % 8 != 0))
+            return fail(DRADD_ERR_MISALIGNED);
+        if (rows > 1 && m->stride < cols)
+            return fail(DRADD_ERR_BAD_SHAPE);
+        add(matrix_view(m->data, rows, cols, m->stride, 2), out, exact);
+    }
+    void buffer(const void* p, int64_t n, int64_t elem, int64_t align, bool out)
+    {
+        if (!p)
+            return fail(DRADD_ERR_NULL_PTR);
+        if (!aligned(p, align))
+            return fail(DRADD_ERR_MISALIGNED);
+        add(flat(p, n, elem), out, false);
+    }
+    void add(const View& v, bool out, bool exact)
+    {
+        if (!view_fits(v))
+            return fail(DRADD_ERR_BAD_SHAPE);
+        if (out) {
+            outs[n_out++] = v;
+        } else {
+            exact_ok[n_in] = exact;
+            ins[n_in++] = v;
+        }
+    }
+    void workspace(void* p, size_t have, size_t need)
+    {
+        if (need == 0)
+            return;
+        if (!p || have < need)
+            return fail(DRADD_ERR_WORKSPACE);
+        buffer(p, static_cast<int64_t>(need), 1, 16, true);
+    }
+    dradd_status done()
+    {
+        if (st != DRADD_OK)
+            return st;
+        for (int i = 0; i < n_out; ++i) {
+            for (int j = i + 1; j < n_out; ++j)
+                if (views_may_overlap(outs[i], outs[j]))
+                    return DRADD_ERR_ALIAS;
+            for (int j = 0; j < n_in; ++j)
+                if (!(exact_ok[j] && i == 0 && outs[i].same(ins[j])) && views_may_overlap(outs[i], ins[j]))
+                    return DRADD_ERR_ALIAS;
+        }
+        return DRADD_OK;
+    }
+};
+
+dradd_status inner_ok(int64_t n)
+{
+    if (n <= 0)
+        return DRADD_ERR_BAD_SHAPE;
+    return n % 8 != 0 || n >= kMaxInner ? DRADD_ERR_UNSUPPORTED_HIDDEN : DRADD_OK;
+}
+
+dradd_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DRADD_OK : DRADD_ERR_CUDA; }
+
+#define DRADD_TRY(call)            \
+    do {                           \
+        const dradd_status tried = (call); \
+        if (tried != DRADD_OK)         \
+            return tried;              \
+    } while (0)
+
+// ---------------------------------------------------------------- products
+struct Side {  // an operand: a matrix in memory, its rows along k or not
+    const void* data;
+    int64_t rows, cols, stride;
+    bool mn;
+};
+
+// A row stride for a matrix of one row, which a map wants to be a whole and
+// sufficient number of bytes all the same.
+int64_t map_stride(const Side& s) { return s.rows > 1 ? s.stride : up(s.cols, 8); }
+
+dradd_status set_shape(ProductShape* s, const Plan& p, const Side& a, const Side& b)
+{
+    s->a_mn = a.mn;
+    s->b_mn = b.mn;
+    s->tiles_m = p.tiles_m;
+    s->tiles_n = p.tiles_n;
+    s->k_blocks = p.k_blocks;
+    s->splits = p.splits;
+    const bool ok = make_map(&s->a, a.data, a.rows, a.cols, map_stride(a), a.mn ? 64 : kTileRows) &&
+                    make_map(&s->b, b.data, b.rows, b.cols, map_stride(b), b.mn ? 64 : kTileCols / p.group);
+    return ok ? DRADD_OK : DRADD_ERR_CUDA;
+}
+
+template <class K>
+dradd_status start(ProductArgs<K>* a, int dtype, int* sms)
+{
+    DeviceLimits L;
+    DRADD_TRY(query_limits(&L));
+    *sms = L.sm_count;
+    a->bf16 = dtype == DRADD_BF16;
+    a->wait_limit_ns = kDefaultWaitLimitNs;
+    return from_cuda(device_status_ptr(&a->status));
+}
+
+template <class K>
+dradd_status run_product(const Plan& p, const Side& a, const Side& b, const typename K::Params& epi, int dtype, cudaStream_t stream)
+{
+    static_assert(sizeof(ProductArgs<K>) <= 4096, "kernel parameters");
+    ProductArgs<K> args = {};
+    int sms = 0;
+    DRADD_TRY(start(&args, dtype, &sms));
+    DRADD_TRY(set_shape(&args.shape[0], p, a, b));
+    args.epi[0] = epi;
+    const int64_t tiles = p.tiles() * p.splits;
+    args.tiles0 = args.tiles = static_cast<int>(tiles);
+    return from_cuda(launch_product<K>(args, p.group, sms, stream));
+}
+
+// Two products whose results are gradients, the longer tiles first; q with
+// no tiles: one.
+struct GradProduct {
+    Plan plan;
+    Side a, b;
+    GradParams epi;
+    bool on;
+};
+
+dradd_status run_gradients(GradProduct p, GradProduct q, int dtype, cudaStream_t stream)
+{
+    if (!p.on && !q.on)
+        return DRADD_OK;
+    const auto blocks = [](const GradProduct& g) { return parts_of(g.plan.k_blocks, g.plan.splits); };
+    if (!p.on || (q.on && blocks(q) > blocks(p))) {
+        const GradProduct t = p;
+        p = q;
+        q = t;
+    }
+    ProductArgs<GradProducts> args = {};
+    int sms = 0;
+    DRADD_TRY(start(&args, dtype, &sms));
+    DRADD_TRY(set_shape(&args.shape[0], p.plan, p.a, p.b));
+    args.epi[0] = p.epi;
+    args.tiles0 = args.tiles = static_cast<int>(p.plan.tiles() * p.plan.splits);
+    if (q.on) {
+        DRADD_TRY(set_shape(&args.shape[1], q.plan, q.a, q.b));
+        args.epi[1] = q.epi;
+        args.tiles += static_cast<int>(q.plan.tiles() * q.plan.splits);
+        args.worth = static_cast<int>((blocks(p) + blocks(q) / 2) / blocks(q));
+    }
+    return from_cuda(launch_product<GradProducts>(args, p.plan.group, sms, stream));
+}
+
+dradd_status finish_sums(const float* partials, int splits, int64_t rows, int64_t cols, void* out, const float* factor,
+                         int dtype, cudaStream_t stream)
+{
+    FinishParams f = {};
+    f.partials = partials;
+    f.splits = splits;
+    f.factor = factor;
+    f.act.out = out;
+    f.act.out_stride = cols;
+    f.act.rows = static_cast<int>(rows);
+    f.act.cols = static_cast<int>(cols);
+    f.act.act = -1;
+    f.bf16 = dtype == DRADD_BF16;
+    return from_cuda(launch_finish(f, stream));
+}
+
+// ------------------------------------------------------- linear_act_add
+Plan forward_plan(int64_t rows, int64_t inner, int64_t cols)
+{
+    Plan p = plan_of(rows, cols, inner, group_for(rows));
+    split_alone(&p);
+    return p;
+}
+
+bool few(int64_t rows) { return rows <= kFewRows; }
+
+dradd_status linear_shape(int64_t rows, int64_t inner, int64_t cols)
+{
+    if (rows < 0 || rows > kMaxRows)
+        return DRADD_ERR_BAD_SHAPE;
+    DRADD_TRY(inner_ok(inner));
+    DRADD_TRY(inner_ok(cols));
+    // tiles of every product below are counted in 32 bits
+    return parts_of(rows, kTileRows) * parts_of(inner > cols ? inner : cols, kTileCols) * kMostSplits > kMaxRows
+               ? DRADD_ERR_BAD_SHAPE
+               : DRADD_OK;
+}
+
+struct LinearGradPlan {
+    Plan z, dx, dw;
+    int chunks;
+    int64_t dz, partial_z, partial_dx, partial_dw, partial_db;
+    int64_t bytes;
+};
+
+LinearGradPlan linear_grad_plan(int64_t rows, int64_t inner, int64_t cols, int act, bool want_dx, bool want_dw,
+                                bool want_db)
+{
+    LinearGradPlan g = {};
+    g.z = forward_plan(rows, inner, cols);
+    const int group = rows <= kTileRows && cols <= kTileRows ? 1 : 2;
+    g.dx = plan_of(rows, inner, cols, group);
+    g.dw = plan_of(cols, inner, rows, group);
+    if (!want_dx)
+        g.dx.tiles_m = 0;
+    if (!want_dw)
+        g.dw.tiles_m = 0;
+    split_pair(&g.dx, &g.dw);
+    const int64_t c = parts_of(rows, 64);
+    g.chunks = static_cast<int>(c < 64 ? c : 64);
+    g.dz = act == DRADD_ACT_NONE ? 0 : rows * cols * 2;
+    g.partial_z = act == DRADD_ACT_NONE ? 0 : partial_bytes(g.z, rows, cols);
+    g.partial_dx = want_dx ? partial_bytes(g.dx, rows, inner) : 0;
+    g.partial_dw = want_dw ? partial_bytes(g.dw, cols, inner) : 0;
+    g.partial_db = want_db ? g.chunks * cols * 4 : 0;
+    Carver c0(nullptr);
+    for (const int64_t n : {g.dz, g.partial_z, g.partial_dx, g.partial_dw, g.partial_db})
+        c0.take(n);
+    g.bytes = c0.used;
+    return g;
+}
+
+ActParams act_params(void* out, int64_t out_stride, const void* bias, const void* other, int64_t other_stride,
+                     int64_t rows, int64_t cols, int act)
+{
+    return {out, out_stride, bias, other, other_stride, static_cast<int>(rows), static_cast<int>(cols), act};
+}
+
+// out = residual + act(x W^T + bias), or with `grad` dz; by one product, or
+// by split ones and their finish.
+dradd_status run_linear(const Plan& p, const dradd_matrix& x, const dradd_matrix& w, const ActParams& act, bool grad,
+                        int64_t inner, float* partials, int dtype, cudaStream_t stream)
+{
+    const Side a = {x.data, act.rows, inner, x.stride, false}, b = {w.data, act.cols, inner, w.stride, false};
+    if (p.splits == 1)
+        return grad ? run_product<ActGradProduct>(p, a, b, act, dtype, stream)
+                    : run_product<ActProduct>(p, a, b, act, dtype, stream);
+    const SplitParams s = {partials, act.rows, act.cols, 0};
+    DRADD_TRY(run_product<SplitProduct>(p, a, b, s, dtype, stream));
+    FinishParams f = {partials, p.splits, nullptr, act, grad, dtype == DRADD_BF16};
+    return from_cuda(launch_finish(f, stream));
+}
+
+// --------------------------------------------------------------- the losses
+// A loss's words: a target a row, or a teacher's entries.
+struct LossCall {
+    const int64_t* target;
+    int64_t ignore_index;
+    const dradd_teacher* teacher;
+    int64_t rows, hidden, vocab;
+    int64_t top() const { return teacher ? teacher->top : 0; }
+    float inv_temperature() const { return teacher ? 1.0f / teacher->temperature : 1.0f; }
+};
+
+dradd_status loss_shape(const LossCall& c, int dtype)
+{
+    if (!dtype_ok(dtype))
+        return DRADD_ERR_BAD_ARG;
+    if (c.teacher) {
+        const dradd_teacher& t = *c.teacher;
+        if (t.logits_dtype != DRADD_BF16 && t.logits_dtype != DRADD_F16 && t.logits_dtype != DRADD_F32)
+            return DRADD_ERR_BAD_ARG;
+        if (!std::isfinite(t.temperature) || !(t.temperature > 0.0f) || !std::isfinite(1.0f / t.temperature))
+            return DRADD_ERR_BAD_ARG;
+        if (t.top < 1 || t.top > kMaxTop)
+            return DRADD_ERR_BAD_SHAPE;
+    }
+    if (c.rows < 0 || c.rows > kMaxRows || c.vocab < 1 || c.vocab > kMaxVocab)
+        return DRADD_ERR_BAD_SHAPE;
+    DRADD_TRY(inner_ok(c.hidden));
+    const int64_t tr = parts_of(c.rows, kTileRows), tv = parts_of(c.vocab, kTileRows),
+                  th = parts_of(c.hidden, kTileCols);
+    if (tr * parts_of(c.vocab, kTileCols) > kMaxRows || (tr + tv) * th * kMostSplits > kMaxRows)
+        return DRADD_ERR_BAD_SHAPE;
+    return DRADD_OK;
+}
+
+void loss_inputs(Checks* k, const LossCall& c, const dradd_matrix* x, const dradd_matrix* w)
+{
+    k->matrix(x, c.rows, c.hidden, false);
+    k->matrix(w, c.vocab, c.hidden, false);
+    if (c.teacher) {
+        const int64_t eb = c.teacher->logits_dtype == DRADD_F32 ? 4 : 2;
+        k->buffer(c.teacher->index, c.rows * c.teacher->top, 8, 8, false);
+        k->buffer(c.teacher->logits, c.rows * c.teacher->top, eb, eb, false);
+    } else {
+        k->buffer(c.target, c.rows, 8, 8, false);
+    }
+}
+
+// The workspace of a teacher's entries.
+struct TeacherSpace {
+    int* entries;
+    float* shares;
+    float* entropy;
+    uint16_t* first;
+    int parts;
+
+    TeacherSpace(Carver* w, int64_t rows, int64_t vocab, int64_t top, bool with_entropy)
+    {
+        parts = static_cast<int>(2 * parts_of(vocab, kTileCols));
+        entries = w->take<int>(rows * top * 4);
+        shares = w->take<float>(rows * top * 4);
+        entropy = w->take<float>(top && with_entropy ? rows * 4 : 0);
+        first = w->take<uint16_t>(top ? rows * parts * 2 : 0);
+    }
+    cudaError_t run(const LossCall& c, cudaStream_t stream) const
+    {
+        TeacherParams p = {};
+        p.index = c.teacher->index;
+        p.logits = c.teacher->logits;
+        p.logits_type = c.teacher->logits_dtype;
+        p.entries = entries;
+        p.shares = shares;
+        p.entropy = entropy;
+        p.first = first;
+        p.rows = static_cast<int>(c.rows);
+        p.top = static_cast<int>(c.teacher->top);
+        p.vocab = static_cast<int>(c.vocab);
+        p.parts = parts;
+        p.inv_temperature = c.inv_temperature();
+        return launch_teacher(p, stream);
+    }
+};
+
+struct LossForwardSpace {
+    TeacherSpace teacher;
+    float2* part;
+    float* picked;
+
+    LossForwardSpace(Carver* w, int64_t rows, int64_t vocab, int64_t top) : teacher(w, rows, vocab, top, true)
+    {
+        part = w->take<float2>(teacher.parts * rows * 8);
+        picked = w->take<float>((top ? teacher.parts : 1) * rows * 4);
+    }
+};
+
+constexpr float kLog2eHost = 1.4426950408889634f;
+
+size_t loss_fwd_bytes(int64_t rows, int64_t hidden, int64_t vocab, int64_t top)
+{
+    (void)hidden;
+    Carver w(nullptr);
+    LossForwardSpace s(&w, rows, vocab, top);
+    return static_cast<size_t>(w.used);
+}
+
+dradd_status loss_fwd(float* loss, float* lse, const dradd_matrix* x, const dradd_matrix* weight, const LossCall& c,
+                      int dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    DRADD_TRY(loss_shape(c, dtype));
+    if (c.rows == 0)
+        return DRADD_OK;
+    Checks k;
+    k.buffer(loss, c.rows, 4, 4, true);
+    k.buffer(lse, c.rows, 4, 4, true);
+    loss_inputs(&k, c, x, weight);
+    k.workspace(workspace, workspace_bytes, loss_fwd_bytes(c.rows, c.hidden, c.vocab, c.top()));
+    DRADD_TRY(k.done());
+    Carver w(workspace);
+    const LossForwardSpace s(&w, c.rows, c.vocab, c.top());
+    if (c.teacher)
+        DRADD_TRY(from_cuda(s.teacher.run(c, stream)));
+    const Plan p = plan_of(c.rows, c.vocab, c.hidden, group_for(c.rows));
+    StatsParams e = {};
+    e.part = s.part;
+    e.picked = s.picked;
+    e.target = c.target;
+    e.entries = s.teacher.entries;
+    e.shares = s.teacher.shares;
+    e.first = s.teacher.first;
+    e.parts = s.teacher.parts;
+    e.rows = static_cast<int>(c.rows);
+    e.vocab = static_cast<int>(c.vocab);
+    e.top = static_cast<int>(c.top());
+    e.scale = kLog2eHost * c.inv_temperature();
+    DRADD_TRY(run_product<StatsProduct>(p, {x->data, c.rows, c.hidden, x->stride, false},
+                                    {weight->data, c.vocab, c.hidden, weight->stride, false}, e, dtype, stream));
+    LossParams l = {};
+    l.loss = loss;
+    l.lse = lse;
+    l.part = s.part;
+    l.picked = s.picked;
+    l.target = c.target;
+    l.ignore_index = c.ignore_index;
+    l.entries = s.teacher.entries;
+    l.entropy = s.teacher.entropy;
+    l.rows = e.rows;
+    l.vocab = e.vocab;
+    l.top = e.top;
+    l.parts = s.teacher.parts;
+    l.inv_temperature = c.inv_temperature();
+    return from_cuda(launch_loss(l, stream));
+}
+
+// The gradients take the vocabulary in pieces whose dz fills at most
+// kPieceBytes (and at least one column of tiles).
+constexpr int64_t kPieceBytes = 256ll << 20;
+
+struct LossGradPlan {
+    int64_t piece, pieces;
+    Plan dx, dw;  // of a whole piece; the last may be smaller
+};
+
+LossGradPlan loss_grad_plan(int64_t rows, int64_t hidden, int64_t vocab)
+{
+    LossGradPlan g = {};
+    const int64_t whole = up(vocab, kTileCols);
+    int64_t most = kPieceBytes / (2 * rows) / kTileCols * kTileCols;
+    most = most < kTileCols ? kTileCols : most;
+    g.pieces = parts_of(whole, most);
+    g.piece = up(parts_of(whole, g.pieces), kTileCols);  // of about one size
+    g.pieces = parts_of(whole, g.piece);
+    const int64_t width = g.pieces == 1 ? vocab : g.piece;
+    const int group = rows <= kTileRows && width <= kTileRows ? 1 : 2;
+    g.dx = plan_of(rows, hidden, width, group);
+    g.dw = plan_of(width, hidden, rows, group);
+    split_pair(&g.dx, &g.dw);
+    g.dw.splits = 1;  // its sums run over the rows alone
+    return g;
+}
+
+struct LossBackwardSpace {
+    TeacherSpace teacher;
+    float2* coef;
+    float* factor;
+    void* x_live;
+    void* dz;
+    float* partials;  // dx
+
+    LossBackwardSpace(Carver* w, const LossGradPlan& g, int64_t rows, int64_t hidden, int64_t vocab, int64_t top)
+        : teacher(w, rows, vocab, top, false)
+    {
+        coef = w->take<float2>(rows * 8);
+        factor = w->take<float>(8);
+        x_live = w->take(rows * hidden * 2);
+        dz = w->take(rows * g.piece * 2);
+        partials = w->take<float>(g.dx.splits > 1 || g.pieces > 1 ? g.dx.splits * rows * hidden * 4 : 0);
+    }
+};
+
+size_t loss_bwd_bytes(int64_t rows, int64_t hidden, int64_t vocab, int64_t top)
+{
+    Carver w(nullptr);
+    LossBackwardSpace s(&w, loss_grad_plan(rows, hidden, vocab), rows, hidden, vocab, top);
+    return static_cast<size_t>(w.used);
+}
+
+dradd_status loss_bwd(void* dx, void* dweight, const float* dloss, int64_t dloss_stride, const float* dlse,
+                      int64_t dlse_stride, const dradd_matrix* x, const dradd_matrix* weight, const LossCall& c,
+                      const float* lse, int dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    DRADD_TRY(loss_shape(c, dtype));
+    if (dloss_stride < 0 || dloss_stride > 1 || dlse_stride < 0 || dlse_stride > 1)
+        return DRADD_ERR_BAD_SHAPE;
+    if (dweight && !aligned(dweight, 16))
+        return DRADD_ERR_MISALIGNED;
+    if (c.rows == 0)
+        return dweight ? from_cuda(cudaMemsetAsync(dweight, 0, c.vocab * c.hidden * 2, stream)) : DRADD_OK;
+    if (!dx && !dweight)
+        return DRADD_OK;
+    Checks k;
+    const int64_t r = c.rows, h = c.hidden, v = c.vocab;
+    const dradd_matrix mx = {dx, h}, mw = {dweight, h};
+    if (dx)
+        k.matrix(&mx, r, h, true);
+    if (dweight)
+        k.matrix(&mw, v, h, true);
+    loss_inputs(&k, c, x, weight);
+    k.buffer(dloss, dloss_stride ? r : 1, 4, 4, false);
+    if (dlse)
+        k.buffer(dlse, dlse_stride ? r : 1, 4, 4, false);
+    k.buffer(lse, r, 4, 4, false);
+    k.workspace(workspace, workspace_bytes, loss_bwd_bytes(r, h, v, c.top()));
+    DRADD_TRY(k.done());
+    const LossGradPlan g = loss_grad_plan(r, h, v);
+    Carver w(workspace);
+    const LossBackwardSpace s(&w, g, r, h, v, c.top());
+    if (c.teacher)
+        DRADD_TRY(from_cuda(s.teacher.run(c, stream)));
+    CoefParams f = {};
+    f.dloss = dloss;
+    f.dloss_stride = dloss_stride;
+    f.dlse = dlse;
+    f.dlse_stride = dlse_stride;
+    f.target = c.target;
+    f.ignore_index = c.ignore_index;
+    f.entries = s.teacher.entries;
+    f.x = x->data;
+    f.x_stride = x->stride;
+    f.x_live = dweight ? s.x_live : nullptr;
+    f.coef = s.coef;
+    f.factor = dtype == DRADD_F16 ? s.factor : nullptr;
+    f.rows = static_cast<int>(r);
+    f.inner = static_cast<int>(h);
+    f.vocab = static_cast<int>(v);
+    f.top = static_cast<int>(c.top());
+    f.inv_temperature = c.inv_temperature();
+    DRADD_TRY(from_cuda(launch_coef(f, stream)));
+    const float* factor = f.factor ? f.factor + 1 : nullptr;
+    for (int64_t i = 0; i < g.pieces; ++i) {
+        const int64_t col0 = i * g.piece, width = v - col0 < g.piece ? v - col0 : g.piece;
+        const char* w0 = static_cast<const char*>(weight->data) + col0 * weight->stride * 2;
+        SlopeParams e = {};
+        e.out = s.dz;
+        e.stride = g.piece;
+        e.lse = lse;
+        e.coef = s.coef;
+        e.target = c.target;
+        e.entries = s.teacher.entries;
+        e.shares = s.teacher.shares;
+        e.first = s.teacher.first;
+        e.parts = s.teacher.parts;
+        e.rows = f.rows;
+        e.vocab = static_cast<int>(width);
+        e.top = f.top;
+        e.col0 = static_cast<int>(col0);
+        e.scale = kLog2eHost * c.inv_temperature();
+        DRADD_TRY(run_product<SlopeProduct>(plan_of(r, width, h, group_for(r)), {x->data, r, h, x->stride, false},
+                                        {w0, width, h, weight->stride, false}, e, dtype, stream));
+        GradProduct px = {}, pw = {};
+        const bool last = i + 1 == g.pieces;
+        px.on = dx != nullptr;
+        px.plan = plan_of(r, h, width, g.dx.group);
+        // the same parts of every piece; of a smaller last one perhaps fewer,
+        // whose other partial sums then stay as they are
+        px.plan.split(parts_of(g.dx.k_blocks, g.dx.splits), kMostSplits);
+        px.a = {s.dz, r, width, g.piece, false};
+        px.b = {w0, width, h, weight->stride, true};
+        px.epi = {last && g.dx.splits == 1 ? dx : nullptr, s.partials, factor, f.rows, f.inner, i > 0};
+        pw.on = dweight != nullptr;
+        pw.plan = plan_of(width, h, r, g.dw.group);
+        pw.a = {s.dz, r, width, g.piece, true};
+        pw.b = {s.x_live, r, h, h, true};
+        pw.epi = {dweight ? static_cast<char*>(dweight) + col0 * h * 2 : nullptr, nullptr, factor,
+                  static_cast<int>(width), f.inner, 0};
+        DRADD_TRY(run_gradients(px, pw, dtype, stream));
+    }
+    if (dx && g.dx.splits > 1)
+        return finish_sums(s.partials, g.dx.splits, r, h, dx, factor, dtype, stream);
+    return DRADD_OK;
+}
+
+LossCall target_call(const int64_t* target, int64_t ignore_index, int64_t rows, int64_t hidden, int64_t vocab)
+{
+    return {target, ignore_index, nullptr, rows, hidden, vocab};
+}
+
+LossCall teacher_call(const dradd_teacher* t, int64_t rows, int64_t hidden, int64_t vocab)
+{
+    return {nullptr, 0, t, rows, hidden, vocab};
+}
+
+bool loss_size_ok(int64_t rows, int64_t hidden, int64_t vocab, int64_t top)
+{
+    dradd_teacher t = {nullptr, nullptr, DRADD_F32, top, 1.0f};
+    return rows > 0 && loss_shape(top ? teacher_call(&t, rows, hidden, vocab)
+                                      : target_call(nullptr, 0, rows, hidden, vocab),
+                                  DRADD_BF16) == DRADD_OK;
+}
+
+}  // namespace
+}  // namespace dradd
+
+using namespace dradd;
+
+extern "C" {
+
+size_t linear_act_add_fwd_workspace_bytes(int64_t rows, int64_t inner, int64_t cols)
+{
+    if (rows <= 0 || linear_shape(rows, inner, cols) != DRADD_OK || few(rows))
+        return 0;
+    return static_cast<size_t>(partial_bytes(forward_plan(rows, inner, cols), rows, cols));
+}
+
+dradd_status linear_act_add_fwd(const dradd_matrix* out, const dradd_matrix* x, const dradd_matrix* weight,
+                                const void* bias, const dradd_matrix* residual, int act, int64_t rows,
+                                int64_t inner, int64_t cols, int dtype, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream)
+{
+    if (!dtype_ok(dtype) || act < DRADD_ACT_NONE || act > DRADD_ACT_SILU)
+        return DRADD_ERR_BAD_ARG;
+    DRADD_TRY(linear_shape(rows, inner, cols));
+    if (rows == 0)
+        return DRADD_OK;
+    const bool has_residual = residual && residual->data;
+    Checks k;
+    k.matrix(out, rows, cols, true);
+    k.matrix(x, rows, inner, false);
+    k.matrix(weight, cols, inner, false);
+    if (bias)
+        k.buffer(bias, cols, 2, 16, false);
+    if (has_residual)
+        k.matrix(residual, rows, cols, false, true);
+    const Plan p = forward_plan(rows, inner, cols);
+    k.workspace(workspace, workspace_bytes, few(rows) ? 0 : partial_bytes(p, rows, cols));
+    DRADD_TRY(k.done());
+    const ActParams a = act_params(out->data, out->stride, bias, has_residual ? residual->data : nullptr,
+                                   has_residual ? residual->stride : 0, rows, cols, act);
+    if (few(rows)) {
+        const FewParams f = {x->data, x->stride, weight->data, weight->stride, static_cast<int>(inner), a,
+                             dtype == DRADD_BF16};
+        return from_cuda(launch_few(f, stream));
+    }
+    return run_linear(p, *x, *weight, a, false, inner, static_cast<float*>(workspace), dtype, stream);
+}
+
+size_t linear_act_add_bwd_workspace_bytes(int64_t rows, int64_t inner, int64_t cols, int act, int want_dx,
+                                          int want_dweight, int want_dbias)
+{
+    if (rows <= 0 || linear_shape(rows, inner, cols) != DRADD_OK || act < DRADD_ACT_NONE || act > DRADD_ACT_SILU)
+        return 0;
+    return static_cast<size_t>(
+        linear_grad_plan(rows, inner, cols, act, want_dx != 0, want_dweight != 0, want_dbias != 0).bytes);
+}
+
+dradd_status linear_act_add_bwd(void* dx, void* dweight, void* dbias, const dradd_matrix* dout,
+                                const dradd_matrix* x, const dradd_matrix* weight, const void* bias, int act,
+                                int64_t rows, int64_t inner, int64_t cols, int dtype, void* workspace,
+                                size_t workspace_bytes, cudaStream_t stream)
+{
+    if (!dtype_ok(dtype) || act < DRADD_ACT_NONE || act > DRADD_ACT_SILU)
+        return DRADD_ERR_BAD_ARG;
+    DRADD_TRY(linear_shape(rows, inner, cols));
+    if (!aligned(dweight, 16) || !aligned(dbias, 16))
+        return DRADD_ERR_MISALIGNED;
+    if (rows == 0) {
+        if (dweight)
+            DRADD_TRY(from_cuda(cudaMemsetAsync(dweight, 0, cols * inner * 2, stream)));
+        return dbias ? from_cuda(cudaMemsetAsync(dbias, 0, cols * 2, stream)) : DRADD_OK;
+    }
+    if (!dx && !dweight && !dbias)
+        return DRADD_OK;
+    const LinearGradPlan g = linear_grad_plan(rows, inner, cols, act, dx, dweight, dbias);
+    Checks k;
+    const dradd_matrix mx = {dx, inner}, mw = {dweight, inner};
+    if (dx)
+        k.matrix(&mx, rows, inner, true);
+    if (dweight)
+        k.matrix(&mw, cols, inner, true);
+    if (dbias)
+        k.buffer(dbias, cols, 2, 16, true);
+    k.matrix(dout, rows, cols, false);
+    k.matrix(x, rows, inner, false);
+    k.matrix(weight, cols, inner, false);
+    if (bias)
+        k.buffer(bias, cols, 2, 16, false);
+    k.workspace(workspace, workspace_bytes, static_cast<size_t>(g.bytes));
+    DRADD_TRY(k.done());
+    Carver w(workspace);
+    void* dz_space = w.take(g.dz);
+    float* partial_z = w.take<float>(g.partial_z);
+    float* partial_dx = w.take<float>(g.partial_dx);
+    float* partial_dw = w.take<float>(g.partial_dw);
+    float* partial_db = w.take<float>(g.partial_db);
+    const void* dz = dout->data;
+    int64_t dz_stride = dout->stride;
+    if (act != DRADD_ACT_NONE) {
+        const ActParams a = act_params(dz_space, cols, bias, dout->data, dout->stride, rows, cols, act);
+        DRADD_TRY(run_linear(g.z, *x, *weight, a, true, inner, partial_z, dtype, stream));
+        dz = dz_space;
+        dz_stride = cols;
+    }
+    if (dbias) {
+        DRADD_TRY(from_cuda(launch_row_sums(dz, dz_stride, static_cast<int>(rows), static_cast<int>(cols),
+                                            dtype == DRADD_BF16, g.chunks, partial_db, stream)));
+        DRADD_TRY(finish_sums(partial_db, g.chunks, 1, cols, dbias, nullptr, dtype, stream));
+    }
+    GradProduct px = {}, pw = {};
+    px.on = dx != nullptr;
+    px.plan = g.dx;
+    px.a = {dz, rows, cols, dz_stride, false};
+    px.b = {weight->data, cols, inner, weight->stride, true};
+    px.epi = {g.dx.splits == 1 ? dx : nullptr, partial_dx, nullptr, static_cast<int>(rows), static_cast<int>(inner), 0};
+    pw.on = dweight != nullptr;
+    pw.plan = g.dw;
+    pw.a = {dz, rows, cols, dz_stride, true};
+    pw.b = {x->data, rows, inner, x->stride, true};
+    pw.epi = {g.dw.splits == 1 ? dweight : nullptr, partial_dw, nullptr, static_cast<int>(cols),
+              static_cast<int>(inner), 0};
+    DRADD_TRY(run_gradients(px, pw, dtype, stream));
+    if (dx && g.dx.splits > 1)
+        DRADD_TRY(finish_sums(partial_dx, g.dx.splits, rows, inner, dx, nullptr, dtype, stream));
+    if (dweight && g.dw.splits > 1)
+        DRADD_TRY(finish_sums(partial_dw, g.dw.splits, cols, inner, dweight, nullptr, dtype, stream));
+    return DRADD_OK;
+}
+
+size_t linear_cross_entropy_fwd_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab)
+{
+    return loss_size_ok(rows, hidden, vocab, 0) ? loss_fwd_bytes(rows, hidden, vocab, 0) : 0;
+}
+
+dradd_status linear_cross_entropy_fwd(float* loss, float* lse, const dradd_matrix* x, const dradd_matrix* weight,
+                                      const int64_t* target, int64_t ignore_index, int64_t rows, int64_t hidden,
+                                      int64_t vocab, int dtype, void* workspace, size_t workspace_bytes,
+                                      cudaStream_t stream)
+{
+    return loss_fwd(loss, lse, x, weight, target_call(target, ignore_index, rows, hidden, vocab), dtype, workspace,
+                    workspace_bytes, stream);
+}
+
+size_t linear_cross_entropy_bwd_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab)
+{
+    return loss_size_ok(rows, hidden, vocab, 0) ? loss_bwd_bytes(rows, hidden, vocab, 0) : 0;
+}
+
+dradd_status linear_cross_entropy_bwd(void* dx, void* dweight, const float* dloss, int64_t dloss_stride,
+                                      const float* dlse, int64_t dlse_stride, const dradd_matrix* x,
+                                      const dradd_matrix* weight, const int64_t* target, int64_t ignore_index,
+                                      const float* lse, int64_t rows, int64_t hidden, int64_t vocab, int dtype,
+                                      void* workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    return loss_bwd(dx, dweight, dloss, dloss_stride, dlse, dlse_stride, x, weight,
+                    target_call(target, ignore_index, rows, hidden, vocab), lse, dtype, workspace, workspace_bytes,
+                    stream);
+}
+
+size_t linear_distill_fwd_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab, int64_t top)
+{
+    return top > 0 && loss_size_ok(rows, hidden, vocab, top) ? loss_fwd_bytes(rows, hidden, vocab, top) : 0;
+}
+
+dradd_status linear_distill_fwd(float* loss, float* lse, const dradd_matrix* x, const dradd_matrix* weight,
+                                const dradd_teacher* teacher, int64_t rows, int64_t hidden, int64_t vocab,
+                                int dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    if (!teacher)
+        return DRADD_ERR_NULL_PTR;
+    return loss_fwd(loss, lse, x, weight, teacher_call(teacher, rows, hidden, vocab), dtype, workspace,
+                    workspace_bytes, stream);
+}
+
+size_t linear_distill_bwd_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab, int64_t top)
+{
+    return top > 0 && loss_size_ok(rows, hidden, vocab, top) ? loss_bwd_bytes(rows, hidden, vocab, top) : 0;
+}
+
+dradd_status linear_distill_bwd(void* dx, void* dweight, const float* dloss, int64_t dloss_stride,
+                                const float* dlse, int64_t dlse_stride, const dradd_matrix* x,
+                                const dradd_matrix* weight, const dradd_teacher* teacher, const float* lse,
+                                int64_t rows, int64_t hidden, int64_t vocab, int dtype, void* workspace,
+                                size_t workspace_bytes, cudaStream_t stream)
+{
+    if (!teacher)
+        return DRADD_ERR_NULL_PTR;
+    return loss_bwd(dx, dweight, dloss, dloss_stride, dlse, dlse_stride, x, weight,
+                    teacher_call(teacher, rows, hidden, vocab), lse, dtype, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

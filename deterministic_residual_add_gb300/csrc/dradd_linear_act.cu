@@ -1,0 +1,114 @@
+// dradd_linear_act.cu -- products with bias, activation and residual behind
+// them, and with the activation's derivative.
+#include "dradd_act.cuh"
+#include "dradd_linear.cuh"
+
+namespace dradd {
+
+// out = residual + act(z + bias).  The residual's next 32 values are on their
+// way while the present ones are worked on.
+struct EpiAct {
+    using Kind = ActProduct;
+    using Params = ActParams;
+    const Params& p;
+    const bool bf16;
+    const int row, col;
+    uint32_t other[16];
+
+    __device__ __forceinline__ EpiAct(const Params& p_, int bf16_, int row_, int col_, int)
+        : p(p_), bf16(bf16_), row(row_), col(col_)
+    {
+        fetch(0);
+    }
+    __device__ __forceinline__ void fetch(int c)
+    {
+        if (p.other && row < p.rows)
+            load32(static_cast<const uint16_t*>(p.other) + row * p.other_stride + col + c, p.cols - col - c, other);
+    }
+    __device__ __forceinline__ void add_bias(const uint32_t (&bits)[32], int c, int n, float (&z)[32])
+    {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            z[j] = __uint_as_float(bits[j]);
+        if (p.bias) {
+            uint32_t b[16];
+            load32(static_cast<const uint16_t*>(p.bias) + col + c, n, b);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                float lo, hi;
+                unpack2(b[j], bf16, lo, hi);
+                z[2 * j] += lo;
+                z[2 * j + 1] += hi;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(const float (&z)[32], int c, int n)
+    {
+        if (row < p.rows) {
+            uint32_t w[16];
+            pack32(z, bf16, w);
+            store32(static_cast<uint16_t*>(p.out) + row * p.out_stride + col + c, w, n);
+        }
+    }
+    __device__ __forceinline__ void columns(const uint32_t (&bits)[32], int c)
+    {
+        const int n = p.cols - col - c;
+        if (n <= 0)
+            return;
+        float z[32];
+        add_bias(bits, c, n, z);
+        act_values(z, p.act);
+        if (p.other) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                float lo, hi;
+                unpack2(other[j], bf16, lo, hi);
+                z[2 * j] += lo;
+                z[2 * j + 1] += hi;
+            }
+            if (c + 32 < kHalfCols)
+                fetch(c + 32);
+        }
+        store(z, c, n);
+    }
+    __device__ __forceinline__ void end() {}
+};
+
+// dz = dout * act'(z + bias).
+struct EpiActGrad : EpiAct {
+    using Kind = ActGradProduct;
+    using EpiAct::EpiAct;
+    __device__ __forceinline__ void columns(const uint32_t (&bits)[32], int c)
+    {
+        const int n = p.cols - col - c;
+        if (n <= 0)
+            return;
+        float z[32];
+        add_bias(bits, c, n, z);
+        act_slopes(z, p.act);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            float lo, hi;
+            unpack2(other[j], bf16, lo, hi);
+            z[2 * j] *= lo;
+            z[2 * j + 1] *= hi;
+        }
+        if (c + 32 < kHalfCols)
+            fetch(c + 32);
+        store(z, c, n);
+    }
+};
+
+template <>
+cudaError_t launch_product<ActProduct>(const ProductArgs<ActProduct>& a, int cta_group, int sm_count, cudaStream_t stream)
+{
+    return launch_with<EpiAct>(a, cta_group, sm_count, stream);
+}
+
+template <>
+cudaError_t launch_product<ActGradProduct>(const ProductArgs<ActGradProduct>& a, int cta_group, int sm_count, cudaStream_t stream)
+{
+    return launch_with<EpiActGrad>(a, cta_group, sm_count, stream);
+}
+
+}  // namespace dradd

@@ -1,0 +1,110 @@
+// dradd_linear_grad.cu -- products whose results are gradients (two of them
+// in one launch), and the partial sums of split products.
+#include "dradd_linear.cuh"
+
+namespace dradd {
+
+__device__ __forceinline__ void add_partials(float* p, float (&v)[32], int n)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (4 * i < n) {
+            const float4 f = *reinterpret_cast<const float4*>(p + 4 * i);
+            v[4 * i] += f.x;
+            v[4 * i + 1] += f.y;
+            v[4 * i + 2] += f.z;
+            v[4 * i + 3] += f.w;
+        }
+}
+
+// Columns come in eights.
+__device__ __forceinline__ void store_partials(float* p, const float (&v)[32], int n)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (8 * i < n)
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 8 * i), "f"(v[8 * i]),
+                         "f"(v[8 * i + 1]), "f"(v[8 * i + 2]), "f"(v[8 * i + 3]), "f"(v[8 * i + 4]),
+                         "f"(v[8 * i + 5]), "f"(v[8 * i + 6]), "f"(v[8 * i + 7])
+                         : "memory");
+}
+
+struct EpiGrad {
+    using Kind = GradProducts;
+    using Params = GradParams;
+    const Params& p;
+    const bool bf16;
+    const int row, col;
+    float* sums;
+    float factor;
+
+    __device__ __forceinline__ EpiGrad(const Params& p_, int bf16_, int row_, int col_, int split)
+        : p(p_), bf16(bf16_), row(row_), col(col_)
+    {
+        sums = p.partials + (static_cast<int64_t>(split) * p.rows + row) * p.cols + col;
+        factor = p.factor ? *p.factor : 1.0f;
+    }
+    __device__ __forceinline__ void columns(const uint32_t (&bits)[32], int c)
+    {
+        const int n = p.cols - col - c;
+        if (n <= 0 || row >= p.rows)
+            return;
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            v[j] = __uint_as_float(bits[j]);
+        if (p.add)
+            add_partials(sums + c, v, n);
+        if (!p.out) {
+            store_partials(sums + c, v, n);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            v[j] *= factor;
+        uint32_t w[16];
+        pack32(v, bf16, w);
+        store32(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(row) * p.cols + col + c, w, n);
+    }
+    __device__ __forceinline__ void end() {}
+};
+
+struct EpiSplit {
+    using Kind = SplitProduct;
+    using Params = SplitParams;
+    const Params& p;
+    const int row, col;
+    float* sums;
+
+    __device__ __forceinline__ EpiSplit(const Params& p_, int, int row_, int col_, int split)
+        : p(p_), row(row_), col(col_)
+    {
+        sums = p.partials + (static_cast<int64_t>(split) * p.rows + row) * p.cols + col;
+    }
+    __device__ __forceinline__ void columns(const uint32_t (&bits)[32], int c)
+    {
+        const int n = p.cols - col - c;
+        if (n <= 0 || row >= p.rows)
+            return;
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            v[j] = __uint_as_float(bits[j]);
+        store_partials(sums + c, v, n);
+    }
+    __device__ __forceinline__ void end() {}
+};
+
+template <>
+cudaError_t launch_product<GradProducts>(const ProductArgs<GradProducts>& a, int cta_group, int sm_count, cudaStream_t stream)
+{
+    return launch_with<EpiGrad>(a, cta_group, sm_count, stream);
+}
+
+template <>
+cudaError_t launch_product<SplitProduct>(const ProductArgs<SplitProduct>& a, int cta_group, int sm_count, cudaStream_t stream)
+{
+    return launch_with<EpiSplit>(a, cta_group, sm_count, stream);
+}
+
+}  // namespace dradd

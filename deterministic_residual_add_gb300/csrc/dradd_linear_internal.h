@@ -1,0 +1,195 @@
+// dradd_linear_internal.h -- argument blocks and launchers of the matrix
+// products of dradd_linear.h.  Not part of the public interface.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace dradd {
+
+// Tiles: 128 rows a CTA (a pair of CTAs: 256) by 256 columns, summed in
+// steps of 64.
+constexpr int kTileRows = 128;
+constexpr int kTileCols = 256;
+constexpr int kTileDepth = 64;
+constexpr int kHalfCols = kTileCols / 2;  // the columns of one epilogue warp
+
+// One product C[m, n] = sum over k of A[m, k] B[n, k].
+struct ProductShape {
+    CUtensorMap a, b;
+    int a_mn, b_mn;        // 1: the operand's rows in memory run along k
+    int tiles_m, tiles_n;
+    int k_blocks;          // steps of 64
+    int splits;            // parts of the k dimension, each a tile of its own
+};
+
+// ------------------------------------------------------------- epilogues
+// A partial sum of a split, fp32 [splits, rows, cols].
+struct SplitParams {
+    float* partials;
+    int rows, cols;
+    int add;  // to what is there
+};
+
+// out = residual + act(z + bias), or dz = dout * act'(z + bias)
+struct ActParams {
+    void* out;
+    int64_t out_stride;
+    const void* bias;      // or NULL
+    const void* other;     // residual or NULL; the gradient: dout
+    int64_t other_stride;
+    int rows, cols;
+    int act;
+};
+
+// Statistics of the logits' rows, a part of 128 columns at a time.
+struct StatsParams {
+    float2* part;            // [parts, rows]: maximum and sum of 2^(z scale - maximum), in base-2 units
+    float* picked;           // cross entropy: [rows], the target's logit; distillation: [parts, rows] sums of share * logit
+    const int64_t* target;   // cross entropy
+    const int* entries;      // distillation: [rows, top] words in rising order, INT_MAX behind the last
+    const float* shares;     // [rows, top]
+    const uint16_t* first;   // [rows, parts] the first entry at or behind a part's first column
+    int parts;
+    int rows, vocab, top;
+    float scale;             // log2(e) / temperature
+};
+
+// dz = coef.x * p - coef.y * share, one piece of the vocabulary at a time.
+struct SlopeParams {
+    void* out;               // [rows, stride]
+    int64_t stride;
+    const float* lse;        // [rows]
+    const float2* coef;      // [rows]
+    const int64_t* target;
+    const int* entries;
+    const float* shares;
+    const uint16_t* first;
+    int parts;
+    int rows, vocab, top;    // vocab: the piece's words
+    int col0;                // its first one, a multiple of 256
+    float scale;
+};
+
+// out = rounded(sum * factor), or into fp32 partials [splits, rows, cols].
+struct GradParams {
+    void* out;               // 16-bit, or NULL: partials
+    float* partials;
+    const float* factor;     // device, or NULL: 1
+    int rows, cols;
+    int add;
+};
+
+// What a launch does with its products, and how many it makes.
+template <class P, int N, int Variant = 0>
+struct ProductKind {
+    using Params = P;
+    static constexpr int kProblems = N;
+};
+using ActProduct = ProductKind<ActParams, 1, 0>;
+using ActGradProduct = ProductKind<ActParams, 1, 1>;
+using SplitProduct = ProductKind<SplitParams, 1>;
+using StatsProduct = ProductKind<StatsParams, 1>;
+using SlopeProduct = ProductKind<SlopeParams, 1>;
+using GradProducts = ProductKind<GradParams, 2>;
+
+template <class K>
+struct ProductArgs {
+    ProductShape shape[K::kProblems];
+    typename K::Params epi[K::kProblems];
+    int tiles0, tiles;       // of the first problem, of all
+    int worth;               // tiles of the second problem that cost as much as one of the first
+    int bf16;
+    unsigned* status;
+    uint64_t wait_limit_ns;
+};
+
+// Sums of splits, finished: out = rounded(sum * factor), or with the
+// activation's parameters as EpiAct (grad: EpiActGrad) does.
+struct FinishParams {
+    const float* partials;   // [splits, rows, cols]
+    int splits;
+    const float* factor;     // device, or NULL: 1
+    ActParams act;           // act.act < 0: the plain sum
+    int grad;
+    int bf16;
+};
+cudaError_t launch_finish(const FinishParams& p, cudaStream_t stream);
+
+// The product for a few rows, its epilogue with it.
+struct FewParams {
+    const void* x;
+    int64_t x_stride;
+    const void* weight;
+    int64_t weight_stride;
+    int inner;
+    ActParams act;
+    int bf16;
+};
+constexpr int kFewRows = 16;
+cudaError_t launch_few(const FewParams& p, cudaStream_t stream);
+
+// Sums of a 16-bit matrix's columns over `chunks` parts of its rows, fp32
+// [chunks, cols].
+cudaError_t launch_row_sums(const void* x, int64_t stride, int rows, int cols, int bf16, int chunks, float* partials,
+                            cudaStream_t stream);
+
+// A teacher's entries in rising order of their words.
+struct TeacherParams {
+    const int64_t* index;    // [rows, top]
+    const void* logits;      // [rows, top]
+    int logits_type;         // DRADD_*
+    int* entries;            // [rows, top]
+    float* shares;           // [rows, top]
+    float* entropy;          // [rows] sum of share log share, or NULL
+    uint16_t* first;         // [rows, parts]
+    int rows, top, vocab, parts;
+    float inv_temperature;
+};
+cudaError_t launch_teacher(const TeacherParams& p, cudaStream_t stream);
+
+// Row statistics joined: lse and loss.
+struct LossParams {
+    float* loss;
+    float* lse;
+    const float2* part;
+    const float* picked;
+    const int64_t* target;   // cross entropy
+    int64_t ignore_index;
+    const int* entries;      // distillation
+    const float* entropy;
+    int rows, vocab, top, parts;
+    float inv_temperature;
+};
+cudaError_t launch_loss(const LossParams& p, cudaStream_t stream);
+
+// A row's two factors, and x with the rows that count for nothing as zeros.
+struct CoefParams {
+    const float* dloss;
+    int64_t dloss_stride;    // 0 or 1
+    const float* dlse;       // or NULL
+    int64_t dlse_stride;
+    const int64_t* target;
+    int64_t ignore_index;
+    const int* entries;
+    const void* x;
+    int64_t x_stride;
+    void* x_live;            // [rows, inner], or NULL
+    float2* coef;
+    float* factor;           // two numbers: what dz is scaled by, and its inverse; or NULL
+    int rows, inner, vocab, top;
+    float inv_temperature;
+};
+cudaError_t launch_coef(const CoefParams& p, cudaStream_t stream);
+
+// Makes the map of a 16-bit matrix of `rows` rows of `cols` elements, `stride`
+// apart, read in boxes of 64 elements by box_rows rows.
+bool make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t stride, int box_rows);
+
+template <class K>
+cudaError_t launch_product(const ProductArgs<K>& a, int cta_group, int sm_count, cudaStream_t stream);
+
+}  // namespace dradd

@@ -1,0 +1,202 @@
+// dradd_linear_loss.cu -- products whose results are logits: their rows'
+// statistics, and the gradients with respect to them.
+#include "dradd_act.cuh"
+#include "dradd_linear.cuh"
+
+namespace dradd {
+
+// The words of a row that count in a part of 128 columns: a target, or the
+// entries of a teacher in rising order.
+struct Words {
+    const int* entry = nullptr;
+    const float* share = nullptr;
+    int left = 0;
+    int next = -1;       // the next word's column in the part; outside [0, 128): none
+    float weight = 1.0f;
+
+    __device__ __forceinline__ void target(int64_t word, int64_t col)
+    {
+        const int64_t at = word - col;
+        next = at >= 0 && at < kHalfCols ? static_cast<int>(at) : kHalfCols;
+    }
+    __device__ __forceinline__ void teacher(const int* e, const float* s, int first, int top, int64_t col)
+    {
+        entry = e + first;
+        share = s + first;
+        left = top - first;
+        base = col;
+        fetch();
+    }
+    __device__ __forceinline__ void advance()
+    {
+        if (left > 0) {
+            ++entry;
+            ++share;
+            --left;
+            fetch();
+        } else {
+            next = kHalfCols;
+        }
+    }
+
+private:
+    int64_t base = 0;
+    __device__ __forceinline__ void fetch()
+    {
+        next = kHalfCols;
+        if (left > 0) {
+            const int64_t at = *entry - base;
+            if (at < kHalfCols) {  // entries are not below the part's first column
+                next = static_cast<int>(at);
+                weight = *share;
+            }
+        }
+    }
+};
+
+struct EpiStats {
+    using Kind = StatsProduct;
+    using Params = StatsParams;
+    const Params& p;
+    const int row, col;
+    const int part;
+    Words words;
+    float high = -INFINITY, sum = 0.0f, picked = 0.0f;
+    bool found = false;
+
+    __device__ __forceinline__ EpiStats(const Params& p_, int, int row_, int col_, int)
+        : p(p_), row(row_), col(col_), part(col_ / kHalfCols)
+    {
+        words.next = kHalfCols;
+        if (row < p.rows) {
+            if (p.top == 0)
+                words.target(p.target[row], col);
+            else
+                words.teacher(p.entries + static_cast<int64_t>(row) * p.top,
+                              p.shares + static_cast<int64_t>(row) * p.top,
+                              p.first[static_cast<int64_t>(row) * p.parts + part], p.top, col);
+        }
+    }
+    __device__ __forceinline__ void columns(const uint32_t (&bits)[32], int c)
+    {
+        float z[32];
+        const int n = p.vocab - col - c;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            z[j] = __uint_as_float(bits[j]);
+        while (words.next < c + 32) {
+            const int at = words.next - c;
+            float v = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                v = j == at ? z[j] : v;
+            picked = p.top == 0 ? v : fmaf(words.weight, v, picked);
+            found = true;
+            words.advance();
+        }
+        if (n < 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                z[j] = j < n ? z[j] : -INFINITY;
+        }
+        float m[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            m[j] = fmaxf(fmaxf(z[j], z[j + 8]), fmaxf(z[j + 16], z[j + 24]));
+#pragma unroll
+        for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+            for (int j = 0; j < d; ++j)
+                m[j] = fmaxf(m[j], m[j + d]);
+        const float now = fmaxf(high, m[0] * p.scale);
+        const float shift = now == -INFINITY ? 0.0f : now;
+        float s[4] = {sum * exp2_fast(high - shift), 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            s[j & 3] += exp2_fast(fmaf(z[j], p.scale, -shift));
+        sum = (s[0] + s[1]) + (s[2] + s[3]);
+        high = now;
+    }
+    __device__ __forceinline__ void end()
+    {
+        if (row >= p.rows)
+            return;
+        const int64_t at = static_cast<int64_t>(part) * p.rows + row;
+        p.part[at] = make_float2(high, sum);
+        if (p.top != 0)
+            p.picked[at] = picked;
+        else if (found)
+            p.picked[row] = picked;
+    }
+};
+
+struct EpiSlope {
+    using Kind = SlopeProduct;
+    using Params = SlopeParams;
+    const Params& p;
+    const bool bf16;
+    const int row, col;
+    Words words;
+    float lse2 = 0.0f;
+    float2 coef = make_float2(0.0f, 0.0f);
+    bool live = false;
+
+    __device__ __forceinline__ EpiSlope(const Params& p_, int bf16_, int row_, int col_, int)
+        : p(p_), bf16(bf16_), row(row_), col(col_)
+    {
+        words.next = kHalfCols;
+        if (row < p.rows) {
+            lse2 = p.lse[row] * kLog2e;
+            coef = p.coef[row];
+            live = coef.x != 0.0f || coef.y != 0.0f;
+            const int64_t at = static_cast<int64_t>(p.col0) + col;
+            if (p.top == 0)
+                words.target(p.target[row], at);
+            else
+                words.teacher(p.entries + static_cast<int64_t>(row) * p.top,
+                              p.shares + static_cast<int64_t>(row) * p.top,
+                              p.first[static_cast<int64_t>(row) * p.parts + at / kHalfCols], p.top, at);
+        }
+    }
+    __device__ __forceinline__ void columns(const uint32_t (&bits)[32], int c)
+    {
+        if (row >= p.rows)
+            return;
+        const int n = p.vocab - col - c;
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            v[j] = coef.x * exp2_fast(fmaf(__uint_as_float(bits[j]), p.scale, -lse2));
+        while (words.next < c + 32) {
+            const int at = words.next - c;
+            const float less = coef.y * words.weight;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                v[j] = j == at ? v[j] - less : v[j];
+            words.advance();
+        }
+        if (n < 32 || !live) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                v[j] = live && j < n ? v[j] : 0.0f;
+        }
+        uint32_t w[16];
+        pack32(v, bf16, w);
+        store32(static_cast<uint16_t*>(p.out) + row * p.stride + col + c, w, 32);
+    }
+    __device__ __forceinline__ void end() {}
+};
+
+template <>
+cudaError_t launch_product<StatsProduct>(const ProductArgs<StatsProduct>& a, int cta_group, int sm_count, cudaStream_t stream)
+{
+    return launch_with<EpiStats>(a, cta_group, sm_count, stream);
+}
+
+template <>
+cudaError_t launch_product<SlopeProduct>(const ProductArgs<SlopeProduct>& a, int cta_group, int sm_count, cudaStream_t stream)
+{
+    return launch_with<EpiSlope>(a, cta_group, sm_count, stream);
+}
+
+}  // namespace dradd

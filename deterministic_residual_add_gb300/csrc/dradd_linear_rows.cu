@@ -1,0 +1,474 @@
+// dradd_linear_rows.cu -- the passes around the products of dradd_linear.h:
+// finishing split sums, column sums, a teacher's entries in order, row
+// factors, and the joining of row statistics.
+#include <climits>
+
+#include "dradd_act.cuh"
+#include "dradd_elem.cuh"
+#include "dradd_internal.h"
+#include "dradd_linear_internal.h"
+
+namespace dradd {
+
+namespace {
+
+__device__ __forceinline__ void widen8(const uint4& v, bool bf16, float (&f)[8])
+{
+    if (bf16)
+        Elem<kElemBf16>::unpack(v, f);
+    else
+        Elem<kElemF16>::unpack(v, f);
+}
+
+__device__ __forceinline__ uint4 narrow8(const float (&f)[8], bool bf16)
+{
+    return bf16 ? Elem<kElemBf16>::pack(f) : Elem<kElemF16>::pack(f);
+}
+
+}  // namespace
+
+// --------------------------------------------------------------- split sums
+// A thread takes 8 columns of a row and adds the splits in order, four of
+// them on their way at a time.
+__global__ void __launch_bounds__(256) finish_kernel(const FinishParams p)
+{
+    wait_prior_grids();
+    allow_next_grid();
+    const int blocks = p.act.cols >> 3;
+    const int64_t all = static_cast<int64_t>(p.act.rows) * blocks;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= all)
+        return;
+    const int64_t row = i / blocks;
+    const int col = static_cast<int>(i - row * blocks) * 8;
+    const bool bf16 = p.bf16;
+    uint4 other = make_uint4(0, 0, 0, 0), bias = other;
+    if (p.act.act >= 0) {
+        if (p.act.other)
+            other = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.act.other) +
+                                                    row * p.act.other_stride + col);
+        if (p.act.bias)
+            bias = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.act.bias) + col);
+    }
+    const int64_t step = static_cast<int64_t>(p.act.rows) * p.act.cols;
+    const float* from = p.partials + row * p.act.cols + col;
+    float z[8] = {};
+    for (int s = 0; s < p.splits; s += 4) {
+        float4 v[4][2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool in = s + j < p.splits;
+            v[j][0] = in ? *reinterpret_cast<const float4*>(from + (s + j) * step) : make_float4(0, 0, 0, 0);
+            v[j][1] = in ? *reinterpret_cast<const float4*>(from + (s + j) * step + 4) : make_float4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            z[0] += v[j][0].x;
+            z[1] += v[j][0].y;
+            z[2] += v[j][0].z;
+            z[3] += v[j][0].w;
+            z[4] += v[j][1].x;
+            z[5] += v[j][1].y;
+            z[6] += v[j][1].z;
+            z[7] += v[j][1].w;
+        }
+    }
+    uint16_t* out = static_cast<uint16_t*>(p.act.out) + row * p.act.out_stride + col;
+    if (p.act.act < 0) {
+        const float factor = p.factor ? *p.factor : 1.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            z[j] *= factor;
+    } else {
+        float b[8], o[8];
+        widen8(bias, bf16, b);
+        widen8(other, bf16, o);
+        if (p.act.bias) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                z[j] += b[j];
+        }
+        if (p.grad) {
+            act_slopes(z, p.act.act);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                z[j] *= o[j];
+        } else {
+            act_values(z, p.act.act);
+            if (p.act.other) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    z[j] += o[j];
+            }
+        }
+    }
+    *reinterpret_cast<uint4*>(out) = narrow8(z, bf16);
+}
+
+cudaError_t launch_finish(const FinishParams& p, cudaStream_t stream)
+{
+    const int64_t all = static_cast<int64_t>(p.act.rows) * (p.act.cols >> 3);
+    return launch(finish_kernel, static_cast<int>((all + 255) / 256), 256, 0, false, stream, p);
+}
+
+// -------------------------------------------------------------- column sums
+// A CTA takes 256 columns and one part of the rows, a warp every eighth row.
+__global__ void __launch_bounds__(256) row_sums_kernel(const uint16_t* x, int64_t stride, int rows, int cols, int bf16,
+                                                       int each, float* partials)
+{
+    __shared__ float sums[8][256];
+    wait_prior_grids();
+    allow_next_grid();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int col = blockIdx.x * 256 + lane * 8;
+    const int r1 = min(rows, (static_cast<int>(blockIdx.y) + 1) * each);
+    float s[8] = {};
+    if (col < cols) {
+        for (int r = blockIdx.y * each + warp; r < r1; r += 32) {
+            uint4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = r + 8 * j < r1 ? *reinterpret_cast<const uint4*>(x + (r + 8 * j) * stride + col)
+                                      : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float f[8];
+                widen8(v[j], bf16, f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    s[k] += f[k];
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        sums[warp][lane * 8 + k] = s[k];
+    __syncthreads();
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c < cols) {
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w)
+            t += sums[w][threadIdx.x];
+        partials[static_cast<int64_t>(blockIdx.y) * cols + c] = t;
+    }
+}
+
+cudaError_t launch_row_sums(const void* x, int64_t stride, int rows, int cols, int bf16, int chunks, float* partials,
+                            cudaStream_t stream)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((cols + 255) / 256), static_cast<unsigned>(chunks));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, row_sums_kernel, static_cast<const uint16_t*>(x), stride, rows, cols, bf16,
+                              (rows + chunks - 1) / chunks, partials);
+}
+
+// ------------------------------------------------------------------ teacher
+// A CTA sorts one row's entries by (word, place) in shared memory, computes
+// their shares and where each part of 128 columns begins.
+constexpr int kTeacherThreads = 128;
+
+__device__ __forceinline__ float teacher_logit(const TeacherParams& p, int64_t at)
+{
+    if (p.logits_type == kElemF32)
+        return static_cast<const float*>(p.logits)[at];
+    const uint16_t v = static_cast<const uint16_t*>(p.logits)[at];
+    return p.logits_type == kElemBf16 ? Elem<kElemBf16>::widen(v) : Elem<kElemF16>::widen(v);
+}
+
+__global__ void __launch_bounds__(kTeacherThreads) teacher_kernel(const TeacherParams p, int size)
+{
+    extern __shared__ unsigned long long keys[];  // size of them, then as many logits
+    __shared__ float red[4];
+    __shared__ int bad;
+    wait_prior_grids();
+    allow_next_grid();
+    float* logits = reinterpret_cast<float*>(keys + size);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t row = blockIdx.x;
+    if (tid == 0)
+        bad = 0;
+    __syncthreads();
+    float high = -INFINITY;
+    for (int i = tid; i < size; i += kTeacherThreads) {
+        unsigned long long key = ~0ull;
+        float v = -INFINITY;
+        if (i < p.top) {
+            const int64_t word = p.index[row * p.top + i];
+            if (word >= p.vocab)
+                bad = 1;
+            if (word >= 0 && word < p.vocab) {
+                v = teacher_logit(p, row * p.top + i) * p.inv_temperature;
+                key = (static_cast<unsigned long long>(word) << 32) | static_cast<unsigned>(i);
+                high = v > high || v != v ? v : high;  // a NaN stays
+            }
+        }
+        keys[i] = key;
+        logits[i] = v;
+    }
+    for (int span = 2; span <= size; span *= 2) {
+        for (int gap = span / 2; gap > 0; gap /= 2) {
+            __syncthreads();
+            for (int i = tid; i < size / 2; i += kTeacherThreads) {
+                const int lo = 2 * gap * (i / gap) + i % gap;
+                const bool up = (lo & span) == 0;
+                const unsigned long long x = keys[lo], y = keys[lo + gap];
+                if ((x > y) == up) {
+                    keys[lo] = y;
+                    keys[lo + gap] = x;
+                }
+            }
+        }
+    }
+    high = warp_max_nan(high);
+    if (lane == 0)
+        red[warp] = high;
+    __syncthreads();
+    high = red[0];
+#pragma unroll
+    for (int w = 1; w < 4; ++w)
+        high = red[w] > high || red[w] != red[w] ? red[w] : high;
+    const bool nan_row = bad != 0;
+    const bool counted = nan_row || high != -INFINITY;
+    __syncthreads();
+    // the sum of a row's exponentials: each thread's in order, then lanes, then warps
+    float sum = 0.0f, weighted = 0.0f;
+    if (counted) {
+        for (int i = tid; i < size; i += kTeacherThreads) {
+            if (keys[i] != ~0ull) {
+                const float d = logits[static_cast<unsigned>(keys[i])] - high;
+                const float e = exp2_fast(d * kLog2e);
+                sum += e;
+                weighted += e > 0.0f ? e * d : e;  // a share of 0 has no entropy; NaN stays
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        weighted += __shfl_xor_sync(0xffffffffu, weighted, d);
+    }
+    __shared__ float parts[2][4];
+    if (lane == 0) {
+        parts[0][warp] = sum;
+        parts[1][warp] = weighted;
+    }
+    __syncthreads();
+    sum = (parts[0][0] + parts[0][1]) + (parts[0][2] + parts[0][3]);
+    weighted = (parts[1][0] + parts[1][1]) + (parts[1][2] + parts[1][3]);
+    const float nan = __int_as_float(0x7FC00000);
+    for (int i = tid; i < p.top; i += kTeacherThreads) {
+        const unsigned long long key = keys[i];
+        int word = key == ~0ull ? INT_MAX : static_cast<int>(key >> 32);
+        float share = 0.0f;
+        if (nan_row) {
+            word = i == 0 ? 0 : INT_MAX;
+            share = nan;
+        } else if (!counted) {
+            word = INT_MAX;
+        } else if (word != INT_MAX) {
+            share = exp2_fast((logits[static_cast<unsigned>(key)] - high) * kLog2e) / sum;
+        }
+        p.entries[row * p.top + i] = word;
+        p.shares[row * p.top + i] = share;
+    }
+    if (p.entropy && tid == 0)
+        p.entropy[row] = nan_row ? nan : counted ? weighted / sum - logf(sum) : 0.0f;
+    // the first entry at or behind each part's first column
+    for (int g = tid; g < p.parts; g += kTeacherThreads) {
+        int at = 0;
+        if (!nan_row && counted) {
+            const unsigned long long from = static_cast<unsigned long long>(g) * kHalfCols << 32;
+            int hi = size;
+            while (at < hi) {
+                const int mid = (at + hi) >> 1;
+                if (keys[mid] < from)
+                    at = mid + 1;
+                else
+                    hi = mid;
+            }
+            at = min(at, p.top);
+        } else if (nan_row) {
+            at = g > 0;
+        }
+        p.first[row * p.parts + g] = static_cast<uint16_t>(at);
+    }
+}
+
+cudaError_t launch_teacher(const TeacherParams& p, cudaStream_t stream)
+{
+    int size = 2;
+    while (size < p.top)
+        size *= 2;
+    return launch(teacher_kernel, p.rows, kTeacherThreads, static_cast<size_t>(size) * 12, false, stream, p, size);
+}
+
+// --------------------------------------------------------- joined statistics
+// A CTA takes 32 rows, a lane each; its warps every 32nd part.
+__global__ void __launch_bounds__(1024) loss_kernel(const LossParams p)
+{
+    __shared__ float highs[32][33], sums[32][33], picks[32][33];
+    wait_prior_grids();
+    allow_next_grid();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    const bool teacher = p.top != 0;
+    float high = -INFINITY, sum = 0.0f, picked = 0.0f;
+    if (row < p.rows) {
+        for (int g = warp; g < p.parts; g += 128) {
+            float2 v[4];
+            float k[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t at = static_cast<int64_t>(g + 32 * j) * p.rows + row;
+                const bool in = g + 32 * j < p.parts;
+                v[j] = in ? p.part[at] : make_float2(-INFINITY, 0.0f);
+                k[j] = in && teacher ? p.picked[at] : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float now = fmaxf(high, v[j].x), shift = now == -INFINITY ? 0.0f : now;
+                sum = sum * exp2_fast(high - shift) + v[j].y * exp2_fast(v[j].x - shift);
+                high = now;
+                picked += k[j];
+            }
+        }
+    }
+    highs[warp][lane] = high;
+    sums[warp][lane] = sum;
+    picks[warp][lane] = picked;
+    __syncthreads();
+    if (warp != 0 || row >= p.rows)
+        return;
+    high = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 32; ++w)
+        high = fmaxf(high, highs[w][lane]);
+    const float shift = high == -INFINITY ? 0.0f : high;
+    sum = 0.0f;
+    picked = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) {
+        sum += sums[w][lane] * exp2_fast(highs[w][lane] - shift);
+        picked += picks[w][lane];
+    }
+    const float lse = (high + log2f(sum)) * kLn2;
+    p.lse[row] = lse;
+    if (teacher) {
+        const bool counted = p.entries[row * p.top] != INT_MAX;
+        p.loss[row] = counted ? p.entropy[row] + (lse - picked * p.inv_temperature) : 0.0f;
+    } else {
+        const int64_t target = p.target[row];
+        const bool word = target >= 0 && target < p.vocab;
+        p.loss[row] = target == p.ignore_index ? 0.0f
+                      : word                   ? lse - p.picked[row]
+                                               : __int_as_float(0x7FC00000);
+    }
+}
+
+cudaError_t launch_loss(const LossParams& p, cudaStream_t stream)
+{
+    return launch(loss_kernel, (p.rows + 31) / 32, 1024, 0, false, stream, p);
+}
+
+// -------------------------------------------------------------- row factors
+__device__ __forceinline__ void row_factors(const CoefParams& p, int64_t row, float& loss, float& both)
+{
+    bool counted, valid = true;
+    if (p.top == 0) {
+        const int64_t target = p.target[row];
+        counted = target != p.ignore_index;
+        valid = target >= 0 && target < p.vocab;
+    } else {
+        counted = p.entries[row * p.top] != INT_MAX;
+    }
+    loss = counted ? p.dloss[row * p.dloss_stride] : 0.0f;
+    if (counted && !valid)
+        loss = __int_as_float(0x7FC00000);
+    both = loss + (p.dlse ? p.dlse[row * p.dlse_stride] : 0.0f);
+}
+
+// What dz is multiplied by before it is rounded to fp16, whose smallest
+// numbers a mean over many tokens would fall below: the power of two that
+// takes the largest factor of a row to between 2^13 and 2^14.
+__global__ void __launch_bounds__(1024) factor_kernel(const CoefParams p)
+{
+    __shared__ float red[32];
+    wait_prior_grids();
+    allow_next_grid();
+    float most = 0.0f;
+    for (int64_t r = threadIdx.x; r < p.rows; r += 1024) {
+        float loss, both;
+        row_factors(p, r, loss, both);
+        const float m = (fabsf(loss) + fabsf(both)) * p.inv_temperature;
+        most = m < INFINITY ? fmaxf(most, m) : most;
+    }
+    most = warp_max(most);
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = most;
+    __syncthreads();
+    if (threadIdx.x >= 32)
+        return;
+    most = warp_max(red[threadIdx.x]);
+    if (threadIdx.x == 0) {
+        int e = 0;
+        if (most > 0.0f) {
+            frexpf(most, &e);
+            e = max(-100, min(100, 14 - e));
+        }
+        p.factor[0] = ldexpf(1.0f, e);
+        p.factor[1] = ldexpf(1.0f, -e);
+    }
+}
+
+// A warp a row.
+__global__ void __launch_bounds__(256) coef_kernel(const CoefParams p)
+{
+    wait_prior_grids();
+    allow_next_grid();
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (row >= p.rows)
+        return;
+    float loss, both;
+    row_factors(p, row, loss, both);
+    const float scale = (p.factor ? p.factor[0] : 1.0f) * p.inv_temperature;
+    loss *= scale;
+    both *= scale;
+    if (lane == 0)
+        p.coef[row] = make_float2(both, loss);
+    if (!p.x_live)
+        return;
+    const bool live = both != 0.0f || loss != 0.0f;
+    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + row * p.x_stride);
+    uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.x_live) + row * p.inner);
+    for (int i = lane; i < p.inner >> 3; i += 128) {
+        uint4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = live && i + 32 * j < p.inner >> 3 ? from[i + 32 * j] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + 32 * j < p.inner >> 3)
+                to[i + 32 * j] = v[j];
+    }
+}
+
+cudaError_t launch_coef(const CoefParams& p, cudaStream_t stream)
+{
+    if (p.factor) {
+        const cudaError_t e = launch(factor_kernel, 1, 1024, 0, false, stream, p);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return launch(coef_kernel, (p.rows + 7) / 8, 256, 0, false, stream, p);
+}
+
+}  // namespace dradd
