@@ -162,7 +162,7 @@ struct LossParams {
     const int* entries;      // distillation
     const float* entropy;
     int rows, vocab, top, parts;
-    float inv_temperature;
+    float logit_factor;      // of a picked logit
 };
 cudaError_t launch_loss(const LossParams& p, cudaStream_t stream);
 

@@ -363,12 +363,12 @@ __global__ void __launch_bounds__(1024) loss_kernel(const LossParams p)
     p.lse[row] = lse;
     if (teacher) {
         const bool counted = p.entries[row * p.top] != INT_MAX;
-        p.loss[row] = counted ? p.entropy[row] + (lse - picked * p.inv_temperature) : 0.0f;
+        p.loss[row] = counted ? p.entropy[row] + (lse - picked * p.logit_factor) : 0.0f;
     } else {
         const int64_t target = p.target[row];
         const bool word = target >= 0 && target < p.vocab;
         p.loss[row] = target == p.ignore_index ? 0.0f
-                      : word                   ? lse - p.picked[row]
+                      : word                   ? lse - p.picked[row] * p.logit_factor
                                                : __int_as_float(0x7FC00000);
     }
 }
