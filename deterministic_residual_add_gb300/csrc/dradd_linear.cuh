@@ -128,8 +128,9 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
         cluster_sync_all();
     tmem_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
-    wait_prior_grids();
     allow_next_grid();
+    if (!a.early || warp >= 4)
+        wait_prior_grids();
 
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (mbar_wait_bounded(bar, parity, a.wait_limit_ns))

@@ -81,29 +81,106 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, int group)
 
 int group_for(int64_t m) { return m <= kTileRows ? 1 : 2; }
 
-// The split of one product that runs alone: as many parts as fill the
-// workers once, of at least kLeastBlocks steps.
 constexpr int kLeastBlocks = 8;
 constexpr int kMostSplits = 32;
-void split_alone(Plan* p)
+
+// What a plan is thought to cost, in steps of one tile (256 x 256 x 64 by a
+// pair or 128 x 256 x 64 by one CTA: 512 cycles): the steps of the busiest
+// worker, kTileSteps more a tile, and for split sums the pass that finishes
+// them, kFinishSteps and the time that its bytes take.
+constexpr int64_t kTileSteps = 2;
+constexpr int64_t kFinishSteps = 16;
+int64_t finish_cost(const Plan& p, int64_t m, int64_t n)
 {
-    const int64_t workers = kPlanSms / p->group, tiles = p->tiles();
-    if (tiles * 2 > workers)
-        return;
-    const int64_t parts = workers / tiles;
-    const int64_t each = parts_of(p->k_blocks, parts);
-    p->split(each < kLeastBlocks ? kLeastBlocks : each, kMostSplits);
+    return p.splits > 1 ? kFinishSteps + p.splits * m * n * 8 / (3 << 20) : 0;
 }
 
-// Two products in one launch (either may be absent: no tiles): no tile longer than a
-// quarter of a worker's share.
-void split_pair(Plan* p, Plan* q)
+// The split of one product that runs alone.
+void split_alone(Plan* p, int64_t m, int64_t n)
 {
-    const int64_t workers = kPlanSms / p->group, all = p->units() + q->units();
-    int64_t most = all / (4 * workers);
-    most = most < 2 * kLeastBlocks ? 2 * kLeastBlocks : most;
-    p->split(most, kMostSplits);
-    q->split(most, kMostSplits);
+    const int64_t workers = kPlanSms / p->group;
+    if (p->tiles() * 2 > workers)
+        return;
+    int64_t best = 0;
+    Plan found = *p;
+    for (int64_t s = 1; s <= workers / p->tiles() && s <= kMostSplits; ++s) {
+        Plan t = *p;
+        t.split(parts_of(t.k_blocks, s), kMostSplits);
+        const int64_t each = parts_of(t.k_blocks, t.splits);
+        if (s > 1 && each < kLeastBlocks)
+            break;
+        const int64_t cost = parts_of(t.tiles() * t.splits, workers) * (each + kTileSteps) + finish_cost(t, m, n);
+        if (s == 1 || cost < best) {
+            best = cost;
+            found = t;
+        }
+    }
+    *p = found;
+}
+
+// How tiles of the second of two products are worth those of the first, and
+// the steps of the busiest worker, as tile_of deals them out.
+int64_t worth_of(int64_t len0, int64_t len1) { return (len0 + len1 / 2) / len1; }
+
+int64_t busiest(int64_t n0, int64_t len0, int64_t n1, int64_t len1, int64_t workers)
+{
+    const int64_t odd = n0 % workers, rest = odd ? workers - odd : 0, worth = n1 ? worth_of(len0, len1) : 0;
+    int64_t most = 0;
+    for (int64_t w = 0; w < workers; ++w) {
+        const int64_t own = n0 / workers + (w < odd);
+        int64_t more = 0;
+        if (odd && w >= odd && n1 > w - odd) {
+            const int64_t first = parts_of(n1 - (w - odd), rest);
+            more = first < worth ? first : worth;
+        }
+        const int64_t left = n1 - rest * worth - w;
+        more += left > 0 ? parts_of(left, workers) : 0;
+        const int64_t steps = own * (len0 + kTileSteps) + more * (len1 + kTileSteps);
+        most = steps > most ? steps : most;
+    }
+    return most;
+}
+
+// Two products m x n x k in one launch (either may be absent: no rows): by
+// pairs of CTAs or by single ones, which cost a sixteenth more, and with how
+// long tiles at most.
+struct Size {
+    int64_t m, n, k;
+};
+void plan_pair(const Size& a, const Size& b, bool split_b, Plan* p, Plan* q)
+{
+    int64_t best = -1;
+    for (int group = 2; group >= 1; --group) {
+        const int64_t workers = kPlanSms / group;
+        const Plan p0 = plan_of(a.m, a.n, a.k, group), q0 = plan_of(b.m, b.n, b.k, group);
+        const int64_t all = p0.units() + q0.units();
+        int64_t before = 0;
+        for (int part = 0; part <= 4; part = part ? part * 2 : 1) {
+            Plan s = p0, t = q0;
+            int64_t most = part ? all / (part * workers) : 1 << 30;
+            most = most < kLeastBlocks ? kLeastBlocks : most;
+            if (most == before)
+                break;
+            before = most;
+            s.split(most, kMostSplits);
+            if (split_b)
+                t.split(most, kMostSplits);
+            int64_t n0 = s.tiles() * s.splits, n1 = t.tiles() * t.splits;
+            int64_t l0 = parts_of(s.k_blocks, s.splits), l1 = parts_of(t.k_blocks, t.splits);
+            if (n0 == 0 || (n1 != 0 && l1 > l0)) {
+                const int64_t x = n0, y = l0;
+                n0 = n1, l0 = l1, n1 = x, l1 = y;
+            }
+            int64_t cost = busiest(n0, l0, n1, l1, workers);
+            cost += group == 1 ? cost / 16 : 0;
+            cost += finish_cost(s, a.m, a.n) + finish_cost(t, b.m, b.n);
+            if (best < 0 || cost < best) {
+                best = cost;
+                *p = s;
+                *q = t;
+            }
+        }
+    }
 }
 
 int64_t partial_bytes(const Plan& p, int64_t m, int64_t n) { return p.splits > 1 ? p.splits * m * n * 4 : 0; }
@@ -253,7 +330,8 @@ dradd_status start(ProductArgs<K>* a, int dtype, int* sms)
 }
 
 template <class K>
-dradd_status run_product(const Plan& p, const Side& a, const Side& b, const typename K::Params& epi, int dtype, cudaStream_t stream)
+dradd_status run_product(const Plan& p, const Side& a, const Side& b, const typename K::Params& epi, bool early,
+                         int dtype, cudaStream_t stream)
 {
     static_assert(sizeof(ProductArgs<K>) <= 4096, "kernel parameters");
     ProductArgs<K> args = {};
@@ -261,13 +339,17 @@ dradd_status run_product(const Plan& p, const Side& a, const Side& b, const type
     DRADD_TRY(start(&args, dtype, &sms));
     DRADD_TRY(set_shape(&args.shape[0], p, a, b));
     args.epi[0] = epi;
+    args.early = early;
     const int64_t tiles = p.tiles() * p.splits;
     args.tiles0 = args.tiles = static_cast<int>(tiles);
     return from_cuda(launch_product<K>(args, p.group, sms, stream));
 }
 
-// Two products whose results are gradients, the longer tiles first; q with
-// no tiles: one.
+// Whether a product may be `early`: the grid before it in this call has
+// waited for every grid before itself (and so for the product's operands)
+// before it let its successor start.  The products' own early grids have not.
+
+// Two products whose results are gradients, the longer tiles first.
 struct GradProduct {
     Plan plan;
     Side a, b;
@@ -275,7 +357,7 @@ struct GradProduct {
     bool on;
 };
 
-dradd_status run_gradients(GradProduct p, GradProduct q, int dtype, cudaStream_t stream)
+dradd_status run_gradients(GradProduct p, GradProduct q, bool early, int dtype, cudaStream_t stream)
 {
     if (!p.on && !q.on)
         return DRADD_OK;
@@ -290,12 +372,13 @@ dradd_status run_gradients(GradProduct p, GradProduct q, int dtype, cudaStream_t
     DRADD_TRY(start(&args, dtype, &sms));
     DRADD_TRY(set_shape(&args.shape[0], p.plan, p.a, p.b));
     args.epi[0] = p.epi;
+    args.early = early;
     args.tiles0 = args.tiles = static_cast<int>(p.plan.tiles() * p.plan.splits);
     if (q.on) {
         DRADD_TRY(set_shape(&args.shape[1], q.plan, q.a, q.b));
         args.epi[1] = q.epi;
         args.tiles += static_cast<int>(q.plan.tiles() * q.plan.splits);
-        args.worth = static_cast<int>((blocks(p) + blocks(q) / 2) / blocks(q));
+        args.worth = static_cast<int>(worth_of(blocks(p), blocks(q)));
     }
     return from_cuda(launch_product<GradProducts>(args, p.plan.group, sms, stream));
 }
@@ -320,7 +403,7 @@ dradd_status finish_sums(const float* partials, int splits, int64_t rows, int64_
 Plan forward_plan(int64_t rows, int64_t inner, int64_t cols)
 {
     Plan p = plan_of(rows, cols, inner, group_for(rows));
-    split_alone(&p);
+    split_alone(&p, rows, cols);
     return p;
 }
 
@@ -340,6 +423,7 @@ dradd_status linear_shape(int64_t rows, int64_t inner, int64_t cols)
 
 struct LinearGradPlan {
     Plan z, dx, dw;
+    bool sums;
     int chunks;
     int64_t dz, partial_z, partial_dx, partial_dw, partial_db;
     int64_t bytes;
@@ -350,21 +434,16 @@ LinearGradPlan linear_grad_plan(int64_t rows, int64_t inner, int64_t cols, int a
 {
     LinearGradPlan g = {};
     g.z = forward_plan(rows, inner, cols);
-    const int group = rows <= kTileRows && cols <= kTileRows ? 1 : 2;
-    g.dx = plan_of(rows, inner, cols, group);
-    g.dw = plan_of(cols, inner, rows, group);
-    if (!want_dx)
-        g.dx.tiles_m = 0;
-    if (!want_dw)
-        g.dw.tiles_m = 0;
-    split_pair(&g.dx, &g.dw);
+    plan_pair({want_dx ? rows : 0, inner, cols}, {want_dw ? cols : 0, inner, rows}, true, &g.dx, &g.dw);
     const int64_t c = parts_of(rows, 64);
-    g.chunks = static_cast<int>(c < 64 ? c : 64);
+    // with an activation and whole sums dz's product adds its columns up itself
+    g.sums = act != DRADD_ACT_NONE && g.z.splits == 1;
+    g.chunks = g.sums ? g.z.tiles_m * g.z.group * (kTileRows / 32) : static_cast<int>(c < 64 ? c : 64);
     g.dz = act == DRADD_ACT_NONE ? 0 : rows * cols * 2;
     g.partial_z = act == DRADD_ACT_NONE ? 0 : partial_bytes(g.z, rows, cols);
     g.partial_dx = want_dx ? partial_bytes(g.dx, rows, inner) : 0;
     g.partial_dw = want_dw ? partial_bytes(g.dw, cols, inner) : 0;
-    g.partial_db = want_db ? g.chunks * cols * 4 : 0;
+    g.partial_db = want_db ? static_cast<int64_t>(g.chunks) * cols * 4 : 0;
     Carver c0(nullptr);
     for (const int64_t n : {g.dz, g.partial_z, g.partial_dx, g.partial_dw, g.partial_db})
         c0.take(n);
@@ -375,7 +454,8 @@ LinearGradPlan linear_grad_plan(int64_t rows, int64_t inner, int64_t cols, int a
 ActParams act_params(void* out, int64_t out_stride, const void* bias, const void* other, int64_t other_stride,
                      int64_t rows, int64_t cols, int act)
 {
-    return {out, out_stride, bias, other, other_stride, static_cast<int>(rows), static_cast<int>(cols), act};
+    return {out, out_stride, bias, other, other_stride, static_cast<int>(rows), static_cast<int>(cols), act,
+            nullptr};
 }
 
 // out = residual + act(x W^T + bias), or with `grad` dz; by one product, or
@@ -385,10 +465,10 @@ dradd_status run_linear(const Plan& p, const dradd_matrix& x, const dradd_matrix
 {
     const Side a = {x.data, act.rows, inner, x.stride, false}, b = {w.data, act.cols, inner, w.stride, false};
     if (p.splits == 1)
-        return grad ? run_product<ActGradProduct>(p, a, b, act, dtype, stream)
-                    : run_product<ActProduct>(p, a, b, act, dtype, stream);
+        return grad ? run_product<ActGradProduct>(p, a, b, act, false, dtype, stream)
+                    : run_product<ActProduct>(p, a, b, act, false, dtype, stream);
     const SplitParams s = {partials, act.rows, act.cols, 0};
-    DRADD_TRY(run_product<SplitProduct>(p, a, b, s, dtype, stream));
+    DRADD_TRY(run_product<SplitProduct>(p, a, b, s, false, dtype, stream));
     FinishParams f = {partials, p.splits, nullptr, act, grad, dtype == DRADD_BF16};
     return from_cuda(launch_finish(f, stream));
 }
@@ -543,7 +623,8 @@ dradd_status loss_fwd(float* loss, float* lse, const dradd_matrix* x, const drad
     e.top = static_cast<int>(c.top());
     e.scale = logit_scale(c.hidden, c.inv_temperature());
     DRADD_TRY(run_product<StatsProduct>(p, {x->data, c.rows, c.hidden, x->stride, false},
-                                    {weight->data, c.vocab, c.hidden, weight->stride, false}, e, dtype, stream));
+                                    {weight->data, c.vocab, c.hidden, weight->stride, false}, e, c.teacher != nullptr,
+                                    dtype, stream));
     LossParams l = {};
     l.loss = loss;
     l.lse = lse;
@@ -580,11 +661,7 @@ LossGradPlan loss_grad_plan(int64_t rows, int64_t hidden, int64_t vocab)
     g.piece = up(parts_of(whole, g.pieces), kTileCols);  // of about one size
     g.pieces = parts_of(whole, g.piece);
     const int64_t width = g.pieces == 1 ? vocab : g.piece;
-    const int group = rows <= kTileRows && width <= kTileRows ? 1 : 2;
-    g.dx = plan_of(rows, hidden, width, group);
-    g.dw = plan_of(width, hidden, rows, group);
-    split_pair(&g.dx, &g.dw);
-    g.dw.splits = 1;  // its sums run over the rows alone
+    plan_pair({rows, hidden, width}, {width, hidden, rows}, false, &g.dx, &g.dw);
     return g;
 }
 
@@ -685,7 +762,7 @@ dradd_status loss_bwd(void* dx, void* dweight, const float* dloss, int64_t dloss
         e.col0 = static_cast<int>(col0);
         e.scale = logit_scale(c.hidden, c.inv_temperature());
         DRADD_TRY(run_product<SlopeProduct>(plan_of(r, width, h, group_for(r)), {x->data, r, h, x->stride, false},
-                                        {w0, width, h, weight->stride, false}, e, dtype, stream));
+                                            {w0, width, h, weight->stride, false}, e, true, dtype, stream));
         GradProduct px = {}, pw = {};
         const bool last = i + 1 == g.pieces;
         px.on = dx != nullptr;
@@ -702,7 +779,7 @@ dradd_status loss_bwd(void* dx, void* dweight, const float* dloss, int64_t dloss
         pw.b = {s.x_live, r, h, h, true};
         pw.epi = {dweight ? static_cast<char*>(dweight) + col0 * h * 2 : nullptr, nullptr, factor,
                   static_cast<int>(width), f.inner, 0};
-        DRADD_TRY(run_gradients(px, pw, dtype, stream));
+        DRADD_TRY(run_gradients(px, pw, false, dtype, stream));
     }
     if (dx && g.dx.splits > 1)
         return finish_sums(s.partials, g.dx.splits, r, h, dx, factor, dtype, stream);
@@ -824,15 +901,18 @@ dradd_status linear_act_add_bwd(void* dx, void* dweight, void* dbias, const drad
     const void* dz = dout->data;
     int64_t dz_stride = dout->stride;
     if (act != DRADD_ACT_NONE) {
-        const ActParams a = act_params(dz_space, cols, bias, dout->data, dout->stride, rows, cols, act);
+        ActParams a = act_params(dz_space, cols, bias, dout->data, dout->stride, rows, cols, act);
+        a.col_sums = dbias && g.sums ? partial_db : nullptr;
         DRADD_TRY(run_linear(g.z, *x, *weight, a, true, inner, partial_z, dtype, stream));
         dz = dz_space;
         dz_stride = cols;
     }
     if (dbias) {
-        DRADD_TRY(from_cuda(launch_row_sums(dz, dz_stride, static_cast<int>(rows), static_cast<int>(cols),
-                                            dtype == DRADD_BF16, g.chunks, partial_db, stream)));
-        DRADD_TRY(finish_sums(partial_db, g.chunks, 1, cols, dbias, nullptr, dtype, stream));
+        if (!g.sums)
+            DRADD_TRY(from_cuda(launch_row_sums(dz, dz_stride, static_cast<int>(rows), static_cast<int>(cols),
+                                                dtype == DRADD_BF16, g.chunks, partial_db, stream)));
+        DRADD_TRY(from_cuda(
+            launch_bias(partial_db, g.chunks, static_cast<int>(cols), dbias, dtype == DRADD_BF16, stream)));
     }
     GradProduct px = {}, pw = {};
     px.on = dx != nullptr;
@@ -846,7 +926,8 @@ dradd_status linear_act_add_bwd(void* dx, void* dweight, void* dbias, const drad
     pw.b = {x->data, rows, inner, x->stride, true};
     pw.epi = {g.dw.splits == 1 ? dweight : nullptr, partial_dw, nullptr, static_cast<int>(cols),
               static_cast<int>(inner), 0};
-    DRADD_TRY(run_gradients(px, pw, dtype, stream));
+    // the bias's kernel starts its successor when dz is complete
+    DRADD_TRY(run_gradients(px, pw, dbias != nullptr, dtype, stream));
     if (dx && g.dx.splits > 1)
         DRADD_TRY(finish_sums(partial_dx, g.dx.splits, rows, inner, dx, nullptr, dtype, stream));
     if (dweight && g.dw.splits > 1)

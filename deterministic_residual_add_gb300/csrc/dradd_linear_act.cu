@@ -78,6 +78,26 @@ struct EpiAct {
 struct EpiActGrad : EpiAct {
     using Kind = ActGradProduct;
     using EpiAct::EpiAct;
+    // The warp's 32 rows of each column: at every level a lane keeps one half
+    // of its columns and hands the other one over, until it has its own.
+    __device__ __forceinline__ void add_up(const float (&z)[32], int c, int n)
+    {
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            v[j] = row < p.rows ? z[j] : 0.0f;
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+            for (int j = 0; j < d; ++j) {
+                const bool upper = lane & d;
+                const float give = upper ? v[j] : v[j + d];
+                v[j] = (upper ? v[j + d] : v[j]) + __shfl_xor_sync(0xffffffffu, give, d);
+            }
+        if (lane < n)
+            p.col_sums[static_cast<int64_t>(row >> 5) * p.cols + col + c + lane] = v[0];
+    }
     __device__ __forceinline__ void columns(const uint32_t (&bits)[32], int c)
     {
         const int n = p.cols - col - c;
@@ -93,6 +113,8 @@ struct EpiActGrad : EpiAct {
             z[2 * j] *= lo;
             z[2 * j + 1] *= hi;
         }
+        if (p.col_sums)
+            add_up(z, c, n);
         if (c + 32 < kHalfCols)
             fetch(c + 32);
         store(z, c, n);

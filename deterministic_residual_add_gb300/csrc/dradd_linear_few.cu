@@ -19,6 +19,9 @@ namespace {
 constexpr int kFewWarps = 8;
 constexpr int kFewCols = 16;
 constexpr int kFewUnroll = 4;  // steps of 32 of the inner dimension in flight
+// Bytes of each row of W asked into L2 while the grid before may still run:
+// with the up to 600 CTAs that the device holds, 80 MB at most.
+constexpr int kFewPrefetch = 8192;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1, bool bf16)
@@ -40,11 +43,14 @@ template <int T>
 __global__ void __launch_bounds__(kFewWarps * 32) few_kernel(const FewParams p)
 {
     __shared__ float sums[kFewWarps][T * 8][kFewCols + 1];
-    wait_prior_grids();
-    allow_next_grid();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int col0 = blockIdx.x * kFewCols;
+    if (threadIdx.x < kFewCols && col0 + static_cast<int>(threadIdx.x) < p.act.cols)
+        prefetch_l2(static_cast<const uint16_t*>(p.weight) + (col0 + threadIdx.x) * p.weight_stride,
+                    min(p.inner * 2, kFewPrefetch));
+    allow_next_grid();
+    wait_prior_grids();
     const bool bf16 = p.bf16;
     const uint4 none = make_uint4(0, 0, 0, 0);
     const uint16_t* w = static_cast<const uint16_t*>(p.weight);

@@ -43,6 +43,7 @@ struct ActParams {
     int64_t other_stride;
     int rows, cols;
     int act;
+    float* col_sums;       // the gradient: [rows / 32, cols] sums of dz over 32 rows each, or NULL
 };
 
 // Statistics of the logits' rows, a part of 128 columns at a time.
@@ -102,6 +103,7 @@ struct ProductArgs {
     typename K::Params epi[K::kProblems];
     int tiles0, tiles;       // of the first problem, of all
     int worth;               // tiles of the second problem that cost as much as one of the first
+    int early;               // the operands are complete when this grid may start; only the epilogue waits
     int bf16;
     unsigned* status;
     uint64_t wait_limit_ns;
@@ -131,6 +133,9 @@ struct FewParams {
 };
 constexpr int kFewRows = 16;
 cudaError_t launch_few(const FewParams& p, cudaStream_t stream);
+
+// Column sums of fp32 [parts, cols], rounded.
+cudaError_t launch_bias(const float* partials, int parts, int cols, void* out, int bf16, cudaStream_t stream);
 
 // Sums of a 16-bit matrix's columns over `chunks` parts of its rows, fp32
 // [chunks, cols].

@@ -170,6 +170,41 @@ cudaError_t launch_row_sums(const void* x, int64_t stride, int rows, int cols, i
                               (rows + chunks - 1) / chunks, partials);
 }
 
+// A CTA takes 32 columns, a lane each; its warps every 32nd part.
+__global__ void __launch_bounds__(1024) bias_kernel(const float* partials, int parts, int cols, uint16_t* out, int bf16)
+{
+    __shared__ float sums[32][33];
+    wait_prior_grids();
+    allow_next_grid();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (col < cols) {
+        for (int i = warp; i < parts; i += 128) {
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = i + 32 * j < parts ? partials[static_cast<int64_t>(i + 32 * j) * cols + col] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                s += v[j];
+        }
+    }
+    sums[warp][lane] = s;
+    __syncthreads();
+    // warp w now holds column w of the CTA, one warp's sum a lane
+    s = butterfly_sum(sums[lane][warp], 32);
+    const int c = blockIdx.x * 32 + warp;
+    if (lane == 0 && c < cols)
+        out[c] = bf16 ? Elem<kElemBf16>::narrow(s) : Elem<kElemF16>::narrow(s);
+}
+
+cudaError_t launch_bias(const float* partials, int parts, int cols, void* out, int bf16, cudaStream_t stream)
+{
+    return launch(bias_kernel, (cols + 31) / 32, 1024, 0, false, stream, partials, parts, cols,
+                  static_cast<uint16_t*>(out), bf16);
+}
+
 // ------------------------------------------------------------------ teacher
 // A CTA sorts one row's entries by (word, place) in shared memory, computes
 // their shares and where each part of 128 columns begins.
@@ -311,24 +346,24 @@ cudaError_t launch_teacher(const TeacherParams& p, cudaStream_t stream)
 }
 
 // --------------------------------------------------------- joined statistics
-// A CTA takes 32 rows, a lane each; its warps every 32nd part.
+// A CTA takes 16 rows; 64 half warps take every 64th part, a lane a row.
 __global__ void __launch_bounds__(1024) loss_kernel(const LossParams p)
 {
-    __shared__ float highs[32][33], sums[32][33], picks[32][33];
+    __shared__ float highs[64][17], sums[64][17], picks[64][17];
     wait_prior_grids();
     allow_next_grid();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    const int lane = threadIdx.x & 15, warp = threadIdx.x >> 4;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + lane;
     const bool teacher = p.top != 0;
     float high = -INFINITY, sum = 0.0f, picked = 0.0f;
     if (row < p.rows) {
-        for (int g = warp; g < p.parts; g += 128) {
+        for (int g = warp; g < p.parts; g += 256) {
             float2 v[4];
             float k[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int64_t at = static_cast<int64_t>(g + 32 * j) * p.rows + row;
-                const bool in = g + 32 * j < p.parts;
+                const int64_t at = static_cast<int64_t>(g + 64 * j) * p.rows + row;
+                const bool in = g + 64 * j < p.parts;
                 v[j] = in ? p.part[at] : make_float2(-INFINITY, 0.0f);
                 k[j] = in && teacher ? p.picked[at] : 0.0f;
             }
@@ -349,13 +384,13 @@ __global__ void __launch_bounds__(1024) loss_kernel(const LossParams p)
         return;
     high = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < 32; ++w)
+    for (int w = 0; w < 64; ++w)
         high = fmaxf(high, highs[w][lane]);
     const float shift = high == -INFINITY ? 0.0f : high;
     sum = 0.0f;
     picked = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 32; ++w) {
+    for (int w = 0; w < 64; ++w) {
         sum += sums[w][lane] * exp2_fast(highs[w][lane] - shift);
         picked += picks[w][lane];
     }
@@ -375,7 +410,7 @@ __global__ void __launch_bounds__(1024) loss_kernel(const LossParams p)
 
 cudaError_t launch_loss(const LossParams& p, cudaStream_t stream)
 {
-    return launch(loss_kernel, (p.rows + 31) / 32, 1024, 0, false, stream, p);
+    return launch(loss_kernel, (p.rows + 15) / 16, 1024, 0, false, stream, p);
 }
 
 // -------------------------------------------------------------- row factors
