@@ -128,6 +128,17 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
         cluster_sync_all();
     tmem_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
+    if constexpr (CG == 1) {
+        // Few rows: the second operand, the weights, is read once and its
+        // bytes are what the product takes.  The first of them are asked into
+        // L2 while the grid before ends: 12 steps a CTA, 60 MB in all.
+        const int t = tile_of(a, worker, workers, 0);
+        if (warp == 3 && lane == 0 && a.prefetch && t >= 0) {
+            const TileAt at = tile_at(a, t);
+            for (int k = at.k0; k < at.k1 && k < at.k0 + 12; ++k)
+                prefetch_box(&a.shape[0].b, k * kTileDepth, at.n * kTileCols);
+        }
+    }
     allow_next_grid();
     if (!a.early || warp >= 4)
         wait_prior_grids();

@@ -340,6 +340,7 @@ dradd_status run_product(const Plan& p, const Side& a, const Side& b, const type
     DRADD_TRY(set_shape(&args.shape[0], p, a, b));
     args.epi[0] = epi;
     args.early = early;
+    args.prefetch = p.tiles_m == 1 && !b.mn;
     const int64_t tiles = p.tiles() * p.splits;
     args.tiles0 = args.tiles = static_cast<int>(tiles);
     return from_cuda(launch_product<K>(args, p.group, sms, stream));
@@ -843,8 +844,9 @@ dradd_status linear_act_add_fwd(const dradd_matrix* out, const dradd_matrix* x, 
     const ActParams a = act_params(out->data, out->stride, bias, has_residual ? residual->data : nullptr,
                                    has_residual ? residual->stride : 0, rows, cols, act);
     if (few(rows)) {
-        const FewParams f = {x->data, x->stride, weight->data, weight->stride, static_cast<int>(inner), a,
-                             dtype == DRADD_BF16};
+        FewParams f = {x->data, x->stride, weight->data, weight->stride, static_cast<int>(inner), a,
+                       dtype == DRADD_BF16, nullptr, kDefaultWaitLimitNs};
+        DRADD_TRY(from_cuda(device_status_ptr(&f.status)));
         return from_cuda(launch_few(f, stream));
     }
     return run_linear(p, *x, *weight, a, false, inner, static_cast<float*>(workspace), dtype, stream);

@@ -103,6 +103,7 @@ struct ProductArgs {
     typename K::Params epi[K::kProblems];
     int tiles0, tiles;       // of the first problem, of all
     int worth;               // tiles of the second problem that cost as much as one of the first
+    int prefetch;            // one CTA a tile and few rows: see product_kernel
     int early;               // the operands are complete when this grid may start; only the epilogue waits
     int bf16;
     unsigned* status;
@@ -130,6 +131,8 @@ struct FewParams {
     int inner;
     ActParams act;
     int bf16;
+    unsigned* status;
+    uint64_t wait_limit_ns;
 };
 constexpr int kFewRows = 16;
 cudaError_t launch_few(const FewParams& p, cudaStream_t stream);

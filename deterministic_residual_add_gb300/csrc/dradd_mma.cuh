@@ -144,6 +144,18 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, i
                      : "memory");
 }
 
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// A box of the map into L2, nothing to the SM: a hint, as prefetch_l2.
+__device__ __forceinline__ void prefetch_box(const CUtensorMap* map, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y)
+                 : "memory");
+}
+
 // Arrives on the barrier at the place of `bar` in CTA `rank` of the cluster.
 __device__ __forceinline__ void mbar_arrive_at(uint64_t* bar, uint32_t rank)
 {
