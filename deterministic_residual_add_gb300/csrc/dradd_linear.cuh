@@ -4,9 +4,10 @@
 // A persistent grid of CTAs (CG = 1) or CTA pairs (CG = 2) walks the tiles.
 // In a CTA one thread copies operands through a ring in shared memory, one
 // thread (CG = 2: of the pair's first CTA) issues the products into one of
-// two accumulators in tensor memory, and eight warps turn the other one into
-// the call's results, so that the epilogue runs beside the next tile's
-// products.  What the epilogue does is the template's argument E.
+// two accumulators in tensor memory, and 8 or 16 warps turn the other one
+// into the call's results, so that the epilogue runs beside the next tile's
+// products.  What the epilogue does is the template's argument E, which sees
+// 16 columns of a row at a time, the next ones already on their way.
 #pragma once
 
 #include "dradd_elem.cuh"
@@ -17,8 +18,9 @@
 
 namespace dradd {
 
-constexpr int kProductThreads = 384;  // a copying warp, an issuing one, two spare, eight for the epilogue
-constexpr int kEpiWarps = 8;
+// A copying warp, an issuing one, two spare, and those of the epilogue.
+template <class E>
+constexpr int kProductThreads = 128 + 32 * E::kWarps;
 constexpr uint32_t kBoxBytes = 64 * 64 * 2;  // 64 rows of 128 bytes
 
 __host__ __device__ constexpr uint32_t product_stage_bytes(int CG) { return (2u + 4u / CG) * kBoxBytes; }
@@ -63,13 +65,12 @@ __device__ __forceinline__ int tile_of(const ProductArgs<K>& a, int worker, int 
     return t < a.tiles ? t : -1;
 }
 
-// Tiles of one problem: splits outermost, then bands of 8 tile rows that are
+// Tiles of one problem: splits outermost, then bands of tile rows that are
 // walked down column by column, so that the tiles at work at one time share
 // few rows and columns.
 template <class K>
 __device__ __forceinline__ TileAt tile_at(const ProductArgs<K>& a, int t)
 {
-    constexpr int kBand = 8;
     TileAt r;
     r.problem = K::kProblems > 1 && t >= a.tiles0 ? 1 : 0;
     if (r.problem)
@@ -78,12 +79,12 @@ __device__ __forceinline__ TileAt tile_at(const ProductArgs<K>& a, int t)
     const int per = s.tiles_m * s.tiles_n;
     r.split = t / per;
     t -= r.split * per;
-    const int band_tiles = kBand * s.tiles_n;
+    const int band_tiles = s.band * s.tiles_n;
     const int band = t / band_tiles;
     t -= band * band_tiles;
-    const int high = min(kBand, s.tiles_m - band * kBand);
+    const int high = min(s.band, s.tiles_m - band * s.band);
     r.n = t / high;
-    r.m = band * kBand + t - r.n * high;
+    r.m = band * s.band + t - r.n * high;
     const int each = (s.k_blocks + s.splits - 1) / s.splits;
     r.k0 = r.split * each;
     r.k1 = min(r.k0 + each, s.k_blocks);
@@ -91,7 +92,7 @@ __device__ __forceinline__ TileAt tile_at(const ProductArgs<K>& a, int t)
 }
 
 template <int CG, class E>
-__global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __grid_constant__ ProductArgs<typename E::Kind> a)
+__global__ void __launch_bounds__(kProductThreads<E>, 1) product_kernel(const __grid_constant__ ProductArgs<typename E::Kind> a)
 {
     constexpr int kStages = product_stages(CG);
     constexpr uint32_t kStageBytes = product_stage_bytes(CG);
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.acc_full[i], 1);
-            mbar_init(&bars.acc_empty[i], kEpiWarps * CG);
+            mbar_init(&bars.acc_empty[i], E::kWarps * CG);
         }
         mbar_init(&bars.drain, 1);
         fence_mbar_init();
@@ -259,31 +260,36 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
             }
         }
     } else if (warp >= 4) {
-        const int quadrant = warp & 3, half = (warp - 4) >> 2;
+        constexpr int kCols = kTileCols * 4 / E::kWarps;  // a warp's columns
+        const int quadrant = warp & 3, part = (warp - 4) >> 2;
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int i = 0, t; (t = tile_of(a, worker, workers, i)) >= 0; ++i) {
             const TileAt at = tile_at(a, t);
             const int row = (at.m * CG + static_cast<int>(rank)) * kTileRows + quadrant * 32 + lane;
-            const int col = at.n * kTileCols + half * kHalfCols;
+            const int col = at.n * kTileCols + part * kCols;
             E epi(a.epi[E::Kind::kProblems > 1 ? at.problem : 0], a.bf16, row, col, at.split);
             if (!__all_sync(0xffffffffu, wait(&bars.acc_full[acc], acc_phase)))
                 break;
             tmem_fence_after();
-            const uint32_t from = tmem + (static_cast<uint32_t>(quadrant * 32) << 16) + acc * kTileCols +
-                                  half * kHalfCols;
+            const uint32_t from = tmem + (static_cast<uint32_t>(quadrant * 32) << 16) + acc * kTileCols + part * kCols;
+            uint32_t v0[16], v1[16];
+            tmem_load16(from, v0);
 #pragma unroll 1
-            for (int c = 0; c < kHalfCols; c += 32) {
-                uint32_t bits[32];
-                tmem_load32(from + c, bits);
-                tmem_wait_loads();
-                if (c + 32 == kHalfCols) {
+            for (int c = 0; c < kCols; c += 32) {
+                tmem_wait(v0);
+                tmem_load16(from + c + 16, v1);
+                epi.template columns<0>(v0, c);
+                tmem_wait(v1);
+                if (c + 32 < kCols) {
+                    tmem_load16(from + c + 32, v0);
+                } else {
                     tmem_fence_before();
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive_at(&bars.acc_empty[acc], 0);
                 }
-                epi.columns(bits, c);
+                epi.template columns<1>(v1, c + 16);
             }
             epi.end();
             if (++acc == 2) {
@@ -317,7 +323,7 @@ cudaError_t launch_product_group(const ProductArgs<typename E::Kind>& a, int sm_
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(workers * CG));
-    cfg.blockDim = dim3(kProductThreads);
+    cfg.blockDim = dim3(kProductThreads<E>);
     cfg.dynamicSmemBytes = product_smem(CG);
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -332,36 +338,39 @@ cudaError_t launch_with(const ProductArgs<typename E::Kind>& a, int cta_group, i
                           : launch_product_group<1, E>(a, sm_count, stream);
 }
 
-// 32 consecutive values of a 16-bit row, `n` of them inside it (a multiple of
-// 8): stored in whole 32-byte sectors where the address allows.
-__device__ __forceinline__ void pack32(const float (&f)[32], bool bf16, uint32_t (&w)[16])
+// 16 values as eight pairs of a 16-bit type.
+__device__ __forceinline__ void pack16(const float (&f)[16], bool bf16, uint32_t (&w)[8])
 {
     if (bf16) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < 8; ++i)
             w[i] = pack_rne(f[2 * i], f[2 * i + 1]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < 8; ++i)
             w[i] = Elem<kElemF16>::pack2(f[2 * i], f[2 * i + 1]);
     }
 }
 
-__device__ __forceinline__ void store32(uint16_t* p, const uint32_t (&w)[16], int n)
+__device__ __forceinline__ void store_sector(void* p, const uint32_t (&w)[8])
 {
-    if (n >= 32 && (reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 16 * i), "r"(w[8 * i]),
-                         "r"(w[8 * i + 1]), "r"(w[8 * i + 2]), "r"(w[8 * i + 3]), "r"(w[8 * i + 4]),
-                         "r"(w[8 * i + 5]), "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
-                         : "memory");
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// 16 consecutive values of a 16-bit row, `n` of them inside it (a multiple of
+// 8): a whole 32-byte sector where the address allows.
+__device__ __forceinline__ void store16(uint16_t* p, const uint32_t (&w)[8], int n)
+{
+    if (n >= 16 && (reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+        store_sector(p, w);
         return;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (8 * i < n)
-            reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    if (n > 0)
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (n > 8)
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 __device__ __forceinline__ void unpack2(uint32_t w, bool bf16, float& lo, float& hi)
@@ -375,11 +384,11 @@ __device__ __forceinline__ void unpack2(uint32_t w, bool bf16, float& lo, float&
     }
 }
 
-// 32 consecutive values of a 16-bit row, zeros past the n inside it.
-__device__ __forceinline__ void load32(const uint16_t* p, int n, uint32_t (&w)[16])
+// 16 consecutive values of a 16-bit row, zeros past the n inside it.
+__device__ __forceinline__ void load16(const uint16_t* p, int n, uint32_t (&w)[8])
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         uint4 v = make_uint4(0, 0, 0, 0);
         if (8 * i < n)
             v = __ldg(reinterpret_cast<const uint4*>(p) + i);

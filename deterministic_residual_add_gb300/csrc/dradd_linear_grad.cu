@@ -4,10 +4,11 @@
 
 namespace dradd {
 
-__device__ __forceinline__ void add_partials(float* p, float (&v)[32], int n)
+// Columns come in eights.
+__device__ __forceinline__ void add_partials(const float* p, float (&v)[16], int n)
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
         if (4 * i < n) {
             const float4 f = *reinterpret_cast<const float4*>(p + 4 * i);
             v[4 * i] += f.x;
@@ -17,21 +18,21 @@ __device__ __forceinline__ void add_partials(float* p, float (&v)[32], int n)
         }
 }
 
-// Columns come in eights.
-__device__ __forceinline__ void store_partials(float* p, const float (&v)[32], int n)
+__device__ __forceinline__ void store_partials(float* p, const uint32_t (&w)[16], int n)
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (8 * i < n)
-            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 8 * i), "f"(v[8 * i]),
-                         "f"(v[8 * i + 1]), "f"(v[8 * i + 2]), "f"(v[8 * i + 3]), "f"(v[8 * i + 4]),
-                         "f"(v[8 * i + 5]), "f"(v[8 * i + 6]), "f"(v[8 * i + 7])
-                         : "memory");
+    for (int i = 0; i < 2; ++i)
+        if (8 * i < n) {
+            const uint32_t half[8] = {w[8 * i],     w[8 * i + 1], w[8 * i + 2], w[8 * i + 3],
+                                      w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]};
+            store_sector(p + 8 * i, half);
+        }
 }
 
 struct EpiGrad {
     using Kind = GradProducts;
     using Params = GradParams;
+    static constexpr int kWarps = 8;
     const Params& p;
     const bool bf16;
     const int row, col;
@@ -44,27 +45,32 @@ struct EpiGrad {
         sums = p.partials + (static_cast<int64_t>(split) * p.rows + row) * p.cols + col;
         factor = p.factor ? *p.factor : 1.0f;
     }
-    __device__ __forceinline__ void columns(const uint32_t (&bits)[32], int c)
+    template <int>
+    __device__ __forceinline__ void columns(const uint32_t (&bits)[16], int c)
     {
         const int n = p.cols - col - c;
         if (n <= 0 || row >= p.rows)
             return;
-        float v[32];
+        float v[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < 16; ++j)
             v[j] = __uint_as_float(bits[j]);
         if (p.add)
             add_partials(sums + c, v, n);
         if (!p.out) {
-            store_partials(sums + c, v, n);
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                w[j] = __float_as_uint(v[j]);
+            store_partials(sums + c, w, n);
             return;
         }
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < 16; ++j)
             v[j] *= factor;
-        uint32_t w[16];
-        pack32(v, bf16, w);
-        store32(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(row) * p.cols + col + c, w, n);
+        uint32_t w[8];
+        pack16(v, bf16, w);
+        store16(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(row) * p.cols + col + c, w, n);
     }
     __device__ __forceinline__ void end() {}
 };
@@ -72,6 +78,7 @@ struct EpiGrad {
 struct EpiSplit {
     using Kind = SplitProduct;
     using Params = SplitParams;
+    static constexpr int kWarps = 8;
     const Params& p;
     const int row, col;
     float* sums;
@@ -81,16 +88,12 @@ struct EpiSplit {
     {
         sums = p.partials + (static_cast<int64_t>(split) * p.rows + row) * p.cols + col;
     }
-    __device__ __forceinline__ void columns(const uint32_t (&bits)[32], int c)
+    template <int>
+    __device__ __forceinline__ void columns(const uint32_t (&bits)[16], int c)
     {
         const int n = p.cols - col - c;
-        if (n <= 0 || row >= p.rows)
-            return;
-        float v[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            v[j] = __uint_as_float(bits[j]);
-        store_partials(sums + c, v, n);
+        if (n > 0 && row < p.rows)
+            store_partials(sums + c, bits, n);
     }
     __device__ __forceinline__ void end() {}
 };

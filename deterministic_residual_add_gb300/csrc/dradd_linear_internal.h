@@ -24,6 +24,7 @@ struct ProductShape {
     int tiles_m, tiles_n;
     int k_blocks;          // steps of 64
     int splits;            // parts of the k dimension, each a tile of its own
+    int band;              // tile rows that are walked down together
 };
 
 // ------------------------------------------------------------- epilogues

@@ -57,6 +57,7 @@ private:
 struct EpiStats {
     using Kind = StatsProduct;
     using Params = StatsParams;
+    static constexpr int kWarps = 8;
     const Params& p;
     const int row, col;
     const int part;
@@ -77,32 +78,33 @@ struct EpiStats {
                               p.first[static_cast<int64_t>(row) * p.parts + part], p.top, col);
         }
     }
-    __device__ __forceinline__ void columns(const uint32_t (&bits)[32], int c)
+    template <int>
+    __device__ __forceinline__ void columns(const uint32_t (&bits)[16], int c)
     {
-        float z[32];
+        float z[16];
         const int n = p.vocab - col - c;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < 16; ++j)
             z[j] = __uint_as_float(bits[j]);
-        while (words.next < c + 32) {
+        while (words.next < c + 16) {
             const int at = words.next - c;
             float v = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < 16; ++j)
                 v = j == at ? z[j] : v;
             picked = p.top == 0 ? v : fmaf(words.weight, v, picked);
             found = true;
             words.advance();
         }
-        if (n < 32) {
+        if (n < 16) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < 16; ++j)
                 z[j] = j < n ? z[j] : -INFINITY;
         }
         float m[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            m[j] = fmaxf(fmaxf(z[j], z[j + 8]), fmaxf(z[j + 16], z[j + 24]));
+            m[j] = fmaxf(z[j], z[j + 8]);
 #pragma unroll
         for (int d = 4; d > 0; d >>= 1)
 #pragma unroll
@@ -112,7 +114,7 @@ struct EpiStats {
         const float shift = now == -INFINITY ? 0.0f : now;
         float s[4] = {sum * exp2_fast(high - shift), 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < 16; ++j)
             s[j & 3] += exp2_fast(fmaf(z[j], p.scale, -shift));
         sum = (s[0] + s[1]) + (s[2] + s[3]);
         high = now;
@@ -133,6 +135,7 @@ struct EpiStats {
 struct EpiSlope {
     using Kind = SlopeProduct;
     using Params = SlopeParams;
+    static constexpr int kWarps = 8;
     const Params& p;
     const bool bf16;
     const int row, col;
@@ -158,31 +161,32 @@ struct EpiSlope {
                               p.first[static_cast<int64_t>(row) * p.parts + at / kHalfCols], p.top, at);
         }
     }
-    __device__ __forceinline__ void columns(const uint32_t (&bits)[32], int c)
+    template <int>
+    __device__ __forceinline__ void columns(const uint32_t (&bits)[16], int c)
     {
         if (row >= p.rows)
             return;
         const int n = p.vocab - col - c;
-        float v[32];
+        float v[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < 16; ++j)
             v[j] = coef.x * exp2_fast(fmaf(__uint_as_float(bits[j]), p.scale, -lse2));
-        while (words.next < c + 32) {
+        while (words.next < c + 16) {
             const int at = words.next - c;
             const float less = coef.y * words.weight;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < 16; ++j)
                 v[j] = j == at ? v[j] - less : v[j];
             words.advance();
         }
-        if (n < 32 || !live) {
+        if (n < 16 || !live) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < 16; ++j)
                 v[j] = live && j < n ? v[j] : 0.0f;
         }
-        uint32_t w[16];
-        pack32(v, bf16, w);
-        store32(static_cast<uint16_t*>(p.out) + row * p.stride + col + c, w, 32);
+        uint32_t w[8];
+        pack16(v, bf16, w);
+        store_sector(static_cast<uint16_t*>(p.out) + row * p.stride + col + c, w);
     }
     __device__ __forceinline__ void end() {}
 };
