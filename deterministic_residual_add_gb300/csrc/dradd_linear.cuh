@@ -24,13 +24,89 @@ constexpr int kProductThreads = 128 + 32 * E::kWarps;
 constexpr uint32_t kBoxBytes = 64 * 64 * 2;  // 64 rows of 128 bytes
 
 __host__ __device__ constexpr uint32_t product_stage_bytes(int CG) { return (2u + 4u / CG) * kBoxBytes; }
-__host__ __device__ constexpr int product_stages(int CG) { return static_cast<int>(200u * 1024u / product_stage_bytes(CG)); }
-constexpr uint32_t product_smem(int CG) { return product_stages(CG) * product_stage_bytes(CG) + 1024u; }
+__host__ __device__ // What the results of a tile take on their way out (and the residual, or the
+// gradient that comes in, on its way in): 128 x 256 of 16 bits.
+constexpr uint32_t kStagingBytes = kTileRows * kTileCols * 2;
+__host__ __device__ constexpr int product_stages(int CG, bool staged)
+{
+    return static_cast<int>((225u * 1024u - (staged ? kStagingBytes : 0u)) / product_stage_bytes(CG));
+}
+constexpr uint32_t product_smem(int CG, bool staged)
+{
+    return product_stages(CG, staged) * product_stage_bytes(CG) + (staged ? kStagingBytes : 0u) + 1024u;
+}
+
+// An epilogue warp's share of the staging space: its 32 rows in boxes of 64
+// columns (4 KB each), one beside the other.  Lane i has row i.  A 16-byte
+// piece lies at its place xor the row's lowest bits, as the tensor map's
+// swizzle has it, and eight lanes that move a piece each touch all banks.
+//
+// Results stored by the lanes themselves, a 32-byte sector of a row each,
+// took 5.6 us for a tile of 128 x 256 (8192 x 512 by 8192: 78 us); through
+// here whole lines leave.
+struct Staging {
+    uint32_t at;     // shared address
+    uint64_t* bar;   // counts what comes in
+    uint32_t phase;
+    int lane;
+
+    // What has been stored from here has been read, and what was read or
+    // written here comes before what is loaded next.
+    __device__ __forceinline__ void acquire()
+    {
+        fence_proxy_async_smem();
+        if (lane == 0)
+            bulk_wait_read();
+        __syncwarp();
+    }
+    __device__ __forceinline__ void load(const CUtensorMap* map, int x, int y, int boxes)
+    {
+        if (lane != 0)
+            return;
+        mbar_arrive_expect_tx(bar, boxes * 4096u);
+        for (int i = 0; i < boxes; ++i)
+            copy_box<1>(at + i * 4096u, map, x + i * 64, y, bar);
+    }
+    __device__ __forceinline__ bool loaded(uint64_t limit_ns)
+    {
+        const bool ok = mbar_wait_bounded(bar, phase, limit_ns);
+        phase ^= 1u;
+        return ok;
+    }
+    // Columns c to c + 15 of the lane's row.
+    __device__ __forceinline__ uint32_t piece(int c, int i) const
+    {
+        return at + (c >> 6) * 4096u + lane * 128u + (((((c & 63) >> 3) + i) ^ (lane & 7)) << 4);
+    }
+    __device__ __forceinline__ void read(int c, uint32_t (&w)[8]) const
+    {
+        const uint4 a = ld_shared(piece(c, 0)), b = ld_shared(piece(c, 1));
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    }
+    __device__ __forceinline__ void write(int c, const uint32_t (&w)[8]) const
+    {
+        st_shared(piece(c, 0), w[0], w[1], w[2], w[3]);
+        st_shared(piece(c, 1), w[4], w[5], w[6], w[7]);
+    }
+    // The box that column c is the last 16 of goes out, once it is full.
+    __device__ __forceinline__ void store_full(const CUtensorMap* map, int c, int x, int y, bool inside) const
+    {
+        if ((c & 63) != 48)
+            return;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && inside) {
+            store_box(map, x + c - 48, y, at + (c >> 6) * 4096u);
+            bulk_commit();
+        }
+    }
+};
 
 // Waits that have given up end every role's loop; the CTA then drains what
 // it has in flight and returns.
 struct ProductBars {
-    uint64_t full[8], empty[8], acc_full[2], acc_empty[2], drain;
+    uint64_t full[8], empty[8], acc_full[2], acc_empty[2], drain, loaded[16];
     uint32_t tmem;
 };
 
@@ -94,7 +170,7 @@ __device__ __forceinline__ TileAt tile_at(const ProductArgs<K>& a, int t)
 template <int CG, class E>
 __global__ void __launch_bounds__(kProductThreads<E>, 1) product_kernel(const __grid_constant__ ProductArgs<typename E::Kind> a)
 {
-    constexpr int kStages = product_stages(CG);
+    constexpr int kStages = product_stages(CG, E::kStaged);
     constexpr uint32_t kStageBytes = product_stage_bytes(CG);
     constexpr uint32_t kBytesA = 2 * kBoxBytes;
     constexpr int kRowsB = kTileCols / CG;
@@ -114,6 +190,8 @@ __global__ void __launch_bounds__(kProductThreads<E>, 1) product_kernel(const __
             mbar_init(&bars.acc_full[i], 1);
             mbar_init(&bars.acc_empty[i], E::kWarps * CG);
         }
+        for (int i = 0; i < E::kWarps; ++i)
+            mbar_init(&bars.loaded[i], 1);
         mbar_init(&bars.drain, 1);
         fence_mbar_init();
         for (int i = 0; i < E::Kind::kProblems && (i == 0 || a.tiles > a.tiles0); ++i) {
@@ -264,13 +342,19 @@ __global__ void __launch_bounds__(kProductThreads<E>, 1) product_kernel(const __
         const int quadrant = warp & 3, part = (warp - 4) >> 2;
         int acc = 0;
         uint32_t acc_phase = 0;
+        Staging staging = {ring + kStages * kStageBytes + (warp - 4) * (kStagingBytes / E::kWarps),
+                           &bars.loaded[warp - 4], 0, lane};
         for (int i = 0, t; (t = tile_of(a, worker, workers, i)) >= 0; ++i) {
             const TileAt at = tile_at(a, t);
             const int row = (at.m * CG + static_cast<int>(rank)) * kTileRows + quadrant * 32 + lane;
             const int col = at.n * kTileCols + part * kCols;
-            E epi(a.epi[E::Kind::kProblems > 1 ? at.problem : 0], a.bf16, row, col, at.split);
-            if (!__all_sync(0xffffffffu, wait(&bars.acc_full[acc], acc_phase)))
+            E epi(a.epi[E::Kind::kProblems > 1 ? at.problem : 0], a.bf16, row, col, at.split, staging);
+            const bool ok = epi.ready(a.wait_limit_ns) && wait(&bars.acc_full[acc], acc_phase);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0)
+                    atomicOr(a.status, kDeviceStatusTimeout);
                 break;
+            }
             tmem_fence_after();
             const uint32_t from = tmem + (static_cast<uint32_t>(quadrant * 32) << 16) + acc * kTileCols + part * kCols;
             uint32_t v0[16], v1[16];
@@ -279,7 +363,7 @@ __global__ void __launch_bounds__(kProductThreads<E>, 1) product_kernel(const __
             for (int c = 0; c < kCols; c += 32) {
                 tmem_wait(v0);
                 tmem_load16(from + c + 16, v1);
-                epi.template columns<0>(v0, c);
+                epi.columns(v0, c);
                 tmem_wait(v1);
                 if (c + 32 < kCols) {
                     tmem_load16(from + c + 32, v0);
@@ -289,7 +373,7 @@ __global__ void __launch_bounds__(kProductThreads<E>, 1) product_kernel(const __
                     if (lane == 0)
                         mbar_arrive_at(&bars.acc_empty[acc], 0);
                 }
-                epi.template columns<1>(v1, c + 16);
+                epi.columns(v1, c + 16);
             }
             epi.end();
             if (++acc == 2) {
@@ -297,6 +381,8 @@ __global__ void __launch_bounds__(kProductThreads<E>, 1) product_kernel(const __
                 acc_phase ^= 1u;
             }
         }
+        if (E::kStaged && lane == 0)
+            bulk_wait();
     }
     tmem_fence_before();
     __syncthreads();
@@ -324,7 +410,7 @@ cudaError_t launch_product_group(const ProductArgs<typename E::Kind>& a, int sm_
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(workers * CG));
     cfg.blockDim = dim3(kProductThreads<E>);
-    cfg.dynamicSmemBytes = product_smem(CG);
+    cfg.dynamicSmemBytes = product_smem(CG, E::kStaged);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
@@ -357,20 +443,6 @@ __device__ __forceinline__ void store_sector(void* p, const uint32_t (&w)[8])
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                  "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
-}
-
-// 16 consecutive values of a 16-bit row, `n` of them inside it (a multiple of
-// 8): a whole 32-byte sector where the address allows.
-__device__ __forceinline__ void store16(uint16_t* p, const uint32_t (&w)[8], int n)
-{
-    if (n >= 16 && (reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
-        store_sector(p, w);
-        return;
-    }
-    if (n > 0)
-        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    if (n > 8)
-        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 __device__ __forceinline__ void unpack2(uint32_t w, bool bf16, float& lo, float& hi)

@@ -336,6 +336,13 @@ dradd_status set_shape(ProductShape* s, const Plan& p, const Side& a, const Side
     return ok ? DRADD_OK : DRADD_ERR_CUDA;
 }
 
+// The map that an epilogue's boxes of 32 rows and 64 columns leave through,
+// or come in.
+dradd_status staging_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t stride)
+{
+    return make_map(map, p, rows, cols, rows > 1 ? stride : up(cols, 8), 32) ? DRADD_OK : DRADD_ERR_CUDA;
+}
+
 template <class K>
 dradd_status start(ProductArgs<K>* a, int dtype, int* sms)
 {
@@ -375,6 +382,19 @@ struct GradProduct {
     GradParams epi;
     bool on;
 };
+
+dradd_status grad_params(GradParams* p, void* out, float* partials, const float* factor, int64_t rows, int64_t cols,
+                         bool add)
+{
+    *p = {};
+    p->to_out = out != nullptr;
+    p->partials = partials;
+    p->factor = factor;
+    p->rows = static_cast<int>(rows);
+    p->cols = static_cast<int>(cols);
+    p->add = add;
+    return out ? staging_map(&p->out_map, out, rows, cols, cols) : DRADD_OK;
+}
 
 dradd_status run_gradients(GradProduct p, GradProduct q, bool early, int dtype, cudaStream_t stream)
 {
@@ -457,7 +477,7 @@ LinearGradPlan linear_grad_plan(int64_t rows, int64_t inner, int64_t cols, int a
     const int64_t c = parts_of(rows, 64);
     // with an activation and whole sums dz's product adds its columns up itself
     g.sums = act != DRADD_ACT_NONE && g.z.splits == 1;
-    g.chunks = g.sums ? g.z.tiles_m * g.z.group * (kTileRows / 32) : static_cast<int>(c < 64 ? c : 64);
+    g.chunks = static_cast<int>(g.sums ? parts_of(rows, 32) : c < 64 ? c : 64);
     g.dz = act == DRADD_ACT_NONE ? 0 : rows * cols * 2;
     g.partial_z = act == DRADD_ACT_NONE ? 0 : partial_bytes(g.z, rows, cols);
     g.partial_dx = want_dx ? partial_bytes(g.dx, rows, inner) : 0;
@@ -483,9 +503,15 @@ dradd_status run_linear(const Plan& p, const dradd_matrix& x, const dradd_matrix
                         int64_t inner, float* partials, int dtype, cudaStream_t stream)
 {
     const Side a = {x.data, act.rows, inner, x.stride, false}, b = {w.data, act.cols, inner, w.stride, false};
-    if (p.splits == 1)
-        return grad ? run_product<ActGradProduct>(p, a, b, act, false, dtype, stream)
-                    : run_product<ActProduct>(p, a, b, act, false, dtype, stream);
+    if (p.splits == 1) {
+        ActProductParams e = {};
+        e.act = act;
+        DRADD_TRY(staging_map(&e.out_map, act.out, act.rows, act.cols, act.out_stride));
+        if (act.other)
+            DRADD_TRY(staging_map(&e.other_map, act.other, act.rows, act.cols, act.other_stride));
+        return grad ? run_product<ActGradProduct>(p, a, b, e, false, dtype, stream)
+                    : run_product<ActProduct>(p, a, b, e, false, dtype, stream);
+    }
     const SplitParams s = {partials, act.rows, act.cols, 0};
     DRADD_TRY(run_product<SplitProduct>(p, a, b, s, false, dtype, stream));
     FinishParams f = {partials, p.splits, nullptr, act, grad, dtype == DRADD_BF16};
@@ -766,8 +792,7 @@ dradd_status loss_bwd(void* dx, void* dweight, const float* dloss, int64_t dloss
         const int64_t col0 = i * g.piece, width = v - col0 < g.piece ? v - col0 : g.piece;
         const char* w0 = static_cast<const char*>(weight->data) + col0 * weight->stride * 2;
         SlopeParams e = {};
-        e.out = s.dz;
-        e.stride = g.piece;
+        DRADD_TRY(staging_map(&e.out_map, s.dz, r, g.piece, g.piece));
         e.lse = lse;
         e.coef = s.coef;
         e.target = c.target;
@@ -791,13 +816,14 @@ dradd_status loss_bwd(void* dx, void* dweight, const float* dloss, int64_t dloss
         px.plan.split(parts_of(g.dx.k_blocks, g.dx.splits), kMostSplits);
         px.a = {s.dz, r, width, g.piece, false};
         px.b = {w0, width, h, weight->stride, true};
-        px.epi = {last && g.dx.splits == 1 ? dx : nullptr, s.partials, factor, f.rows, f.inner, i > 0};
+        DRADD_TRY(
+            grad_params(&px.epi, last && g.dx.splits == 1 ? dx : nullptr, s.partials, factor, r, h, i > 0));
         pw.on = dweight != nullptr;
         pw.plan = plan_of(width, h, r, g.dw.group);
         pw.a = {s.dz, r, width, g.piece, true};
         pw.b = {s.x_live, r, h, h, true};
-        pw.epi = {dweight ? static_cast<char*>(dweight) + col0 * h * 2 : nullptr, nullptr, factor,
-                  static_cast<int>(width), f.inner, 0};
+        DRADD_TRY(grad_params(&pw.epi, dweight ? static_cast<char*>(dweight) + col0 * h * 2 : nullptr, nullptr, factor,
+                              width, h, false));
         DRADD_TRY(run_gradients(px, pw, false, dtype, stream));
     }
     if (dx && g.dx.splits > 1)
@@ -939,13 +965,12 @@ dradd_status linear_act_add_bwd(void* dx, void* dweight, void* dbias, const drad
     px.plan = g.dx;
     px.a = {dz, rows, cols, dz_stride, false};
     px.b = {weight->data, cols, inner, weight->stride, true};
-    px.epi = {g.dx.splits == 1 ? dx : nullptr, partial_dx, nullptr, static_cast<int>(rows), static_cast<int>(inner), 0};
+    DRADD_TRY(grad_params(&px.epi, g.dx.splits == 1 ? dx : nullptr, partial_dx, nullptr, rows, inner, false));
     pw.on = dweight != nullptr;
     pw.plan = g.dw;
     pw.a = {dz, rows, cols, dz_stride, true};
     pw.b = {x->data, rows, inner, x->stride, true};
-    pw.epi = {g.dw.splits == 1 ? dweight : nullptr, partial_dw, nullptr, static_cast<int>(cols),
-              static_cast<int>(inner), 0};
+    DRADD_TRY(grad_params(&pw.epi, g.dw.splits == 1 ? dweight : nullptr, partial_dw, nullptr, cols, inner, false));
     // the bias's kernel starts its successor when dz is complete
     DRADD_TRY(run_gradients(px, pw, dbias != nullptr, dtype, stream));
     if (dx && g.dx.splits > 1)

@@ -5,33 +5,36 @@
 
 namespace dradd {
 
-// out = residual + act(z + bias).  The residual's values of the two next
-// steps of 16 columns are on their way while the present ones are worked on.
+// out = residual + act(z + bias).  The residual of a warp's part of the tile
+// comes into the space that the results leave from, while the products run.
 //
 // Bound by the products where the inner dimension is long; below some 2000
 // by these steps, up to 60 instructions an element, for which the kernel has
 // 16 warps: four a scheduler.
 struct EpiAct {
     using Kind = ActProduct;
-    using Params = ActParams;
+    using Params = ActProductParams;
     static constexpr int kWarps = 16;
+    static constexpr bool kStaged = true;
     static constexpr int kCols = kTileCols * 4 / kWarps;
-    const Params& p;
+    const Params& q;
+    const ActParams& p;
     const bool bf16;
     const int row, col;
-    uint32_t other[2][8];
+    Staging& staging;
+    const bool inside;  // some of the warp's rows and columns are
 
-    __device__ __forceinline__ EpiAct(const Params& p_, int bf16_, int row_, int col_, int)
-        : p(p_), bf16(bf16_), row(row_), col(col_)
+    __device__ __forceinline__ EpiAct(const Params& q_, int bf16_, int row_, int col_, int, Staging& staging_)
+        : q(q_), p(q_.act), bf16(bf16_), row(row_), col(col_), staging(staging_),
+          inside((row_ & ~31) < q_.act.rows && col_ < q_.act.cols)
     {
-        fetch<0>(0);
-        fetch<1>(16);
+        staging.acquire();
+        if (p.other && inside)
+            staging.load(&q.other_map, col, row & ~31, kCols / 64);
     }
-    template <int B>
-    __device__ __forceinline__ void fetch(int c)
+    __device__ __forceinline__ bool ready(uint64_t limit_ns)
     {
-        if (p.other && row < p.rows)
-            load16(static_cast<const uint16_t*>(p.other) + row * p.other_stride + col + c, p.cols - col - c, other[B]);
+        return !(p.other && inside) || staging.loaded(limit_ns);
     }
     __device__ __forceinline__ void add_bias(const uint32_t (&bits)[16], int c, int n, float (&z)[16])
     {
@@ -50,35 +53,32 @@ struct EpiAct {
             }
         }
     }
-    __device__ __forceinline__ void store(const float (&z)[16], int c, int n)
+    __device__ __forceinline__ void store(const float (&z)[16], int c)
     {
-        if (row < p.rows) {
-            uint32_t w[8];
-            pack16(z, bf16, w);
-            store16(static_cast<uint16_t*>(p.out) + row * p.out_stride + col + c, w, n);
-        }
+        uint32_t w[8];
+        pack16(z, bf16, w);
+        staging.write(c, w);
+        staging.store_full(&q.out_map, c, col, row & ~31, col + c - 48 < p.cols);
     }
-    template <int B>
     __device__ __forceinline__ void columns(const uint32_t (&bits)[16], int c)
     {
-        const int n = p.cols - col - c;
-        if (n <= 0)
+        if (!inside)
             return;
         float z[16];
-        add_bias(bits, c, n, z);
+        add_bias(bits, c, p.cols - col - c, z);
         act_values(z, p.act);
         if (p.other) {
+            uint32_t other[8];
+            staging.read(c, other);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 float lo, hi;
-                unpack2(other[B][j], bf16, lo, hi);
+                unpack2(other[j], bf16, lo, hi);
                 z[2 * j] += lo;
                 z[2 * j + 1] += hi;
             }
-            if (c + 32 < kCols)
-                fetch<B>(c + 32);
         }
-        store(z, c, n);
+        store(z, c);
     }
     __device__ __forceinline__ void end() {}
 };
@@ -109,27 +109,26 @@ struct EpiActGrad : EpiAct {
         if (lane < 16 && lane < n)
             p.col_sums[static_cast<int64_t>(row >> 5) * p.cols + col + c + lane] = sum;
     }
-    template <int B>
     __device__ __forceinline__ void columns(const uint32_t (&bits)[16], int c)
     {
-        const int n = p.cols - col - c;
-        if (n <= 0)
+        if (!inside)
             return;
+        const int n = p.cols - col - c;
         float z[16];
+        uint32_t other[8];
         add_bias(bits, c, n, z);
         act_slopes(z, p.act);
+        staging.read(c, other);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             float lo, hi;
-            unpack2(other[B][j], bf16, lo, hi);
+            unpack2(other[j], bf16, lo, hi);
             z[2 * j] *= lo;
             z[2 * j + 1] *= hi;
         }
-        if (c + 32 < kCols)
-            fetch<B>(c + 32);
-        if (p.col_sums)
+        if (p.col_sums && n > 0)
             add_up(z, c, n);
-        store(z, c, n);
+        store(z, c);
     }
 };
 

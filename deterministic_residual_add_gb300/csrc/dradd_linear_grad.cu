@@ -33,36 +33,39 @@ struct EpiGrad {
     using Kind = GradProducts;
     using Params = GradParams;
     static constexpr int kWarps = 8;
+    static constexpr bool kStaged = true;
     const Params& p;
     const bool bf16;
     const int row, col;
+    Staging& staging;
     float* sums;
     float factor;
 
-    __device__ __forceinline__ EpiGrad(const Params& p_, int bf16_, int row_, int col_, int split)
-        : p(p_), bf16(bf16_), row(row_), col(col_)
+    __device__ __forceinline__ EpiGrad(const Params& p_, int bf16_, int row_, int col_, int split, Staging& staging_)
+        : p(p_), bf16(bf16_), row(row_), col(col_), staging(staging_)
     {
+        staging.acquire();
         sums = p.partials + (static_cast<int64_t>(split) * p.rows + row) * p.cols + col;
         factor = p.factor ? *p.factor : 1.0f;
     }
-    template <int>
+    __device__ __forceinline__ bool ready(uint64_t) { return true; }
     __device__ __forceinline__ void columns(const uint32_t (&bits)[16], int c)
     {
         const int n = p.cols - col - c;
-        if (n <= 0 || row >= p.rows)
-            return;
         float v[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j)
             v[j] = __uint_as_float(bits[j]);
-        if (p.add)
+        if (p.add && row < p.rows)
             add_partials(sums + c, v, n);
-        if (!p.out) {
-            uint32_t w[16];
+        if (!p.to_out) {
+            if (n > 0 && row < p.rows) {
+                uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                w[j] = __float_as_uint(v[j]);
-            store_partials(sums + c, w, n);
+                for (int j = 0; j < 16; ++j)
+                    w[j] = __float_as_uint(v[j]);
+                store_partials(sums + c, w, n);
+            }
             return;
         }
 #pragma unroll
@@ -70,7 +73,8 @@ struct EpiGrad {
             v[j] *= factor;
         uint32_t w[8];
         pack16(v, bf16, w);
-        store16(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(row) * p.cols + col + c, w, n);
+        staging.write(c, w);
+        staging.store_full(&p.out_map, c, col, row & ~31, (row & ~31) < p.rows && col + c - 48 < p.cols);
     }
     __device__ __forceinline__ void end() {}
 };
@@ -79,16 +83,17 @@ struct EpiSplit {
     using Kind = SplitProduct;
     using Params = SplitParams;
     static constexpr int kWarps = 8;
+    static constexpr bool kStaged = false;
     const Params& p;
     const int row, col;
     float* sums;
 
-    __device__ __forceinline__ EpiSplit(const Params& p_, int, int row_, int col_, int split)
+    __device__ __forceinline__ EpiSplit(const Params& p_, int, int row_, int col_, int split, Staging&)
         : p(p_), row(row_), col(col_)
     {
         sums = p.partials + (static_cast<int64_t>(split) * p.rows + row) * p.cols + col;
     }
-    template <int>
+    __device__ __forceinline__ bool ready(uint64_t) { return true; }
     __device__ __forceinline__ void columns(const uint32_t (&bits)[16], int c)
     {
         const int n = p.cols - col - c;

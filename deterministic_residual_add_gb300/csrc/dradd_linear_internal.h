@@ -47,6 +47,11 @@ struct ActParams {
     float* col_sums;       // the gradient: [rows / 32, cols] sums of dz over 32 rows each, or NULL
 };
 
+struct ActProductParams {
+    ActParams act;
+    CUtensorMap out_map, other_map;  // 32 rows of 64 columns
+};
+
 // Statistics of the logits' rows, a part of 128 columns at a time.
 struct StatsParams {
     float2* part;            // [parts, rows]: maximum and sum of 2^(z scale - maximum), in base-2 units
@@ -62,8 +67,6 @@ struct StatsParams {
 
 // dz = coef.x * p - coef.y * share, one piece of the vocabulary at a time.
 struct SlopeParams {
-    void* out;               // [rows, stride]
-    int64_t stride;
     const float* lse;        // [rows]
     const float2* coef;      // [rows]
     const int64_t* target;
@@ -74,11 +77,13 @@ struct SlopeParams {
     int rows, vocab, top;    // vocab: the piece's words
     int col0;                // its first one, a multiple of 256
     float scale;
+    CUtensorMap out_map;
 };
 
 // out = rounded(sum * factor), or into fp32 partials [splits, rows, cols].
 struct GradParams {
-    void* out;               // 16-bit, or NULL: partials
+    CUtensorMap out_map;
+    int to_out;              // 16-bit results; else partials
     float* partials;
     const float* factor;     // device, or NULL: 1
     int rows, cols;
@@ -91,8 +96,8 @@ struct ProductKind {
     using Params = P;
     static constexpr int kProblems = N;
 };
-using ActProduct = ProductKind<ActParams, 1, 0>;
-using ActGradProduct = ProductKind<ActParams, 1, 1>;
+using ActProduct = ProductKind<ActProductParams, 1, 0>;
+using ActGradProduct = ProductKind<ActProductParams, 1, 1>;
 using SplitProduct = ProductKind<SplitParams, 1>;
 using StatsProduct = ProductKind<StatsParams, 1>;
 using SlopeProduct = ProductKind<SlopeParams, 1>;

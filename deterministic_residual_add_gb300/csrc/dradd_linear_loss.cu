@@ -58,6 +58,7 @@ struct EpiStats {
     using Kind = StatsProduct;
     using Params = StatsParams;
     static constexpr int kWarps = 8;
+    static constexpr bool kStaged = false;
     const Params& p;
     const int row, col;
     const int part;
@@ -65,7 +66,7 @@ struct EpiStats {
     float high = -INFINITY, sum = 0.0f, picked = 0.0f;
     bool found = false;
 
-    __device__ __forceinline__ EpiStats(const Params& p_, int, int row_, int col_, int)
+    __device__ __forceinline__ EpiStats(const Params& p_, int, int row_, int col_, int, Staging&)
         : p(p_), row(row_), col(col_), part(col_ / kHalfCols)
     {
         words.next = kHalfCols;
@@ -78,7 +79,7 @@ struct EpiStats {
                               p.first[static_cast<int64_t>(row) * p.parts + part], p.top, col);
         }
     }
-    template <int>
+    __device__ __forceinline__ bool ready(uint64_t) { return true; }
     __device__ __forceinline__ void columns(const uint32_t (&bits)[16], int c)
     {
         float z[16];
@@ -136,17 +137,20 @@ struct EpiSlope {
     using Kind = SlopeProduct;
     using Params = SlopeParams;
     static constexpr int kWarps = 8;
+    static constexpr bool kStaged = true;
     const Params& p;
     const bool bf16;
     const int row, col;
+    Staging& staging;
     Words words;
     float lse2 = 0.0f;
     float2 coef = make_float2(0.0f, 0.0f);
     bool live = false;
 
-    __device__ __forceinline__ EpiSlope(const Params& p_, int bf16_, int row_, int col_, int)
-        : p(p_), bf16(bf16_), row(row_), col(col_)
+    __device__ __forceinline__ EpiSlope(const Params& p_, int bf16_, int row_, int col_, int, Staging& staging_)
+        : p(p_), bf16(bf16_), row(row_), col(col_), staging(staging_)
     {
+        staging.acquire();
         words.next = kHalfCols;
         if (row < p.rows) {
             lse2 = p.lse[row] * kLog2e;
@@ -161,11 +165,9 @@ struct EpiSlope {
                               p.first[static_cast<int64_t>(row) * p.parts + at / kHalfCols], p.top, at);
         }
     }
-    template <int>
+    __device__ __forceinline__ bool ready(uint64_t) { return true; }
     __device__ __forceinline__ void columns(const uint32_t (&bits)[16], int c)
     {
-        if (row >= p.rows)
-            return;
         const int n = p.vocab - col - c;
         float v[16];
 #pragma unroll
@@ -186,7 +188,8 @@ struct EpiSlope {
         }
         uint32_t w[8];
         pack16(v, bf16, w);
-        store_sector(static_cast<uint16_t*>(p.out) + row * p.stride + col + c, w);
+        staging.write(c, w);
+        staging.store_full(&p.out_map, c, col, row & ~31, (row & ~31) < p.rows);
     }
     __device__ __forceinline__ void end() {}
 };
