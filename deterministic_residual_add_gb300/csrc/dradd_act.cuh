@@ -32,21 +32,51 @@ __device__ __forceinline__ float logistic(float x) { return rcp_fast(1.0f + exp2
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-// act(z).  The tails of both forms of gelu are computed as z times a small
-// number, not as a difference of numbers near 1.
+// erfc(x) for x >= 0 as e^(-x^2) times this: t e^(P(t)), t = 1 / (1 + x / 2),
+// with the Chebyshev fit of Press, Flannery, Teukolsky and Vetterling
+// ("Numerical Recipes", erfcc), whose relative error is below 1.2e-7
+// everywhere.  erfcf took 10.6 us for a tile's 32768 values.
+__device__ __forceinline__ float erfc_factor(float x)
+{
+    const float t = rcp_fast(fmaf(0.5f, x, 1.0f));
+    float p = 0.17087277f;
+    p = fmaf(p, t, -0.82215223f);
+    p = fmaf(p, t, 1.48851587f);
+    p = fmaf(p, t, -1.13520398f);
+    p = fmaf(p, t, 0.27886807f);
+    p = fmaf(p, t, -0.18628806f);
+    p = fmaf(p, t, 0.09678418f);
+    p = fmaf(p, t, 0.37409196f);
+    p = fmaf(p, t, 1.00002368f);
+    p = fmaf(p, t, -1.26551223f);
+    return t * exp2_fast(kLog2e * p);
+}
+
+// Phi(z), the normal distribution's function, and e^(-z^2 / 2).  The tail on
+// the left is a small number of its own, not a difference of numbers near 1.
+__device__ __forceinline__ float normal_cdf(float z, float& e)
+{
+    const float x = fabsf(z) * 0.70710678118654752f;
+    e = exp2_fast(-kLog2e * (x * x));
+    const float tail = 0.5f * e * erfc_factor(x);
+    return z < 0.0f ? tail : 1.0f - tail;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float z)
 {
-    if constexpr (ACT == DRADD_ACT_RELU)
+    if constexpr (ACT == DRADD_ACT_RELU) {
         return z < 0.0f ? 0.0f : z;
-    else if constexpr (ACT == DRADD_ACT_GELU)
-        return 0.5f * z * erfcf(z * -0.70710678118654752f);
-    else if constexpr (ACT == DRADD_ACT_GELU_TANH)
+    } else if constexpr (ACT == DRADD_ACT_GELU) {
+        float e;
+        return z * normal_cdf(z, e);
+    } else if constexpr (ACT == DRADD_ACT_GELU_TANH) {
         return z * logistic(2.0f * kGeluC * fmaf(kGeluA * z * z, z, z));
-    else if constexpr (ACT == DRADD_ACT_SILU)
+    } else if constexpr (ACT == DRADD_ACT_SILU) {
         return z * logistic(z);
-    else
+    } else {
         return z;
+    }
 }
 
 // act'(z); where its first factor has vanished, z times it counts as 0
@@ -57,9 +87,9 @@ __device__ __forceinline__ float act_slope(float z)
     if constexpr (ACT == DRADD_ACT_RELU) {
         return z > 0.0f ? 1.0f : 0.0f;
     } else if constexpr (ACT == DRADD_ACT_GELU) {
-        const float g = 0.3989422804014327f * exp2_fast(-0.5f * kLog2e * z * z);  // the normal density
-        const float f = 0.5f * erfcf(z * -0.70710678118654752f);
-        return g == 0.0f ? f : fmaf(z, g, f);
+        float e;
+        const float f = normal_cdf(z, e);
+        return e == 0.0f ? f : fmaf(z * e, 0.3989422804014327f, f);
     } else if constexpr (ACT == DRADD_ACT_GELU_TANH) {
         const float f = logistic(2.0f * kGeluC * fmaf(kGeluA * z * z, z, z));
         const float w = f * (1.0f - f);

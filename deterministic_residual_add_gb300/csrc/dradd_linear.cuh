@@ -50,13 +50,24 @@ struct Staging {
     uint32_t phase;
     int lane;
 
-    // What has been stored from here has been read, and what was read or
+    // All that has been stored from here has been read, and what was read or
     // written here comes before what is loaded next.
     __device__ __forceinline__ void acquire()
     {
         fence_proxy_async_smem();
         if (lane == 0)
-            bulk_wait_read();
+            bulk_wait_read<0>();
+        __syncwarp();
+    }
+    // The box that column c is the first 16 of may be written: stores go out
+    // box by box, so all but those of the BOXES - 1 others are read.
+    template <int BOXES>
+    __device__ __forceinline__ void acquire_box(int c)
+    {
+        if ((c & 63) != 0)
+            return;
+        if (lane == 0)
+            bulk_wait_read<BOXES - 1>();
         __syncwarp();
     }
     __device__ __forceinline__ void load(const CUtensorMap* map, int x, int y, int boxes)
@@ -96,8 +107,9 @@ struct Staging {
             return;
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && inside) {
-            store_box(map, x + c - 48, y, at + (c >> 6) * 4096u);
+        if (lane == 0) {
+            if (inside)
+                store_box(map, x + c - 48, y, at + (c >> 6) * 4096u);
             bulk_commit();
         }
     }
@@ -126,8 +138,8 @@ __device__ __forceinline__ int tile_of(const ProductArgs<K>& a, int worker, int 
         return t < a.tiles ? t : -1;
     if (t < a.tiles0)
         return t;
-    const int odd = a.tiles0 % workers;
-    i -= a.tiles0 / workers + (worker < odd);
+    const int odd = a.odd;
+    i -= a.rounds + (worker < odd);
     t = worker + i * workers;
     if (odd > 0) {
         const int rest = workers - odd;
@@ -152,18 +164,15 @@ __device__ __forceinline__ TileAt tile_at(const ProductArgs<K>& a, int t)
     if (r.problem)
         t -= a.tiles0;
     const ProductShape& s = a.shape[K::kProblems > 1 ? r.problem : 0];
-    const int per = s.tiles_m * s.tiles_n;
-    r.split = t / per;
-    t -= r.split * per;
-    const int band_tiles = s.band * s.tiles_n;
-    const int band = t / band_tiles;
-    t -= band * band_tiles;
-    const int high = min(s.band, s.tiles_m - band * s.band);
-    r.n = t / high;
-    r.m = band * s.band + t - r.n * high;
-    const int each = (s.k_blocks + s.splits - 1) / s.splits;
-    r.k0 = r.split * each;
-    r.k1 = min(r.k0 + each, s.k_blocks);
+    r.split = s.per_split.divide(t);
+    t -= r.split * s.per_split.d;
+    const int band = s.per_band.divide(t);
+    t -= band * s.per_band.d;
+    const bool last = (band + 1) * s.band > s.tiles_m;
+    r.n = last ? s.in_last.divide(t) : s.in_band.divide(t);
+    r.m = band * s.band + t - r.n * (last ? s.in_last.d : s.in_band.d);
+    r.k0 = r.split * s.k_each;
+    r.k1 = min(r.k0 + s.k_each, s.k_blocks);
     return r;
 }
 
@@ -394,13 +403,15 @@ __global__ void __launch_bounds__(kProductThreads<E>, 1) product_kernel(const __
 }
 
 template <int CG, class E>
-cudaError_t launch_product_group(const ProductArgs<typename E::Kind>& a, int sm_count, cudaStream_t stream)
+cudaError_t launch_product_group(ProductArgs<typename E::Kind> a, int sm_count, cudaStream_t stream)
 {
     constexpr auto fn = &product_kernel<CG, E>;
     cudaError_t e = allow_all_shared<product_kernel<CG, E>>();
     if (e != cudaSuccess)
         return e;
     const int workers = a.tiles < sm_count / CG ? a.tiles : sm_count / CG;
+    a.rounds = a.tiles0 / workers;
+    a.odd = a.tiles0 % workers;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -445,15 +456,26 @@ __device__ __forceinline__ void store_sector(void* p, const uint32_t (&w)[8])
                  : "memory");
 }
 
-__device__ __forceinline__ void unpack2(uint32_t w, bool bf16, float& lo, float& hi)
+__device__ __forceinline__ void unpack16(const uint32_t (&w)[8], bool bf16, float (&f)[16])
 {
     if (bf16) {
-        lo = bf16_lo(w);
-        hi = bf16_hi(w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            f[2 * i] = bf16_lo(w[i]);
+            f[2 * i + 1] = bf16_hi(w[i]);
+        }
     } else {
-        lo = Elem<kElemF16>::widen(static_cast<uint16_t>(w & 0xFFFFu));
-        hi = Elem<kElemF16>::widen(static_cast<uint16_t>(w >> 16));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            f[2 * i] = Elem<kElemF16>::widen(static_cast<uint16_t>(w[i] & 0xFFFFu));
+            f[2 * i + 1] = Elem<kElemF16>::widen(static_cast<uint16_t>(w[i] >> 16));
+        }
     }
+}
+
+__device__ __forceinline__ void prefetch_l1(const void* p)
+{
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
 }
 
 // 16 consecutive values of a 16-bit row, zeros past the n inside it.
@@ -462,7 +484,7 @@ __device__ __forceinline__ void load16(const uint16_t* p, int n, uint32_t (&w)[8
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (8 * i < n)
+        if (8 * i < n)  // columns come in eights
             v = __ldg(reinterpret_cast<const uint4*>(p) + i);
         w[4 * i] = v.x;
         w[4 * i + 1] = v.y;

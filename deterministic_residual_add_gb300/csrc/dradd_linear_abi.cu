@@ -331,6 +331,11 @@ dradd_status set_shape(ProductShape* s, const Plan& p, const Side& a, const Side
     s->k_blocks = p.k_blocks;
     s->splits = p.splits;
     s->band = band < p.tiles_m ? band : p.tiles_m;
+    s->per_split = Divisor::of(p.tiles_m * p.tiles_n);
+    s->per_band = Divisor::of(s->band * p.tiles_n);
+    s->in_band = Divisor::of(s->band);
+    s->in_last = Divisor::of(p.tiles_m % s->band ? p.tiles_m % s->band : s->band);
+    s->k_each = static_cast<int>(parts_of(p.k_blocks, p.splits));
     const bool ok = make_map(&s->a, a.data, a.rows, a.cols, map_stride(a), a.mn ? 64 : kTileRows) &&
                     make_map(&s->b, b.data, b.rows, b.cols, map_stride(b), b.mn ? 64 : kTileCols / p.group);
     return ok ? DRADD_OK : DRADD_ERR_CUDA;

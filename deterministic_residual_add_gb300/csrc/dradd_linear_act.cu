@@ -28,8 +28,12 @@ struct EpiAct {
         : q(q_), p(q_.act), bf16(bf16_), row(row_), col(col_), staging(staging_),
           inside((row_ & ~31) < q_.act.rows && col_ < q_.act.cols)
     {
+        if (p.bias && col < p.cols)
+            prefetch_l1(static_cast<const uint16_t*>(p.bias) + col);
+        if (!p.other)
+            return;
         staging.acquire();
-        if (p.other && inside)
+        if (inside)
             staging.load(&q.other_map, col, row & ~31, kCols / 64);
     }
     __device__ __forceinline__ bool ready(uint64_t limit_ns)
@@ -42,21 +46,21 @@ struct EpiAct {
         for (int j = 0; j < 16; ++j)
             z[j] = __uint_as_float(bits[j]);
         if (p.bias) {
-            uint32_t b[8];
-            load16(static_cast<const uint16_t*>(p.bias) + col + c, n, b);
+            uint32_t w[8];
+            float b[16];
+            load16(static_cast<const uint16_t*>(p.bias) + col + c, n, w);
+            unpack16(w, bf16, b);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float lo, hi;
-                unpack2(b[j], bf16, lo, hi);
-                z[2 * j] += lo;
-                z[2 * j + 1] += hi;
-            }
+            for (int j = 0; j < 16; ++j)
+                z[j] += b[j];
         }
     }
     __device__ __forceinline__ void store(const float (&z)[16], int c)
     {
         uint32_t w[8];
         pack16(z, bf16, w);
+        if (!p.other)
+            staging.acquire_box<kCols / 64>(c);
         staging.write(c, w);
         staging.store_full(&q.out_map, c, col, row & ~31, col + c - 48 < p.cols);
     }
@@ -68,15 +72,13 @@ struct EpiAct {
         add_bias(bits, c, p.cols - col - c, z);
         act_values(z, p.act);
         if (p.other) {
-            uint32_t other[8];
-            staging.read(c, other);
+            uint32_t w[8];
+            float other[16];
+            staging.read(c, w);
+            unpack16(w, bf16, other);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float lo, hi;
-                unpack2(other[j], bf16, lo, hi);
-                z[2 * j] += lo;
-                z[2 * j + 1] += hi;
-            }
+            for (int j = 0; j < 16; ++j)
+                z[j] += other[j];
         }
         store(z, c);
     }
@@ -114,18 +116,15 @@ struct EpiActGrad : EpiAct {
         if (!inside)
             return;
         const int n = p.cols - col - c;
-        float z[16];
-        uint32_t other[8];
+        float z[16], other[16];
+        uint32_t w[8];
         add_bias(bits, c, n, z);
         act_slopes(z, p.act);
-        staging.read(c, other);
+        staging.read(c, w);
+        unpack16(w, bf16, other);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float lo, hi;
-            unpack2(other[j], bf16, lo, hi);
-            z[2 * j] *= lo;
-            z[2 * j + 1] *= hi;
-        }
+        for (int j = 0; j < 16; ++j)
+            z[j] *= other[j];
         if (p.col_sums && n > 0)
             add_up(z, c, n);
         store(z, c);

@@ -44,7 +44,6 @@ struct EpiGrad {
     __device__ __forceinline__ EpiGrad(const Params& p_, int bf16_, int row_, int col_, int split, Staging& staging_)
         : p(p_), bf16(bf16_), row(row_), col(col_), staging(staging_)
     {
-        staging.acquire();
         sums = p.partials + (static_cast<int64_t>(split) * p.rows + row) * p.cols + col;
         factor = p.factor ? *p.factor : 1.0f;
     }
@@ -73,6 +72,7 @@ struct EpiGrad {
             v[j] *= factor;
         uint32_t w[8];
         pack16(v, bf16, w);
+        staging.acquire_box<2>(c);
         staging.write(c, w);
         staging.store_full(&p.out_map, c, col, row & ~31, (row & ~31) < p.rows && col + c - 48 < p.cols);
     }

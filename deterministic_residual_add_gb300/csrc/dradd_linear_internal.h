@@ -17,6 +17,28 @@ constexpr int kTileCols = 256;
 constexpr int kTileDepth = 64;
 constexpr int kHalfCols = kTileCols / 2;  // the columns of one epilogue warp
 
+// n / d for 0 <= n < 2^31 by a multiplication: the quotient of the round-up
+// method (Granlund and Montgomery, 1994), m = floor(2^32 (2^s - d) / d) + 1
+// with s = ceil(log2 d).
+struct Divisor {
+    uint32_t m, s;
+    int d;
+    static Divisor of(int d)
+    {
+        Divisor r = {0, 0, d < 1 ? 1 : d};
+        while ((1ull << r.s) < static_cast<uint64_t>(r.d))
+            ++r.s;
+        r.m = static_cast<uint32_t>((((1ull << r.s) - r.d) << 32) / r.d + 1);
+        return r;
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int divide(int n) const
+    {
+        return static_cast<int>((__umulhi(static_cast<uint32_t>(n), m) + static_cast<uint32_t>(n)) >> s);
+    }
+#endif
+};
+
 // One product C[m, n] = sum over k of A[m, k] B[n, k].
 struct ProductShape {
     CUtensorMap a, b;
@@ -25,6 +47,8 @@ struct ProductShape {
     int k_blocks;          // steps of 64
     int splits;            // parts of the k dimension, each a tile of its own
     int band;              // tile rows that are walked down together
+    Divisor per_split, per_band, in_band, in_last;  // tiles of a split, of a band, of a band's column
+    int k_each;            // steps of a split
 };
 
 // ------------------------------------------------------------- epilogues
@@ -109,6 +133,7 @@ struct ProductArgs {
     typename K::Params epi[K::kProblems];
     int tiles0, tiles;       // of the first problem, of all
     int worth;               // tiles of the second problem that cost as much as one of the first
+    int rounds, odd;         // tiles0 / workers and its remainder (set with the launch)
     int prefetch;            // one CTA a tile and few rows: see product_kernel
     int early;               // the operands are complete when this grid may start; only the epilogue waits
     int bf16;

@@ -150,7 +150,6 @@ struct EpiSlope {
     __device__ __forceinline__ EpiSlope(const Params& p_, int bf16_, int row_, int col_, int, Staging& staging_)
         : p(p_), bf16(bf16_), row(row_), col(col_), staging(staging_)
     {
-        staging.acquire();
         words.next = kHalfCols;
         if (row < p.rows) {
             lse2 = p.lse[row] * kLog2e;
@@ -188,6 +187,7 @@ struct EpiSlope {
         }
         uint32_t w[8];
         pack16(v, bf16, w);
+        staging.acquire_box<2>(c);
         staging.write(c, w);
         staging.store_full(&p.out_map, c, col, row & ~31, (row & ~31) < p.rows);
     }
