@@ -24,22 +24,37 @@ constexpr int kProductThreads = 128 + 32 * E::kWarps;
 constexpr uint32_t kBoxBytes = 64 * 64 * 2;  // 64 rows of 128 bytes
 
 __host__ __device__ constexpr uint32_t product_stage_bytes(int CG) { return (2u + 4u / CG) * kBoxBytes; }
-__host__ __device__ // What the results of a tile take on their way out (and the residual, or the
-// gradient that comes in, on its way in): 128 x 256 of 16 bits.
-constexpr uint32_t kStagingBytes = kTileRows * kTileCols * 2;
-__host__ __device__ constexpr int product_stages(int CG, bool staged)
+__host__ __device__ // What 16-bit results take on their way out (and the residual, or the
+// gradient that comes in, on its way in): a box of 32 rows and 64 columns for
+// every warp of an epilogue that is `staged`.
+//
+// Such an epilogue comes in two forms.  Sums of at least kDeepSteps steps a
+// tile leave it time, so 8 warps with two boxes of columns each do, and 32
+// more KB go to the ring, a sixth stage for a pair of CTAs; short sums want
+// 16 warps.  4096 x 4096 over 65536 words, gradients: 4002 us with 4 stages,
+// 3905 with 5; 8192 x 16384 by 4096: 682 and 656.  8192 x 512 by 8192 with
+// silu: 94.5 us with 8 warps, 65.6 with 16.
+constexpr uint32_t kStagingBox = 4096;
+constexpr int kDeepSteps = 32;
+template <class E>
+__host__ __device__ constexpr uint32_t staging_bytes()
 {
-    return static_cast<int>((225u * 1024u - (staged ? kStagingBytes : 0u)) / product_stage_bytes(CG));
+    return E::kStaged ? E::kWarps * kStagingBox : 0;
 }
-constexpr uint32_t product_smem(int CG, bool staged)
+template <int CG, class E>
+__host__ __device__ constexpr int product_stages()
 {
-    return product_stages(CG, staged) * product_stage_bytes(CG) + (staged ? kStagingBytes : 0u) + 1024u;
+    return static_cast<int>((225u * 1024u - staging_bytes<E>()) / product_stage_bytes(CG));
+}
+template <int CG, class E>
+constexpr uint32_t product_smem()
+{
+    return product_stages<CG, E>() * product_stage_bytes(CG) + staging_bytes<E>() + 1024u;
 }
 
-// An epilogue warp's share of the staging space: its 32 rows in boxes of 64
-// columns (4 KB each), one beside the other.  Lane i has row i.  A 16-byte
-// piece lies at its place xor the row's lowest bits, as the tensor map's
-// swizzle has it, and eight lanes that move a piece each touch all banks.
+// An epilogue warp's box.  Lane i has row i.  A 16-byte piece lies at its
+// place xor the row's lowest bits, as the tensor map's swizzle has it, and
+// eight lanes that move a piece each touch all banks.
 //
 // Results stored by the lanes themselves, a 32-byte sector of a row each,
 // took 5.6 us for a tile of 128 x 256 (8192 x 512 by 8192: 78 us); through
@@ -47,47 +62,44 @@ constexpr uint32_t product_smem(int CG, bool staged)
 struct Staging {
     uint32_t at;     // shared address
     uint64_t* bar;   // counts what comes in
+    uint64_t limit_ns;
     uint32_t phase;
     int lane;
+    bool failed;
 
-    // All that has been stored from here has been read, and what was read or
-    // written here comes before what is loaded next.
-    __device__ __forceinline__ void acquire()
-    {
-        fence_proxy_async_smem();
-        if (lane == 0)
-            bulk_wait_read<0>();
-        __syncwarp();
-    }
-    // The box that column c is the first 16 of may be written: stores go out
-    // box by box, so all but those of the BOXES - 1 others are read.
-    template <int BOXES>
-    __device__ __forceinline__ void acquire_box(int c)
+    // Before the first of a box's columns is written: what was stored from
+    // here has been read.
+    __device__ __forceinline__ void acquire(int c)
     {
         if ((c & 63) != 0)
             return;
         if (lane == 0)
-            bulk_wait_read<BOXES - 1>();
+            bulk_wait_read();
         __syncwarp();
     }
-    __device__ __forceinline__ void load(const CUtensorMap* map, int x, int y, int boxes)
+    // The same, and then something comes in.
+    __device__ __forceinline__ void load(const CUtensorMap* map, int x, int y)
     {
-        if (lane != 0)
-            return;
-        mbar_arrive_expect_tx(bar, boxes * 4096u);
-        for (int i = 0; i < boxes; ++i)
-            copy_box<1>(at + i * 4096u, map, x + i * 64, y, bar);
+        fence_proxy_async_smem();  // behind what was read and written here
+        if (lane == 0)
+            bulk_wait_read();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar, kStagingBox);
+            copy_box<1>(at, map, x, y, bar);
+        }
     }
-    __device__ __forceinline__ bool loaded(uint64_t limit_ns)
+    // Waits for it; a wait that gave up ends the warp's work behind this tile,
+    // whose results are then not to be used.
+    __device__ __forceinline__ void loaded()
     {
-        const bool ok = mbar_wait_bounded(bar, phase, limit_ns);
+        failed |= !__all_sync(0xffffffffu, mbar_wait_bounded(bar, phase, limit_ns));
         phase ^= 1u;
-        return ok;
     }
     // Columns c to c + 15 of the lane's row.
     __device__ __forceinline__ uint32_t piece(int c, int i) const
     {
-        return at + (c >> 6) * 4096u + lane * 128u + (((((c & 63) >> 3) + i) ^ (lane & 7)) << 4);
+        return at + lane * 128u + (((((c & 63) >> 3) + i) ^ (lane & 7)) << 4);
     }
     __device__ __forceinline__ void read(int c, uint32_t (&w)[8]) const
     {
@@ -107,9 +119,8 @@ struct Staging {
             return;
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-            if (inside)
-                store_box(map, x + c - 48, y, at + (c >> 6) * 4096u);
+        if (lane == 0 && inside) {
+            store_box(map, x + c - 48, y, at);
             bulk_commit();
         }
     }
@@ -179,7 +190,7 @@ __device__ __forceinline__ TileAt tile_at(const ProductArgs<K>& a, int t)
 template <int CG, class E>
 __global__ void __launch_bounds__(kProductThreads<E>, 1) product_kernel(const __grid_constant__ ProductArgs<typename E::Kind> a)
 {
-    constexpr int kStages = product_stages(CG, E::kStaged);
+    constexpr int kStages = product_stages<CG, E>();
     constexpr uint32_t kStageBytes = product_stage_bytes(CG);
     constexpr uint32_t kBytesA = 2 * kBoxBytes;
     constexpr int kRowsB = kTileCols / CG;
@@ -351,19 +362,15 @@ __global__ void __launch_bounds__(kProductThreads<E>, 1) product_kernel(const __
         const int quadrant = warp & 3, part = (warp - 4) >> 2;
         int acc = 0;
         uint32_t acc_phase = 0;
-        Staging staging = {ring + kStages * kStageBytes + (warp - 4) * (kStagingBytes / E::kWarps),
-                           &bars.loaded[warp - 4], 0, lane};
+        Staging staging = {ring + kStages * kStageBytes + (warp - 4) * kStagingBox,
+                           &bars.loaded[warp - 4], a.wait_limit_ns, 0, lane, false};
         for (int i = 0, t; (t = tile_of(a, worker, workers, i)) >= 0; ++i) {
             const TileAt at = tile_at(a, t);
             const int row = (at.m * CG + static_cast<int>(rank)) * kTileRows + quadrant * 32 + lane;
             const int col = at.n * kTileCols + part * kCols;
             E epi(a.epi[E::Kind::kProblems > 1 ? at.problem : 0], a.bf16, row, col, at.split, staging);
-            const bool ok = epi.ready(a.wait_limit_ns) && wait(&bars.acc_full[acc], acc_phase);
-            if (!__all_sync(0xffffffffu, ok)) {
-                if (lane == 0)
-                    atomicOr(a.status, kDeviceStatusTimeout);
+            if (!__all_sync(0xffffffffu, wait(&bars.acc_full[acc], acc_phase)))
                 break;
-            }
             tmem_fence_after();
             const uint32_t from = tmem + (static_cast<uint32_t>(quadrant * 32) << 16) + acc * kTileCols + part * kCols;
             uint32_t v0[16], v1[16];
@@ -385,6 +392,10 @@ __global__ void __launch_bounds__(kProductThreads<E>, 1) product_kernel(const __
                 epi.columns(v1, c + 16);
             }
             epi.end();
+            if (staging.failed) {
+                atomicOr(a.status, kDeviceStatusTimeout);
+                break;
+            }
             if (++acc == 2) {
                 acc = 0;
                 acc_phase ^= 1u;
@@ -421,11 +432,21 @@ cudaError_t launch_product_group(ProductArgs<typename E::Kind> a, int sm_count, 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(workers * CG));
     cfg.blockDim = dim3(kProductThreads<E>);
-    cfg.dynamicSmemBytes = product_smem(CG, E::kStaged);
+    cfg.dynamicSmemBytes = product_smem<CG, E>();
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, fn, a);
+}
+
+// Whether every tile's sum is long enough for the deep form of a staged epilogue.
+template <class K>
+bool long_sums(const ProductArgs<K>& a)
+{
+    for (int i = 0; i < K::kProblems; ++i)
+        if ((i == 0 || a.tiles > a.tiles0) && a.shape[i].k_each < kDeepSteps)
+            return false;
+    return true;
 }
 
 template <class E>

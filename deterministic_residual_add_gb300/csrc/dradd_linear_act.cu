@@ -5,16 +5,13 @@
 
 namespace dradd {
 
-// out = residual + act(z + bias).  The residual of a warp's part of the tile
-// comes into the space that the results leave from, while the products run.
-//
-// Bound by the products where the inner dimension is long; below some 2000
-// by these steps, up to 60 instructions an element, for which the kernel has
-// 16 warps: four a scheduler.
+// out = residual + act(z + bias).  The residual comes into the box that the
+// results leave from, its first one while the products run.
+template <bool DEEP>
 struct EpiAct {
     using Kind = ActProduct;
     using Params = ActProductParams;
-    static constexpr int kWarps = 16;
+    static constexpr int kWarps = DEEP ? 8 : 16;
     static constexpr bool kStaged = true;
     static constexpr int kCols = kTileCols * 4 / kWarps;
     const Params& q;
@@ -30,15 +27,21 @@ struct EpiAct {
     {
         if (p.bias && col < p.cols)
             prefetch_l1(static_cast<const uint16_t*>(p.bias) + col);
-        if (!p.other)
-            return;
-        staging.acquire();
-        if (inside)
-            staging.load(&q.other_map, col, row & ~31, kCols / 64);
+        if (p.other && inside)
+            staging.load(&q.other_map, col, row & ~31);
     }
-    __device__ __forceinline__ bool ready(uint64_t limit_ns)
+    // At the first of a box's columns: the box may be used, and what comes in is there.
+    __device__ __forceinline__ void enter_box(int c)
     {
-        return !(p.other && inside) || staging.loaded(limit_ns);
+        if ((c & 63) != 0)
+            return;
+        if (!p.other) {
+            staging.acquire(c);
+            return;
+        }
+        if (c > 0)
+            staging.load(&q.other_map, col + c, row & ~31);
+        staging.loaded();
     }
     __device__ __forceinline__ void add_bias(const uint32_t (&bits)[16], int c, int n, float (&z)[16])
     {
@@ -59,8 +62,6 @@ struct EpiAct {
     {
         uint32_t w[8];
         pack16(z, bf16, w);
-        if (!p.other)
-            staging.acquire_box<kCols / 64>(c);
         staging.write(c, w);
         staging.store_full(&q.out_map, c, col, row & ~31, col + c - 48 < p.cols);
     }
@@ -70,6 +71,7 @@ struct EpiAct {
             return;
         float z[16];
         add_bias(bits, c, p.cols - col - c, z);
+        enter_box(c);
         act_values(z, p.act);
         if (p.other) {
             uint32_t w[8];
@@ -86,9 +88,12 @@ struct EpiAct {
 };
 
 // dz = dout * act'(z + bias), and its sums over 32 rows for the bias.
-struct EpiActGrad : EpiAct {
+template <bool DEEP>
+struct EpiActGrad : EpiAct<DEEP> {
     using Kind = ActGradProduct;
-    using EpiAct::EpiAct;
+    using Base = EpiAct<DEEP>;
+    using Base::Base;
+    using Base::p, Base::q, Base::row, Base::col, Base::inside, Base::bf16, Base::staging;
     // The warp's 32 rows of each of 16 columns: at every level a lane keeps
     // one half of its columns and hands the other one over, until it has one;
     // two lanes then have half of the rows each.
@@ -118,7 +123,8 @@ struct EpiActGrad : EpiAct {
         const int n = p.cols - col - c;
         float z[16], other[16];
         uint32_t w[8];
-        add_bias(bits, c, n, z);
+        Base::add_bias(bits, c, n, z);
+        Base::enter_box(c);
         act_slopes(z, p.act);
         staging.read(c, w);
         unpack16(w, bf16, other);
@@ -127,7 +133,7 @@ struct EpiActGrad : EpiAct {
             z[j] *= other[j];
         if (p.col_sums && n > 0)
             add_up(z, c, n);
-        store(z, c);
+        Base::store(z, c);
     }
 };
 
@@ -135,14 +141,16 @@ template <>
 cudaError_t launch_product<ActProduct>(const ProductArgs<ActProduct>& a, int cta_group, int sm_count,
                                        cudaStream_t stream)
 {
-    return launch_with<EpiAct>(a, cta_group, sm_count, stream);
+    return long_sums(a) ? launch_with<EpiAct<true>>(a, cta_group, sm_count, stream)
+                        : launch_with<EpiAct<false>>(a, cta_group, sm_count, stream);
 }
 
 template <>
 cudaError_t launch_product<ActGradProduct>(const ProductArgs<ActGradProduct>& a, int cta_group, int sm_count,
                                            cudaStream_t stream)
 {
-    return launch_with<EpiActGrad>(a, cta_group, sm_count, stream);
+    return long_sums(a) ? launch_with<EpiActGrad<true>>(a, cta_group, sm_count, stream)
+                        : launch_with<EpiActGrad<false>>(a, cta_group, sm_count, stream);
 }
 
 }  // namespace dradd

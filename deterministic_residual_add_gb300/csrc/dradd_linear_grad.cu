@@ -29,10 +29,11 @@ __device__ __forceinline__ void store_partials(float* p, const uint32_t (&w)[16]
         }
 }
 
+template <bool DEEP>
 struct EpiGrad {
     using Kind = GradProducts;
     using Params = GradParams;
-    static constexpr int kWarps = 8;
+    static constexpr int kWarps = DEEP ? 8 : 16;
     static constexpr bool kStaged = true;
     const Params& p;
     const bool bf16;
@@ -47,7 +48,6 @@ struct EpiGrad {
         sums = p.partials + (static_cast<int64_t>(split) * p.rows + row) * p.cols + col;
         factor = p.factor ? *p.factor : 1.0f;
     }
-    __device__ __forceinline__ bool ready(uint64_t) { return true; }
     __device__ __forceinline__ void columns(const uint32_t (&bits)[16], int c)
     {
         const int n = p.cols - col - c;
@@ -72,7 +72,7 @@ struct EpiGrad {
             v[j] *= factor;
         uint32_t w[8];
         pack16(v, bf16, w);
-        staging.acquire_box<2>(c);
+        staging.acquire(c);
         staging.write(c, w);
         staging.store_full(&p.out_map, c, col, row & ~31, (row & ~31) < p.rows && col + c - 48 < p.cols);
     }
@@ -93,7 +93,6 @@ struct EpiSplit {
     {
         sums = p.partials + (static_cast<int64_t>(split) * p.rows + row) * p.cols + col;
     }
-    __device__ __forceinline__ bool ready(uint64_t) { return true; }
     __device__ __forceinline__ void columns(const uint32_t (&bits)[16], int c)
     {
         const int n = p.cols - col - c;
@@ -106,7 +105,8 @@ struct EpiSplit {
 template <>
 cudaError_t launch_product<GradProducts>(const ProductArgs<GradProducts>& a, int cta_group, int sm_count, cudaStream_t stream)
 {
-    return launch_with<EpiGrad>(a, cta_group, sm_count, stream);
+    return long_sums(a) ? launch_with<EpiGrad<true>>(a, cta_group, sm_count, stream)
+                        : launch_with<EpiGrad<false>>(a, cta_group, sm_count, stream);
 }
 
 template <>

@@ -5,13 +5,14 @@
 
 namespace dradd {
 
-// The words of a row that count in a part of 128 columns: a target, or the
-// entries of a teacher in rising order.
+// The words of a row that count from a warp's first column on, a multiple of
+// 64: a target, or the entries of a teacher in rising order, from the first
+// in this part of 128 columns.
 struct Words {
     const int* entry = nullptr;
     const float* share = nullptr;
     int left = 0;
-    int next = -1;       // the next word's column in the part; outside [0, 128): none
+    int next = -1;       // the next word's column from there; kHalfCols: none
     float weight = 1.0f;
 
     __device__ __forceinline__ void target(int64_t word, int64_t col)
@@ -45,8 +46,14 @@ private:
     {
         next = kHalfCols;
         if (left > 0) {
-            const int64_t at = *entry - base;
-            if (at < kHalfCols) {  // entries are not below the part's first column
+            int64_t at = *entry - base;
+            while (at < 0 && left > 1) {  // of the 64 columns in front
+                ++entry;
+                ++share;
+                --left;
+                at = *entry - base;
+            }
+            if (at >= 0 && at < kHalfCols) {
                 next = static_cast<int>(at);
                 weight = *share;
             }
@@ -79,7 +86,6 @@ struct EpiStats {
                               p.first[static_cast<int64_t>(row) * p.parts + part], p.top, col);
         }
     }
-    __device__ __forceinline__ bool ready(uint64_t) { return true; }
     __device__ __forceinline__ void columns(const uint32_t (&bits)[16], int c)
     {
         float z[16];
@@ -133,10 +139,11 @@ struct EpiStats {
     }
 };
 
+template <bool DEEP>
 struct EpiSlope {
     using Kind = SlopeProduct;
     using Params = SlopeParams;
-    static constexpr int kWarps = 8;
+    static constexpr int kWarps = DEEP ? 8 : 16;
     static constexpr bool kStaged = true;
     const Params& p;
     const bool bf16;
@@ -164,7 +171,6 @@ struct EpiSlope {
                               p.first[static_cast<int64_t>(row) * p.parts + at / kHalfCols], p.top, at);
         }
     }
-    __device__ __forceinline__ bool ready(uint64_t) { return true; }
     __device__ __forceinline__ void columns(const uint32_t (&bits)[16], int c)
     {
         const int n = p.vocab - col - c;
@@ -187,7 +193,7 @@ struct EpiSlope {
         }
         uint32_t w[8];
         pack16(v, bf16, w);
-        staging.acquire_box<2>(c);
+        staging.acquire(c);
         staging.write(c, w);
         staging.store_full(&p.out_map, c, col, row & ~31, (row & ~31) < p.rows);
     }
@@ -203,7 +209,8 @@ cudaError_t launch_product<StatsProduct>(const ProductArgs<StatsProduct>& a, int
 template <>
 cudaError_t launch_product<SlopeProduct>(const ProductArgs<SlopeProduct>& a, int cta_group, int sm_count, cudaStream_t stream)
 {
-    return launch_with<EpiSlope>(a, cta_group, sm_count, stream);
+    return long_sums(a) ? launch_with<EpiSlope<true>>(a, cta_group, sm_count, stream)
+                        : launch_with<EpiSlope<false>>(a, cta_group, sm_count, stream);
 }
 
 }  // namespace dradd
