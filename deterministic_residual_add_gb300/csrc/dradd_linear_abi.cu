@@ -657,9 +657,9 @@ dradd_status loss_fwd(float* loss, float* lse, const dradd_matrix* x, const drad
     DRADD_TRY(k.done());
     Carver w(workspace);
     const LossForwardSpace s(&w, c.rows, c.vocab, c.top());
+    const Plan p = plan_of(c.rows, c.vocab, c.hidden, group_for(c.rows));
     if (c.teacher)
         DRADD_TRY(from_cuda(s.teacher.run(c, stream)));
-    const Plan p = plan_of(c.rows, c.vocab, c.hidden, group_for(c.rows));
     StatsParams e = {};
     e.part = s.part;
     e.picked = s.picked;

@@ -60,6 +60,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 3) few_kernel(const FewParams 
     const int stages = (p.inner + kDepth - 1) / kDepth;
     const bool bf16 = p.bf16;
     const uint4 none = make_uint4(0, 0, 0, 0);
+    const uint16_t* w = static_cast<const uint16_t*>(p.weight) + col0 * p.weight_stride;
+    // The first stages are asked into L2 while the grid before ends.
+    if (static_cast<int>(threadIdx.x) < cols)
+        prefetch_l2(w + threadIdx.x * p.weight_stride, static_cast<uint32_t>(min(kDepth * kFewStages, p.inner)) * 2);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kFewStages; ++i) {
             mbar_init(&full[i], 1);
@@ -70,7 +74,6 @@ __global__ void __launch_bounds__(kFewWarps * 32, 3) few_kernel(const FewParams 
     __syncthreads();
     allow_next_grid();
     wait_prior_grids();
-    const uint16_t* w = static_cast<const uint16_t*>(p.weight) + col0 * p.weight_stride;
     const uint16_t* x = static_cast<const uint16_t*>(p.x);
     // Lane i < cols of warp 0 copies row i of stage s; lane 0 has said how
     // many bytes come before any of them starts.

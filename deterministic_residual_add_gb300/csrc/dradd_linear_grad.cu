@@ -29,11 +29,10 @@ __device__ __forceinline__ void store_partials(float* p, const uint32_t (&w)[16]
         }
 }
 
-template <bool DEEP>
 struct EpiGrad {
     using Kind = GradProducts;
     using Params = GradParams;
-    static constexpr int kWarps = DEEP ? 8 : 16;
+    static constexpr int kWarps = 8;
     static constexpr bool kStaged = true;
     const Params& p;
     const bool bf16;
@@ -105,8 +104,7 @@ struct EpiSplit {
 template <>
 cudaError_t launch_product<GradProducts>(const ProductArgs<GradProducts>& a, int cta_group, int sm_count, cudaStream_t stream)
 {
-    return long_sums(a) ? launch_with<EpiGrad<true>>(a, cta_group, sm_count, stream)
-                        : launch_with<EpiGrad<false>>(a, cta_group, sm_count, stream);
+    return launch_with<EpiGrad>(a, cta_group, sm_count, stream);
 }
 
 template <>

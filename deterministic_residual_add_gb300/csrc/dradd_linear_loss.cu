@@ -5,14 +5,13 @@
 
 namespace dradd {
 
-// The words of a row that count from a warp's first column on, a multiple of
-// 64: a target, or the entries of a teacher in rising order, from the first
-// in this part of 128 columns.
+// The words of a row that count in a part of 128 columns: a target, or the
+// entries of a teacher in rising order.
 struct Words {
     const int* entry = nullptr;
     const float* share = nullptr;
     int left = 0;
-    int next = -1;       // the next word's column from there; kHalfCols: none
+    int next = -1;       // the next word's column in the part; kHalfCols: none
     float weight = 1.0f;
 
     __device__ __forceinline__ void target(int64_t word, int64_t col)
@@ -46,14 +45,8 @@ private:
     {
         next = kHalfCols;
         if (left > 0) {
-            int64_t at = *entry - base;
-            while (at < 0 && left > 1) {  // of the 64 columns in front
-                ++entry;
-                ++share;
-                --left;
-                at = *entry - base;
-            }
-            if (at >= 0 && at < kHalfCols) {
+            const int64_t at = *entry - base;
+            if (at < kHalfCols) {  // entries are not below the part's first column
                 next = static_cast<int>(at);
                 weight = *share;
             }
@@ -139,11 +132,10 @@ struct EpiStats {
     }
 };
 
-template <bool DEEP>
 struct EpiSlope {
     using Kind = SlopeProduct;
     using Params = SlopeParams;
-    static constexpr int kWarps = DEEP ? 8 : 16;
+    static constexpr int kWarps = 8;
     static constexpr bool kStaged = true;
     const Params& p;
     const bool bf16;
@@ -209,8 +201,7 @@ cudaError_t launch_product<StatsProduct>(const ProductArgs<StatsProduct>& a, int
 template <>
 cudaError_t launch_product<SlopeProduct>(const ProductArgs<SlopeProduct>& a, int cta_group, int sm_count, cudaStream_t stream)
 {
-    return long_sums(a) ? launch_with<EpiSlope<true>>(a, cta_group, sm_count, stream)
-                        : launch_with<EpiSlope<false>>(a, cta_group, sm_count, stream);
+    return launch_with<EpiSlope>(a, cta_group, sm_count, stream);
 }
 
 }  // namespace dradd

@@ -350,8 +350,8 @@ cudaError_t launch_teacher(const TeacherParams& p, cudaStream_t stream)
 __global__ void __launch_bounds__(1024) loss_kernel(const LossParams p)
 {
     __shared__ float highs[64][17], sums[64][17], picks[64][17];
-    wait_prior_grids();
     allow_next_grid();
+    wait_prior_grids();
     const int lane = threadIdx.x & 15, warp = threadIdx.x >> 4;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + lane;
     const bool teacher = p.top != 0;
