@@ -574,7 +574,7 @@ void loss_inputs(Checks* k, const LossCall& c, const dradd_matrix* x, const drad
 struct TeacherSpace {
     int* entries;
     float* shares;
-    float* entropy;
+    float2* entropy;
     uint16_t* first;
     int parts;
 
@@ -583,7 +583,7 @@ struct TeacherSpace {
         parts = static_cast<int>(2 * parts_of(vocab, kTileCols));
         entries = w->take<int>(rows * top * 4);
         shares = w->take<float>(rows * top * 4);
-        entropy = w->take<float>(top && with_entropy ? rows * 4 : 0);
+        entropy = w->take<float2>(top && with_entropy ? rows * 8 : 0);
         first = w->take<uint16_t>(top ? rows * parts * 2 : 0);
     }
     cudaError_t run(const LossCall& c, cudaStream_t stream) const
@@ -605,41 +605,60 @@ struct TeacherSpace {
     }
 };
 
+// The product that makes a loss's logits: where its tiles do not fill the
+// device it is split, and the logits of these few rows or few words are
+// summed up in the workspace.
+Plan logit_plan(int64_t rows, int64_t hidden, int64_t words)
+{
+    Plan p = plan_of(rows, words, hidden, group_for(rows));
+    split_alone(&p, rows, words);
+    return p;
+}
+
+int64_t logit_bytes(const Plan& p, int64_t rows, int64_t words) { return partial_bytes(p, rows, up(words, 8)); }
+
 struct LossForwardSpace {
     TeacherSpace teacher;
     float2* part;
     float* picked;
+    float* partials;
 
-    LossForwardSpace(Carver* w, int64_t rows, int64_t vocab, int64_t top) : teacher(w, rows, vocab, top, true)
+    LossForwardSpace(Carver* w, int64_t rows, int64_t hidden, int64_t vocab, int64_t top)
+        : teacher(w, rows, vocab, top, true)
     {
+        partials = w->take<float>(logit_bytes(logit_plan(rows, hidden, vocab), rows, vocab));
         part = w->take<float2>(teacher.parts * rows * 8);
         picked = w->take<float>((top ? teacher.parts : 1) * rows * 4);
     }
 };
 
-// What a logit's sum is multiplied by.  The tensor cores cut off what does
+// What a logit's sum is multiplied by, in units of powers of two.  The tensor cores cut off what does
 // not fit their fp32 sum, 16 terms at a time, so sums come out nearer to 0
 // the longer they are.  Measured over 4096 rows against fp64, sums of random
 // terms are short by 0.88e-6 at 1024 terms, 3.73e-6 at 4096 and 7.50e-6 at
 // 8192, sums whose terms have one sign by 1.00e-6, 4.30e-6 and 8.71e-6: 1e-9
-// of their size a term.  Losses are differences of such sums.
+// of their size a term that is added without a break (the partial sums of a
+// split product are joined by rounded additions).  Losses are differences of
+// such sums.
 constexpr double kShortPerTerm = 1.0e-9;
-float logit_factor(int64_t hidden, float inv_temperature)
+float logit_scale(const Plan& p, int64_t hidden, float inv_temperature)
 {
-    return static_cast<float>(inv_temperature * (1.0 + kShortPerTerm * static_cast<double>(hidden)));
-}
-// In units of powers of two.
-float logit_scale(int64_t hidden, float inv_temperature)
-{
+    const int64_t each = parts_of(p.k_blocks, p.splits) * kTileDepth, run = each < hidden ? each : hidden;
     return static_cast<float>(1.4426950408889634 * inv_temperature *
-                              (1.0 + kShortPerTerm * static_cast<double>(hidden)));
+                              (1.0 + kShortPerTerm * static_cast<double>(run)));
+}
+
+dradd_status run_logits(const Plan& p, const Side& x, const Side& w, float* partials, bool early, int dtype,
+                        cudaStream_t stream)
+{
+    const SplitParams e = {partials, static_cast<int>(x.rows), static_cast<int>(up(w.rows, 8)), 0};
+    return run_product<SplitProduct>(p, x, w, e, early, dtype, stream);
 }
 
 size_t loss_fwd_bytes(int64_t rows, int64_t hidden, int64_t vocab, int64_t top)
 {
-    (void)hidden;
     Carver w(nullptr);
-    LossForwardSpace s(&w, rows, vocab, top);
+    LossForwardSpace s(&w, rows, hidden, vocab, top);
     return static_cast<size_t>(w.used);
 }
 
@@ -656,8 +675,10 @@ dradd_status loss_fwd(float* loss, float* lse, const dradd_matrix* x, const drad
     k.workspace(workspace, workspace_bytes, loss_fwd_bytes(c.rows, c.hidden, c.vocab, c.top()));
     DRADD_TRY(k.done());
     Carver w(workspace);
-    const LossForwardSpace s(&w, c.rows, c.vocab, c.top());
-    const Plan p = plan_of(c.rows, c.vocab, c.hidden, group_for(c.rows));
+    const LossForwardSpace s(&w, c.rows, c.hidden, c.vocab, c.top());
+    const Plan p = logit_plan(c.rows, c.hidden, c.vocab);
+    const Side sx = {x->data, c.rows, c.hidden, x->stride, false},
+               sw = {weight->data, c.vocab, c.hidden, weight->stride, false};
     if (c.teacher)
         DRADD_TRY(from_cuda(s.teacher.run(c, stream)));
     StatsParams e = {};
@@ -671,10 +692,13 @@ dradd_status loss_fwd(float* loss, float* lse, const dradd_matrix* x, const drad
     e.rows = static_cast<int>(c.rows);
     e.vocab = static_cast<int>(c.vocab);
     e.top = static_cast<int>(c.top());
-    e.scale = logit_scale(c.hidden, c.inv_temperature());
-    DRADD_TRY(run_product<StatsProduct>(p, {x->data, c.rows, c.hidden, x->stride, false},
-                                    {weight->data, c.vocab, c.hidden, weight->stride, false}, e, c.teacher != nullptr,
-                                    dtype, stream));
+    e.scale = logit_scale(p, c.hidden, c.inv_temperature());
+    if (p.splits == 1) {
+        DRADD_TRY(run_product<StatsProduct>(p, sx, sw, e, c.teacher != nullptr, dtype, stream));
+    } else {
+        DRADD_TRY(run_logits(p, sx, sw, s.partials, c.teacher != nullptr, dtype, stream));
+        DRADD_TRY(from_cuda(launch_stats({s.partials, p.splits, up(c.vocab, 8)}, e, stream)));
+    }
     LossParams l = {};
     l.loss = loss;
     l.lse = lse;
@@ -688,7 +712,7 @@ dradd_status loss_fwd(float* loss, float* lse, const dradd_matrix* x, const drad
     l.vocab = e.vocab;
     l.top = e.top;
     l.parts = s.teacher.parts;
-    l.logit_factor = logit_factor(c.hidden, c.inv_temperature());
+    l.scale = e.scale;
     return from_cuda(launch_loss(l, stream));
 }
 
@@ -698,7 +722,7 @@ constexpr int64_t kPieceBytes = 256ll << 20;
 
 struct LossGradPlan {
     int64_t piece, pieces;
-    Plan dx, dw;  // of a whole piece; the last may be smaller
+    Plan z, dx, dw;  // of a whole piece; the last may be smaller
 };
 
 LossGradPlan loss_grad_plan(int64_t rows, int64_t hidden, int64_t vocab)
@@ -711,6 +735,7 @@ LossGradPlan loss_grad_plan(int64_t rows, int64_t hidden, int64_t vocab)
     g.piece = up(parts_of(whole, g.pieces), kTileCols);  // of about one size
     g.pieces = parts_of(whole, g.piece);
     const int64_t width = g.pieces == 1 ? vocab : g.piece;
+    g.z = g.pieces == 1 ? logit_plan(rows, hidden, width) : plan_of(rows, width, hidden, group_for(rows));
     plan_pair({rows, hidden, width}, {width, hidden, rows}, false, &g.dx, &g.dw);
     return g;
 }
@@ -721,7 +746,8 @@ struct LossBackwardSpace {
     float* factor;
     void* x_live;
     void* dz;
-    float* partials;  // dx
+    float* logits;    // partial sums of z
+    float* partials;  // of dx
 
     LossBackwardSpace(Carver* w, const LossGradPlan& g, int64_t rows, int64_t hidden, int64_t vocab, int64_t top)
         : teacher(w, rows, vocab, top, false)
@@ -730,6 +756,7 @@ struct LossBackwardSpace {
         factor = w->take<float>(8);
         x_live = w->take(rows * hidden * 2);
         dz = w->take(rows * g.piece * 2);
+        logits = w->take<float>(logit_bytes(g.z, rows, vocab));
         partials = w->take<float>(g.dx.splits > 1 || g.pieces > 1 ? g.dx.splits * rows * hidden * 4 : 0);
     }
 };
@@ -809,9 +836,15 @@ dradd_status loss_bwd(void* dx, void* dweight, const float* dloss, int64_t dloss
         e.vocab = static_cast<int>(width);
         e.top = f.top;
         e.col0 = static_cast<int>(col0);
-        e.scale = logit_scale(c.hidden, c.inv_temperature());
-        DRADD_TRY(run_product<SlopeProduct>(plan_of(r, width, h, group_for(r)), {x->data, r, h, x->stride, false},
-                                            {w0, width, h, weight->stride, false}, e, true, dtype, stream));
+        e.scale = logit_scale(g.z, c.hidden, c.inv_temperature());
+        const Side sx = {x->data, r, h, x->stride, false}, sw = {w0, width, h, weight->stride, false};
+        if (g.z.splits == 1) {
+            DRADD_TRY(run_product<SlopeProduct>(plan_of(r, width, h, g.z.group), sx, sw, e, true, dtype, stream));
+        } else {
+            DRADD_TRY(run_logits(g.z, sx, sw, s.logits, true, dtype, stream));
+            DRADD_TRY(from_cuda(launch_slope({s.logits, g.z.splits, up(width, 8)}, e, s.dz, g.piece,
+                                             dtype == DRADD_BF16, stream)));
+        }
         GradProduct px = {}, pw = {};
         const bool last = i + 1 == g.pieces;
         px.on = dx != nullptr;
@@ -959,11 +992,14 @@ dradd_status linear_act_add_bwd(void* dx, void* dweight, void* dbias, const drad
         dz_stride = cols;
     }
     if (dbias) {
+        const bool once = !g.sums && g.chunks == 1;
         if (!g.sums)
             DRADD_TRY(from_cuda(launch_row_sums(dz, dz_stride, static_cast<int>(rows), static_cast<int>(cols),
-                                                dtype == DRADD_BF16, g.chunks, partial_db, stream)));
-        DRADD_TRY(from_cuda(
-            launch_bias(partial_db, g.chunks, static_cast<int>(cols), dbias, dtype == DRADD_BF16, stream)));
+                                                dtype == DRADD_BF16, g.chunks, partial_db, once ? dbias : nullptr,
+                                                stream)));
+        if (!once)
+            DRADD_TRY(from_cuda(
+                launch_bias(partial_db, g.chunks, static_cast<int>(cols), dbias, dtype == DRADD_BF16, stream)));
     }
     GradProduct px = {}, pw = {};
     px.on = dx != nullptr;

@@ -168,13 +168,23 @@ struct FewParams {
 constexpr int kFewRows = 16;
 cudaError_t launch_few(const FewParams& p, cudaStream_t stream);
 
+// What the epilogues of logits do, from partial sums [splits, rows, pitch].
+struct LogitParts {
+    const float* partials;
+    int splits;
+    int64_t pitch;           // a multiple of 8
+};
+cudaError_t launch_stats(const LogitParts& l, const StatsParams& p, cudaStream_t stream);
+cudaError_t launch_slope(const LogitParts& l, const SlopeParams& p, void* out, int64_t stride, int bf16,
+                         cudaStream_t stream);
+
 // Column sums of fp32 [parts, cols], rounded.
 cudaError_t launch_bias(const float* partials, int parts, int cols, void* out, int bf16, cudaStream_t stream);
 
 // Sums of a 16-bit matrix's columns over `chunks` parts of its rows, fp32
-// [chunks, cols].
+// [chunks, cols]; with `out` (and one chunk) rounded to it.
 cudaError_t launch_row_sums(const void* x, int64_t stride, int rows, int cols, int bf16, int chunks, float* partials,
-                            cudaStream_t stream);
+                            void* out, cudaStream_t stream);
 
 // A teacher's entries in rising order of their words.
 struct TeacherParams {
@@ -183,7 +193,8 @@ struct TeacherParams {
     int logits_type;         // DRADD_*
     int* entries;            // [rows, top]
     float* shares;           // [rows, top]
-    float* entropy;          // [rows] sum of share log share, or NULL
+    float2* entropy;         // [rows] sum of e d / sum of e, and sum of e, with d = logit - the highest and e = exp(d);
+                             // or NULL
     uint16_t* first;         // [rows, parts]
     int rows, top, vocab, parts;
     float inv_temperature;
@@ -199,9 +210,9 @@ struct LossParams {
     const int64_t* target;   // cross entropy
     int64_t ignore_index;
     const int* entries;      // distillation
-    const float* entropy;
+    const float2* entropy;
     int rows, vocab, top, parts;
-    float logit_factor;      // of a picked logit
+    float scale;             // log2(e) / temperature, as in StatsParams
 };
 cudaError_t launch_loss(const LossParams& p, cudaStream_t stream);
 

@@ -114,7 +114,7 @@ cudaError_t launch_finish(const FinishParams& p, cudaStream_t stream)
 // -------------------------------------------------------------- column sums
 // A CTA takes 256 columns and one part of the rows, a warp every eighth row.
 __global__ void __launch_bounds__(256) row_sums_kernel(const uint16_t* x, int64_t stride, int rows, int cols, int bf16,
-                                                       int each, float* partials)
+                                                       int each, float* partials, uint16_t* out)
 {
     __shared__ float sums[8][256];
     wait_prior_grids();
@@ -150,12 +150,15 @@ __global__ void __launch_bounds__(256) row_sums_kernel(const uint16_t* x, int64_
 #pragma unroll
         for (int w = 0; w < 8; ++w)
             t += sums[w][threadIdx.x];
-        partials[static_cast<int64_t>(blockIdx.y) * cols + c] = t;
+        if (out)
+            out[c] = bf16 ? Elem<kElemBf16>::narrow(t) : Elem<kElemF16>::narrow(t);
+        else
+            partials[static_cast<int64_t>(blockIdx.y) * cols + c] = t;
     }
 }
 
 cudaError_t launch_row_sums(const void* x, int64_t stride, int rows, int cols, int bf16, int chunks, float* partials,
-                            cudaStream_t stream)
+                            void* out, cudaStream_t stream)
 {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -167,7 +170,7 @@ cudaError_t launch_row_sums(const void* x, int64_t stride, int rows, int cols, i
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, row_sums_kernel, static_cast<const uint16_t*>(x), stride, rows, cols, bf16,
-                              (rows + chunks - 1) / chunks, partials);
+                              (rows + chunks - 1) / chunks, partials, static_cast<uint16_t*>(out));
 }
 
 // A CTA takes 32 columns, a lane each; its warps every 32nd part.
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(kTeacherThreads) teacher_kernel(const TeacherP
         p.shares[row * p.top + i] = share;
     }
     if (p.entropy && tid == 0)
-        p.entropy[row] = nan_row ? nan : counted ? weighted / sum - logf(sum) : 0.0f;
+        p.entropy[row] = nan_row ? make_float2(nan, 1.0f) : make_float2(counted ? weighted / sum : 0.0f, sum);
     // the first entry at or behind each part's first column
     for (int g = tid; g < p.parts; g += kTeacherThreads) {
         int at = 0;
@@ -343,6 +346,130 @@ cudaError_t launch_teacher(const TeacherParams& p, cudaStream_t stream)
     while (size < p.top)
         size *= 2;
     return launch(teacher_kernel, p.rows, kTeacherThreads, static_cast<size_t>(size) * 12, false, stream, p, size);
+}
+
+// --------------------------------------------- logits from partial sums
+// A warp takes a row's part of 128 columns, a lane four neighbours.
+template <bool GRAD, class P>
+__global__ void __launch_bounds__(256) logits_kernel(const LogitParts l, const P p, uint16_t* out, int64_t stride,
+                                                     int bf16)
+{
+    wait_prior_grids();
+    allow_next_grid();
+    const int lane = threadIdx.x & 31, part = blockIdx.x;
+    const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (row >= p.rows)
+        return;
+    const int col = part * kHalfCols + lane * 4;
+    const int n = p.vocab - col;  // of the lane's columns
+    float v[4] = {};
+    if (n > 0) {
+        const float* from = l.partials + row * l.pitch + col;
+        for (int s = 0; s < l.splits; ++s) {
+            const float4 f = *reinterpret_cast<const float4*>(from + s * (l.pitch * p.rows));
+            v[0] += f.x;
+            v[1] += f.y;
+            v[2] += f.z;
+            v[3] += f.w;
+        }
+    }
+    const int* entry = p.entries + static_cast<int64_t>(row) * p.top;
+    const float* share = p.shares + static_cast<int64_t>(row) * p.top;
+    const int first = p.top ? p.first[static_cast<int64_t>(row) * p.parts + part] : 0;
+    if constexpr (!GRAD) {
+        const auto value = [&](int at) {  // of a column of the part, in every lane
+            const float x = (at & 3) == 0 ? v[0] : (at & 3) == 1 ? v[1] : (at & 3) == 2 ? v[2] : v[3];
+            return __shfl_sync(0xffffffffu, x, at >> 2);
+        };
+        float picked = 0.0f;
+        if (p.top == 0) {
+            const int64_t at = p.target[row] - part * kHalfCols;
+            if (at >= 0 && at < kHalfCols) {
+                picked = value(static_cast<int>(at));
+                if (lane == 0)
+                    p.picked[row] = picked;
+            }
+        } else {
+            for (int i = first; i < p.top; ++i) {
+                const int at = entry[i] - part * kHalfCols;
+                if (at >= kHalfCols)
+                    break;
+                picked = fmaf(share[i], value(at), picked);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = j < n ? v[j] : -INFINITY;
+        const float high = warp_max(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]))) * p.scale;
+        const float shift = high == -INFINITY ? 0.0f : high;
+        float s[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            s[j] = exp2_fast(fmaf(v[j], p.scale, -shift));
+        const float sum = butterfly_sum((s[0] + s[1]) + (s[2] + s[3]), 32);
+        if (lane == 0) {
+            const int64_t at = static_cast<int64_t>(part) * p.rows + row;
+            p.part[at] = make_float2(high, sum);
+            if (p.top != 0)
+                p.picked[at] = picked;
+        }
+    } else {
+        const float lse2 = p.lse[row] * kLog2e;
+        const float2 coef = p.coef[row];
+        const bool live = coef.x != 0.0f || coef.y != 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = coef.x * exp2_fast(fmaf(v[j], p.scale, -lse2));
+        const auto take = [&](int64_t at, float less) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = at == lane * 4 + j ? v[j] - less : v[j];
+        };
+        if (p.top == 0) {
+            take(p.target[row] - part * kHalfCols, coef.y);
+        } else {
+            for (int i = first; i < p.top; ++i) {
+                const int at = entry[i] - part * kHalfCols;
+                if (at >= kHalfCols)
+                    break;
+                take(at, coef.y * share[i]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = live && j < n ? v[j] : 0.0f;
+        *reinterpret_cast<uint2*>(out + row * stride + col) =
+            bf16 ? make_uint2(pack_rne(v[0], v[1]), pack_rne(v[2], v[3]))
+                 : make_uint2(Elem<kElemF16>::pack2(v[0], v[1]), Elem<kElemF16>::pack2(v[2], v[3]));
+    }
+}
+
+template <bool GRAD, class P>
+cudaError_t launch_logits(const LogitParts& l, const P& p, uint16_t* out, int64_t stride, int bf16, int parts,
+                          cudaStream_t stream)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(parts), static_cast<unsigned>((p.rows + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, logits_kernel<GRAD, P>, l, p, out, stride, bf16);
+}
+
+cudaError_t launch_stats(const LogitParts& l, const StatsParams& p, cudaStream_t stream)
+{
+    return launch_logits<false>(l, p, nullptr, 0, 0, p.parts, stream);
+}
+
+cudaError_t launch_slope(const LogitParts& l, const SlopeParams& p, void* out, int64_t stride, int bf16,
+                         cudaStream_t stream)
+{
+    return launch_logits<true>(l, p, static_cast<uint16_t*>(out), stride, bf16, (p.vocab + kHalfCols - 1) / kHalfCols,
+                               stream);
 }
 
 // --------------------------------------------------------- joined statistics
@@ -394,18 +521,20 @@ __global__ void __launch_bounds__(1024) loss_kernel(const LossParams p)
         sum += sums[w][lane] * exp2_fast(highs[w][lane] - shift);
         picked += picks[w][lane];
     }
-    const float lse = (high + log2f(sum)) * kLn2;
-    p.lse[row] = lse;
-    if (teacher) {
-        const bool counted = p.entries[row * p.top] != INT_MAX;
-        p.loss[row] = counted ? p.entropy[row] + (lse - picked * p.logit_factor) : 0.0f;
-    } else {
+    p.lse[row] = (high + log2f(sum)) * kLn2;
+    // A loss may be a small difference of large numbers: the highest logit
+    // and the picked one are subtracted from one another, the product's
+    // rounding with them, before anything else is added; and one logarithm
+    // stands for the student's and the teacher's.
+    const bool counted = teacher ? p.entries[row * p.top] != INT_MAX : p.target[row] != p.ignore_index;
+    if (!teacher && counted) {
         const int64_t target = p.target[row];
-        const bool word = target >= 0 && target < p.vocab;
-        p.loss[row] = target == p.ignore_index ? 0.0f
-                      : word                   ? lse - p.picked[row] * p.logit_factor
-                                               : __int_as_float(0x7FC00000);
+        picked = target >= 0 && target < p.vocab ? p.picked[row] : __int_as_float(0x7FC00000);
     }
+    const float at = picked * p.scale, off = fmaf(picked, p.scale, -at);
+    const float2 h = teacher ? p.entropy[row] : make_float2(0.0f, 1.0f);
+    const float loss = h.x + kLn2 * ((high - at) + (log2f(sum / h.y) - off));
+    p.loss[row] = counted ? loss : 0.0f;
 }
 
 cudaError_t launch_loss(const LossParams& p, cudaStream_t stream)
