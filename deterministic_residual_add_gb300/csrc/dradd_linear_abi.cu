@@ -451,7 +451,14 @@ Plan forward_plan(int64_t rows, int64_t inner, int64_t cols)
     return p;
 }
 
-bool few(int64_t rows) { return rows <= kFewRows; }
+// Whether the few rows' own kernel takes a product.  Its copies of 2 KB (from
+// 9 rows on 1 KB) cost more than the tiles' 32 KB where there are many:
+// 4096 -> 4096, 1 and 16 rows, 10.7 and 11.0 us against 13.1; 5120 -> 8192
+// 18.1 and 26.2 against 19.9; 11520 -> 11928 50.8 and 84.4 against 47.7.
+bool few(int64_t rows, int64_t inner, int64_t cols)
+{
+    return rows <= 8 ? inner * cols <= 1 << 25 : rows <= kFewRows && inner * cols <= 1 << 24;
+}
 
 dradd_status linear_shape(int64_t rows, int64_t inner, int64_t cols)
 {
@@ -896,7 +903,7 @@ extern "C" {
 
 size_t linear_act_add_fwd_workspace_bytes(int64_t rows, int64_t inner, int64_t cols)
 {
-    if (rows <= 0 || linear_shape(rows, inner, cols) != DRADD_OK || few(rows))
+    if (rows <= 0 || linear_shape(rows, inner, cols) != DRADD_OK || few(rows, inner, cols))
         return 0;
     return static_cast<size_t>(partial_bytes(forward_plan(rows, inner, cols), rows, cols));
 }
@@ -921,11 +928,11 @@ dradd_status linear_act_add_fwd(const dradd_matrix* out, const dradd_matrix* x, 
     if (has_residual)
         k.matrix(residual, rows, cols, false, true);
     const Plan p = forward_plan(rows, inner, cols);
-    k.workspace(workspace, workspace_bytes, few(rows) ? 0 : partial_bytes(p, rows, cols));
+    k.workspace(workspace, workspace_bytes, few(rows, inner, cols) ? 0 : partial_bytes(p, rows, cols));
     DRADD_TRY(k.done());
     const ActParams a = act_params(out->data, out->stride, bias, has_residual ? residual->data : nullptr,
                                    has_residual ? residual->stride : 0, rows, cols, act);
-    if (few(rows)) {
+    if (few(rows, inner, cols)) {
         FewParams f = {x->data, x->stride, weight->data, weight->stride, static_cast<int>(inner), a,
                        dtype == DRADD_BF16, nullptr, kDefaultWaitLimitNs};
         DRADD_TRY(from_cuda(device_status_ptr(&f.status)));
