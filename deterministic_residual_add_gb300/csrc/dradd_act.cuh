@@ -94,11 +94,10 @@ __device__ __forceinline__ float act_slope(float z)
         const float f = logistic(2.0f * kGeluC * fmaf(kGeluA * z * z, z, z));
         const float w = f * (1.0f - f);
         return w == 0.0f ? f : fmaf(z * w, 2.0f * kGeluC * fmaf(3.0f * kGeluA * z, z, 1.0f), f);
-    } else if constexpr (ACT == DRADD_ACT_SILU) {
+    } else {
+        static_assert(ACT == DRADD_ACT_SILU);
         const float f = logistic(z), w = f * (1.0f - f);
         return w == 0.0f ? f : fmaf(z, w, f);
-    } else {
-        return 1.0f;
     }
 }
 
@@ -131,7 +130,7 @@ __device__ __forceinline__ void act_values(float (&z)[N], int act)
     }
 }
 
-// z = act'(z).
+// z = act'(z); not for DRADD_ACT_NONE, whose dz is the gradient that comes in.
 template <int N>
 __device__ __forceinline__ void act_slopes(float (&z)[N], int act)
 {
@@ -139,8 +138,7 @@ __device__ __forceinline__ void act_slopes(float (&z)[N], int act)
     case DRADD_ACT_RELU: act_slopes<DRADD_ACT_RELU>(z); break;
     case DRADD_ACT_GELU: act_slopes<DRADD_ACT_GELU>(z); break;
     case DRADD_ACT_GELU_TANH: act_slopes<DRADD_ACT_GELU_TANH>(z); break;
-    case DRADD_ACT_SILU: act_slopes<DRADD_ACT_SILU>(z); break;
-    default: act_slopes<DRADD_ACT_NONE>(z); break;
+    default: act_slopes<DRADD_ACT_SILU>(z); break;
     }
 }
 

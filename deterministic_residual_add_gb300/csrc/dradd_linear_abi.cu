@@ -44,7 +44,8 @@ namespace {
 
 constexpr int64_t kMaxInner = 1 << 24;
 constexpr int64_t kMaxVocab = 1 << 30;
-constexpr int64_t kMaxRows = 0x7FFFFFFF;
+constexpr int64_t kMaxRows = 0x7FFFFFFF - 4095;  // a last tile's rows are still counted in 32 bits
+constexpr int64_t kMaxTiles = 1 << 30;
 constexpr int64_t kMaxTop = 1024;
 // What plans count on, whatever device the call runs on: they decide the
 // order of sums.
@@ -467,9 +468,9 @@ dradd_status linear_shape(int64_t rows, int64_t inner, int64_t cols)
     DRADD_TRY(inner_ok(inner));
     DRADD_TRY(inner_ok(cols));
     // tiles of every product below are counted in 32 bits
-    return parts_of(rows, kTileRows) * parts_of(inner > cols ? inner : cols, kTileCols) * kMostSplits > kMaxRows
-               ? DRADD_ERR_BAD_SHAPE
-               : DRADD_OK;
+    const int64_t most = parts_of(inner > cols ? inner : cols, kTileCols);
+    return parts_of(rows > cols ? rows : cols, kTileRows) * most * kMostSplits > kMaxTiles ? DRADD_ERR_BAD_SHAPE
+                                                                                          : DRADD_OK;
 }
 
 struct LinearGradPlan {
@@ -524,7 +525,7 @@ dradd_status run_linear(const Plan& p, const dradd_matrix& x, const dradd_matrix
         return grad ? run_product<ActGradProduct>(p, a, b, e, false, dtype, stream)
                     : run_product<ActProduct>(p, a, b, e, false, dtype, stream);
     }
-    const SplitParams s = {partials, act.rows, act.cols, 0};
+    const SplitParams s = {partials, act.rows, act.cols};
     DRADD_TRY(run_product<SplitProduct>(p, a, b, s, false, dtype, stream));
     FinishParams f = {partials, p.splits, nullptr, act, grad, dtype == DRADD_BF16};
     return from_cuda(launch_finish(f, stream));
@@ -559,7 +560,7 @@ dradd_status loss_shape(const LossCall& c, int dtype)
     DRADD_TRY(inner_ok(c.hidden));
     const int64_t tr = parts_of(c.rows, kTileRows), tv = parts_of(c.vocab, kTileRows),
                   th = parts_of(c.hidden, kTileCols);
-    if (tr * parts_of(c.vocab, kTileCols) > kMaxRows || (tr + tv) * th * kMostSplits > kMaxRows)
+    if (tr * parts_of(c.vocab, kTileCols) > kMaxTiles || (tr + tv) * th * kMostSplits > kMaxTiles)
         return DRADD_ERR_BAD_SHAPE;
     return DRADD_OK;
 }
@@ -658,7 +659,7 @@ float logit_scale(const Plan& p, int64_t hidden, float inv_temperature)
 dradd_status run_logits(const Plan& p, const Side& x, const Side& w, float* partials, bool early, int dtype,
                         cudaStream_t stream)
 {
-    const SplitParams e = {partials, static_cast<int>(x.rows), static_cast<int>(up(w.rows, 8)), 0};
+    const SplitParams e = {partials, static_cast<int>(x.rows), static_cast<int>(up(w.rows, 8))};
     return run_product<SplitProduct>(p, x, w, e, early, dtype, stream);
 }
 

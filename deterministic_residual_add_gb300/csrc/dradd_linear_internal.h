@@ -56,7 +56,6 @@ struct ProductShape {
 struct SplitParams {
     float* partials;
     int rows, cols;
-    int add;  // to what is there
 };
 
 // out = residual + act(z + bias), or dz = dout * act'(z + bias)

@@ -10,14 +10,6 @@
 
 namespace dradd {
 
-// One lane of a converged warp, the same one for every call.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
 // ------------------------------------------------------------ tensor memory
 template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t columns)

@@ -15,7 +15,10 @@
  *   - dtype: DRADD_BF16 or DRADD_F16, the type of every tensor declared
  *     void*.  Products are summed in fp32; each stored element is rounded
  *     once.  The gradients pass through dz, the gradient of the product's
- *     output, which is rounded to dtype before it is multiplied again.
+ *     output, which is rounded to dtype before it is multiplied again (the
+ *     losses' in fp16 at a power of two that puts the largest factor of a
+ *     row between 2^13 and 2^14).  Calls whose tiles (128 x 256) would be
+ *     more than 2^30 are DRADD_ERR_BAD_SHAPE.
  *   - Tensors are device memory, 16-byte aligned; rows have unit column
  *     stride and a row stride that is a multiple of 8 elements.  Inner
  *     dimensions (and the columns of linear_act_add) are multiples of 8.
@@ -56,7 +59,7 @@ typedef struct dradd_matrix {
  *   weight    [cols, inner]
  *   bias      [cols] or NULL
  *   residual  [rows, cols], its data NULL or the pointer NULL: none
- *   rows < 2^31, 8 <= inner, cols < 2^24, both multiples of 8
+ *   rows <= 2^31 - 4096, 8 <= inner, cols < 2^24, both multiples of 8
  * Workspace: linear_act_add_fwd_workspace_bytes (may be 0).
  */
 dradd_status linear_act_add_fwd(const dradd_matrix* out, const dradd_matrix* x, const dradd_matrix* weight,
@@ -89,7 +92,7 @@ size_t linear_act_add_bwd_workspace_bytes(int64_t rows, int64_t inner, int64_t c
  *             NaN where it is neither that nor a word
  * both fp32 [rows]; target int64 [rows].  Logits that are not finite make
  * their own row's results infinite or NaN.
- *   rows < 2^31, 8 <= hidden < 2^24 a multiple of 8, 1 <= vocab <= 2^30
+ *   rows <= 2^31 - 4096, 8 <= hidden < 2^24 a multiple of 8, 1 <= vocab <= 2^30
  */
 dradd_status linear_cross_entropy_fwd(float* loss, float* lse, const dradd_matrix* x, const dradd_matrix* weight,
                                       const int64_t* target, int64_t ignore_index, int64_t rows, int64_t hidden,

@@ -68,7 +68,7 @@ def check_linear(x, w, b, r, dout, act):
     (1, 8, 8, "none"), (1, 4096, 1024, "silu"), (2, 72, 24, "gelu"), (8, 264, 1000, "gelu_tanh"),
     (9, 1000, 264, "relu"), (16, 520, 136, "none"), (17, 64, 256, "silu"), (64, 4096, 264, "gelu"),
     (127, 72, 520, "relu"), (128, 128, 128, "none"), (129, 136, 248, "gelu_tanh"), (255, 64, 8, "silu"),
-    (5, 8192, 4104, "none"), (12, 4096, 4104, "silu"), (257, 2048, 264, "none"), (300, 520, 1032, "gelu"), (1000, 256, 512, "silu"), (1536, 1024, 776, "gelu_tanh")])
+    (5, 8192, 4104, "none"), (12, 4096, 4104, "silu"), (40, 2048, 20008, "silu"), (257, 2048, 264, "none"), (300, 520, 1032, "gelu"), (1000, 256, 512, "silu"), (1536, 1024, 776, "gelu_tanh")])
 def test_linear(rows, inner, cols, act, dtype):
     check_linear(*linear_case(rows, inner, cols, dtype), act)
 
@@ -224,7 +224,7 @@ def check_ce(x, w, target, ignore_index=-100):
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("rows,hidden,vocab", [
     (1, 8, 1), (1, 64, 1001), (2, 136, 2), (33, 264, 127), (64, 4096, 255), (100, 512, 3001), (128, 64, 256),
-    (129, 72, 257), (257, 1024, 1000), (511, 256, 5001), (1024, 128, 8000)])
+    (20, 2056, 20001), (129, 72, 257), (257, 1024, 1000), (511, 256, 5001), (1024, 128, 8000)])
 def test_cross_entropy(rows, hidden, vocab, dtype):
     check_ce(*loss_case(rows, hidden, vocab, dtype))
 
