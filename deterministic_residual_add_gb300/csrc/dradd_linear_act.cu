@@ -7,6 +7,11 @@ namespace dradd {
 
 // out = residual + act(z + bias).  The residual comes into the box that the
 // results leave from, its first one while the products run.
+//
+// Bound by the products where the inner dimension is long (8192 x 16384 by
+// 4096 656 to 680 us, 1620 to 1680 TFLOP/s under the power limit); below some
+// 1000 by these steps (8192 x 512 by 8192 51 us plain, 57 with a bias, 66
+// with silu, 93 with gelu; what has to move takes 23).
 template <bool DEEP>
 struct EpiAct {
     using Kind = ActProduct;
@@ -87,7 +92,9 @@ struct EpiAct {
     __device__ __forceinline__ void end() {}
 };
 
-// dz = dout * act'(z + bias), and its sums over 32 rows for the bias.
+// dz = dout * act'(z + bias), and its sums over 32 rows for the bias, from
+// the values before they are rounded.  (A pass of its own over dz for the
+// bias took 45 us for 8192 x 16384.)
 template <bool DEEP>
 struct EpiActGrad : EpiAct<DEEP> {
     using Kind = ActGradProduct;

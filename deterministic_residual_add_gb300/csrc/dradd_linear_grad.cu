@@ -29,6 +29,17 @@ __device__ __forceinline__ void store_partials(float* p, const uint32_t (&w)[16]
         }
 }
 
+// A gradient's tile: rounded, or added to the fp32 sums of earlier pieces of
+// the vocabulary, or a split's partial sum.  dx = dz W and dweight = dz^T x
+// run in one launch, the longer tiles first, so that the shorter ones fill
+// what the last round of the longer leaves idle (4096 tokens, a piece of 32768
+// words: 3522 steps of the busiest pair for 3449 on average).  The operands
+// whose rows lie along the summed dimension are read as they are: the
+// products take either order from shared memory.
+//
+// Bound by the products, under the power limit 1630 to 1690 TFLOP/s (90 % of
+// the cycles with the tensor pipe active at 16384 words); by the stores of
+// dweight where there are few rows.
 struct EpiGrad {
     using Kind = GradProducts;
     using Params = GradParams;
