@@ -10,8 +10,8 @@ namespace dradd {
 //
 // Bound by the products where the inner dimension is long (8192 x 16384 by
 // 4096 656 to 680 us, 1620 to 1680 TFLOP/s under the power limit); below some
-// 1000 by these steps (8192 x 512 by 8192 51 us plain, 57 with a bias, 66
-// with silu, 93 with gelu; what has to move takes 23).
+// 1000 by these steps (8192 x 512 by 8192 51 us plain, 59 with a bias, 66
+// with silu, 86 with gelu; what has to move takes 23).
 template <bool DEEP>
 struct EpiAct {
     using Kind = ActProduct;
@@ -109,7 +109,7 @@ struct EpiActGrad : EpiAct<DEEP> {
         float v[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-            v[j] = row < p.rows ? z[j] : 0.0f;
+            v[j] = z[j];  // rows outside have a dout of zeros, and so no dz but where the column's is NaN anyway
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int d = 8; d > 0; d >>= 1)
