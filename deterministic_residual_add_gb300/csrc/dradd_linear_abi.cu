@@ -580,8 +580,7 @@ void loss_inputs(Checks* k, const LossCall& c, const dradd_matrix* x, const drad
 
 // The workspace of a teacher's entries.
 struct TeacherSpace {
-    int* entries;
-    float* shares;
+    Entry* entries;
     float2* entropy;
     uint16_t* first;
     int parts;
@@ -589,8 +588,7 @@ struct TeacherSpace {
     TeacherSpace(Carver* w, int64_t rows, int64_t vocab, int64_t top, bool with_entropy)
     {
         parts = static_cast<int>(2 * parts_of(vocab, kTileCols));
-        entries = w->take<int>(rows * top * 4);
-        shares = w->take<float>(rows * top * 4);
+        entries = w->take<Entry>(rows * top * 8);
         entropy = w->take<float2>(top && with_entropy ? rows * 8 : 0);
         first = w->take<uint16_t>(top ? rows * parts * 2 : 0);
     }
@@ -601,7 +599,6 @@ struct TeacherSpace {
         p.logits = c.teacher->logits;
         p.logits_type = c.teacher->logits_dtype;
         p.entries = entries;
-        p.shares = shares;
         p.entropy = entropy;
         p.first = first;
         p.rows = static_cast<int>(c.rows);
@@ -694,7 +691,6 @@ dradd_status loss_fwd(float* loss, float* lse, const dradd_matrix* x, const drad
     e.picked = s.picked;
     e.target = c.target;
     e.entries = s.teacher.entries;
-    e.shares = s.teacher.shares;
     e.first = s.teacher.first;
     e.parts = s.teacher.parts;
     e.rows = static_cast<int>(c.rows);
@@ -837,7 +833,6 @@ dradd_status loss_bwd(void* dx, void* dweight, const float* dloss, int64_t dloss
         e.coef = s.coef;
         e.target = c.target;
         e.entries = s.teacher.entries;
-        e.shares = s.teacher.shares;
         e.first = s.teacher.first;
         e.parts = s.teacher.parts;
         e.rows = f.rows;

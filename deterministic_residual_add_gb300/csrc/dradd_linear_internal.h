@@ -75,13 +75,18 @@ struct ActProductParams {
     CUtensorMap out_map, other_map;  // 32 rows of 64 columns
 };
 
+// One of a teacher's words in a row and its share.
+struct alignas(8) Entry {
+    int word;
+    float share;
+};
+
 // Statistics of the logits' rows, a part of 128 columns at a time.
 struct StatsParams {
     float2* part;            // [parts, rows]: maximum and sum of 2^(z scale - maximum), in base-2 units
     float* picked;           // cross entropy: [rows], the target's logit; distillation: [parts, rows] sums of share * logit
     const int64_t* target;   // cross entropy
-    const int* entries;      // distillation: [rows, top] words in rising order, INT_MAX behind the last
-    const float* shares;     // [rows, top]
+    const Entry* entries;    // distillation: [rows, top] words in rising order, INT_MAX behind the last
     const uint16_t* first;   // [rows, parts] the first entry at or behind a part's first column
     int parts;
     int rows, vocab, top;
@@ -93,8 +98,7 @@ struct SlopeParams {
     const float* lse;        // [rows]
     const float2* coef;      // [rows]
     const int64_t* target;
-    const int* entries;
-    const float* shares;
+    const Entry* entries;
     const uint16_t* first;
     int parts;
     int rows, vocab, top;    // vocab: the piece's words
@@ -190,8 +194,7 @@ struct TeacherParams {
     const int64_t* index;    // [rows, top]
     const void* logits;      // [rows, top]
     int logits_type;         // DRADD_*
-    int* entries;            // [rows, top]
-    float* shares;           // [rows, top]
+    Entry* entries;          // [rows, top]
     float2* entropy;         // [rows] sum of e d / sum of e, and sum of e, with d = logit - the highest and e = exp(d);
                              // or NULL
     uint16_t* first;         // [rows, parts]
@@ -208,7 +211,7 @@ struct LossParams {
     const float* picked;
     const int64_t* target;   // cross entropy
     int64_t ignore_index;
-    const int* entries;      // distillation
+    const Entry* entries;    // distillation
     const float2* entropy;
     int rows, vocab, top, parts;
     float scale;             // log2(e) / temperature, as in StatsParams
@@ -223,7 +226,7 @@ struct CoefParams {
     int64_t dlse_stride;
     const int64_t* target;
     int64_t ignore_index;
-    const int* entries;
+    const Entry* entries;
     const void* x;
     int64_t x_stride;
     void* x_live;            // [rows, inner], or NULL

@@ -6,12 +6,11 @@
 namespace dradd {
 
 // The words of a row that count in a part of 128 columns: a target, or the
-// entries of a teacher in rising order.
+// entries of a teacher in rising order, the one after the next on its way.
 struct Words {
-    const int* entry = nullptr;
-    const float* share = nullptr;
-    int left = 0;
-    int next = -1;       // the next word's column in the part; kHalfCols: none
+    const Entry* entry = nullptr;  // the next one
+    int left = 0;                  // from it on
+    int next = kHalfCols;          // its column in the part; kHalfCols or more: not in it
     float weight = 1.0f;
 
     __device__ __forceinline__ void target(int64_t word, int64_t col)
@@ -19,37 +18,35 @@ struct Words {
         const int64_t at = word - col;
         next = at >= 0 && at < kHalfCols ? static_cast<int>(at) : kHalfCols;
     }
-    __device__ __forceinline__ void teacher(const int* e, const float* s, int first, int top, int64_t col)
+    __device__ __forceinline__ void teacher(const Entry* e, int first, int top, int64_t col)
     {
         entry = e + first;
-        share = s + first;
         left = top - first;
-        base = col;
-        fetch();
+        base = static_cast<int>(col);
+        if (left > 0)
+            ahead = entry[0];
+        take();
     }
     __device__ __forceinline__ void advance()
     {
-        if (left > 0) {
-            ++entry;
-            ++share;
-            --left;
-            fetch();
-        } else {
-            next = kHalfCols;
-        }
+        ++entry;
+        --left;
+        take();
     }
 
 private:
-    int64_t base = 0;
-    __device__ __forceinline__ void fetch()
+    int base = 0;
+    Entry ahead;
+    // Entries are not below the part's first column, and INT_MAX less that is
+    // behind the part's last.
+    __device__ __forceinline__ void take()
     {
         next = kHalfCols;
         if (left > 0) {
-            const int64_t at = *entry - base;
-            if (at < kHalfCols) {  // entries are not below the part's first column
-                next = static_cast<int>(at);
-                weight = *share;
-            }
+            next = ahead.word - base;
+            weight = ahead.share;
+            if (left > 1)
+                ahead = entry[1];
         }
     }
 };
@@ -79,13 +76,11 @@ struct EpiStats {
     __device__ __forceinline__ EpiStats(const Params& p_, int, int row_, int col_, int, Staging&)
         : p(p_), row(row_), col(col_), part(col_ / kHalfCols)
     {
-        words.next = kHalfCols;
         if (row < p.rows) {
             if (p.top == 0)
                 words.target(p.target[row], col);
             else
                 words.teacher(p.entries + static_cast<int64_t>(row) * p.top,
-                              p.shares + static_cast<int64_t>(row) * p.top,
                               p.first[static_cast<int64_t>(row) * p.parts + part], p.top, col);
         }
     }
@@ -164,7 +159,6 @@ struct EpiSlope {
     __device__ __forceinline__ EpiSlope(const Params& p_, int bf16_, int row_, int col_, int, Staging& staging_)
         : p(p_), bf16(bf16_), row(row_), col(col_), staging(staging_)
     {
-        words.next = kHalfCols;
         if (row < p.rows) {
             lse2 = p.lse[row] * kLog2e;
             coef = p.coef[row];
@@ -174,7 +168,6 @@ struct EpiSlope {
                 words.target(p.target[row], at);
             else
                 words.teacher(p.entries + static_cast<int64_t>(row) * p.top,
-                              p.shares + static_cast<int64_t>(row) * p.top,
                               p.first[static_cast<int64_t>(row) * p.parts + at / kHalfCols], p.top, at);
         }
     }

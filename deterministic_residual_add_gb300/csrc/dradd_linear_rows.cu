@@ -209,9 +209,11 @@ cudaError_t launch_bias(const float* partials, int parts, int cols, void* out, i
 }
 
 // ------------------------------------------------------------------ teacher
-// A CTA sorts one row's entries by (word, place) in shared memory, computes
-// their shares and where each part of 128 columns begins.
-constexpr int kTeacherThreads = 128;
+// A CTA puts one row's entries into the order of (word, place), computes
+// their shares and where each part of 128 columns begins.  An entry's place is
+// the number of those before it, counted against the words in shared memory,
+// four to a load.
+constexpr int kTeacherMost = 256;  // threads
 
 __device__ __forceinline__ float teacher_logit(const TeacherParams& p, int64_t at)
 {
@@ -221,22 +223,27 @@ __device__ __forceinline__ float teacher_logit(const TeacherParams& p, int64_t a
     return p.logits_type == kElemBf16 ? Elem<kElemBf16>::widen(v) : Elem<kElemF16>::widen(v);
 }
 
-__global__ void __launch_bounds__(kTeacherThreads) teacher_kernel(const TeacherParams p, int size)
+// size: top rounded up to fours.
+__global__ void __launch_bounds__(kTeacherMost) teacher_kernel(const TeacherParams p, int size)
 {
-    extern __shared__ unsigned long long keys[];  // size of them, then as many logits
-    __shared__ float red[4];
-    __shared__ int bad;
+    extern __shared__ __align__(16) uint32_t words[];  // size, then the logits, the ordered words and their shares
+    __shared__ float red[3][kTeacherMost / 32];
+    __shared__ int bad, counted_entries;
     wait_prior_grids();
     allow_next_grid();
-    float* logits = reinterpret_cast<float*>(keys + size);
+    constexpr uint32_t kNone = 0xFFFFFFFFu;
+    float* logits = reinterpret_cast<float*>(words + size);
+    uint32_t* ordered = words + 2 * size;
+    float* shares = reinterpret_cast<float*>(words + 3 * size);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int threads = blockDim.x, warps = threads >> 5;
     const int64_t row = blockIdx.x;
     if (tid == 0)
-        bad = 0;
+        bad = counted_entries = 0;
     __syncthreads();
     float high = -INFINITY;
-    for (int i = tid; i < size; i += kTeacherThreads) {
-        unsigned long long key = ~0ull;
+    for (int i = tid; i < size; i += threads) {
+        uint32_t key = kNone;
         float v = -INFINITY;
         if (i < p.top) {
             const int64_t word = p.index[row * p.top + i];
@@ -244,97 +251,93 @@ __global__ void __launch_bounds__(kTeacherThreads) teacher_kernel(const TeacherP
                 bad = 1;
             if (word >= 0 && word < p.vocab) {
                 v = teacher_logit(p, row * p.top + i) * p.inv_temperature;
-                key = (static_cast<unsigned long long>(word) << 32) | static_cast<unsigned>(i);
+                key = static_cast<uint32_t>(word);
                 high = v > high || v != v ? v : high;  // a NaN stays
             }
         }
-        keys[i] = key;
+        words[i] = key;
         logits[i] = v;
-    }
-    for (int span = 2; span <= size; span *= 2) {
-        for (int gap = span / 2; gap > 0; gap /= 2) {
-            __syncthreads();
-            for (int i = tid; i < size / 2; i += kTeacherThreads) {
-                const int lo = 2 * gap * (i / gap) + i % gap;
-                const bool up = (lo & span) == 0;
-                const unsigned long long x = keys[lo], y = keys[lo + gap];
-                if ((x > y) == up) {
-                    keys[lo] = y;
-                    keys[lo + gap] = x;
-                }
-            }
-        }
     }
     high = warp_max_nan(high);
     if (lane == 0)
-        red[warp] = high;
+        red[0][warp] = high;
     __syncthreads();
-    high = red[0];
-#pragma unroll
-    for (int w = 1; w < 4; ++w)
-        high = red[w] > high || red[w] != red[w] ? red[w] : high;
+    high = red[0][0];
+    for (int w = 1; w < warps; ++w)
+        high = red[0][w] > high || red[0][w] != red[0][w] ? red[0][w] : high;
     const bool nan_row = bad != 0;
     const bool counted = nan_row || high != -INFINITY;
-    __syncthreads();
     // the sum of a row's exponentials: each thread's in order, then lanes, then warps
     float sum = 0.0f, weighted = 0.0f;
+    int own = 0;
     if (counted) {
-        for (int i = tid; i < size; i += kTeacherThreads) {
-            if (keys[i] != ~0ull) {
-                const float d = logits[static_cast<unsigned>(keys[i])] - high;
+        for (int i = tid; i < p.top; i += threads) {
+            if (words[i] != kNone) {
+                const float d = logits[i] - high;
                 const float e = exp2_fast(d * kLog2e);
                 sum += e;
                 weighted += e > 0.0f ? e * d : e;  // a share of 0 has no entropy; NaN stays
+                ++own;
             }
         }
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        weighted += __shfl_xor_sync(0xffffffffu, weighted, d);
-    }
-    __shared__ float parts[2][4];
+    sum = butterfly_sum(sum, 32);
+    weighted = butterfly_sum(weighted, 32);
+    own = __reduce_add_sync(0xffffffffu, own);
     if (lane == 0) {
-        parts[0][warp] = sum;
-        parts[1][warp] = weighted;
+        red[1][warp] = sum;
+        red[2][warp] = weighted;
+        atomicAdd(&counted_entries, own);  // whole numbers: any order
     }
     __syncthreads();
-    sum = (parts[0][0] + parts[0][1]) + (parts[0][2] + parts[0][3]);
-    weighted = (parts[1][0] + parts[1][1]) + (parts[1][2] + parts[1][3]);
+    sum = red[1][0];
+    weighted = red[2][0];
+    for (int w = 1; w < warps; ++w) {
+        sum += red[1][w];
+        weighted += red[2][w];
+    }
+    const int entries = nan_row ? 1 : counted_entries;
     const float nan = __int_as_float(0x7FC00000);
-    for (int i = tid; i < p.top; i += kTeacherThreads) {
-        const unsigned long long key = keys[i];
-        int word = key == ~0ull ? INT_MAX : static_cast<int>(key >> 32);
-        float share = 0.0f;
-        if (nan_row) {
-            word = i == 0 ? 0 : INT_MAX;
-            share = nan;
-        } else if (!counted) {
-            word = INT_MAX;
-        } else if (word != INT_MAX) {
-            share = exp2_fast((logits[static_cast<unsigned>(key)] - high) * kLog2e) / sum;
+    if (nan_row) {
+        if (tid == 0) {
+            ordered[0] = 0;
+            shares[0] = nan;
         }
-        p.entries[row * p.top + i] = word;
-        p.shares[row * p.top + i] = share;
+    } else if (counted) {
+        for (int i = tid; i < p.top; i += threads) {
+            const uint32_t word = words[i];
+            if (word == kNone)
+                continue;
+            const int block = i >> 2;
+            int place = 0;
+            for (int j = 0; j < size >> 2; ++j) {
+                const uint4 w = reinterpret_cast<const uint4*>(words)[j];
+                const uint32_t below = word + (j < block);  // the same word at an earlier place comes first
+                place += (w.x < below) + (w.y < below) + (w.z < below) + (w.w < below);
+            }
+            for (int j = block << 2; j < i; ++j)
+                place += words[j] == word;
+            ordered[place] = word;
+            shares[place] = exp2_fast((logits[i] - high) * kLog2e) / sum;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < p.top; i += threads) {
+        const bool in = i < entries;
+        p.entries[row * p.top + i] = {in ? static_cast<int>(ordered[i]) : INT_MAX, in ? shares[i] : 0.0f};
     }
     if (p.entropy && tid == 0)
         p.entropy[row] = nan_row ? make_float2(nan, 1.0f) : make_float2(counted ? weighted / sum : 0.0f, sum);
     // the first entry at or behind each part's first column
-    for (int g = tid; g < p.parts; g += kTeacherThreads) {
-        int at = 0;
-        if (!nan_row && counted) {
-            const unsigned long long from = static_cast<unsigned long long>(g) * kHalfCols << 32;
-            int hi = size;
-            while (at < hi) {
-                const int mid = (at + hi) >> 1;
-                if (keys[mid] < from)
-                    at = mid + 1;
-                else
-                    hi = mid;
-            }
-            at = min(at, p.top);
-        } else if (nan_row) {
-            at = g > 0;
+    for (int g = tid; g < p.parts; g += threads) {
+        const uint32_t from = static_cast<uint32_t>(g) * kHalfCols;
+        int at = 0, hi = entries;
+        while (at < hi) {
+            const int mid = (at + hi) >> 1;
+            if (ordered[mid] < from)
+                at = mid + 1;
+            else
+                hi = mid;
         }
         p.first[row * p.parts + g] = static_cast<uint16_t>(at);
     }
@@ -342,10 +345,9 @@ __global__ void __launch_bounds__(kTeacherThreads) teacher_kernel(const TeacherP
 
 cudaError_t launch_teacher(const TeacherParams& p, cudaStream_t stream)
 {
-    int size = 2;
-    while (size < p.top)
-        size *= 2;
-    return launch(teacher_kernel, p.rows, kTeacherThreads, static_cast<size_t>(size) * 12, false, stream, p, size);
+    const int size = (p.top + 3) & ~3, threads = (p.top + 31) & ~31;
+    return launch(teacher_kernel, p.rows, threads < kTeacherMost ? threads : kTeacherMost,
+                  static_cast<size_t>(size) * 16, false, stream, p, size);
 }
 
 // --------------------------------------------- logits from partial sums
@@ -373,8 +375,7 @@ __global__ void __launch_bounds__(256) logits_kernel(const LogitParts l, const P
             v[3] += f.w;
         }
     }
-    const int* entry = p.entries + static_cast<int64_t>(row) * p.top;
-    const float* share = p.shares + static_cast<int64_t>(row) * p.top;
+    const Entry* entry = p.entries + static_cast<int64_t>(row) * p.top;
     const int first = p.top ? p.first[static_cast<int64_t>(row) * p.parts + part] : 0;
     if constexpr (!GRAD) {
         const auto value = [&](int at) {  // of a column of the part, in every lane
@@ -391,10 +392,10 @@ __global__ void __launch_bounds__(256) logits_kernel(const LogitParts l, const P
             }
         } else {
             for (int i = first; i < p.top; ++i) {
-                const int at = entry[i] - part * kHalfCols;
+                const int at = entry[i].word - part * kHalfCols;
                 if (at >= kHalfCols)
                     break;
-                picked = fmaf(share[i], value(at), picked);
+                picked = fmaf(entry[i].share, value(at), picked);
             }
         }
 #pragma unroll
@@ -429,10 +430,10 @@ __global__ void __launch_bounds__(256) logits_kernel(const LogitParts l, const P
             take(p.target[row] - part * kHalfCols, coef.y);
         } else {
             for (int i = first; i < p.top; ++i) {
-                const int at = entry[i] - part * kHalfCols;
+                const int at = entry[i].word - part * kHalfCols;
                 if (at >= kHalfCols)
                     break;
-                take(at, coef.y * share[i]);
+                take(at, coef.y * entry[i].share);
             }
         }
 #pragma unroll
@@ -473,24 +474,25 @@ cudaError_t launch_slope(const LogitParts& l, const SlopeParams& p, void* out, i
 }
 
 // --------------------------------------------------------- joined statistics
-// A CTA takes 16 rows; 64 half warps take every 64th part, a lane a row.
+// A CTA takes 16 rows, a lane each of half warps that take every slices-th
+// part; as many half warps, up to 64, as leave four parts each.
 __global__ void __launch_bounds__(1024) loss_kernel(const LossParams p)
 {
     __shared__ float highs[64][17], sums[64][17], picks[64][17];
     allow_next_grid();
     wait_prior_grids();
-    const int lane = threadIdx.x & 15, warp = threadIdx.x >> 4;
+    const int lane = threadIdx.x & 15, warp = threadIdx.x >> 4, slices = static_cast<int>(blockDim.x) >> 4;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + lane;
     const bool teacher = p.top != 0;
     float high = -INFINITY, sum = 0.0f, picked = 0.0f;
     if (row < p.rows) {
-        for (int g = warp; g < p.parts; g += 256) {
+        for (int g = warp; g < p.parts; g += 4 * slices) {
             float2 v[4];
             float k[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int64_t at = static_cast<int64_t>(g + 64 * j) * p.rows + row;
-                const bool in = g + 64 * j < p.parts;
+                const int64_t at = static_cast<int64_t>(g + slices * j) * p.rows + row;
+                const bool in = g + slices * j < p.parts;
                 v[j] = in ? p.part[at] : make_float2(-INFINITY, 0.0f);
                 k[j] = in && teacher ? p.picked[at] : 0.0f;
             }
@@ -510,14 +512,14 @@ __global__ void __launch_bounds__(1024) loss_kernel(const LossParams p)
     if (warp != 0 || row >= p.rows)
         return;
     high = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < 64; ++w)
+#pragma unroll 8
+    for (int w = 0; w < slices; ++w)
         high = fmaxf(high, highs[w][lane]);
     const float shift = high == -INFINITY ? 0.0f : high;
     sum = 0.0f;
     picked = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 64; ++w) {
+#pragma unroll 8
+    for (int w = 0; w < slices; ++w) {
         sum += sums[w][lane] * exp2_fast(highs[w][lane] - shift);
         picked += picks[w][lane];
     }
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(1024) loss_kernel(const LossParams p)
     // and the picked one are subtracted from one another, the product's
     // rounding with them, before anything else is added; and one logarithm
     // stands for the student's and the teacher's.
-    const bool counted = teacher ? p.entries[row * p.top] != INT_MAX : p.target[row] != p.ignore_index;
+    const bool counted = teacher ? p.entries[row * p.top].word != INT_MAX : p.target[row] != p.ignore_index;
     if (!teacher && counted) {
         const int64_t target = p.target[row];
         picked = target >= 0 && target < p.vocab ? p.picked[row] : __int_as_float(0x7FC00000);
@@ -539,7 +541,10 @@ __global__ void __launch_bounds__(1024) loss_kernel(const LossParams p)
 
 cudaError_t launch_loss(const LossParams& p, cudaStream_t stream)
 {
-    return launch(loss_kernel, (p.rows + 15) / 16, 1024, 0, false, stream, p);
+    int slices = 8;
+    while (slices < 64 && 4 * slices < p.parts)
+        slices *= 2;
+    return launch(loss_kernel, (p.rows + 15) / 16, 16 * slices, 0, false, stream, p);
 }
 
 // -------------------------------------------------------------- row factors
@@ -551,7 +556,7 @@ __device__ __forceinline__ void row_factors(const CoefParams& p, int64_t row, fl
         counted = target != p.ignore_index;
         valid = target >= 0 && target < p.vocab;
     } else {
-        counted = p.entries[row * p.top] != INT_MAX;
+        counted = p.entries[row * p.top].word != INT_MAX;
     }
     loss = counted ? p.dloss[row * p.dloss_stride] : 0.0f;
     if (counted && !valid)
