@@ -194,7 +194,8 @@ __device__ __forceinline__ TileAt tile_at(const ProductArgs<K>& a, int t)
 }
 
 template <int CG, class E>
-__global__ void __launch_bounds__(kProductThreads<E>, 1) product_kernel(const __grid_constant__ ProductArgs<typename E::Kind> a)
+__global__ void __launch_bounds__(kProductThreads<E>, 1)
+    product_kernel(const __grid_constant__ ProductArgs<typename E::Kind> a)
 {
     constexpr int kStages = product_stages<CG, E>();
     constexpr uint32_t kStageBytes = product_stage_bytes(CG);

@@ -113,13 +113,15 @@ struct EpiSplit {
 };
 
 template <>
-cudaError_t launch_product<GradProducts>(const ProductArgs<GradProducts>& a, int cta_group, int sm_count, cudaStream_t stream)
+cudaError_t launch_product<GradProducts>(const ProductArgs<GradProducts>& a, int cta_group, int sm_count,
+                                         cudaStream_t stream)
 {
     return launch_with<EpiGrad>(a, cta_group, sm_count, stream);
 }
 
 template <>
-cudaError_t launch_product<SplitProduct>(const ProductArgs<SplitProduct>& a, int cta_group, int sm_count, cudaStream_t stream)
+cudaError_t launch_product<SplitProduct>(const ProductArgs<SplitProduct>& a, int cta_group, int sm_count,
+                                         cudaStream_t stream)
 {
     return launch_with<EpiSplit>(a, cta_group, sm_count, stream);
 }

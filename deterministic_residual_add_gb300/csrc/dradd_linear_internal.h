@@ -84,7 +84,8 @@ struct alignas(8) Entry {
 // Statistics of the logits' rows, a part of 128 columns at a time.
 struct StatsParams {
     float2* part;            // [parts, rows]: maximum and sum of 2^(z scale - maximum), in base-2 units
-    float* picked;           // cross entropy: [rows], the target's logit; distillation: [parts, rows] sums of share * logit
+    float* picked;           // cross entropy: [rows], the target's logit; distillation: [parts, rows], sums of
+                             // share * logit
     const int64_t* target;   // cross entropy
     const Entry* entries;    // distillation: [rows, top] words in rising order, INT_MAX behind the last
     const uint16_t* first;   // [rows, parts] the first entry at or behind a part's first column

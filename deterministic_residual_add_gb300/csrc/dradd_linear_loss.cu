@@ -201,13 +201,15 @@ struct EpiSlope {
 };
 
 template <>
-cudaError_t launch_product<StatsProduct>(const ProductArgs<StatsProduct>& a, int cta_group, int sm_count, cudaStream_t stream)
+cudaError_t launch_product<StatsProduct>(const ProductArgs<StatsProduct>& a, int cta_group, int sm_count,
+                                         cudaStream_t stream)
 {
     return launch_with<EpiStats>(a, cta_group, sm_count, stream);
 }
 
 template <>
-cudaError_t launch_product<SlopeProduct>(const ProductArgs<SlopeProduct>& a, int cta_group, int sm_count, cudaStream_t stream)
+cudaError_t launch_product<SlopeProduct>(const ProductArgs<SlopeProduct>& a, int cta_group, int sm_count,
+                                         cudaStream_t stream)
 {
     return launch_with<EpiSlope>(a, cta_group, sm_count, stream);
 }

@@ -68,7 +68,8 @@ def check_linear(x, w, b, r, dout, act):
     (1, 8, 8, "none"), (1, 4096, 1024, "silu"), (2, 72, 24, "gelu"), (8, 264, 1000, "gelu_tanh"),
     (9, 1000, 264, "relu"), (16, 520, 136, "none"), (17, 64, 256, "silu"), (64, 4096, 264, "gelu"),
     (127, 72, 520, "relu"), (128, 128, 128, "none"), (129, 136, 248, "gelu_tanh"), (255, 64, 8, "silu"),
-    (5, 8192, 4104, "none"), (12, 4096, 4104, "silu"), (40, 2048, 20008, "silu"), (257, 2048, 264, "none"), (300, 520, 1032, "gelu"), (1000, 256, 512, "silu"), (1536, 1024, 776, "gelu_tanh")])
+    (5, 8192, 4104, "none"), (12, 4096, 4104, "silu"), (40, 2048, 20008, "silu"), (257, 2048, 264, "none"),
+    (300, 520, 1032, "gelu"), (1000, 256, 512, "silu"), (1536, 1024, 776, "gelu_tanh")])
 def test_linear(rows, inner, cols, act, dtype):
     check_linear(*linear_case(rows, inner, cols, dtype), act)
 

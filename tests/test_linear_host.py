@@ -45,7 +45,8 @@ def bwd(L, dx=A, dw=B, db=C, dout=D, x=E, w=F, bias=G, act=4, rows=40, inner=64,
 
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=2), ARG), (dict(dtype=-1), ARG), (dict(act=5), ARG), (dict(act=-1), ARG), (dict(rows=-1), SHAPE),
-    (dict(rows=1 << 31), SHAPE), (dict(rows=(1 << 31) - 4095), SHAPE), (dict(inner=0), SHAPE), (dict(inner=60), HIDDEN), (dict(cols=0), SHAPE),
+    (dict(rows=1 << 31), SHAPE), (dict(rows=(1 << 31) - 4095), SHAPE), (dict(inner=0), SHAPE),
+    (dict(inner=60), HIDDEN), (dict(cols=0), SHAPE),
     (dict(cols=28), HIDDEN), (dict(inner=1 << 24), HIDDEN), (dict(cols=1 << 24), HIDDEN),
     (dict(rows=(1 << 31) - 4096, inner=(1 << 24) - 8), SHAPE), (dict(inner=(1 << 24) - 8, cols=(1 << 24) - 8), SHAPE),
     (dict(out=0), NULL), (dict(x=0), NULL), (dict(w=0), NULL), (dict(out=A + 8), ALIGN), (dict(x=B + 2), ALIGN),
