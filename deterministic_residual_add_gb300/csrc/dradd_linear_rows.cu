@@ -566,14 +566,12 @@ __device__ __forceinline__ void row_factors(const CoefParams& p, int64_t row, fl
 
 // What dz is multiplied by before it is rounded to fp16, whose smallest
 // numbers a mean over many tokens would fall below: the power of two that
-// takes the largest factor of a row to between 2^13 and 2^14.
-__global__ void __launch_bounds__(1024) factor_kernel(const CoefParams p)
+// takes the largest factor of a row to between 2^13 and 2^14.  By a whole CTA,
+// every thread gets it.
+__device__ __forceinline__ int factor_exponent(const CoefParams& p, float* red)
 {
-    __shared__ float red[32];
-    wait_prior_grids();
-    allow_next_grid();
     float most = 0.0f;
-    for (int64_t r = threadIdx.x; r < p.rows; r += 1024) {
+    for (int64_t r = threadIdx.x; r < p.rows; r += blockDim.x) {
         float loss, both;
         row_factors(p, r, loss, both);
         const float m = (fabsf(loss) + fabsf(both)) * p.inv_temperature;
@@ -583,15 +581,28 @@ __global__ void __launch_bounds__(1024) factor_kernel(const CoefParams p)
     if ((threadIdx.x & 31) == 0)
         red[threadIdx.x >> 5] = most;
     __syncthreads();
-    if (threadIdx.x >= 32)
-        return;
-    most = warp_max(red[threadIdx.x]);
+    most = red[0];
+    for (int w = 1; w < static_cast<int>(blockDim.x) >> 5; ++w)
+        most = fmaxf(most, red[w]);
+    int e = 0;
+    if (most > 0.0f) {
+        frexpf(most, &e);
+        e = max(-100, min(100, 14 - e));
+    }
+    return e;
+}
+
+// Up to this many rows every CTA of coef_kernel finds the factor for itself,
+// which costs less than a grid in front of it (511 tokens: 1 us of a call).
+constexpr int kFactorRows = 1024;
+
+__global__ void __launch_bounds__(1024) factor_kernel(const CoefParams p)
+{
+    __shared__ float red[32];
+    wait_prior_grids();
+    allow_next_grid();
+    const int e = factor_exponent(p, red);
     if (threadIdx.x == 0) {
-        int e = 0;
-        if (most > 0.0f) {
-            frexpf(most, &e);
-            e = max(-100, min(100, 14 - e));
-        }
         p.factor[0] = ldexpf(1.0f, e);
         p.factor[1] = ldexpf(1.0f, -e);
     }
@@ -600,15 +611,27 @@ __global__ void __launch_bounds__(1024) factor_kernel(const CoefParams p)
 // A warp a row.
 __global__ void __launch_bounds__(256) coef_kernel(const CoefParams p)
 {
+    __shared__ float red[8];
     wait_prior_grids();
     allow_next_grid();
+    float factor = 1.0f;
+    if (p.factor && p.rows <= kFactorRows) {
+        const int e = factor_exponent(p, red);
+        factor = ldexpf(1.0f, e);
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            p.factor[0] = factor;
+            p.factor[1] = ldexpf(1.0f, -e);
+        }
+    } else if (p.factor) {
+        factor = p.factor[0];
+    }
     const int lane = threadIdx.x & 31;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     if (row >= p.rows)
         return;
     float loss, both;
     row_factors(p, row, loss, both);
-    const float scale = (p.factor ? p.factor[0] : 1.0f) * p.inv_temperature;
+    const float scale = factor * p.inv_temperature;
     loss *= scale;
     both *= scale;
     if (lane == 0)
@@ -632,7 +655,7 @@ __global__ void __launch_bounds__(256) coef_kernel(const CoefParams p)
 
 cudaError_t launch_coef(const CoefParams& p, cudaStream_t stream)
 {
-    if (p.factor) {
+    if (p.factor && p.rows > kFactorRows) {
         const cudaError_t e = launch(factor_kernel, 1, 1024, 0, false, stream, p);
         if (e != cudaSuccess)
             return e;

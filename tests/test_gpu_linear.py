@@ -225,7 +225,8 @@ def check_ce(x, w, target, ignore_index=-100):
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("rows,hidden,vocab", [
     (1, 8, 1), (1, 64, 1001), (2, 136, 2), (33, 264, 127), (64, 4096, 255), (100, 512, 3001), (128, 64, 256),
-    (20, 2056, 20001), (129, 72, 257), (257, 1024, 1000), (511, 256, 5001), (1024, 128, 8000)])
+    (20, 2056, 20001), (129, 72, 257), (257, 1024, 1000), (511, 256, 5001), (1024, 128, 8000),
+    (1500, 64, 300)])
 def test_cross_entropy(rows, hidden, vocab, dtype):
     check_ce(*loss_case(rows, hidden, vocab, dtype))
 
