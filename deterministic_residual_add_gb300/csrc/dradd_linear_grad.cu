@@ -18,15 +18,26 @@ __device__ __forceinline__ void add_partials(const float* p, float (&v)[16], int
         }
 }
 
+// A sector in one store where the workspace, which need lie on 16 bytes alone,
+// allows it: partials come in rows of whole eights, so their start decides for
+// all of them.
 __device__ __forceinline__ void store_partials(float* p, const uint32_t (&w)[16], int n)
 {
+    const bool sectors = reinterpret_cast<uintptr_t>(p) % 32 == 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (8 * i < n) {
-            const uint32_t half[8] = {w[8 * i],     w[8 * i + 1], w[8 * i + 2], w[8 * i + 3],
-                                      w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]};
+    for (int i = 0; i < 2; ++i) {
+        if (8 * i >= n)
+            continue;
+        const uint32_t half[8] = {w[8 * i],     w[8 * i + 1], w[8 * i + 2], w[8 * i + 3],
+                                  w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]};
+        if (sectors) {
             store_sector(p + 8 * i, half);
+        } else {
+            uint4* to = reinterpret_cast<uint4*>(p + 8 * i);
+            to[0] = make_uint4(half[0], half[1], half[2], half[3]);
+            to[1] = make_uint4(half[4], half[5], half[6], half[7]);
         }
+    }
 }
 
 // A gradient's tile: rounded, or added to the fp32 sums of earlier pieces of
