@@ -1,11 +1,13 @@
 """Matrix products and losses where they could go wrong beside the sizes of
-test_gpu_linear.py: workspaces at their least alignment."""
+test_gpu_linear.py: workspaces at their least alignment, workers that take
+several tiles."""
 import pytest
 import torch
 
 import deterministic_residual_add_gb300 as dr
 import linear_refs as lr
-from test_gpu_linear import BF16, F16, linear_case, loss_case, same, status_clear, weights_for  # noqa: F401
+from test_gpu_linear import (BF16, F16, check_ce, check_linear, linear_case, loss_case, same,  # noqa: F401
+                             status_clear, weights_for)
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +61,30 @@ def test_losses_in_a_workspace_on_16_bytes(rows, hidden, vocab):
     ws, kept = workspace_for("linear_distill_bwd", rows, hidden, vocab, 3)
     grads = dr.linear_distill_bwd(dloss, dlse, x, w, index, logits, want[1])
     assert same(dr.linear_distill_bwd(dloss, dlse, x, w, index, logits, want[1], workspace=ws), grads) and kept()
+
+
+# Tiles of 256 rows by pairs of CTAs: 170 for 76 pairs in two bands, the last row and the last 8 columns tiles of their
+# own; sums of 33 steps (the deep form of the epilogues) and of 5.  Tiles of 128 rows by single CTAs: 157 for 152.
+@pytest.mark.parametrize("act,bias,residual", [("none", False, False), ("silu", True, True), ("gelu", True, False),
+                                               ("relu", False, True)])
+@pytest.mark.parametrize("rows,inner,cols", [(2305, 2056, 4104), (2305, 264, 4104), (100, 2056, 40008),
+                                             (100, 264, 40008)])
+def test_several_tiles_a_worker(rows, inner, cols, act, bias, residual):
+    """The next tile's residual or dout comes into the box that the last tile's results leave from."""
+    x, w, b, r, dout = linear_case(rows, inner, cols, BF16 if bias else F16, bias, residual)
+    check_linear(x, w, b, r, dout, act)
+    want = dr.linear_act_add_fwd(x, w, b, r, activation=act)
+    grads = dr.linear_act_add_bwd(dout, x, w, b, activation=act)
+    for _ in range(3):
+        assert torch.equal(dr.linear_act_add_fwd(x, w, b, r, activation=act), want)
+        again = dr.linear_act_add_bwd(dout, x, w, b, activation=act)
+        assert all(p is q or torch.equal(p, q) for p, q in zip(again, grads))
+    if residual:
+        inplace = r.clone()
+        dr.linear_act_add_fwd(x, w, b, inplace, activation=act, out=inplace)
+        assert torch.equal(inplace, want)
+
+
+def test_losses_of_long_sums_in_two_bands():
+    """10 tile rows, of which L2 keeps 5 with sums this long: bands of 8 and 2."""
+    check_ce(*loss_case(2305, 16392, 700, BF16))
