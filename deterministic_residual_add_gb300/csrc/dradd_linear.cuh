@@ -16,6 +16,8 @@
 // Single CTAs serve up to 128 rows, and gradients that they divide up better.
 #pragma once
 
+#include <atomic>
+
 #include "dradd_elem.cuh"
 #include "dradd_internal.h"
 #include "dradd_linear_internal.h"
@@ -193,6 +195,39 @@ __device__ __forceinline__ TileAt tile_at(const ProductArgs<K>& a, int t)
     return r;
 }
 
+// Sums that are broken (E::kRun steps at most are added without a break): the
+// tensor cores cut off what does not fit their fp32 sum instead of rounding
+// it, so what they add up comes out short by about 1e-9 of its size a term.
+// Where results are differences of such sums, to more digits than a 16-bit
+// type has, a tile's sum is taken out of tensor memory in runs, and those are
+// added with rounding in the registers of the epilogue: 128 columns a lane.
+// These do not fit the 168 registers a thread that 12 warps share, so the four
+// warps that need few hand theirs over.
+constexpr int kOtherRegisters = 56, kSumRegisters = 224;
+constexpr int kLaunchRegisters = 65536 / 384 / 8 * 8;
+static_assert(128 * kOtherRegisters + 256 * kSumRegisters <= 384 * kLaunchRegisters,
+              "the epilogue's warps would wait for registers that there are not");
+
+// Where the run of a tile's sum that begins at step k ends.
+template <class E>
+__device__ __forceinline__ int run_end(const TileAt& at, int k)
+{
+    return E::kRun > 0 && at.k1 - k > E::kRun ? k + E::kRun : at.k1;
+}
+
+// sums += v, fp32
+__device__ __forceinline__ void add16(uint32_t (&sums)[16], const uint32_t (&v)[16])
+{
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+        float a, b;
+        add2_rn(__uint_as_float(sums[j]), __uint_as_float(sums[j + 1]), __uint_as_float(v[j]),
+                __uint_as_float(v[j + 1]), a, b);
+        sums[j] = __float_as_uint(a);
+        sums[j + 1] = __float_as_uint(b);
+    }
+}
+
 template <int CG, class E>
 __global__ void __launch_bounds__(kProductThreads<E>, 1)
     product_kernel(const __grid_constant__ ProductArgs<typename E::Kind> a)
@@ -256,7 +291,7 @@ __global__ void __launch_bounds__(kProductThreads<E>, 1)
         return false;
     };
 
-    if (warp == 0) {
+    const auto copy_operands = [&] {
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
@@ -318,8 +353,14 @@ __global__ void __launch_bounds__(kProductThreads<E>, 1)
                 }
             }
         }
-    } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
+    };
+    // A whole warp, so that what one lane issues is known to be the same for
+    // all: by a lone lane the four products of a step took 320 of its 512
+    // cycles to issue, and every run's first waits stopped the tensor cores
+    // (4096 x 4096 over 128000 words: 3838 k cycles, so 3532).
+    const auto issue_products = [&] {
+        if (rank == 0) {
+            const bool chosen = elect_one();
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
@@ -329,42 +370,51 @@ __global__ void __launch_bounds__(kProductThreads<E>, 1)
                 const uint32_t desc = product_desc(a.bf16, s.a_mn, s.b_mn, kTileRows * CG, kTileCols);
                 // 16 of the summed dimension: 32 bytes along a row, or 16 rows
                 const uint64_t step_a = s.a_mn ? 16 * 128 >> 4 : 32 >> 4, step_b = s.b_mn ? 16 * 128 >> 4 : 32 >> 4;
-                ok = wait(&bars.acc_empty[acc], acc_phase ^ 1u);
-                if (!ok)
-                    break;
-                tmem_fence_after();
-                const uint32_t d = tmem + acc * kTileCols;
-                for (int k = at.k0; k < at.k1; ++k) {
-                    ok = wait(&bars.full[stage], phase);
+                for (int k0 = at.k0; ok && k0 < at.k1; k0 = run_end<E>(at, k0)) {
+                    ok = __all_sync(0xffffffffu, wait(&bars.acc_empty[acc], acc_phase ^ 1u));
                     if (!ok)
                         break;
                     tmem_fence_after();
-                    const uint32_t from = ring + stage * kStageBytes;
-                    const uint64_t da = operand_desc(from, kBoxBytes), db = operand_desc(from + kBytesA, kBoxBytes);
+                    const uint32_t d = tmem + acc * kTileCols;
+                    const int k1 = run_end<E>(at, k0);
+                    for (int k = k0; k < k1; ++k) {
+                        ok = __all_sync(0xffffffffu, wait(&bars.full[stage], phase));
+                        if (!ok)
+                            break;
+                        tmem_fence_after();
+                        const uint32_t from = ring + stage * kStageBytes;
+                        const uint64_t da = operand_desc(from, kBoxBytes), db = operand_desc(from + kBytesA, kBoxBytes);
+                        if (chosen) {
 #pragma unroll
-                    for (int j = 0; j < kTileDepth / 16; ++j)
-                        mma_f16<CG>(d, da + j * step_a, db + j * step_b, desc, k > at.k0 || j > 0);
-                    mma_commit<CG>(&bars.empty[stage]);
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
+                            for (int j = 0; j < kTileDepth / 16; ++j)
+                                mma_f16<CG>(d, da + j * step_a, db + j * step_b, desc, k > k0 || j > 0);
+                            mma_commit<CG>(&bars.empty[stage]);
+                        }
+                        __syncwarp();
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (!ok)
+                        break;
+                    if (chosen)
+                        mma_commit<CG>(&bars.acc_full[acc]);
+                    __syncwarp();
+                    if (++acc == 2) {
+                        acc = 0;
+                        acc_phase ^= 1u;
                     }
                 }
-                if (!ok)
-                    break;
-                mma_commit<CG>(&bars.acc_full[acc]);
-                if (++acc == 2) {
-                    acc = 0;
-                    acc_phase ^= 1u;
-                }
             }
-            if (!ok) {
+            if (!ok && chosen) {
                 mma_commit<CG>(&bars.drain);
                 if (!mbar_wait_bounded(&bars.drain, 0, a.wait_limit_ns))
                     atomicOr(a.status, kDeviceStatusUndrained);
             }
         }
-    } else if (warp >= 4) {
+    };
+    const auto finish_tiles = [&] {
         constexpr int kCols = kTileCols * 4 / E::kWarps;  // a warp's columns
         const int quadrant = warp & 3, part = (warp - 4) >> 2;
         int acc = 0;
@@ -376,40 +426,97 @@ __global__ void __launch_bounds__(kProductThreads<E>, 1)
             const int row = (at.m * CG + static_cast<int>(rank)) * kTileRows + quadrant * 32 + lane;
             const int col = at.n * kTileCols + part * kCols;
             E epi(a.epi[E::Kind::kProblems > 1 ? at.problem : 0], a.bf16, row, col, at.split, staging);
-            if (!__all_sync(0xffffffffu, wait(&bars.acc_full[acc], acc_phase)))
-                break;
-            tmem_fence_after();
-            const uint32_t from = tmem + (static_cast<uint32_t>(quadrant * 32) << 16) + acc * kTileCols + part * kCols;
-            uint32_t v0[16], v1[16];
-            tmem_load16(from, v0);
-#pragma unroll 1
-            for (int c = 0; c < kCols; c += 32) {
-                tmem_wait(v0);
-                tmem_load16(from + c + 16, v1);
-                epi.columns(v0, c);
-                tmem_wait(v1);
-                if (c + 32 < kCols) {
-                    tmem_load16(from + c + 32, v0);
-                } else {
-                    tmem_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive_at(&bars.acc_empty[acc], 0);
+            const auto arrived = [&] {
+                const bool ok = __all_sync(0xffffffffu, wait(&bars.acc_full[acc], acc_phase));
+                tmem_fence_after();
+                return ok;
+            };
+            const auto let_go = [&] {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_at(&bars.acc_empty[acc], 0);
+            };
+            const auto next_accumulator = [&] {
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1u;
                 }
-                epi.columns(v1, c + 16);
+            };
+            const uint32_t own = tmem + (static_cast<uint32_t>(quadrant * 32) << 16) + part * kCols;
+            uint32_t v0[16], v1[16];
+            if constexpr (E::kRun > 0) {
+                uint32_t sums[kCols / 16][16] = {};
+                bool ok = true;
+#pragma unroll 1
+                for (int k = at.k0; k < at.k1; k = run_end<E>(at, k)) {
+                    ok = arrived();
+                    if (!ok)
+                        break;
+                    const uint32_t from = own + acc * kTileCols;
+                    tmem_load16(from, v0);
+#pragma unroll
+                    for (int i = 0; i < kCols / 16; i += 2) {
+                        tmem_wait(v0);
+                        tmem_load16(from + i * 16 + 16, v1);
+                        add16(sums[i], v0);
+                        tmem_wait(v1);
+                        if (i + 2 < kCols / 16)
+                            tmem_load16(from + i * 16 + 32, v0);
+                        else
+                            let_go();
+                        add16(sums[i + 1], v1);
+                    }
+                    next_accumulator();
+                }
+                if (!ok)
+                    break;
+                epi.whole(sums);
+            } else {
+                if (!arrived())
+                    break;
+                const uint32_t from = own + acc * kTileCols;
+                tmem_load16(from, v0);
+#pragma unroll 1
+                for (int c = 0; c < kCols; c += 32) {
+                    tmem_wait(v0);
+                    tmem_load16(from + c + 16, v1);
+                    epi.columns(v0, c);
+                    tmem_wait(v1);
+                    if (c + 32 < kCols)
+                        tmem_load16(from + c + 32, v0);
+                    else
+                        let_go();
+                    epi.columns(v1, c + 16);
+                }
+                next_accumulator();
             }
             epi.end();
             if (staging.failed) {
                 atomicOr(a.status, kDeviceStatusTimeout);
                 break;
             }
-            if (++acc == 2) {
-                acc = 0;
-                acc_phase ^= 1u;
-            }
         }
         if (E::kStaged && lane == 0)
             bulk_wait();
+    };
+    if constexpr (E::kRun > 0) {
+        if (warp < 4) {
+            give_registers<kOtherRegisters>();
+            if (warp == 0)
+                copy_operands();
+            else if (warp == 1)
+                issue_products();
+        } else {
+            take_registers<kSumRegisters>();
+            finish_tiles();
+        }
+    } else if (warp == 0) {
+        copy_operands();
+    } else if (warp == 1) {
+        issue_products();
+    } else if (warp >= 4) {
+        finish_tiles();
     }
     tmem_fence_before();
     __syncthreads();
@@ -427,6 +534,21 @@ cudaError_t launch_product_group(ProductArgs<typename E::Kind> a, int sm_count, 
     cudaError_t e = allow_all_shared<product_kernel<CG, E>>();
     if (e != cudaSuccess)
         return e;
+    if constexpr (E::kRun > 0) {
+        static_assert(kProductThreads<E> == 384);
+        // What the warps take is counted on the registers that the grid starts with.
+        static std::atomic<int> registers{0};
+        int r = registers.load(std::memory_order_acquire);
+        if (r == 0) {
+            cudaFuncAttributes attr;
+            e = cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(fn));
+            if (e != cudaSuccess)
+                return e;
+            registers.store(r = attr.numRegs, std::memory_order_release);
+        }
+        if (r != kLaunchRegisters)
+            return cudaErrorInvalidConfiguration;
+    }
     const int workers = a.tiles < sm_count / CG ? a.tiles : sm_count / CG;
     a.rounds = a.tiles0 / workers;
     a.odd = a.tiles0 % workers;

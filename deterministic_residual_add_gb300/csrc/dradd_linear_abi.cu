@@ -637,27 +637,13 @@ struct LossForwardSpace {
     }
 };
 
-// What a logit's sum is multiplied by, in units of powers of two.  The tensor cores cut off what does
-// not fit their fp32 sum, 16 terms at a time, so sums come out nearer to 0
-// the longer they are.  Measured over 4096 rows against fp64, sums of random
-// terms are short by 0.88e-6 at 1024 terms, 3.73e-6 at 4096 and 7.50e-6 at
-// 8192, sums whose terms have one sign by 1.00e-6, 4.30e-6 and 8.71e-6: 1e-9
-// of their size a term that is added without a break (the partial sums of a
-// split product are joined by rounded additions).  Losses are differences of
-// such sums.
-constexpr double kShortPerTerm = 1.0e-9;
-float logit_scale(const Plan& p, int64_t hidden, float inv_temperature)
-{
-    const int64_t each = parts_of(p.k_blocks, p.splits) * kTileDepth, run = each < hidden ? each : hidden;
-    return static_cast<float>(1.4426950408889634 * inv_temperature *
-                              (1.0 + kShortPerTerm * static_cast<double>(run)));
-}
+float logit_scale(float inv_temperature) { return static_cast<float>(1.4426950408889634 * inv_temperature); }
 
 dradd_status run_logits(const Plan& p, const Side& x, const Side& w, float* partials, bool early, int dtype,
                         cudaStream_t stream)
 {
     const SplitParams e = {partials, static_cast<int>(x.rows), static_cast<int>(up(w.rows, 8))};
-    return run_product<SplitProduct>(p, x, w, e, early, dtype, stream);
+    return run_product<LogitSplitProduct>(p, x, w, e, early, dtype, stream);
 }
 
 size_t loss_fwd_bytes(int64_t rows, int64_t hidden, int64_t vocab, int64_t top)
@@ -696,7 +682,7 @@ dradd_status loss_fwd(float* loss, float* lse, const dradd_matrix* x, const drad
     e.rows = static_cast<int>(c.rows);
     e.vocab = static_cast<int>(c.vocab);
     e.top = static_cast<int>(c.top());
-    e.scale = logit_scale(p, c.hidden, c.inv_temperature());
+    e.scale = logit_scale(c.inv_temperature());
     if (p.splits == 1) {
         DRADD_TRY(run_product<StatsProduct>(p, sx, sw, e, c.teacher != nullptr, dtype, stream));
     } else {
@@ -839,7 +825,7 @@ dradd_status loss_bwd(void* dx, void* dweight, const float* dloss, int64_t dloss
         e.vocab = static_cast<int>(width);
         e.top = f.top;
         e.col0 = static_cast<int>(col0);
-        e.scale = logit_scale(g.z, c.hidden, c.inv_temperature());
+        e.scale = logit_scale(c.inv_temperature());
         const Side sx = {x->data, r, h, x->stride, false}, sw = {w0, width, h, weight->stride, false};
         if (g.z.splits == 1) {
             DRADD_TRY(run_product<SlopeProduct>(plan_of(r, width, h, g.z.group), sx, sw, e, true, dtype, stream));

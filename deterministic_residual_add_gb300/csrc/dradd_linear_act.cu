@@ -18,6 +18,7 @@ struct EpiAct {
     using Params = ActProductParams;
     static constexpr int kWarps = DEEP ? 8 : 16;
     static constexpr bool kStaged = true;
+    static constexpr int kRun = 0;
     static constexpr int kCols = kTileCols * 4 / kWarps;
     const Params& q;
     const ActParams& p;

@@ -56,6 +56,7 @@ struct EpiGrad {
     using Params = GradParams;
     static constexpr int kWarps = 8;
     static constexpr bool kStaged = true;
+    static constexpr int kRun = 0;
     const Params& p;
     const bool bf16;
     const int row, col;
@@ -100,11 +101,13 @@ struct EpiGrad {
     __device__ __forceinline__ void end() {}
 };
 
+template <class K, int RUN>
 struct EpiSplit {
-    using Kind = SplitProduct;
+    using Kind = K;
     using Params = SplitParams;
     static constexpr int kWarps = 8;
     static constexpr bool kStaged = false;
+    static constexpr int kRun = RUN;
     const Params& p;
     const int row, col;
     float* sums;
@@ -120,6 +123,13 @@ struct EpiSplit {
         if (n > 0 && row < p.rows)
             store_partials(sums + c, bits, n);
     }
+    template <int N>
+    __device__ __forceinline__ void whole(const uint32_t (&bits)[N][16])
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            columns(bits[i], i * 16);
+    }
     __device__ __forceinline__ void end() {}
 };
 
@@ -134,7 +144,14 @@ template <>
 cudaError_t launch_product<SplitProduct>(const ProductArgs<SplitProduct>& a, int cta_group, int sm_count,
                                          cudaStream_t stream)
 {
-    return launch_with<EpiSplit>(a, cta_group, sm_count, stream);
+    return launch_with<EpiSplit<SplitProduct, 0>>(a, cta_group, sm_count, stream);
+}
+
+template <>
+cudaError_t launch_product<LogitSplitProduct>(const ProductArgs<LogitSplitProduct>& a, int cta_group, int sm_count,
+                                              cudaStream_t stream)
+{
+    return launch_with<EpiSplit<LogitSplitProduct, kLogitRun>>(a, cta_group, sm_count, stream);
 }
 
 }  // namespace dradd

@@ -51,21 +51,22 @@ private:
     }
 };
 
-// One pass over the logits as they leave the products: a row's running
-// maximum and sum of 2^(z - maximum), in units that take the temperature and
-// the exponential's base into one factor, and the logits of its words.  A
-// warp's 128 columns give one pair a row; loss_kernel joins the pairs in
-// order.  A NaN stays out of the maximum and enters the sum.
+// A row's 128 logits of a warp, once their sums are whole: their maximum and
+// the sum of 2^(z - maximum), in units that take the temperature and the
+// exponential's base into one factor, and the logits of the row's words.
+// loss_kernel joins the parts in order.  A NaN stays out of the maximum and
+// enters the sum.
 //
-// 32768 exponentials a tile and SM take 2048 cycles of the special function
-// units, the products of 4096 terms 32768: bound by the products (4096 x 4096
-// over 128000 words 2350 to 2400 us, 1790 to 1830 TFLOP/s under the power
-// limit; 92 % of the cycles with the tensor pipe active at 16384 words).
+// Losses are differences of logits, so their sums are broken.  32768
+// exponentials a tile and SM take 2048 cycles of the special function units,
+// the products of 4096 terms 32768: bound by the products (4096 x 4096 over
+// 128000 words 2350 to 2420 us, 1780 to 1830 TFLOP/s under the power limit).
 struct EpiStats {
     using Kind = StatsProduct;
     using Params = StatsParams;
     static constexpr int kWarps = 8;
     static constexpr bool kStaged = false;
+    static constexpr int kRun = kLogitRun;
     const Params& p;
     const int row, col;
     const int part;
@@ -84,45 +85,47 @@ struct EpiStats {
                               p.first[static_cast<int64_t>(row) * p.parts + part], p.top, col);
         }
     }
-    __device__ __forceinline__ void columns(const uint32_t (&bits)[16], int c)
+    __device__ __forceinline__ void whole(const uint32_t (&bits)[kHalfCols / 16][16])
     {
-        float z[16];
-        const int n = p.vocab - col - c;
+        float z[kHalfCols];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            z[j] = __uint_as_float(bits[j]);
-        while (words.next < c + 16) {
-            const int at = words.next - c;
-            float v = 0.0f;
+        for (int j = 0; j < kHalfCols; ++j)
+            z[j] = __uint_as_float(bits[j >> 4][j & 15]);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                v = j == at ? z[j] : v;
-            picked = p.top == 0 ? v : fmaf(words.weight, v, picked);
-            found = true;
-            words.advance();
+        for (int c = 0; c < kHalfCols; c += 16) {
+            while (words.next < c + 16) {
+                const int at = words.next - c;
+                float v = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    v = j == at ? z[c + j] : v;
+                picked = p.top == 0 ? v : fmaf(words.weight, v, picked);
+                found = true;
+                words.advance();
+            }
         }
-        if (n < 16) {
+        const int n = p.vocab - col;
+        if (n < kHalfCols) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
+            for (int j = 0; j < kHalfCols; ++j)
                 z[j] = j < n ? z[j] : -INFINITY;
         }
         float m[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            m[j] = fmaxf(z[j], z[j + 8]);
+        for (int j = 0; j < kHalfCols; ++j)
+            m[j & 7] = j < 8 ? z[j] : fmaxf(m[j & 7], z[j]);
 #pragma unroll
         for (int d = 4; d > 0; d >>= 1)
 #pragma unroll
             for (int j = 0; j < d; ++j)
                 m[j] = fmaxf(m[j], m[j + d]);
-        const float now = fmaxf(high, m[0] * p.scale);
-        const float shift = now == -INFINITY ? 0.0f : now;
-        float s[4] = {sum * exp2_fast(high - shift), 0.0f, 0.0f, 0.0f};
+        high = m[0] * p.scale;
+        const float shift = high == -INFINITY ? 0.0f : high;
+        float s[8] = {};
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            s[j & 3] += exp2_fast(fmaf(z[j], p.scale, -shift));
-        sum = (s[0] + s[1]) + (s[2] + s[3]);
-        high = now;
+        for (int j = 0; j < kHalfCols; ++j)
+            s[j & 7] += exp2_fast(fmaf(z[j], p.scale, -shift));
+        sum = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
     }
     __device__ __forceinline__ void end()
     {
@@ -140,13 +143,16 @@ struct EpiStats {
 // dz = coef.x exp(z - lse) - coef.y share, rounded to the operands' type: the
 // tensor cores multiply nothing wider at this rate.  The rounding of each
 // element is independent of the others' (2^-9 of it in bf16), so it adds to dx
-// and dweight about as much as their own rounding does.  Rows whose two
+// and dweight about as much as their own rounding does.  The logits' sums are
+// not broken here: what they are short by (1e-9 of a logit a term, 1e-4 of p
+// at 4096 terms and a logit of 20) is far below that rounding.  Rows whose two
 // factors are 0 are zeros whatever their logits are.
 struct EpiSlope {
     using Kind = SlopeProduct;
     using Params = SlopeParams;
     static constexpr int kWarps = 8;
     static constexpr bool kStaged = true;
+    static constexpr int kRun = 0;
     const Params& p;
     const bool bf16;
     const int row, col;

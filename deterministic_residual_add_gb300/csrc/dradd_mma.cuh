@@ -63,6 +63,29 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&v)[16])
                  : "memory");
 }
 
+// ---------------------------------------------------------------- registers
+// A warpgroup keeps N registers a thread and leaves the others of the CTA's
+// to whoever takes them, or takes as many as make N, waiting until they are
+// free.
+template <int N>
+__device__ __forceinline__ void give_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void take_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// One lane of a whole warp, always the same.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ---------------------------------------------------------- matrix products
 // Shared-memory operand of 16-bit elements in rows of 128 bytes, swizzled by
 // the copy that brought them.  K-major: the 64 elements of a row lie along

@@ -88,3 +88,45 @@ def test_several_tiles_a_worker(rows, inner, cols, act, bias, residual):
 def test_losses_of_long_sums_in_two_bands():
     """10 tile rows, of which L2 keeps 5 with sums this long: bands of 8 and 2."""
     check_ce(*loss_case(2305, 16392, 700, BF16))
+
+
+# logits summed in one go and from splits, by single CTAs and by pairs
+LONG_SUMS = [(40, 8192, 1001), (300, 8192, 500), (64, 8192, 20001), (300, 16384, 20001)]
+
+
+def check_logits(x, w, target, off):
+    """lse and loss against fp64, where every logit may be off by `off` of its size and no more."""
+    z = x.double() @ w.double().t()
+    want = torch.logsumexp(z, 1)
+    at = z.gather(1, target[:, None])[:, 0]
+    loss, lse = dr.linear_cross_entropy_fwd(x, w, target)
+    high = z.abs().amax(1)
+    # beside the logits: exponentials and their sums 2^-22, a rounding for a part joined, the exponents' own
+    bound = off * high + (-(-w.shape[0] // 128) + 96) * 2.0 ** -24 + 8 * 2.0 ** -24 * (want.abs() + high)
+    assert float(((lse - want).abs() / bound).max()) <= 1
+    bound = bound + off * high + 65 * 2.0 ** -24 * (at.abs() + want.abs() + 1)
+    assert float(((loss - (want - at)).abs() / bound).max()) <= 1
+
+
+@pytest.mark.parametrize("rows,hidden,vocab", LONG_SUMS)
+def test_logits_of_one_term_are_exact(rows, hidden, vocab):
+    """One nonzero number a row of x: its products are whole in fp32 and nothing is cut off, however long the rows.
+    Logits of some hundreds: what lies between one of them and the result are a few roundings."""
+    g = torch.Generator(device="cuda").manual_seed(hidden + vocab)
+    x = torch.zeros(rows, hidden, dtype=BF16, device="cuda")
+    x[torch.arange(rows), torch.randint(0, hidden, (rows,), generator=g, device="cuda")] = 150.0
+    w = torch.randn(vocab, hidden, generator=g, device="cuda").to(BF16)
+    check_logits(x, w, torch.randint(0, vocab, (rows,), generator=g, device="cuda"), 0.0)
+
+
+@pytest.mark.parametrize("rows,hidden,vocab", LONG_SUMS)
+def test_long_sums_of_one_sign(rows, hidden, vocab):
+    """A sum is taken out after 512 terms, 32 steps of 16.  A step cuts off at most 2^-23 of the sum so far, which with
+    terms of one sign is i / 32 of the run's: 16.5 * 2^-23 in all, of the run's sum and so of all of them.  Beside it
+    each joined run is rounded, 2^-24 of the sum so far.  Without the breaks 8192 terms lose 8.7e-6."""
+    g = torch.Generator(device="cuda").manual_seed(hidden + vocab)
+    x = torch.randn(rows, hidden, generator=g, device="cuda").abs().to(BF16)
+    w = (torch.randn(vocab, hidden, generator=g, device="cuda").abs() * (80 / hidden)).to(BF16)
+    runs = hidden // 512
+    check_logits(x, w, torch.randint(0, vocab, (rows,), generator=g, device="cuda"),
+                 16.5 * 2.0 ** -23 + (runs + 1) / 2 * 2.0 ** -24)
