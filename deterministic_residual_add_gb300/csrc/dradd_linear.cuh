@@ -32,7 +32,8 @@ constexpr int kProductThreads = 128 + 32 * E::kWarps;
 constexpr uint32_t kBoxBytes = 64 * 64 * 2;  // 64 rows of 128 bytes
 
 __host__ __device__ constexpr uint32_t product_stage_bytes(int CG) { return (2u + 4u / CG) * kBoxBytes; }
-__host__ __device__ // What 16-bit results take on their way out (and the residual, or the
+
+// What 16-bit results take on their way out (and the residual, or the
 // gradient that comes in, on its way in): a box of 32 rows and 64 columns for
 // every warp of an epilogue that is `staged`.
 //
