@@ -22,6 +22,7 @@
 #include "dradd_internal.h"
 #include "dradd_linear_internal.h"
 #include "dradd_mma.cuh"
+#include "dradd_staging.cuh"
 #include "dradd_train_internal.h"
 
 namespace dradd {
@@ -43,7 +44,6 @@ __host__ __device__ constexpr uint32_t product_stage_bytes(int CG) { return (2u 
 // 16 warps.  4096 x 4096 over 65536 words, gradients: 4002 us with 4 stages,
 // 3905 with 5; 8192 x 16384 by 4096: 682 and 656.  8192 x 512 by 8192 with
 // silu: 94.5 us with 8 warps, 65.6 with 16.
-constexpr uint32_t kStagingBox = 4096;
 constexpr int kDeepSteps = 32;
 template <class E>
 __host__ __device__ constexpr uint32_t staging_bytes()
@@ -60,80 +60,6 @@ constexpr uint32_t product_smem()
 {
     return product_stages<CG, E>() * product_stage_bytes(CG) + staging_bytes<E>() + 1024u;
 }
-
-// An epilogue warp's box.  Lane i has row i.  A 16-byte piece lies at its
-// place xor the row's lowest bits, as the tensor map's swizzle has it, and
-// eight lanes that move a piece each touch all banks.
-//
-// Results stored by the lanes themselves, a 32-byte sector of a row each,
-// took 5.6 us for a tile of 128 x 256 (8192 x 512 by 8192: 78 us); through
-// here whole lines leave.
-struct Staging {
-    uint32_t at;     // shared address
-    uint64_t* bar;   // counts what comes in
-    uint64_t limit_ns;
-    uint32_t phase;
-    int lane;
-    bool failed;
-
-    // Before the first of a box's columns is written: what was stored from
-    // here has been read.
-    __device__ __forceinline__ void acquire(int c)
-    {
-        if ((c & 63) != 0)
-            return;
-        if (lane == 0)
-            bulk_wait_read();
-        __syncwarp();
-    }
-    // The same, and then something comes in.
-    __device__ __forceinline__ void load(const CUtensorMap* map, int x, int y)
-    {
-        fence_proxy_async_smem();  // behind what was read and written here
-        if (lane == 0)
-            bulk_wait_read();
-        __syncwarp();
-        if (lane == 0) {
-            mbar_arrive_expect_tx(bar, kStagingBox);
-            copy_box<1>(at, map, x, y, bar);
-        }
-    }
-    // Waits for it; a wait that gave up ends the warp's work behind this tile,
-    // whose results are then not to be used.
-    __device__ __forceinline__ void loaded()
-    {
-        failed |= !__all_sync(0xffffffffu, mbar_wait_bounded(bar, phase, limit_ns));
-        phase ^= 1u;
-    }
-    // Columns c to c + 15 of the lane's row.
-    __device__ __forceinline__ uint32_t piece(int c, int i) const
-    {
-        return at + lane * 128u + (((((c & 63) >> 3) + i) ^ (lane & 7)) << 4);
-    }
-    __device__ __forceinline__ void read(int c, uint32_t (&w)[8]) const
-    {
-        const uint4 a = ld_shared(piece(c, 0)), b = ld_shared(piece(c, 1));
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-    }
-    __device__ __forceinline__ void write(int c, const uint32_t (&w)[8]) const
-    {
-        st_shared(piece(c, 0), w[0], w[1], w[2], w[3]);
-        st_shared(piece(c, 1), w[4], w[5], w[6], w[7]);
-    }
-    // The box that column c is the last 16 of goes out, once it is full.
-    __device__ __forceinline__ void store_full(const CUtensorMap* map, int c, int x, int y, bool inside) const
-    {
-        if ((c & 63) != 48)
-            return;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && inside) {
-            store_box(map, x + c - 48, y, at);
-            bulk_commit();
-        }
-    }
-};
 
 // Waits that have given up end every role's loop; the CTA then drains what
 // it has in flight and returns.
@@ -421,7 +347,7 @@ __global__ void __launch_bounds__(kProductThreads<E>, 1)
         int acc = 0;
         uint32_t acc_phase = 0;
         Staging staging = {ring + kStages * kStageBytes + (warp - 4) * kStagingBox,
-                           &bars.loaded[warp - 4], a.wait_limit_ns, 0, lane, false};
+                           &bars.loaded[warp - 4], a.wait_limit_ns, 0, lane, false, false};
         for (int i = 0, t; (t = tile_of(a, worker, workers, i)) >= 0; ++i) {
             const TileAt at = tile_at(a, t);
             const int row = (at.m * CG + static_cast<int>(rank)) * kTileRows + quadrant * 32 + lane;
@@ -498,8 +424,12 @@ __global__ void __launch_bounds__(kProductThreads<E>, 1)
                 break;
             }
         }
-        if (E::kStaged && lane == 0)
-            bulk_wait();
+        if (E::kStaged) {
+            if (!staging.drained() && lane == 0)
+                atomicOr(a.status, kDeviceStatusUndrained);
+            if (lane == 0)
+                bulk_wait();
+        }
     };
     if constexpr (E::kRun > 0) {
         if (warp < 4) {
