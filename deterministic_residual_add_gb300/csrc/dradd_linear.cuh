@@ -41,9 +41,9 @@ __host__ __device__ constexpr uint32_t product_stage_bytes(int CG) { return (2u 
 // Such an epilogue comes in two forms.  Sums of at least kDeepSteps steps a
 // tile leave it time, so 8 warps with two boxes of columns each do, and 32
 // more KB go to the ring, a sixth stage for a pair of CTAs; short sums want
-// 16 warps.  4096 x 4096 over 65536 words, gradients: 4002 us with 4 stages,
-// 3905 with 5; 8192 x 16384 by 4096: 682 and 656.  8192 x 512 by 8192 with
-// silu: 94.5 us with 8 warps, 65.6 with 16.
+// 16 warps and leave five.  8192 x 4096 by 4096: 142.3 us with 8 warps, 147.4
+// with 16 (the sixth stage alone is 4 us of 643 for 8192 x 16384 by 4096).
+// 8192 x 512 by 8192 with silu: 94.5 us with 8 warps, 65.6 with 16.
 constexpr int kDeepSteps = 32;
 template <class E>
 __host__ __device__ constexpr uint32_t staging_bytes()

@@ -360,6 +360,14 @@ dradd_status start(ProductArgs<K>* a, int dtype, int* sms)
     return from_cuda(device_status_ptr(&a->status));
 }
 
+// A product may be `early`, its operands read while the grid in front of it
+// runs, in two cases.  The operands are the caller's, which no grid of the call
+// writes, and some grid of this call waited for every grid before itself
+// before it let its successor start (the teacher's, the row factors'): all
+// that come behind that one start when the caller's tensors are complete,
+// whatever the grid directly in front does.  Or the grid directly in front did
+// so, and what wrote the operands came before it (the bias's, behind dz).
+// Products themselves let their successor start before they wait.
 template <class K>
 dradd_status run_product(const Plan& p, const Side& a, const Side& b, const typename K::Params& epi, bool early,
                          int dtype, cudaStream_t stream)
@@ -376,10 +384,6 @@ dradd_status run_product(const Plan& p, const Side& a, const Side& b, const type
     args.tiles0 = args.tiles = static_cast<int>(tiles);
     return from_cuda(launch_product<K>(args, p.group, sms, stream));
 }
-
-// Whether a product may be `early`: the grid before it in this call has
-// waited for every grid before itself (and so for the product's operands)
-// before it let its successor start.  The products' own early grids have not.
 
 // Two products whose results are gradients, the longer tiles first.
 struct GradProduct {

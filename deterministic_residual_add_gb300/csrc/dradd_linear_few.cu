@@ -3,8 +3,8 @@
 // The weights are read once and everything else is small, so what counts is
 // how many of their bytes are on their way.  A CTA takes R columns of the
 // output (rows of W) and brings them through a ring of four stages of 16 KB
-// by bulk copies, three CTAs an SM: 192 KB in flight whatever the warps do.
-// Its 8 warps take an eighth of each stage's inner dimension each.  The
+// by bulk copies: 64 KB a CTA in flight whatever the warps do, three CTAs an
+// SM (two from 9 rows on, whose sums take 8 KB more).  Its 8 warps take an eighth of each stage's inner dimension each.  The
 // products are warp-wide m16n8k16: the sum does not mind the order of its
 // terms, so a lane feeds the 8 neighbouring elements that it loaded as if
 // they were the four pairs that two products ask of it.  The warps' sums are

@@ -149,7 +149,8 @@ struct ProductArgs {
     int worth;               // tiles of the second problem that cost as much as one of the first
     int rounds, odd;         // tiles0 / workers and its remainder (set with the launch)
     int prefetch;            // one CTA a tile and few rows: see product_kernel
-    int early;               // the operands are complete when this grid may start; only the epilogue waits
+    int early;               // the operands are complete when this grid may start (run_product says when); only
+                             // the epilogue waits
     int bf16;
     unsigned* status;
     uint64_t wait_limit_ns;

@@ -593,7 +593,9 @@ __device__ __forceinline__ int factor_exponent(const CoefParams& p, float* red)
 }
 
 // Up to this many rows every CTA of coef_kernel finds the factor for itself,
-// which costs less than a grid in front of it (511 tokens: 1 us of a call).
+// which costs less than a grid in front of it: gradients of 128, 511 and 1000
+// tokens of 512 over 4000 words 22.5, 24.9 and 27.3 us, with that grid 24.6,
+// 26.6 and 29.9.
 constexpr int kFactorRows = 1024;
 
 __global__ void __launch_bounds__(1024) factor_kernel(const CoefParams p)
