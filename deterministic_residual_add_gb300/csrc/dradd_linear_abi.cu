@@ -456,13 +456,28 @@ Plan forward_plan(int64_t rows, int64_t inner, int64_t cols)
     return p;
 }
 
-// Whether the few rows' own kernel takes a product.  Its copies of 2 KB (from
-// 9 rows on 1 KB) cost more than the tiles' 32 KB where there are many:
-// 4096 -> 4096, 1 and 16 rows, 10.7 and 11.0 us against 13.1; 5120 -> 8192
-// 18.1 and 26.2 against 19.9; 11520 -> 11928 50.8 and 84.4 against 47.7.
+// Whether the few rows' own kernel takes a product.  A CTA of it has 8 columns
+// (from 9 rows on 16), three (two) of them share an SM, and a wave of them
+// takes 2 us however short the rows of W are, from 9 rows on 2.5 us for every
+// 1024 of them.  Times in us, that kernel's and the tiles':
+//   up to 8 rows, as many columns as 16 times the inner dimension pay off,
+//   from 1024 of it on, where tiles are split, 24 times (256 -> 4096 4.3 and
+//   6.0, -> 8192 6.4 and 6.0; 512 -> 8192 6.4 and 7.4, -> 16384 10.9 and 8.2;
+//   1024 -> 22000 14.6 and 18.9; 1136 -> 22000 19.2 and 21.9, -> 29528 25.0 and
+//   22.2), rows of W up to 8192 (8192 -> 6144 20.4 and 23.0, 10240 -> 4096
+//   23.7 and 20.4 for 8 rows), and some 50 million weights (7168 -> 7168 21.0
+//   and 24.1 for 8 rows, 8192 -> 8192 30.1 and 27.5);
+//   9 to 16 rows, while the waves are short together (4096 -> 4096 10.7 and
+//   11.3, -> 5120 in two waves 19.5 and 16.2; 5120 -> 4096 12.8 and 15.5;
+//   1024 -> 14592 10.6 and 13.0; 8192 -> 2048 20.4 and 13.6) and few (512 ->
+//   14592 in three 8.1 and 8.1, -> 32768 in seven 18.3 and 10.9).
 bool few(int64_t rows, int64_t inner, int64_t cols)
 {
-    return rows <= 8 ? inner * cols <= 1 << 25 : rows <= kFewRows && inner * cols <= 1 << 24;
+    if (rows <= 8)
+        return (cols <= (inner < 1024 ? 16 : 24) * inner || cols <= 3 * kPlanSms * 8) && inner <= 8192 &&
+               inner * cols <= 13 << 22;
+    const int64_t waves = parts_of(cols, 2 * kPlanSms * 16);
+    return rows <= kFewRows && waves <= 3 && waves * inner <= 5120;
 }
 
 dradd_status linear_shape(int64_t rows, int64_t inner, int64_t cols)

@@ -130,3 +130,11 @@ def test_long_sums_of_one_sign(rows, hidden, vocab):
     runs = hidden // 512
     check_logits(x, w, torch.randint(0, vocab, (rows,), generator=g, device="cuda"),
                  16.5 * 2.0 ** -23 + (runs + 1) / 2 * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("rows,inner,cols", [
+    (1, 8192, 6144), (8, 1024, 24576), (3, 8, 3648), (9, 5120, 4096), (16, 1024, 14592),  # their own kernel
+    (8, 10240, 520), (1, 64, 3656), (2, 512, 8200), (2, 1024, 24584), (16, 5128, 264), (9, 2048, 14600), (12, 512, 14600)])  # tiles
+def test_few_rows_on_both_sides_of_the_choice(rows, inner, cols, dtype):
+    check_linear(*linear_case(rows, inner, cols, dtype), "silu")
