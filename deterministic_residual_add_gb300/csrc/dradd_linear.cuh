@@ -559,14 +559,16 @@ __device__ __forceinline__ void prefetch_l1(const void* p)
     asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
 }
 
-// 16 consecutive values of a 16-bit row, zeros past the n inside it.
+// 16 consecutive values of a 16-bit row, zeros past the n inside it.  An
+// ordinary load: the grid in front may still write them when this one starts,
+// so they are not read-only for its lifetime.
 __device__ __forceinline__ void load16(const uint16_t* p, int n, uint32_t (&w)[8])
 {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         uint4 v = make_uint4(0, 0, 0, 0);
         if (8 * i < n)  // columns come in eights
-            v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+            v = reinterpret_cast<const uint4*>(p)[i];
         w[4 * i] = v.x;
         w[4 * i + 1] = v.y;
         w[4 * i + 2] = v.z;

@@ -74,6 +74,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 3) few_kernel(const FewParams 
     __syncthreads();
     allow_next_grid();
     wait_prior_grids();
+    // Ordinary loads: x may be what the grid in front writes, and so is not
+    // read-only as long as this one lives.
     const uint16_t* x = static_cast<const uint16_t*>(p.x);
     // Lane i < cols of warp 0 copies row i of stage s; lane 0 has said how
     // many bytes come before any of them starts.
@@ -105,7 +107,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 3) few_kernel(const FewParams 
             for (int i = 0; i < T; ++i) {
                 const int row = i * 8 + g;
                 b[u][i] = k0 + u * 32 < p.inner && row < p.act.rows  // whole blocks of 8
-                              ? __ldg(reinterpret_cast<const uint4*>(x + row * p.x_stride + k0 + u * 32))
+                              ? *reinterpret_cast<const uint4*>(x + row * p.x_stride + k0 + u * 32)
                               : none;
             }
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[at], parity, p.wait_limit_ns));

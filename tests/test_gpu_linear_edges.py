@@ -1,12 +1,12 @@
 """Matrix products and losses where they could go wrong beside the sizes of
 test_gpu_linear.py: workspaces at their least alignment, workers that take
-several tiles."""
+several tiles, few rows, long sums, rows that the call in front writes."""
 import pytest
 import torch
 
 import deterministic_residual_add_gb300 as dr
 import linear_refs as lr
-from test_gpu_linear import (BF16, F16, check_ce, check_linear, linear_case, loss_case, same,  # noqa: F401
+from test_gpu_linear import (BF16, F16, Make, check_ce, check_linear, linear_case, loss_case, same,  # noqa: F401
                              status_clear, weights_for)
 
 pytestmark = pytest.mark.gpu
@@ -138,3 +138,28 @@ def test_long_sums_of_one_sign(rows, hidden, vocab):
     (8, 10240, 520), (1, 64, 3656), (2, 512, 8200), (2, 1024, 24584), (16, 5128, 264), (9, 2048, 14600), (12, 512, 14600)])  # tiles
 def test_few_rows_on_both_sides_of_the_choice(rows, inner, cols, dtype):
     check_linear(*linear_case(rows, inner, cols, dtype), "silu")
+
+
+@pytest.mark.parametrize("rows", [1, 8, 16, 64, 200])
+def test_rows_from_the_grid_in_front(rows):
+    """x, bias and residual are written by the call in front, which a product may start beside: buffers that are used
+    again and again never give an older content."""
+    n = Make(rows, BF16)
+    inner, cols, turns = 512, 264, 24
+    w, norm = n(cols, inner, std=inner ** -0.5), n(inner)
+    inputs, biases, rest = n(turns, rows, inner), n(turns, 1, cols), n(turns, rows, cols)
+    x, b, r = torch.empty_like(inputs[0]), torch.empty_like(biases[0]), torch.empty_like(rest[0])
+    zero, zeros = torch.zeros_like(b), torch.zeros_like(r)
+    want = []
+    for i in range(turns):
+        y = dr.rmsnorm_fwd(inputs[i], norm, 1e-6)
+        torch.cuda.synchronize()
+        want.append(dr.linear_act_add_fwd(y, w, biases[i, 0], rest[i], activation="silu"))
+        torch.cuda.synchronize()
+    got = []
+    for i in range(turns):
+        dr.residual_add_fwd(biases[i], zero, residual_out=b)
+        dr.residual_add_fwd(rest[i], zeros, residual_out=r)
+        dr.rmsnorm_fwd(inputs[i], norm, 1e-6, out=x)
+        got.append(dr.linear_act_add_fwd(x, w, b[0], r, activation="silu"))
+    assert same(got, want)
