@@ -16,9 +16,9 @@
  *     void*.  Products are summed in fp32 by the tensor cores, which cut off
  *     what does not fit instead of rounding it: a sum of k terms is off by at
  *     most (k / 16 + 32) 2^-23 of the sum of their magnitudes, and comes out
- *     nearer to 0 by about 1e-9 k of its size.  The logits of the losses'
- *     forward calls are taken out after every 512 terms and joined by rounded
- *     additions.  Each stored element is rounded once.  The gradients pass
+ *     nearer to 0 by about 1e-9 k of its size.  The logits of the losses
+ *     and of their gradients are taken out after every 512 terms and joined by
+ *     rounded additions.  Each stored element is rounded once.  The gradients pass
  *     through dz, the gradient of the product's output, which is rounded to
  *     dtype before it is multiplied again (the losses' in fp16 at a power of
  *     two that puts the largest factor of a row between 2^13 and 2^14).  Calls

@@ -6,6 +6,7 @@ import torch
 
 import deterministic_residual_add_gb300 as dr
 import linear_refs as lr
+from linear_refs import HALF_STEP, norm_off
 from test_gpu_linear import (BF16, F16, Make, check_ce, check_linear, linear_case, loss_case, same,  # noqa: F401
                              status_clear, weights_for)
 
@@ -133,9 +134,28 @@ def test_long_sums_of_one_sign(rows, hidden, vocab):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("rows,hidden,vocab", LONG_SUMS)
+def test_gradients_of_long_sums_of_one_sign(rows, hidden, vocab, dtype):
+    """Logits of about 50: what each lacks is the same for all of a row, and 8.7e-6 of them would be 4.4e-4 of every
+    p, which the differences that dx is made of show many times over."""
+    g = torch.Generator(device="cuda").manual_seed(hidden + vocab)
+    x = torch.randn(rows, hidden, generator=g, device="cuda").abs().to(dtype)
+    w = (torch.randn(vocab, hidden, generator=g, device="cuda").abs() * (80 / hidden)).to(dtype)
+    target = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    dloss = torch.full((rows,), 8.0, device="cuda")
+    lse = dr.linear_cross_entropy_fwd(x, w, target)[1]
+    got = dr.linear_cross_entropy_bwd(dloss, None, x, w, target, lse)
+    z = x.double() @ w.double().t()
+    dz = torch.softmax(z, 1).scatter_add_(1, target[:, None], torch.full((rows, 1), -1.0, device="cuda").double()) * 8
+    assert norm_off(got[0], dz @ w.double()) < HALF_STEP[dtype]
+    assert norm_off(got[1], dz.t() @ x.double()) < HALF_STEP[dtype]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("rows,inner,cols", [
     (1, 8192, 6144), (8, 1024, 24576), (3, 8, 3648), (9, 5120, 4096), (16, 1024, 14592),  # their own kernel
-    (8, 10240, 520), (1, 64, 3656), (2, 512, 8200), (2, 1024, 24584), (16, 5128, 264), (9, 2048, 14600), (12, 512, 14600)])  # tiles
+    (8, 10240, 520), (1, 64, 3656), (2, 512, 8200), (2, 1024, 24584), (16, 5128, 264), (9, 2048, 14600),  # tiles
+    (12, 512, 14600)])
 def test_few_rows_on_both_sides_of_the_choice(rows, inner, cols, dtype):
     check_linear(*linear_case(rows, inner, cols, dtype), "silu")
 
