@@ -135,6 +135,9 @@ constexpr int kLaunchRegisters = 65536 / 384 / 8 * 8;
 static_assert(128 * kOtherRegisters + 256 * kSumRegisters <= 384 * kLaunchRegisters,
               "the epilogue's warps would wait for registers that there are not");
 
+// Steps of a sum that an epilogue's wait has its limit for.
+constexpr int kWaitSteps = 1 << 18;
+
 // Where the run of a tile's sum that begins at step k ends.
 template <class E>
 __device__ __forceinline__ int run_end(const TileAt& at, int k)
@@ -353,8 +356,15 @@ __global__ void __launch_bounds__(kProductThreads<E>, 1)
             const int row = (at.m * CG + static_cast<int>(rank)) * kTileRows + quadrant * 32 + lane;
             const int col = at.n * kTileCols + part * kCols;
             E epi(a.epi[E::Kind::kProblems > 1 ? at.problem : 0], a.bf16, row, col, at.split, staging);
-            const auto arrived = [&] {
-                const bool ok = __all_sync(0xffffffffu, wait(&bars.acc_full[acc], acc_phase));
+            // The limit holds for every kWaitSteps of a sum: one over 2^28 rows
+            // takes longer than a second.
+            const auto arrived = [&](int steps) {
+                bool ok = false;
+                for (int s = 0; !ok && s < steps; s += kWaitSteps)
+                    ok = mbar_wait_bounded(&bars.acc_full[acc], acc_phase, a.wait_limit_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok && lane == 0)
+                    atomicOr(a.status, kDeviceStatusTimeout);
                 tmem_fence_after();
                 return ok;
             };
@@ -377,7 +387,7 @@ __global__ void __launch_bounds__(kProductThreads<E>, 1)
                 bool ok = true;
 #pragma unroll 1
                 for (int k = at.k0; k < at.k1; k = run_end<E>(at, k)) {
-                    ok = arrived();
+                    ok = arrived(E::kRun);
                     if (!ok)
                         break;
                     const uint32_t from = own + acc * kTileCols;
@@ -400,7 +410,7 @@ __global__ void __launch_bounds__(kProductThreads<E>, 1)
                     break;
                 epi.whole(sums);
             } else {
-                if (!arrived())
+                if (!arrived(at.k1 - at.k0))
                     break;
                 const uint32_t from = own + acc * kTileCols;
                 tmem_load16(from, v0);
