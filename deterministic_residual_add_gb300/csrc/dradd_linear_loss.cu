@@ -60,7 +60,7 @@ private:
 // Losses are differences of logits, so their sums are broken.  32768
 // exponentials a tile and SM take 2048 cycles of the special function units,
 // the products of 4096 terms 32768: bound by the products (4096 x 4096 over
-// 128000 words 2350 to 2420 us, 1780 to 1830 TFLOP/s under the power limit).
+// 128000 words 2350 to 2430 us, 1770 to 1830 TFLOP/s under the power limit).
 struct EpiStats {
     using Kind = StatsProduct;
     using Params = StatsParams;

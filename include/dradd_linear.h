@@ -113,7 +113,9 @@ size_t linear_cross_entropy_fwd_workspace_bytes(int64_t rows, int64_t hidden, in
  *   dweight = dz^T x  [vocab, hidden] contiguous, or NULL
  * dloss_stride and dlse_stride are 0 (one value for all rows) or 1; dlse
  * NULL: zero.  The vocabulary is taken in pieces, whose dz are held in the
- * workspace one at a time.  A row whose two factors are 0 (an ignored token
+ * workspace one at a time: at most 256 MB, and 256 words at least.  dx's sums
+ * are read and written for every piece, so from some 65536 rows on several
+ * calls are faster.  A row whose two factors are 0 (an ignored token
  * without dlse, a loss masked by its dloss) adds nothing to dweight and has
  * a zero dx, whatever its x and lse hold.
  */
